@@ -17,10 +17,14 @@ from ._lib import (  # noqa: F401
     CFC_ERR_UNSUPPORTED, CFC_OK, CFC_OVERWRITE, CfcError, CfcParams, LIB_PATH, _check,
     declared_symbols, load_library, status_string,
 )
+from ._delta_rule import (  # noqa: F401
+    delta_rule_backward, delta_rule_forward, delta_rule_step, delta_rule_workspace,
+)
 
 __all__ = ["cfc_forward", "cfc_backward", "cfc_backward_window", "cfc_backward_windows",
            "cfc_backward_workspace", "cfc_forward_backward_workspace", "cfc_forward_backward", "reduce_axis0", "reduce_axis0_noalloc",
-           "reduce_axis0_split_workspace", "cfc_scratch_row_len", "CfcError", "load_library"]
+           "reduce_axis0_split_workspace", "cfc_scratch_row_len", "delta_rule_forward",
+           "delta_rule_backward", "delta_rule_step", "delta_rule_workspace", "CfcError", "load_library"]
 
 
 def cfc_scratch_row_len(n_in: int, n_hid: int) -> int:

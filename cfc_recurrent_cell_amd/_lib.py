@@ -35,6 +35,56 @@ class CfcParams(ctypes.Structure):
                 ("cell", ctypes.c_int)]
 
 
+CFC_TYPE_F32 = 0
+CFC_TYPE_BF16 = 1
+CFC_TYPE_F16 = 2
+
+
+class DeltaRuleShape(ctypes.Structure):
+    """delta_rule_shape_t of include/delta_rule.h."""
+    _fields_ = [("type", ctypes.c_int), ("n_seq", ctypes.c_int), ("seq_len", ctypes.c_int),
+                ("n_tokens", ctypes.c_longlong), ("offsets", ctypes.c_void_p), ("heads_k", ctypes.c_int),
+                ("heads_v", ctypes.c_int), ("dim_k", ctypes.c_int), ("dim_v", ctypes.c_int),
+                ("scale", ctypes.c_float)] + [
+                    (f"{n}_stride_{a}", ctypes.c_longlong) for n in ("q", "k", "v", "go") for a in ("t", "h")]
+
+
+def element_type(t, name: str) -> int:
+    """The library's CFC_TYPE_* of a tensor's elements."""
+    import torch
+    types = {torch.float32: CFC_TYPE_F32, torch.bfloat16: CFC_TYPE_BF16, torch.float16: CFC_TYPE_F16}
+    if t.dtype not in types:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return types[t.dtype]
+
+
+def _stream_ptr(device, stream):
+    import torch
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+class _on_device:
+    """Makes ``device`` current, and ``stream`` too where one is given: what is
+    allocated inside belongs to that stream, so memory freed while its kernels
+    still run is not handed to another one."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.contexts = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.contexts.append(torch.cuda.device(device))
+        if stream is not None:
+            self.contexts.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+
+    def __exit__(self, *why):
+        for c in reversed(self.contexts):
+            c.__exit__(*why)
+
+
 class CfcError(RuntimeError):
     def __init__(self, fn: str, code: int, text: str):
         super().__init__(f"{fn} failed with status {code}: {text}")
@@ -85,6 +135,15 @@ def load_library(path: str = LIB_PATH):
     lib.reduce_axis0_split.argtypes = [vp, ll, ll, vp, vp, ll, vp]
     lib.reduce_axis0_split_noalloc.restype = i
     lib.reduce_axis0_split_noalloc.argtypes = [vp, ll, ll, vp, vp]
+    shape = ctypes.POINTER(DeltaRuleShape)
+    for fn in (lib.delta_rule_forward_workspace, lib.delta_rule_backward_workspace):
+        fn.restype, fn.argtypes = ll, [shape]
+    lib.delta_rule_forward.restype = i
+    lib.delta_rule_forward.argtypes = [shape] + [vp] * 9 + [ll, vp]
+    lib.delta_rule_backward.restype = i
+    lib.delta_rule_backward.argtypes = [shape] + [vp] * 15 + [ll, vp]
+    lib.delta_rule_step.restype = i
+    lib.delta_rule_step.argtypes = [shape] + [vp] * 6 + [i, vp, vp, vp]
     lib.cfc_status_string.restype = ctypes.c_char_p
     lib.cfc_status_string.argtypes = [i]
     _lib = lib

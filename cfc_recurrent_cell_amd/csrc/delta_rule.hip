@@ -1,0 +1,1746 @@
+// delta_rule.hip -- gfx950 kernels and C ABI of the gated delta rule (see
+// include/delta_rule.h).
+//
+// The chunked form.  Over a chunk of C = 64 tokens that starts from state S0,
+// with G_i the sum of the chunk's decays up to token i, gamma_i = exp(G_i),
+// e_i = exp(G_63 - G_i), Gamma_ij = exp(G_i - G_j) for i >= j, the recurrence is
+//
+//   L_ij = beta_i Gamma_ij k_i.k_j  (i > j),   T = (I + L)^-1
+//   U    = T diag(beta) (V - diag(gamma) K S0)
+//   O    = scale diag(gamma) Q S0 + M U,       M_ij = scale Gamma_ij q_i.k_j (i >= j)
+//   S1   = gamma_63 S0 + K^T diag(e) U
+//
+// so a chunk is a handful of matrix products, and only S0 -> S1 runs along the
+// sequence.  All decays are exponentials of sums of non-positive numbers (for
+// g <= 0), never of their negatives, so none overflows; the sums are held in 64
+// bits, since differences of large ones count.
+//
+// Arithmetic.  Products run on the bf16 matrix cores with 32-bit sums, at 32-bit
+// accuracy: a float is the sum of three bf16 numbers of 8 bits each (cut off, not
+// rounded, so the sum is exact), and a product takes the six pairs of parts that
+// reach above 2^-24.  bf16 inputs are one part, fp16 two, float32 three.  The
+// matrix cores' own 32-bit form has 1/16 of the rate of bf16, so even six
+// products of parts are 2.7 times faster.  Only M U, which is rounded to 16 bits
+// with o, takes two parts of each where o is bf16 or fp16.
+//
+// Kernels
+//   delta_prep_kernel      for all chunks at once: T, M (transposed for the
+//       gradients) and the parts of K, Q, K^T, Q^T, all stored in the order in
+//       which the matrix cores' operands lie in a wave's registers, so that the
+//       chain below loads them 16 bytes a lane, without masks
+//   delta_chain_kernel     along each sequence, for a tile of dim_v: O and the
+//       states (forward), or U and every chunk's S0 (for the gradients)
+//   delta_reverse_kernel   the gradients' chain from the last chunk to the first
+//   delta_grads_kernel     for all chunks at once: grad_q, grad_k, grad_g, grad_beta
+//   delta_token_kernel     the recurrence token by token (a decode step, and
+//       sequences too short for chunks)
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "delta_rule.h"
+
+namespace {
+
+constexpr int kC = 64;        // tokens of a chunk
+constexpr int kThreads = 256; // 4 wave64
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// ------------------------------------------------------------- element types
+struct F32 {
+    using S = float;
+    static constexpr int NP = 3;  // bf16 parts that hold a value exactly
+    static __device__ __forceinline__ float load(S x) { return x; }
+    static __device__ __forceinline__ S store(float x) { return x; }
+};
+struct BF16 {
+    using S = uint16_t;
+    static constexpr int NP = 1;
+    static __device__ __forceinline__ float load(S x) { return __uint_as_float((uint32_t)x << 16); }
+    static __device__ __forceinline__ S store(float x) { return __builtin_bit_cast(S, (__bf16)x); }
+};
+struct F16 {
+    using S = _Float16;
+    static constexpr int NP = 2;
+    static __device__ __forceinline__ float load(S x) { return (float)x; }
+    static __device__ __forceinline__ S store(float x) { return (_Float16)x; }
+};
+
+// ------------------------------------------------------------------ bf16 parts
+// The high halves of four pairs of floats: bf16 by cutting off.
+__device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
+    return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+}
+__device__ __forceinline__ float without_high(float x) {
+    return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+}
+// x = p[0] + p[1] + ... with 8 bits in each part
+template <int NP>
+__device__ __forceinline__ void split8(float (&x)[8], u32x4 (&p)[NP]) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[n][j] = high_halves(x[2 * j], x[2 * j + 1]);
+        if (n + 1 < NP) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = without_high(x[j]);
+        }
+    }
+}
+template <int NP>
+__device__ __forceinline__ void split4(f32x4 x, u32x2 (&p)[NP]) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        p[n][0] = high_halves(x[0], x[1]);
+        p[n][1] = high_halves(x[2], x[3]);
+        if (n + 1 < NP) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = without_high(x[j]);
+        }
+    }
+}
+// c += a b over the pairs of parts that together reach ORD places of 8 bits
+template <int ORD, int NA, int NB>
+__device__ __forceinline__ void mma(const u32x4 (&a)[NA], const u32x4 (&b)[NB], f32x4& c) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (i + j < ORD)
+                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[i]),
+                                                            __builtin_bit_cast(bf16x8, b[j]), c, 0, 0, 0);
+}
+
+// Operand order.  A 16x16x32 product's operands hold, in lane l, row (column)
+// l & 15 and 8 of the 32 summed places; which 8 is free as long as both operands
+// agree.  Here group g = l >> 4 has places 4g .. 4g+3 of the first 16 and of the
+// second 16: that is how two 16x16 results lie in the registers (row 4g + r,
+// column l & 15), so a result becomes the next product's operand as it is.
+__device__ __forceinline__ int place_of(int ks, int g, int j) { return 32 * ks + (j < 4 ? 4 * g + j : 12 + 4 * g + j); }
+
+// Eight elements, row[c0 .. c0+3] and row[c1 .. c1+3], zero from D on and where !ok.
+template <class TY>
+__device__ __forceinline__ void load8(const typename TY::S* row, int c0, int c1, int D, bool ok, bool vec,
+                                      float (&x)[8]) {
+    if (vec) {  // 4 elements are one aligned load
+        if constexpr (sizeof(typename TY::S) == 4) {
+            f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+            if (ok && c0 < D) a = *reinterpret_cast<const f32x4*>(row + c0);
+            if (ok && c1 < D) b = *reinterpret_cast<const f32x4*>(row + c1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = a[j], x[j + 4] = b[j];
+        } else {
+            u32x2 a = {0, 0}, b = {0, 0};
+            if (ok && c0 < D) a = *reinterpret_cast<const u32x2*>(row + c0);
+            if (ok && c1 < D) b = *reinterpret_cast<const u32x2*>(row + c1);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t two = j < 4 ? a[j >> 1] : b[(j >> 1) & 1];
+                x[j] = TY::load(__builtin_bit_cast(typename TY::S, (uint16_t)(j & 1 ? two >> 16 : two & 0xffff)));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = j < 4 ? c0 + j : c1 + j - 4;
+            x[j] = ok && c < D ? TY::load(row[c]) : 0.0f;
+        }
+    }
+}
+
+// ------------------------------------------------------------ decays
+constexpr float kMinDecay = -1e5f;  // exp of it is 0; keeps sums of -inf finite
+// exp of a 64-bit argument, to 32 bits: what the float argument leaves out counts
+// where it is large.
+__device__ __forceinline__ float exp_of(double d) {
+    const float x = (float)d;
+    const float e = expf(x);
+    return e > 0.0f && e < INFINITY ? e + e * (float)(d - (double)x) : e;
+}
+
+// --------------------------------------------------------------- arguments
+struct Shape {
+    int n_seq, seq_len, n_tokens;
+    const int* offsets;
+    int hk, hv, dk, dv;
+    float scale;
+    long long qt, qh, kt, kh, vt, vh, gt, gh;
+    long long slots;
+    int chunks;  // of a sequence, where all have the same length
+    bool qvec, kvec, vvec, gvec;
+};
+
+// Where a value head's and a key head's parts of a chunk lie in the workspace.
+struct Space {
+    u32x4 *kf, *qf, *kt, *qt;    // a key head's: operands of K, Q, K^T, Q^T
+    u32x4 *t, *m, *tt, *mt;      // a value head's: T, M, T^T, M^T
+    struct Gates* gates;
+    float *s0, *ds, *u, *dr;     // rows [dk padded][dv padded] and [64][dv padded]
+    int dvp;                     // dim_v rounded up to 32
+};
+struct Gates {
+    double G[kC];
+    float gamma[kC], e[kC], beta[kC];
+};
+
+// Slot -> sequence, chunk.  Chunk c of sequence s has slot base(s) + c; with
+// packed tokens base(s) = offsets[s] / 64 + s, which leaves each sequence at
+// least its ceil(length / 64) slots and needs no sums over the lengths.
+struct Chunk {
+    int s, c, tok0, n;  // n <= 0: the slot is empty
+};
+__device__ __forceinline__ int offset_of(const Shape& a, int s) { return min(max(a.offsets[s], 0), a.n_tokens); }
+__device__ __forceinline__ long long base_of(const Shape& a, int s) {
+    return a.offsets ? (long long)(offset_of(a, s) / kC) + s : (long long)s * a.chunks;
+}
+__device__ __forceinline__ void span_of(const Shape& a, int s, int& tok0, int& len) {
+    if (a.offsets) {
+        tok0 = offset_of(a, s);
+        len = max(0, offset_of(a, s + 1) - tok0);
+    } else {
+        tok0 = s * a.seq_len;
+        len = a.seq_len;
+    }
+}
+__device__ __forceinline__ Chunk chunk_of(const Shape& a, long long slot) {
+    Chunk k;
+    if (a.offsets) {
+        int lo = 0, hi = a.n_seq - 1;  // the last sequence whose base is not behind the slot
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (base_of(a, mid) <= slot) lo = mid; else hi = mid - 1;
+        }
+        k.s = lo;
+    } else {
+        k.s = (int)(slot / a.chunks);
+    }
+    k.c = (int)(slot - base_of(a, k.s));
+    int tok0, len;
+    span_of(a, k.s, tok0, len);
+    k.n = k.c < 0 ? 0 : (int)min((long long)kC, (long long)len - (long long)k.c * kC);
+    k.tok0 = tok0 + k.c * kC;
+    return k;
+}
+
+// Workgroups are dealt to the 8 dies in turn; `count` logical ones in order, so
+// that neighbours (tiles of one head, heads of one key head) share a die's L2.
+__device__ __forceinline__ long long on_die(long long block, long long count) {
+    const long long each = (count + 7) / 8;
+    return (block % 8) * each + block / 8;
+}
+inline unsigned dealt(long long count) { return (unsigned)((count + 7) / 8 * 8); }
+
+__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// =========================================================== all chunks: prep
+// grid: (slots, hv + hk).  The first hv make T and M of a value head, the others
+// the operands of a key head.
+template <class TY, int KS, bool GRAD>
+__global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, const typename TY::S* __restrict__ q,
+                                                              const typename TY::S* __restrict__ k,
+                                                              const float* __restrict__ g,
+                                                              const float* __restrict__ beta) {
+    using S = typename TY::S;
+    constexpr int NP = TY::NP;
+    constexpr int NM = GRAD || NP == 3 ? 3 : 2;  // parts of M
+    const long long slot = blockIdx.x;
+    const Chunk ch = chunk_of(a, slot);
+    if (ch.n <= 0) return;
+    const int t = threadIdx.x, lane = t & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
+
+    if ((int)blockIdx.y >= a.hv) {  // operands of a key head
+        const int h = blockIdx.y - a.hv;
+        const long long ks0 = slot * a.hk + h;
+        const S* kp = k + (long long)ch.tok0 * a.kt + h * a.kh;
+        const S* qp = q + (long long)ch.tok0 * a.qt + h * a.qh;
+        for (int f = wv; f < 4 * KS; f += 4) {  // rows are tokens
+            const int row = 16 * (f / KS) + col, ks = f % KS;
+            const int c0 = place_of(ks, grp, 0), c1 = place_of(ks, grp, 4);
+            float x[8];
+            u32x4 p[NP];
+            load8<TY>(kp + row * a.kt, c0, c1, a.dk, row < ch.n, a.kvec, x);
+            split8<NP>(x, p);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) w.kf[((ks0 * 4 * KS + f) * NP + n) * 64 + lane] = p[n];
+            load8<TY>(qp + row * a.qt, c0, c1, a.dk, row < ch.n, a.qvec, x);
+            split8<NP>(x, p);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) w.qf[((ks0 * 4 * KS + f) * NP + n) * 64 + lane] = p[n];
+        }
+        for (int f = wv; f < 4 * KS; f += 4) {  // rows are places of dim_k: two row tiles of 16 for each ks
+            const int row = 16 * (f >> 1) + col, ts = f & 1;
+            const bool ok = row < a.dk;
+            float x[8];
+            u32x4 p[NP];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int tok = place_of(ts, grp, j);
+                x[j] = ok && tok < ch.n ? TY::load(kp[tok * a.kt + row]) : 0.0f;
+            }
+            split8<NP>(x, p);
+#pragma unroll
+            for (int n = 0; n < NP; ++n) w.kt[((ks0 * 4 * KS + f) * NP + n) * 64 + lane] = p[n];
+            if (GRAD) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int tok = place_of(ts, grp, j);
+                    x[j] = ok && tok < ch.n ? TY::load(qp[tok * a.qt + row]) : 0.0f;
+                }
+                split8<NP>(x, p);
+#pragma unroll
+                for (int n = 0; n < NP; ++n) w.qt[((ks0 * 4 * KS + f) * NP + n) * 64 + lane] = p[n];
+            }
+        }
+        return;
+    }
+
+    __shared__ double G[kC];
+    __shared__ float Bt[kC];
+    __shared__ __align__(16) float L[kC][kC + 4];
+    __shared__ __align__(16) float X[kC][kC + 4];
+    __shared__ __align__(16) float Mx[kC][kC + 4];
+    const int h = blockIdx.y;
+    const int hk = h / (a.hv / a.hk);
+    const long long vs = slot * a.hv + h;
+    if (wv == 0) {
+        const long long at = (long long)(ch.tok0 + lane) * a.hv + h;
+        const float gv = lane < ch.n ? g[at] : 0.0f;
+        double G0 = gv < kMinDecay ? kMinDecay : gv;
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(G0, off);
+            if (lane >= off) G0 += o;
+        }
+        const double last = __shfl(G0, 63);
+        const float b = lane < ch.n ? beta[at] : 0.0f;
+        G[lane] = G0;
+        Bt[lane] = b;
+        Gates& ga = w.gates[vs];
+        ga.G[lane] = G0;
+        ga.gamma[lane] = exp_of(G0);
+        ga.e[lane] = exp_of(last - G0);
+        ga.beta[lane] = b;
+    }
+    // k.k and q.k: wave wv has row tile wv of k.k and row tile 3 - wv of q.k, five
+    // tiles of the lower triangle for each wave
+    const S* kp = k + (long long)ch.tok0 * a.kt + hk * a.kh;
+    const S* qp = q + (long long)ch.tok0 * a.qt + hk * a.qh;
+    f32x4 kk[4], qk[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) kk[i] = f32x4{0, 0, 0, 0}, qk[i] = f32x4{0, 0, 0, 0};
+    const int qrow = 3 - wv;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        const int c0 = place_of(ks, grp, 0), c1 = place_of(ks, grp, 4);
+        u32x4 qa[NP], ka[NP];
+        float x[8];
+        load8<TY>(qp + (16 * qrow + col) * a.qt, c0, c1, a.dk, 16 * qrow + col < ch.n, a.qvec, x);
+        split8<NP>(x, qa);
+        load8<TY>(kp + (16 * wv + col) * a.kt, c0, c1, a.dk, 16 * wv + col < ch.n, a.kvec, x);
+        split8<NP>(x, ka);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i > wv && i > qrow) continue;
+            u32x4 kb[NP];
+            load8<TY>(kp + (16 * i + col) * a.kt, c0, c1, a.dk, 16 * i + col < ch.n, a.kvec, x);
+            split8<NP>(x, kb);
+            if (i <= wv) mma<3>(ka, kb, kk[i]);
+            if (i <= qrow) mma<3>(qa, kb, qk[i]);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int c = 16 * i + col;
+            if (i <= wv) {
+                const int row = 16 * wv + 4 * grp + r;
+                L[row][c] = c < row ? Bt[row] * exp_of(G[row] - G[c]) * kk[i][r] : 0.0f;
+            }
+            const int row = 16 * qrow + 4 * grp + r;
+            Mx[row][c] = c <= row ? a.scale * exp_of(G[row] - G[c]) * qk[i][r] : 0.0f;
+        }
+    }
+    __syncthreads();
+    // The 16 x 16 blocks on the diagonal, one for each wave: column `col` of
+    // (I + L)^-1 by substitution, the updates of all later rows at once.
+    {
+        const int r0 = 16 * wv;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.0f : 0.0f;
+#pragma unroll
+        for (int m = 0; m < 15; ++m)
+#pragma unroll
+            for (int i = m + 1; i < 16; ++i) x[i] -= L[r0 + i][r0 + m] * x[m];
+        if (grp == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) X[r0 + i][r0 + col] = x[i];
+        }
+    }
+    __syncthreads();
+    // Below it, block column wv: X_rc = -X_rr sum_m L_rm X_mc, on the 32-bit matrix
+    // cores; summed place 4 s + ... of a product is row 4 grp + s, so a result is
+    // the next product's right operand as it lies.
+    {
+        f32x4 xc[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) xc[0][r] = X[16 * wv + 4 * grp + r][16 * wv + col];
+#pragma unroll
+        for (int d = 1; d < 4; ++d) {
+            const int rt = wv + d;
+            if (rt < 4) {
+                f32x4 y = {0, 0, 0, 0}, z = {0, 0, 0, 0};
+#pragma unroll
+                for (int m = 0; m < d; ++m) {
+                    const f32x4 l = *reinterpret_cast<const f32x4*>(&L[16 * rt + col][16 * (wv + m) + 4 * grp]);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) y = __builtin_amdgcn_mfma_f32_16x16x4f32(l[s], xc[m][s], y, 0, 0, 0);
+                }
+                const f32x4 l = *reinterpret_cast<const f32x4*>(&X[16 * rt + col][16 * rt + 4 * grp]);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f32_16x16x4f32(-l[s], y[s], z, 0, 0, 0);
+                xc[d] = z;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) X[16 * rt + 4 * grp + r][16 * wv + col] = z[r];
+            }
+            if (d <= wv) {  // the blocks above the diagonal
+#pragma unroll
+                for (int r = 0; r < 4; ++r) X[16 * (wv - d) + 4 * grp + r][16 * wv + col] = 0.0f;
+            }
+        }
+    }
+    __syncthreads();
+    // Operands, row tile rt and half ts of the summed tokens; those that are zero
+    // (above the diagonal, below it in the transposed ones) are not stored.
+    for (int f = wv; f < 8; f += 4) {
+        const int rt = f >> 1, ts = f & 1, row = 16 * rt + col;
+        float x[8];
+        if (ts <= (rt >> 1)) {
+            u32x4 p[3];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = X[row][place_of(ts, grp, j)];
+            split8<3>(x, p);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) w.t[((vs * 8 + f) * 3 + n) * 64 + lane] = p[n];
+            if (!GRAD) {
+                u32x4 pm[NM];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = Mx[row][place_of(ts, grp, j)];
+                split8<NM>(x, pm);
+#pragma unroll
+                for (int n = 0; n < NM; ++n) w.m[((vs * 8 + f) * NM + n) * 64 + lane] = pm[n];
+            }
+        }
+        if (GRAD && ts >= (rt >> 1)) {
+            u32x4 p[3];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = X[place_of(ts, grp, j)][row];
+            split8<3>(x, p);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) w.tt[((vs * 8 + f) * 3 + n) * 64 + lane] = p[n];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = Mx[place_of(ts, grp, j)][row];
+            split8<3>(x, p);
+#pragma unroll
+            for (int n = 0; n < 3; ++n) w.mt[((vs * 8 + f) * 3 + n) * 64 + lane] = p[n];
+        }
+    }
+}
+
+// ================================================ along a sequence: the states
+// A workgroup has a head's tile of 16 NCT columns of dim_v; wave wv has token tile
+// wv of the chunk and KS / 2 row tiles of the state, which stays in its registers
+// in 32 bits.  What all waves need of each other (parts of S, of the bracket
+// before T, of U) goes through LDS in operand order.
+template <int N, int NCT, int KSN>
+struct Exchange {  // [part][ks][column tile][lane]
+    u32x4 v[N][KSN][NCT][64];
+    // a result of row tile rt becomes half of the operand of its pair of row tiles
+    __device__ __forceinline__ void put(int rt, int ct, int lane, const u32x2 (&p)[N]) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) reinterpret_cast<u32x2*>(&v[n][rt >> 1][ct][lane])[rt & 1] = p[n];
+    }
+    __device__ __forceinline__ void get(int ks, int ct, int lane, u32x4 (&p)[N]) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) p[n] = v[n][ks][ct][lane];
+    }
+};
+
+template <int A, int B>
+__device__ __forceinline__ void copy(u32x4 (&to)[A][B], const u32x4 (&from)[A][B]) {
+#pragma unroll
+    for (int i = 0; i < A; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j) to[i][j] = from[i][j];
+}
+
+template <class TY, int KS, bool GRAD>
+struct ChainOps {  // a chunk's operands of one wave
+    static constexpr int NP = TY::NP, NM = NP == 3 ? 3 : 2;
+    u32x4 kf[KS][NP], qf[GRAD ? 1 : KS][NP], kt[KS / 2][2][NP], t[2][3], m[GRAD ? 1 : 2][NM];
+    f32x4 gamma, e, beta;
+    float last;
+    __device__ __forceinline__ void load(const Space& w, long long ks0, long long vs, int wv, int lane) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                kf[ks][n] = w.kf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
+                if constexpr (!GRAD) qf[ks][n] = w.qf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
+            }
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i)
+#pragma unroll
+            for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+                    kt[i][ts][n] = w.kt[((ks0 * 4 * KS + (wv * (KS / 2) + i) * 2 + ts) * NP + n) * 64 + lane];
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
+            if (ts <= (wv >> 1)) {
+#pragma unroll
+                for (int n = 0; n < 3; ++n) t[ts][n] = w.t[((vs * 8 + wv * 2 + ts) * 3 + n) * 64 + lane];
+                if constexpr (!GRAD) {
+#pragma unroll
+                    for (int n = 0; n < NM; ++n) m[ts][n] = w.m[((vs * 8 + wv * 2 + ts) * NM + n) * 64 + lane];
+                }
+            }
+        const Gates& ga = w.gates[vs];
+        const int r = 16 * wv + 4 * (lane >> 4);
+        gamma = *reinterpret_cast<const f32x4*>(&ga.gamma[r]);
+        e = *reinterpret_cast<const f32x4*>(&ga.e[r]);
+        beta = *reinterpret_cast<const f32x4*>(&ga.beta[r]);
+        last = ga.gamma[kC - 1];
+    }
+    __device__ __forceinline__ void take(const ChainOps& x) {
+        copy(kf, x.kf);
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) copy(kt[i], x.kt[i]);
+        copy(t, x.t);
+        if constexpr (!GRAD) {
+            copy(qf, x.qf);
+            copy(m, x.m);
+        }
+        gamma = x.gamma, e = x.e, beta = x.beta, last = x.last;
+    }
+};
+
+// Values of token tile wv at columns n0 + 16 ct + (lane & 15), as a result lies.
+template <class TY, int NCT>
+__device__ __forceinline__ void load_tile(const typename TY::S* p, long long stride, int n, int n0, int D, int wv,
+                                          int lane, typename TY::S (&x)[NCT][4]) {
+#pragma unroll
+    for (int ct = 0; ct < NCT; ++ct) {
+        const int c = n0 + 16 * ct + (lane & 15);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * wv + 4 * (lane >> 4) + r;
+            x[ct][r] = row < n && c < D ? p[row * stride + c] : (typename TY::S)0;
+        }
+    }
+}
+
+template <class TY, int KS, int NCT, bool GRAD>
+__global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w, const typename TY::S* __restrict__ v,
+                                                               const float* initial, typename TY::S* __restrict__ o,
+                                                               float* final_state) {
+    using S = typename TY::S;
+    using Ops = ChainOps<TY, KS, GRAD>;
+    constexpr int NP = TY::NP, NM = Ops::NM, NR = KS / 2;
+    constexpr int ORDO = NP == 3 ? 3 : 2;  // o is rounded to 16 bits or to 32
+    __shared__ Exchange<3, NCT, KS> xs;
+    __shared__ Exchange<3, NCT, 2> xp, xe;
+    __shared__ Exchange<GRAD ? 1 : NM, GRAD ? 1 : NCT, 2> xu;
+    // for the gradients all of the padded columns: the workspace's rows are read whole
+    const int tiles = ((GRAD ? w.dvp : a.dv) + 16 * NCT - 1) / (16 * NCT);
+    const long long count = (long long)a.n_seq * a.hv * tiles;
+    const long long at = on_die(blockIdx.x, count);
+    if (at >= count || blockIdx.x / 8 >= (count + 7) / 8) return;
+    const int n0 = (int)(at % tiles) * 16 * NCT;
+    const long long sh = at / tiles;
+    const int h = (int)(sh % a.hv), s = (int)(sh / a.hv), hk = h / (a.hv / a.hk);
+    const int lane = threadIdx.x & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
+    int tok0, len;
+    span_of(a, s, tok0, len);
+    const int chunks = (int)(((long long)len + kC - 1) / kC);
+    const long long base = base_of(a, s);
+
+    f32x4 st[NR][NCT];
+    const long long sbase = sh * a.dk * a.dv;
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * (wv * NR + i) + 4 * grp + r, c = n0 + 16 * ct + col;
+                st[i][ct][r] = initial && row < a.dk && c < a.dv ? initial[sbase + (long long)row * a.dv + c] : 0.0f;
+            }
+    Ops cur;
+    S vc[NCT][4];
+    if (chunks > 0) {
+        cur.load(w, base * a.hk + hk, base * a.hv + h, wv, lane);
+        load_tile<TY, NCT>(v + (long long)tok0 * a.vt + h * a.vh, a.vt, len, n0, a.dv, wv, lane, vc);
+    }
+    for (int c = 0; c < chunks; ++c) {
+        const int n = min(kC, len - c * kC);
+        const long long vs = (base + c) * a.hv + h;
+        // the state's parts, for all waves
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                u32x2 p[3];
+                split4<3>(st[i][ct], p);
+                xs.put(wv * NR + i, ct, lane, p);
+                if (GRAD) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        w.s0[(vs * 32 * KS + 16 * (wv * NR + i) + 4 * grp + r) * w.dvp + n0 + 16 * ct + col] =
+                            st[i][ct][r];
+                }
+            }
+        Ops nxt;
+        S vn[NCT][4];
+        {  // the next chunk's operands (the last one's again, at the end)
+            const int cn = min(c + 1, chunks - 1);
+            nxt.load(w, (base + cn) * a.hk + hk, (base + cn) * a.hv + h, wv, lane);
+            load_tile<TY, NCT>(v + (long long)(tok0 + cn * kC) * a.vt + h * a.vh, a.vt, len - cn * kC, n0, a.dv, wv,
+                               lane, vn);
+        }
+        __syncthreads();
+        f32x4 ks_[NCT], qs[NCT];
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) ks_[ct] = f32x4{0, 0, 0, 0}, qs[ct] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                u32x4 b[3];
+                xs.get(ks, ct, lane, b);
+                mma<3>(cur.kf[ks], b, ks_[ct]);
+                if constexpr (!GRAD) mma<ORDO>(cur.qf[ks], b, qs[ct]);
+            }
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            f32x4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = cur.beta[r] * (TY::load(vc[ct][r]) - cur.gamma[r] * ks_[ct][r]);
+            u32x2 p[3];
+            split4<3>(x, p);
+            xp.put(wv, ct, lane, p);
+        }
+        __syncthreads();
+        f32x4 u[NCT];
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            u[ct] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int ts = 0; ts < 2; ++ts)
+                if (ts <= (wv >> 1)) {
+                    u32x4 b[3];
+                    xp.get(ts, ct, lane, b);
+                    mma<3>(cur.t[ts], b, u[ct]);
+                }
+            u32x2 p[3];
+            split4<3>(u[ct] * cur.e, p);
+            xe.put(wv, ct, lane, p);
+            if constexpr (GRAD) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    w.u[(vs * kC + 16 * wv + 4 * grp + r) * w.dvp + n0 + 16 * ct + col] = u[ct][r];
+            } else {
+                u32x2 pu[NM];
+                split4<NM>(u[ct], pu);
+                xu.put(wv, ct, lane, pu);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) st[i][ct] *= cur.last;
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                u32x4 b[3];
+                xe.get(ts, ct, lane, b);
+#pragma unroll
+                for (int i = 0; i < NR; ++i) mma<3>(cur.kt[i][ts], b, st[i][ct]);
+            }
+        if constexpr (!GRAD) {
+            S* op = o + ((long long)(tok0 + c * kC) * a.hv + h) * a.dv;
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                f32x4 x = qs[ct] * cur.gamma * a.scale;
+#pragma unroll
+                for (int ts = 0; ts < 2; ++ts)
+                    if (ts <= (wv >> 1)) {
+                        u32x4 b[NM];
+                        xu.get(ts, ct, lane, b);
+                        mma<ORDO>(cur.m[ts], b, x);
+                    }
+                const int cc = n0 + 16 * ct + col;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * wv + 4 * grp + r;
+                    if (row < n && cc < a.dv) op[(long long)row * a.hv * a.dv + cc] = TY::store(x[r]);
+                }
+            }
+        }
+        cur.take(nxt);
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) vc[ct][r] = vn[ct][r];
+    }
+    if (final_state) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * (wv * NR + i) + 4 * grp + r, c = n0 + 16 * ct + col;
+                    if (row < a.dk && c < a.dv) final_state[sbase + (long long)row * a.dv + c] = st[i][ct][r];
+                }
+    }
+}
+
+// ========================================= along a sequence: the gradients' chain
+// With dS the gradient of the chunk's last state and dO that of O,
+//   dU  = M^T dO + diag(e) K dS           dR = T^T dU   (of the bracket, by beta)
+//   dV  = diag(beta) dR
+//   dS0 = gamma_63 dS + scale Q^T diag(gamma) dO - K^T diag(gamma beta) dR
+// The same tiles and exchanges as the states' chain, from the last chunk on.
+template <class TY, int KS>
+struct ReverseOps {
+    static constexpr int NP = TY::NP;
+    u32x4 kf[KS][NP], kt[KS / 2][2][NP], qt[KS / 2][2][NP], tt[2][3], mt[2][3];
+    f32x4 gamma, e, beta;
+    float last;
+    __device__ __forceinline__ void load(const Space& w, long long ks0, long long vs, int wv, int lane) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int n = 0; n < NP; ++n) kf[ks][n] = w.kf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i)
+#pragma unroll
+            for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    const long long f = ((ks0 * 4 * KS + (wv * (KS / 2) + i) * 2 + ts) * NP + n) * 64 + lane;
+                    kt[i][ts][n] = w.kt[f];
+                    qt[i][ts][n] = w.qt[f];
+                }
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
+            if (ts >= (wv >> 1)) {
+#pragma unroll
+                for (int n = 0; n < 3; ++n) {
+                    tt[ts][n] = w.tt[((vs * 8 + wv * 2 + ts) * 3 + n) * 64 + lane];
+                    mt[ts][n] = w.mt[((vs * 8 + wv * 2 + ts) * 3 + n) * 64 + lane];
+                }
+            }
+        const Gates& ga = w.gates[vs];
+        const int r = 16 * wv + 4 * (lane >> 4);
+        gamma = *reinterpret_cast<const f32x4*>(&ga.gamma[r]);
+        e = *reinterpret_cast<const f32x4*>(&ga.e[r]);
+        beta = *reinterpret_cast<const f32x4*>(&ga.beta[r]);
+        last = ga.gamma[kC - 1];
+    }
+    __device__ __forceinline__ void take(const ReverseOps& x) {
+        copy(kf, x.kf);
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) copy(kt[i], x.kt[i]), copy(qt[i], x.qt[i]);
+        copy(tt, x.tt);
+        copy(mt, x.mt);
+        gamma = x.gamma, e = x.e, beta = x.beta, last = x.last;
+    }
+};
+
+template <int NP, int NCT, int KS>
+struct ReverseLds {
+    Exchange<3, NCT, KS> s;
+    Exchange<NP, NCT, 2> o;       // dO
+    Exchange<3, NCT, 2> g, u, r;  // scale gamma dO; dU; -gamma beta dR
+};
+
+template <class TY, int KS, int NCT>
+__global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space w,
+                                                                 const typename TY::S* __restrict__ go,
+                                                                 const float* grad_final,
+                                                                 typename TY::S* __restrict__ gv,
+                                                                 float* grad_initial) {
+    using S = typename TY::S;
+    constexpr int NP = TY::NP, NR = KS / 2;
+    extern __shared__ __align__(16) unsigned char lds[];
+    auto& sh_ = *reinterpret_cast<ReverseLds<NP, NCT, KS>*>(lds);
+    auto& xs = sh_.s;
+    auto& xo = sh_.o;
+    auto &xg = sh_.g, &xu = sh_.u, &xr = sh_.r;
+    const int tiles = w.dvp / (16 * NCT);
+    const long long count = (long long)a.n_seq * a.hv * tiles;
+    const long long at = on_die(blockIdx.x, count);
+    if (at >= count || blockIdx.x / 8 >= (count + 7) / 8) return;
+    const int n0 = (int)(at % tiles) * 16 * NCT;
+    const long long sh = at / tiles;
+    const int h = (int)(sh % a.hv), s = (int)(sh / a.hv), hk = h / (a.hv / a.hk);
+    const int lane = threadIdx.x & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
+    int tok0, len;
+    span_of(a, s, tok0, len);
+    const int chunks = (int)(((long long)len + kC - 1) / kC);
+    const long long base = base_of(a, s);
+
+    f32x4 st[NR][NCT];
+    const long long sbase = sh * a.dk * a.dv;
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * (wv * NR + i) + 4 * grp + r, c = n0 + 16 * ct + col;
+                st[i][ct][r] =
+                    grad_final && row < a.dk && c < a.dv ? grad_final[sbase + (long long)row * a.dv + c] : 0.0f;
+            }
+    ReverseOps<TY, KS> cur;
+    S oc[NCT][4];
+    if (chunks > 0) {
+        const int c = chunks - 1;
+        cur.load(w, (base + c) * a.hk + hk, (base + c) * a.hv + h, wv, lane);
+        load_tile<TY, NCT>(go + (long long)(tok0 + c * kC) * a.gt + h * a.gh, a.gt, len - c * kC, n0, a.dv, wv, lane,
+                           oc);
+    }
+    for (int c = chunks - 1; c >= 0; --c) {
+        const int n = min(kC, len - c * kC);
+        const long long vs = (base + c) * a.hv + h;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                u32x2 p[3];
+                split4<3>(st[i][ct], p);
+                xs.put(wv * NR + i, ct, lane, p);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    w.ds[(vs * 32 * KS + 16 * (wv * NR + i) + 4 * grp + r) * w.dvp + n0 + 16 * ct + col] =
+                        st[i][ct][r];
+            }
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            f32x4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = TY::load(oc[ct][r]);
+            u32x2 p[NP], p3[3];
+            split4<NP>(x, p);
+            xo.put(wv, ct, lane, p);
+            split4<3>(x * cur.gamma * a.scale, p3);
+            xg.put(wv, ct, lane, p3);
+        }
+        ReverseOps<TY, KS> nxt;
+        S on[NCT][4];
+        {  // the chunk before (the first one's again, at the end)
+            const int cn = max(c - 1, 0);
+            nxt.load(w, (base + cn) * a.hk + hk, (base + cn) * a.hv + h, wv, lane);
+            load_tile<TY, NCT>(go + (long long)(tok0 + cn * kC) * a.gt + h * a.gh, a.gt, len - cn * kC, n0, a.dv, wv,
+                               lane, on);
+        }
+        __syncthreads();
+        f32x4 x[NCT];
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) x[ct] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                u32x4 b[3];
+                xs.get(ks, ct, lane, b);
+                mma<3>(cur.kf[ks], b, x[ct]);
+            }
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            x[ct] *= cur.e;
+#pragma unroll
+            for (int ts = 0; ts < 2; ++ts)
+                if (ts >= (wv >> 1)) {
+                    u32x4 b[NP];
+                    xo.get(ts, ct, lane, b);
+                    mma<3>(cur.mt[ts], b, x[ct]);
+                }
+            u32x2 p[3];
+            split4<3>(x[ct], p);
+            xu.put(wv, ct, lane, p);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) st[i][ct] *= cur.last;
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            f32x4 y = {0, 0, 0, 0};
+#pragma unroll
+            for (int ts = 0; ts < 2; ++ts)
+                if (ts >= (wv >> 1)) {
+                    u32x4 b[3];
+                    xu.get(ts, ct, lane, b);
+                    mma<3>(cur.tt[ts], b, y);
+                }
+            const f32x4 dv = y * cur.beta;
+            u32x2 p[3];
+            split4<3>(-(dv * cur.gamma), p);
+            xr.put(wv, ct, lane, p);
+            const int cc = n0 + 16 * ct + col;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * wv + 4 * grp + r;
+                w.dr[(vs * kC + row) * w.dvp + cc] = y[r];
+                if (row < n && cc < a.dv)
+                    gv[((long long)(tok0 + c * kC + row) * a.hv + h) * a.dv + cc] = TY::store(dv[r]);
+            }
+        }
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                u32x4 b[3];
+                xg.get(ts, ct, lane, b);
+#pragma unroll
+                for (int i = 0; i < NR; ++i) mma<3>(cur.qt[i][ts], b, st[i][ct]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                u32x4 b[3];
+                xr.get(ts, ct, lane, b);
+#pragma unroll
+                for (int i = 0; i < NR; ++i) mma<3>(cur.kt[i][ts], b, st[i][ct]);
+            }
+        cur.take(nxt);
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) oc[ct][r] = on[ct][r];
+    }
+    if (grad_initial) {
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * (wv * NR + i) + 4 * grp + r, c = n0 + 16 * ct + col;
+                    if (row < a.dk && c < a.dv) grad_initial[sbase + (long long)row * a.dv + c] = st[i][ct][r];
+                }
+    }
+}
+
+// ====================================================== all chunks: the gradients
+// With dM = dO U^T and dL = -dR U^T (their lower triangles), F = scale Gamma dM,
+// E = beta Gamma dL and X = dR S0^T:
+//   dQ = scale gamma dO S0^T + F K
+//   dK = -beta gamma X + e U dS^T + F^T Q + (E + E^T) K
+//   dbeta_i = dR_i.v_i - gamma_i k_i.X_i + sum_j dL_ij Gamma_ij k_i.k_j
+//   dG_i = sum_j D_ij - sum_j D_ji + q_i.(scale gamma dO S0^T)_i - k_i.(beta gamma X)_i - d_i
+// with D = dM M + dL L below the diagonal (on it both sums take the same) and
+// d_i = e_i k_i.(U dS^T)_i; the chunk's last token also gets sum_i d_i +
+// gamma_63 <dS, S0>; dg_i is the sum of dG over i and all later tokens.
+// A workgroup has a key head of a chunk and takes its value heads in turn, adding
+// up dQ and dK in registers; wave wv has token tile wv.
+__device__ __forceinline__ float over_columns(float x) {  // over the 16 lanes of a group
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) x += __shfl_xor(x, off);
+    return x;
+}
+__device__ __forceinline__ float over_groups(float x) {
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+template <class TY, int KS>
+__global__ __launch_bounds__(kThreads) void delta_grads_kernel(
+    Shape a, Space w, const typename TY::S* __restrict__ q, const typename TY::S* __restrict__ k,
+    const typename TY::S* __restrict__ v, const typename TY::S* __restrict__ go, typename TY::S* __restrict__ gq,
+    typename TY::S* __restrict__ gk, float* __restrict__ gg, float* __restrict__ gbeta) {
+    using S = typename TY::S;
+    constexpr int NP = TY::NP, CT = 2 * KS;
+    struct Stage {
+        u32x4 s0[CT][3][64], ds[CT][3][64], u[4][3][64];
+    };
+    struct Square {
+        float f[kC][kC + 4], e[kC][kC + 4];
+    };
+    __shared__ __align__(16) unsigned char raw[sizeof(Stage) > sizeof(Square) ? sizeof(Stage) : sizeof(Square)];
+    __shared__ double G[kC];
+    __shared__ float ga[3][kC];           // gamma, e, beta
+    __shared__ float row_d[kC], col_d[4][kC], end_d[kC], dotted[4];
+    Stage& sg = *reinterpret_cast<Stage*>(raw);
+    Square& sq = *reinterpret_cast<Square*>(raw);
+    const long long slot = blockIdx.x;
+    const Chunk ch = chunk_of(a, slot);
+    if (ch.n <= 0) return;
+    const int t = threadIdx.x, lane = t & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
+    const int hk = blockIdx.y, rep = a.hv / a.hk;
+    const long long ks0 = slot * a.hk + hk;
+    const int arow = 16 * wv + col;  // this lane's row as a left operand
+    const bool aok = arow < ch.n;
+    const S* qp = q + (long long)ch.tok0 * a.qt + hk * a.qh;
+    const S* kp = k + (long long)ch.tok0 * a.kt + hk * a.kh;
+
+    f32x4 dq[CT], dk[CT];
+#pragma unroll
+    for (int i = 0; i < CT; ++i) dq[i] = f32x4{0, 0, 0, 0}, dk[i] = f32x4{0, 0, 0, 0};
+    for (int hr = 0; hr < rep; ++hr) {
+        const int h = hk * rep + hr;
+        const long long vs = slot * a.hv + h;
+        __syncthreads();  // the last head is done with the shared arrays
+        if (t < kC) {
+            const Gates& gs = w.gates[vs];
+            G[t] = gs.G[t];
+            ga[0][t] = gs.gamma[t];
+            ga[1][t] = gs.e[t];
+            ga[2][t] = gs.beta[t];
+        }
+        f32x4 so[CT], sr[CT], ud[CT], dm[4], dl[4];
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+            so[i] = f32x4{0, 0, 0, 0}, sr[i] = f32x4{0, 0, 0, 0}, ud[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dm[i] = f32x4{0, 0, 0, 0}, dl[i] = f32x4{0, 0, 0, 0};
+        float drv = 0.0f, dss = 0.0f;
+        const S* gop = go + (long long)(ch.tok0 + arow) * a.gt + h * a.gh;
+        const S* vp = v + (long long)(ch.tok0 + arow) * a.vt + h * a.vh;
+        for (int n0 = 0; n0 < w.dvp; n0 += 32) {
+            if (n0) __syncthreads();
+            for (int i = t; i < 32 * KS * 4; i += kThreads) {  // rows of S0 and dS, 8 columns each
+                const int row = i >> 2, g8 = i & 3, to = (row & 15) + 16 * g8;
+                const long long from = (vs * 32 * KS + row) * w.dvp + n0 + 8 * g8;
+                float x[8], y[8];
+                load8<F32>(w.s0 + from, 0, 4, 8, true, true, x);
+                load8<F32>(w.ds + from, 0, 4, 8, true, true, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dss += x[j] * y[j];
+                u32x4 p[3];
+                split8<3>(x, p);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) sg.s0[row >> 4][n][to] = p[n];
+                split8<3>(y, p);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) sg.ds[row >> 4][n][to] = p[n];
+            }
+            {
+                const int row = t >> 2, g8 = t & 3, to = (row & 15) + 16 * g8;
+                float x[8];
+                load8<F32>(w.u + (vs * kC + row) * w.dvp + n0 + 8 * g8, 0, 4, 8, true, true, x);
+                u32x4 p[3];
+                split8<3>(x, p);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) sg.u[row >> 4][n][to] = p[n];
+            }
+            u32x4 oa[NP], ra[3], ua[3];
+            {
+                float x[8], y[8];
+                const int c0 = n0 + 8 * grp;
+                load8<F32>(w.dr + (vs * kC + arow) * w.dvp + c0, 0, 4, 8, true, true, x);
+                load8<TY>(vp, c0, c0 + 4, a.dv, aok, a.vvec, y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) drv += x[j] * y[j];
+                split8<3>(x, ra);
+                load8<TY>(gop, c0, c0 + 4, a.dv, aok, a.gvec, x);
+                split8<NP>(x, oa);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int n = 0; n < 3; ++n) ua[n] = sg.u[wv][n][lane];
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                u32x4 b[3];
+#pragma unroll
+                for (int n = 0; n < 3; ++n) b[n] = sg.s0[i][n][lane];
+                mma<3>(oa, b, so[i]);
+                mma<3>(ra, b, sr[i]);
+#pragma unroll
+                for (int n = 0; n < 3; ++n) b[n] = sg.ds[i][n][lane];
+                mma<3>(ua, b, ud[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i <= wv) {
+                    u32x4 b[3];
+#pragma unroll
+                    for (int n = 0; n < 3; ++n) b[n] = sg.u[i][n][lane];
+                    mma<3>(oa, b, dm[i]);
+                    mma<3>(ra, b, dl[i]);
+                }
+        }
+        // k.k and q.k again, the triangles of F and E, and what the gates get of them
+        f32x4 kk[4], qk[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kk[i] = f32x4{0, 0, 0, 0}, qk[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            u32x4 ka[NP], qa[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                ka[n] = w.kf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
+                qa[n] = w.qf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i <= wv) {
+                    u32x4 b[NP];
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) b[n] = w.kf[(((ks0 * 4 + i) * KS + ks) * NP + n) * 64 + lane];
+                    mma<3>(ka, b, kk[i]);
+                    mma<3>(qa, b, qk[i]);
+                }
+        }
+        __syncthreads();  // the staged slices are read; F and E take their place
+        float dsum[4] = {0, 0, 0, 0}, bsum[4] = {0, 0, 0, 0};  // rows 16 wv + 4 grp + r
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = 16 * i + col;
+            float down = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * wv + 4 * grp + r;
+                float f = 0.0f, e = 0.0f;
+                if (i <= wv && c <= row) {
+                    const float decay = exp_of(G[row] - G[c]);
+                    f = a.scale * decay * dm[i][r];
+                    if (c < row) {
+                        const float x = -decay * dl[i][r];       // dL Gamma
+                        const float b = x * kk[i][r];
+                        e = ga[2][row] * x;
+                        const float d = f * qk[i][r] + ga[2][row] * b;
+                        bsum[r] += b;
+                        dsum[r] += d;
+                        down += d;
+                    }
+                }
+                sq.f[row][c] = f;
+                sq.e[row][c] = e;
+            }
+            down = over_groups(down);
+            if (grp == 0) col_d[wv][c] = down;
+        }
+        drv = over_groups(drv);  // for row arow, in all groups
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) dss += __shfl_xor(dss, off);
+        if (lane == 0) dotted[wv] = dss;
+        // the states' parts of dQ and dK, and their products with q and k
+        float qdot[4] = {0, 0, 0, 0}, kdot[4] = {0, 0, 0, 0}, gone[4] = {0, 0, 0, 0};
+        const f32x4 gam = *reinterpret_cast<const f32x4*>(&ga[0][16 * wv + 4 * grp]);
+        const f32x4 end = *reinterpret_cast<const f32x4*>(&ga[1][16 * wv + 4 * grp]);
+        const f32x4 bet = *reinterpret_cast<const f32x4*>(&ga[2][16 * wv + 4 * grp]);
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {
+            const int c = 16 * i + col;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * wv + 4 * grp + r;
+                const bool ok = row < ch.n && c < a.dk;
+                const float qv = ok ? TY::load(qp[row * a.qt + c]) : 0.0f;
+                const float kv = ok ? TY::load(kp[row * a.kt + c]) : 0.0f;
+                const float x = a.scale * gam[r] * so[i][r], y = gam[r] * sr[i][r], z = end[r] * ud[i][r];
+                qdot[r] += qv * x;
+                kdot[r] += kv * y;
+                gone[r] += kv * z;
+                dq[i][r] += x;
+                dk[i][r] += z - bet[r] * y;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * wv + 4 * grp + r;
+            const float d = over_columns(dsum[r]), b = over_columns(bsum[r]);
+            const float x = over_columns(qdot[r]), y = over_columns(kdot[r]), z = over_columns(gone[r]);
+            const float rv = __shfl(drv, 4 * grp + r);
+            if (col == 0) {
+                row_d[row] = d + (x - bet[r] * y);
+                end_d[row] = z;
+                if (row < ch.n) gbeta[(long long)(ch.tok0 + row) * a.hv + h] = rv - y + b;
+            }
+        }
+        __syncthreads();
+        if (wv == 0) {
+            const float z = end_d[lane];
+            float all = z;
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) all += __shfl_xor(all, off);
+            float d = row_d[lane] - z;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i >= (lane >> 4)) d -= col_d[i][lane];
+            double x = d;
+            if (lane == kC - 1) {
+                const float sum = (dotted[0] + dotted[1]) + (dotted[2] + dotted[3]);
+                x += (double)all + (double)exp_of(G[kC - 1]) * sum;
+            }
+            for (int off = 1; off < 64; off <<= 1) {
+                const double o = __shfl_down(x, off);
+                if (lane + off < 64) x += o;
+            }
+            if (lane < ch.n) gg[(long long)(ch.tok0 + lane) * a.hv + h] = (float)x;
+        }
+        // F K, F^T Q and (E + E^T) K
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts) {
+            u32x4 fa[3], fb[3], ea[3];
+            float x[8], y[8], z[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = place_of(ts, grp, j);
+                x[j] = sq.f[arow][c];
+                y[j] = sq.f[c][arow];
+                z[j] = sq.e[arow][c] + sq.e[c][arow];
+            }
+            split8<3>(x, fa);
+            split8<3>(y, fb);
+            split8<3>(z, ea);
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                u32x4 kb[NP], qb[NP];
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    kb[n] = w.kt[((ks0 * 4 * KS + i * 2 + ts) * NP + n) * 64 + lane];
+                    qb[n] = w.qt[((ks0 * 4 * KS + i * 2 + ts) * NP + n) * 64 + lane];
+                }
+                if (ts <= (wv >> 1)) mma<3>(fa, kb, dq[i]);
+                if (ts >= (wv >> 1)) mma<3>(fb, qb, dk[i]);
+                mma<3>(ea, kb, dk[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+        const int c = 16 * i + col;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * wv + 4 * grp + r;
+            if (row < ch.n && c < a.dk) {
+                const long long to = ((long long)(ch.tok0 + row) * a.hk + hk) * a.dk + c;
+                gq[to] = TY::store(dq[i][r]);
+                gk[to] = TY::store(dk[i][r]);
+            }
+        }
+    }
+}
+
+// ======================================================== token by token
+// A wave has a tile of 32 columns of a head's state (a cache line of each row) in
+// registers: lane l has columns 4 (l & 7) ... + 3 of the NR rows from NR (l >> 3)
+// on, so all of the tile's loads are in flight at once and the sums over dim_k are
+// in-lane and then over 8 lanes.  S'^T k and S'^T q are summed together, and
+// o = S'^T q + u (k.q), so a token is one pass over the state.
+//
+// As a decode step (`slots`, or all rows in order) and as the sequence form of
+// short sequences.
+template <class TY, int NR>
+__global__ __launch_bounds__(kThreads) void delta_token_kernel(
+    Shape a, const typename TY::S* __restrict__ q, const typename TY::S* __restrict__ k,
+    const typename TY::S* __restrict__ v, const float* __restrict__ g, const float* __restrict__ beta,
+    const float* in, float* out, typename TY::S* __restrict__ o, int step, const int* __restrict__ slots, int pool,
+    bool vec) {
+    using S = typename TY::S;
+    const int tiles = (a.dv + 31) / 32;
+    const long long count = (long long)a.n_seq * a.hv * tiles, blocks = (count + 3) / 4;
+    const long long block = on_die(blockIdx.x, blocks);
+    if (blockIdx.x / 8 >= (blocks + 7) / 8) return;
+    const long long at = block * 4 + wave_of();
+    if (at >= count) return;
+    const int lane = threadIdx.x & 63, rg = lane >> 3;
+    const int c0 = (int)(at % tiles) * 32 + 4 * (lane & 7);
+    const long long sh = at / tiles;
+    const int h = (int)(sh % a.hv), hk = h / (a.hv / a.hk), r0 = NR * rg;
+    int b = (int)(sh / a.hv), tok, end;
+    long long state = b;
+    if (step) {
+        tok = b;
+        end = b + 1;
+        if (slots) {
+            const int sl = slots[b];
+            if (sl < 0 || sl >= pool) {
+                if (rg == 0)
+                    for (int j = 0; j < 4; ++j)
+                        if (c0 + j < a.dv) o[((long long)b * a.hv + h) * a.dv + c0 + j] = TY::store(0.0f);
+                return;
+            }
+            state = sl;
+        }
+    } else {
+        int len;
+        span_of(a, b, tok, len);
+        end = tok + len;
+    }
+    const long long sbase = (state * a.hv + h) * a.dk * a.dv + c0;
+    f32x4 s[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int row = r0 + i;
+        s[i] = f32x4{0, 0, 0, 0};
+        if (in && row < a.dk) {
+            const float* p = in + sbase + (long long)row * a.dv;
+            if (vec) {
+                if (c0 < a.dv) s[i] = *reinterpret_cast<const f32x4*>(p);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j < a.dv) s[i][j] = p[j];
+            }
+        }
+    }
+    if (step && slots)  // rows of one slot: the first of them takes all
+        for (int j0 = 0; j0 < b; j0 += 64)
+            if (__ballot(j0 + lane < b && slots[j0 + lane] == (int)state)) return;
+    while (tok < end) {
+        const S* qr = q + (long long)tok * a.qt + hk * a.qh + r0;
+        const S* kr = k + (long long)tok * a.kt + hk * a.kh + r0;
+        const S* vr = v + (long long)tok * a.vt + h * a.vh + c0;
+        const long long gi = (long long)tok * a.hv + h;
+        float kx[NR], qx[NR];
+        f32x4 x = {0, 0, 0, 0};
+        const float al = expf(g[gi]), be = beta[gi];
+        if constexpr (NR >= 8) {
+#pragma unroll
+            for (int i = 0; i < NR; i += 8) {
+                float e[8];
+                load8<TY>(kr, i, i + 4, a.dk - r0, true, a.kvec, e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) kx[i + j] = e[j];
+                load8<TY>(qr, i, i + 4, a.dk - r0, true, a.qvec, e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) qx[i + j] = e[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                kx[i] = r0 + i < a.dk ? TY::load(kr[i]) : 0.0f;
+                qx[i] = r0 + i < a.dk ? TY::load(qr[i]) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c0 + j < a.dv) x[j] = TY::load(vr[j]);
+        f32x4 pk = {0, 0, 0, 0}, pq = {0, 0, 0, 0};
+        float kq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            s[i] *= al;
+            pk += s[i] * kx[i];
+            pq += s[i] * qx[i];
+            kq += kx[i] * qx[i];
+        }
+#pragma unroll
+        for (int off = 8; off < 64; off <<= 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                pk[j] += __shfl_xor(pk[j], off);
+                pq[j] += __shfl_xor(pq[j], off);
+            }
+            kq += __shfl_xor(kq, off);
+        }
+        const f32x4 u = (x - pk) * be;
+        const f32x4 y = (pq + u * kq) * a.scale;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) s[i] += u * kx[i];
+        if (rg == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c0 + j < a.dv) o[gi * a.dv + c0 + j] = TY::store(y[j]);
+        }
+        ++tok;
+        if (step && slots) {  // the next row of the same slot
+            end = tok;
+            for (int j0 = tok; j0 < a.n_seq; j0 += 64) {
+                const unsigned long long m = __ballot(j0 + lane < a.n_seq && slots[j0 + lane] == (int)state);
+                if (m) {
+                    tok = j0 + __builtin_ctzll(m);
+                    end = tok + 1;
+                    break;
+                }
+            }
+        }
+    }
+    if (!out) return;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int row = r0 + i;
+        if (row < a.dk) {
+            float* p = out + sbase + (long long)row * a.dv;
+            if (vec) {
+                if (c0 < a.dv) *reinterpret_cast<f32x4*>(p) = s[i];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (c0 + j < a.dv) p[j] = s[i][j];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------- host helpers
+struct Range {
+    uintptr_t lo, hi;  // [lo, hi)
+};
+inline Range bytes_of(const void* p, long long n) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return Range{lo, lo + (uintptr_t)(p ? n : 0)};
+}
+inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+inline bool same(Range a, Range b) { return a.lo == b.lo && a.hi == b.hi; }
+inline bool outputs_disjoint(const Range* outs, int n_out, const Range* ins, int n_in) {
+    for (int o = 0; o < n_out; ++o) {
+        for (int i = 0; i < n_in; ++i)
+            if (overlap(outs[o], ins[i])) return false;
+        for (int p = o + 1; p < n_out; ++p)
+            if (overlap(outs[o], outs[p])) return false;
+    }
+    return true;
+}
+inline bool mul_ok(long long a, long long b, long long* r) {
+    if (a < 0 || b < 0) return false;
+    if (a != 0 && b > (LLONG_MAX / 16) / a) return false;
+    *r = a * b;
+    return true;
+}
+inline int size_of(int type) { return type == CFC_TYPE_F32 ? 4 : 2; }
+
+// Bytes from the first to the last element of a strided [tokens, heads, dim] array.
+inline bool extent(long long tokens, int heads, int dim, long long st, long long sh, int size, long long* r) {
+    long long x, y;
+    if (tokens == 0) {
+        *r = 0;
+        return true;
+    }
+    if (!mul_ok(tokens - 1, st, &x) || !mul_ok(heads - 1, sh, &y)) return false;
+    return mul_ok(x + y + dim, size, r);
+}
+
+constexpr long long kMaxBlocks = (1LL << 32) / kThreads - 8;  // a grid has fewer than 2^32 work-items
+
+// Chunks that sequences of at most so many tokens are run without.
+constexpr int kShort = 16;
+
+int check_shape(const delta_rule_shape_t* p, bool step, Shape* a) {
+    if (!p) return CFC_ERR_NULL;
+    const int n_seq = step ? (int)std::min(p->n_tokens, (long long)INT_MAX) : p->n_seq;
+    if (p->type != CFC_TYPE_F32 && p->type != CFC_TYPE_BF16 && p->type != CFC_TYPE_F16) return CFC_ERR_UNSUPPORTED;
+    if (n_seq < 0 || p->n_tokens < 0 || p->n_tokens > INT_MAX - 2 * kC) return CFC_ERR_DIM;
+    if (p->heads_k < 1 || p->heads_v < 1 || p->heads_v % p->heads_k || p->dim_k < 1 || p->dim_v < 1) return CFC_ERR_DIM;
+    if (!std::isfinite(p->scale)) return CFC_ERR_DT;
+    for (long long st : {p->q_stride_t, p->q_stride_h, p->k_stride_t, p->k_stride_h, p->v_stride_t, p->v_stride_h,
+                         p->go_stride_t, p->go_stride_h})
+        if (st < 0) return CFC_ERR_DIM;
+    const bool dense = !step && !p->offsets;
+    if (dense && (p->seq_len < 0 || (long long)p->seq_len * n_seq != p->n_tokens)) return CFC_ERR_DIM;
+    if (p->dim_k > DELTA_MAX_DIM_K || p->dim_v > DELTA_MAX_DIM_V) return CFC_ERR_UNSUPPORTED;
+    if ((long long)p->heads_v + p->heads_k > 65535) return CFC_ERR_UNSUPPORTED;
+    long long n;
+    if (!mul_ok((long long)p->dim_k * p->dim_v * 4, p->heads_v, &n) || !mul_ok(n, n_seq, &n)) return CFC_ERR_DIM;
+    *a = Shape{};
+    a->n_seq = n_seq;
+    a->seq_len = dense ? p->seq_len : 0;
+    a->n_tokens = (int)p->n_tokens;
+    a->offsets = step ? nullptr : p->offsets;
+    a->hk = p->heads_k;
+    a->hv = p->heads_v;
+    a->dk = p->dim_k;
+    a->dv = p->dim_v;
+    a->scale = p->scale;
+    a->qt = p->q_stride_t, a->qh = p->q_stride_h;
+    a->kt = p->k_stride_t, a->kh = p->k_stride_h;
+    a->vt = p->v_stride_t, a->vh = p->v_stride_h;
+    a->gt = p->go_stride_t, a->gh = p->go_stride_h;
+    a->chunks = dense ? (int)(((long long)p->seq_len + kC - 1) / kC) : 0;
+    a->slots = dense ? (long long)a->chunks * n_seq : p->n_tokens / kC + n_seq;
+    const long long tiles = (p->dim_v + 31) / 32 * 2;
+    if (a->slots > kMaxBlocks || (long long)n_seq * p->heads_v > kMaxBlocks / tiles) return CFC_ERR_UNSUPPORTED;
+    return CFC_OK;
+}
+// Four elements of a row are one aligned load.
+inline bool fours(const void* p, long long st, long long sh, int dim, int size) {
+    const uintptr_t step = 4 * size;
+    return (reinterpret_cast<uintptr_t>(p) % step) == 0 && st % 4 == 0 && sh % 4 == 0 && dim % 4 == 0;
+}
+inline void set_vec(const delta_rule_shape_t* p, Shape* a, const void* q, const void* k, const void* v,
+                    const void* go) {
+    const int z = size_of(p->type);
+    a->qvec = fours(q, a->qt, a->qh, a->dk, z);
+    a->kvec = fours(k, a->kt, a->kh, a->dk, z);
+    a->vvec = fours(v, a->vt, a->vh, a->dv, z);
+    a->gvec = go && fours(go, a->gt, a->gh, a->dv, z);
+}
+
+inline bool is_short(const Shape& a) { return (a.offsets ? a.n_tokens : a.seq_len) <= kShort; }
+
+// The workspace's arrays, one behind the other; returns its bytes.
+long long lay_out(const Shape& a, int type, bool grad, void* base, Space* w) {
+    const int np = type == CFC_TYPE_BF16 ? 1 : type == CFC_TYPE_F16 ? 2 : 3;
+    const int ks = a.dk <= 64 ? 2 : 4, nm = grad || np == 3 ? 3 : 2;
+    const long long kslots = a.slots * a.hk, vslots = a.slots * a.hv;
+    char* at = static_cast<char*>(base);
+    long long total = 0;
+    auto take = [&](long long bytes) {
+        char* p = at ? at + total : nullptr;
+        total += bytes;
+        return p;
+    };
+    w->dvp = (a.dv + 31) / 32 * 32;
+    const long long kb = kslots * 4 * ks * np * 1024, state = vslots * ks * 32 * w->dvp * 4,
+                    rows = vslots * kC * w->dvp * 4;
+    w->kf = (u32x4*)take(kb);
+    w->qf = (u32x4*)take(kb);
+    w->kt = (u32x4*)take(kb);
+    w->qt = (u32x4*)take(grad ? kb : 0);
+    w->t = (u32x4*)take(vslots * 8 * 3 * 1024);
+    w->m = (u32x4*)take(grad ? 0 : vslots * 8 * nm * 1024);
+    w->tt = (u32x4*)take(grad ? vslots * 8 * 3 * 1024 : 0);
+    w->mt = (u32x4*)take(grad ? vslots * 8 * 3 * 1024 : 0);
+    w->gates = (Gates*)take(vslots * (long long)sizeof(Gates));
+    w->s0 = (float*)take(grad ? state : 0);
+    w->ds = (float*)take(grad ? state : 0);
+    w->u = (float*)take(grad ? rows : 0);
+    w->dr = (float*)take(grad ? rows : 0);
+    return total;
+}
+
+inline int launch_status() { return hipGetLastError() == hipSuccess ? CFC_OK : CFC_ERR_HIP; }
+
+// Columns of a chain's workgroup.  Its products are the same whatever the tile,
+// so a wide one only saves loads; narrow ones make more workgroups.
+inline int chain_tiles(const Shape& a) {
+    const long long wide = (long long)a.n_seq * a.hv * ((a.dv + 31) / 32);
+    return wide >= 256 && a.dv > 16 ? 2 : 1;
+}
+
+template <class TY, int KS, bool GRAD>
+void launch_prep(const Shape& a, const Space& w, const void* q, const void* k, const float* g, const float* beta,
+                 hipStream_t stream) {
+    using S = typename TY::S;
+    if (a.slots == 0) return;
+    hipLaunchKernelGGL((delta_prep_kernel<TY, KS, GRAD>), dim3((unsigned)a.slots, a.hv + a.hk), dim3(kThreads), 0,
+                       stream, a, w, (const S*)q, (const S*)k, g, beta);
+}
+template <class TY, int KS, int NCT, bool GRAD>
+void launch_chain(const Shape& a, const Space& w, const void* v, const float* initial, void* o, float* final_state,
+                  hipStream_t stream) {
+    using S = typename TY::S;
+    const long long count = (long long)a.n_seq * a.hv * (((GRAD ? w.dvp : a.dv) + 16 * NCT - 1) / (16 * NCT));
+    hipLaunchKernelGGL((delta_chain_kernel<TY, KS, NCT, GRAD>), dim3(dealt(count)), dim3(kThreads), 0, stream, a, w,
+                       (const S*)v, initial, (S*)o, final_state);
+}
+
+template <class TY, int KS>
+int run_forward(const Shape& a, const Space& w, const void* q, const void* k, const void* v, const float* g,
+                const float* beta, const float* initial, void* o, float* final_state, hipStream_t stream) {
+    launch_prep<TY, KS, false>(a, w, q, k, g, beta, stream);
+    if (chain_tiles(a) == 2)
+        launch_chain<TY, KS, 2, false>(a, w, v, initial, o, final_state, stream);
+    else
+        launch_chain<TY, KS, 1, false>(a, w, v, initial, o, final_state, stream);
+    return launch_status();
+}
+
+template <class TY, int KS, int NCT>
+int run_backward(const Shape& a, const Space& w, const void* q, const void* k, const void* v, const float* g,
+                 const float* beta, const float* initial, const void* go, const float* grad_final, void* gq, void* gk,
+                 void* gv, float* gg, float* gbeta, float* grad_initial, hipStream_t stream) {
+    using S = typename TY::S;
+    constexpr size_t lds = sizeof(ReverseLds<TY::NP, NCT, KS>);
+    // idempotent, and 160 KB is what a gfx950 workgroup can have
+    if (lds > 64 * 1024 &&
+        hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_reverse_kernel<TY, KS, NCT>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+        return CFC_ERR_HIP;
+    launch_prep<TY, KS, true>(a, w, q, k, g, beta, stream);
+    if (a.slots) launch_chain<TY, KS, NCT, true>(a, w, v, initial, nullptr, nullptr, stream);
+    const long long count = (long long)a.n_seq * a.hv * (w.dvp / (16 * NCT));
+    hipLaunchKernelGGL((delta_reverse_kernel<TY, KS, NCT>), dim3(dealt(count)), dim3(kThreads), lds, stream, a, w,
+                       (const S*)go, grad_final, (S*)gv, grad_initial);
+    if (a.slots)
+        hipLaunchKernelGGL((delta_grads_kernel<TY, KS>), dim3((unsigned)a.slots, a.hk), dim3(kThreads), 0, stream, a,
+                           w, (const S*)q, (const S*)k, (const S*)v, (const S*)go, (S*)gq, (S*)gk, gg, gbeta);
+    return launch_status();
+}
+
+template <class TY>
+int run_tokens(const Shape& a, const void* q, const void* k, const void* v, const float* g, const float* beta,
+               const float* in, float* out, void* o, int step, const int* slots, int pool, hipStream_t stream) {
+    using S = typename TY::S;
+    const long long count = (long long)a.n_seq * a.hv * ((a.dv + 31) / 32);
+    const bool vec = a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(in) % 16 == 0 &&
+                     reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(dealt((count + 3) / 4)), dim3(kThreads), 0, stream, a, (const S*)q,
+                           (const S*)k, (const S*)v, g, beta, in, out, (S*)o, step, slots, pool, vec);
+    };
+    if (a.dk <= 16)
+        go(delta_token_kernel<TY, 2>);
+    else if (a.dk <= 32)
+        go(delta_token_kernel<TY, 4>);
+    else if (a.dk <= 64)
+        go(delta_token_kernel<TY, 8>);
+    else
+        go(delta_token_kernel<TY, 16>);
+    return launch_status();
+}
+
+struct Sizes {  // bytes of the arguments
+    long long q, k, v, go, dq, dv, gates, states;
+};
+bool sizes_of(const delta_rule_shape_t* p, const Shape& a, Sizes* z) {
+    const int size = size_of(p->type);
+    const long long t = p->n_tokens;
+    return extent(t, a.hk, a.dk, a.qt, a.qh, size, &z->q) && extent(t, a.hk, a.dk, a.kt, a.kh, size, &z->k) &&
+           extent(t, a.hv, a.dv, a.vt, a.vh, size, &z->v) && extent(t, a.hv, a.dv, a.gt, a.gh, size, &z->go) &&
+           mul_ok(t, (long long)a.hk * a.dk * size, &z->dq) && mul_ok(t, (long long)a.hv * a.dv * size, &z->dv) &&
+           mul_ok(t, (long long)a.hv * 4, &z->gates) &&
+           mul_ok((long long)a.n_seq * a.hv, (long long)a.dk * a.dv * 4, &z->states);
+}
+inline Range offsets_range(const Shape& a) {
+    return bytes_of(a.offsets, a.offsets ? ((long long)a.n_seq + 1) * 4 : 0);
+}
+
+}  // namespace
+
+// ================================================================ C ABI
+extern "C" long long delta_rule_forward_workspace(const delta_rule_shape_t* shape) {
+    Shape a;
+    Space w;
+    if (check_shape(shape, false, &a) != CFC_OK) return -1;
+    return is_short(a) ? 0 : lay_out(a, shape->type, false, nullptr, &w);
+}
+
+extern "C" long long delta_rule_backward_workspace(const delta_rule_shape_t* shape) {
+    Shape a;
+    Space w;
+    if (check_shape(shape, false, &a) != CFC_OK) return -1;
+    return lay_out(a, shape->type, true, nullptr, &w);
+}
+
+extern "C" int delta_rule_forward(const delta_rule_shape_t* shape, const void* q, const void* k, const void* v,
+                                  const float* g, const float* beta, const float* initial_state, void* o,
+                                  float* final_state, void* workspace, long long workspace_bytes,
+                                  hipStream_t stream) {
+    Shape a;
+    if (const int e = check_shape(shape, false, &a)) return e;
+    Sizes z;
+    if (!sizes_of(shape, a, &z)) return CFC_ERR_DIM;
+    if (a.n_seq == 0) return CFC_OK;
+    if (a.n_tokens && (!q || !k || !v || !g || !beta || !o)) return CFC_ERR_NULL;
+    const bool brief = is_short(a);
+    Space w{};
+    const long long need = brief ? 0 : lay_out(a, shape->type, false, workspace, &w);
+    if (need) {
+        if (!workspace) return CFC_ERR_NULL;
+        if (workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16) return CFC_ERR_DIM;
+    }
+    const Range fin = bytes_of(final_state, z.states), ini = bytes_of(initial_state, z.states);
+    const Range outs[] = {bytes_of(o, z.dv), fin, bytes_of(need ? workspace : nullptr, need)};
+    const Range ins[] = {bytes_of(q, z.q),        bytes_of(k, z.k), bytes_of(v, z.v), bytes_of(g, z.gates),
+                         bytes_of(beta, z.gates), offsets_range(a), same(fin, ini) ? Range{0, 0} : ini};
+    if (!outputs_disjoint(outs, 3, ins, 7)) return CFC_ERR_OVERLAP;
+    if (same(fin, ini) && initial_state &&
+        (overlap(outs[0], ini) || overlap(outs[2], ini))) return CFC_ERR_OVERLAP;
+    set_vec(shape, &a, q, k, v, nullptr);
+    if (brief) {
+        switch (shape->type) {
+            case CFC_TYPE_F32: return run_tokens<F32>(a, q, k, v, g, beta, initial_state, final_state, o, 0, nullptr, 0, stream);
+            case CFC_TYPE_BF16: return run_tokens<BF16>(a, q, k, v, g, beta, initial_state, final_state, o, 0, nullptr, 0, stream);
+            default: return run_tokens<F16>(a, q, k, v, g, beta, initial_state, final_state, o, 0, nullptr, 0, stream);
+        }
+    }
+    auto go = [&](auto type) {
+        using TY = decltype(type);
+        return a.dk <= 64 ? run_forward<TY, 2>(a, w, q, k, v, g, beta, initial_state, o, final_state, stream)
+                          : run_forward<TY, 4>(a, w, q, k, v, g, beta, initial_state, o, final_state, stream);
+    };
+    switch (shape->type) {
+        case CFC_TYPE_F32: return go(F32{});
+        case CFC_TYPE_BF16: return go(BF16{});
+        default: return go(F16{});
+    }
+}
+
+extern "C" int delta_rule_backward(const delta_rule_shape_t* shape, const void* q, const void* k, const void* v,
+                                   const float* g, const float* beta, const float* initial_state,
+                                   const void* grad_o, const float* grad_final_state, void* grad_q, void* grad_k,
+                                   void* grad_v, float* grad_g, float* grad_beta, float* grad_initial_state,
+                                   void* workspace, long long workspace_bytes, hipStream_t stream) {
+    Shape a;
+    if (const int e = check_shape(shape, false, &a)) return e;
+    Sizes z;
+    if (!sizes_of(shape, a, &z)) return CFC_ERR_DIM;
+    if (a.n_seq == 0) return CFC_OK;
+    if (a.n_tokens &&
+        (!q || !k || !v || !g || !beta || !grad_o || !grad_q || !grad_k || !grad_v || !grad_g || !grad_beta))
+        return CFC_ERR_NULL;
+    Space w{};
+    const long long need = lay_out(a, shape->type, true, workspace, &w);
+    if (need) {
+        if (!workspace) return CFC_ERR_NULL;
+        if (workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16) return CFC_ERR_DIM;
+    }
+    const Range gin = bytes_of(grad_initial_state, z.states), gfin = bytes_of(grad_final_state, z.states);
+    const Range outs[] = {bytes_of(grad_q, z.dq), bytes_of(grad_k, z.dq), bytes_of(grad_v, z.dv),
+                          bytes_of(grad_g, z.gates), bytes_of(grad_beta, z.gates), bytes_of(workspace, need), gin};
+    const Range ins[] = {bytes_of(q, z.q), bytes_of(k, z.k), bytes_of(v, z.v), bytes_of(g, z.gates),
+                         bytes_of(beta, z.gates), bytes_of(grad_o, z.go), bytes_of(initial_state, z.states),
+                         offsets_range(a), same(gin, gfin) ? Range{0, 0} : gfin};
+    if (!outputs_disjoint(outs, 7, ins, 9)) return CFC_ERR_OVERLAP;
+    set_vec(shape, &a, q, k, v, grad_o);
+    const bool wide = chain_tiles(a) == 2;
+    auto go = [&](auto type) {
+        using TY = decltype(type);
+        auto run = [&](auto f) {
+            return f(a, w, q, k, v, g, beta, initial_state, grad_o, grad_final_state, grad_q, grad_k, grad_v, grad_g,
+                     grad_beta, grad_initial_state, stream);
+        };
+        if (a.dk <= 64) return wide ? run(run_backward<TY, 2, 2>) : run(run_backward<TY, 2, 1>);
+        return wide ? run(run_backward<TY, 4, 2>) : run(run_backward<TY, 4, 1>);
+    };
+    switch (shape->type) {
+        case CFC_TYPE_F32: return go(F32{});
+        case CFC_TYPE_BF16: return go(BF16{});
+        default: return go(F16{});
+    }
+}
+
+extern "C" int delta_rule_step(const delta_rule_shape_t* shape, const void* q, const void* k, const void* v,
+                               const float* g, const float* beta, float* states, int pool, const int* slots, void* o,
+                               hipStream_t stream) {
+    Shape a;
+    if (const int e = check_shape(shape, true, &a)) return e;
+    Sizes z;
+    long long held;
+    if (pool < 0 || (!slots && pool < a.n_seq) || !sizes_of(shape, a, &z) ||
+        !mul_ok((long long)pool * a.hv, (long long)a.dk * a.dv * 4, &held))
+        return CFC_ERR_DIM;
+    if (a.n_seq == 0) return CFC_OK;
+    if (!q || !k || !v || !g || !beta || !o || (pool && !states)) return CFC_ERR_NULL;
+    const Range outs[] = {bytes_of(o, z.dv), bytes_of(states, held)};
+    const Range ins[] = {bytes_of(q, z.q), bytes_of(k, z.k), bytes_of(v, z.v), bytes_of(g, z.gates),
+                         bytes_of(beta, z.gates), bytes_of(slots, (long long)a.n_seq * 4)};
+    if (!outputs_disjoint(outs, 2, ins, 6)) return CFC_ERR_OVERLAP;
+    set_vec(shape, &a, q, k, v, nullptr);
+    switch (shape->type) {
+        case CFC_TYPE_F32: return run_tokens<F32>(a, q, k, v, g, beta, states, states, o, 1, slots, pool, stream);
+        case CFC_TYPE_BF16: return run_tokens<BF16>(a, q, k, v, g, beta, states, states, o, 1, slots, pool, stream);
+        default: return run_tokens<F16>(a, q, k, v, g, beta, states, states, o, 1, slots, pool, stream);
+    }
+}
