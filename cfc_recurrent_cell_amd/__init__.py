@@ -20,11 +20,15 @@ from ._lib import (  # noqa: F401
 from ._delta_rule import (  # noqa: F401
     delta_rule_backward, delta_rule_forward, delta_rule_step, delta_rule_workspace,
 )
+from ._rms_norm import (  # noqa: F401
+    rms_norm_backward, rms_norm_backward_workspace, rms_norm_forward, rms_norm_forward_e4m3,
+)
 
 __all__ = ["cfc_forward", "cfc_backward", "cfc_backward_window", "cfc_backward_windows",
            "cfc_backward_workspace", "cfc_forward_backward_workspace", "cfc_forward_backward", "reduce_axis0", "reduce_axis0_noalloc",
            "reduce_axis0_split_workspace", "cfc_scratch_row_len", "delta_rule_forward",
-           "delta_rule_backward", "delta_rule_step", "delta_rule_workspace", "CfcError", "load_library"]
+           "delta_rule_backward", "delta_rule_step", "delta_rule_workspace", "rms_norm_forward",
+           "rms_norm_forward_e4m3", "rms_norm_backward", "rms_norm_backward_workspace", "CfcError", "load_library"]
 
 
 def cfc_scratch_row_len(n_in: int, n_hid: int) -> int:

@@ -144,6 +144,14 @@ def load_library(path: str = LIB_PATH):
     lib.delta_rule_backward.argtypes = [shape] + [vp] * 15 + [ll, vp]
     lib.delta_rule_step.restype = i
     lib.delta_rule_step.argtypes = [shape] + [vp] * 6 + [i, vp, vp, vp]
+    lib.rms_norm_forward.restype = i
+    lib.rms_norm_forward.argtypes = [i, i, ll, ll, vp, vp, vp, f, vp, vp, vp, vp]
+    lib.rms_norm_forward_e4m3.restype = i
+    lib.rms_norm_forward_e4m3.argtypes = [i, i, ll, ll, vp, vp, vp, f, i, vp, vp, vp, vp, vp]
+    lib.rms_norm_backward_workspace.restype = ll
+    lib.rms_norm_backward_workspace.argtypes = [ll, ll]
+    lib.rms_norm_backward.restype = i
+    lib.rms_norm_backward.argtypes = [i, i, ll, ll] + [vp] * 8 + [ll, vp]
     lib.cfc_status_string.restype = ctypes.c_char_p
     lib.cfc_status_string.argtypes = [i]
     _lib = lib

@@ -13,7 +13,7 @@ from concurrent.futures import ThreadPoolExecutor
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "cfc.hip")
-SOURCES = [SRC] + [os.path.join(PKG, "csrc", name) for name in ("delta_rule.hip",)]
+SOURCES = [SRC] + [os.path.join(PKG, "csrc", name) for name in ("delta_rule.hip", "rms_norm.hip")]
 LIB = os.path.join(PKG, "libcfc_amd.so")
 ARCH = "gfx950"
 
