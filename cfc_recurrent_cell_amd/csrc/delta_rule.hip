@@ -157,12 +157,11 @@ __device__ __forceinline__ void load8(const typename TY::S* row, int c0, int c1,
 
 // ------------------------------------------------------------ decays
 constexpr float kMinDecay = -1e5f;  // exp of it is 0; keeps sums of -inf finite
-// exp of a 64-bit argument, to 32 bits: what the float argument leaves out counts
-// where it is large.
-__device__ __forceinline__ float exp_of(double d) {
+// 2^d of a 64-bit argument, to 32 bits: what the float argument leaves out counts
+// where it is large.  (The hardware's exponential flushes results below 2^-126.)
+__device__ __forceinline__ float exp2_of(double d) {
     const float x = (float)d;
-    const float e = expf(x);
-    return e > 0.0f && e < INFINITY ? e + e * (float)(d - (double)x) : e;
+    return __builtin_amdgcn_exp2f(x) * fmaf((float)(d - (double)x), 0.69314718f, 1.0f);
 }
 
 // --------------------------------------------------------------- arguments
@@ -186,7 +185,7 @@ struct Space {
     int dvp;                     // dim_v rounded up to 32
 };
 struct Gates {
-    double G[kC];
+    double G[kC];  // sums of g log2(e)
     float gamma[kC], e[kC], beta[kC];
 };
 
@@ -242,6 +241,68 @@ __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane
 // =========================================================== all chunks: prep
 // grid: (slots, hv + hk).  The first hv make T and M of a value head, the others
 // the operands of a key head.
+//
+// Rows (row tile, summed 32 of dim_k) of a key head's tensor as left operands.
+template <class TY>
+__device__ __forceinline__ void load_parts(const typename TY::S* row, int c0, int c1, int D, bool ok, bool vec,
+                                           u32x4 (&p)[TY::NP]) {
+    if constexpr (TY::NP == 1) {
+        if (vec) {  // the elements are the one part
+            u32x2 a = {0, 0}, b = {0, 0};
+            if (ok && c0 < D) a = *reinterpret_cast<const u32x2*>(row + c0);
+            if (ok && c1 < D) b = *reinterpret_cast<const u32x2*>(row + c1);
+            p[0] = u32x4{a[0], a[1], b[0], b[1]};
+            return;
+        }
+    }
+    float x[8];
+    load8<TY>(row, c0, c1, D, ok, vec, x);
+    split8<TY::NP>(x, p);
+}
+
+// The chunk's 64 tokens of 32 places of dim_k, as rows and, transposed, as columns.
+// The matrix cores turn them: times the identity, rows come out as a result lies
+// (token 4 grp + r, place l & 15), which is half of the operand with tokens summed;
+// ones and zeros leave every part as it is.
+template <class TY, int KS, bool TURN>
+__device__ __forceinline__ void key_operands(const typename TY::S* p, long long stride, int n, int dk, bool vec, int ks,
+                                             int lane, u32x4* rows, u32x4* columns) {
+    constexpr int NP = TY::NP;
+    const int col = lane & 15, grp = lane >> 4;
+    u32x4 x[4][NP];
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+        const int row = 16 * rt + col;
+        load_parts<TY>(p + row * stride, place_of(ks, grp, 0), place_of(ks, grp, 4), dk, row < n, vec, x[rt]);
+    }
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) rows[((rt * KS + ks) * NP + i) * 64 + lane] = x[rt][i];
+    if constexpr (TURN) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            u32x4 one[1] = {{0, 0, 0, 0}};  // column `col` of the identity's half: place 16 half + col
+            if (grp == (col >> 2)) one[0][2 * half + ((col >> 1) & 1)] = col & 1 ? 0x3f800000u : 0x3f80u;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                u32x4 out[2];
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) {
+                    f32x4 y = {0, 0, 0, 0};
+                    const u32x4 part[1] = {x[rt][i]};
+                    mma<1>(part, one, y);
+                    out[rt >> 1][2 * (rt & 1)] = high_halves(y[0], y[1]);
+                    out[rt >> 1][2 * (rt & 1) + 1] = high_halves(y[2], y[3]);
+                }
+#pragma unroll
+                for (int ts = 0; ts < 2; ++ts)
+                    columns[(((2 * ks + half) * 2 + ts) * NP + i) * 64 + lane] = out[ts];
+            }
+        }
+    }
+}
+
 template <class TY, int KS, bool GRAD>
 __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, const typename TY::S* __restrict__ q,
                                                               const typename TY::S* __restrict__ k,
@@ -257,62 +318,29 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
 
     if ((int)blockIdx.y >= a.hv) {  // operands of a key head
         const int h = blockIdx.y - a.hv;
-        const long long ks0 = slot * a.hk + h;
+        const long long at = (slot * a.hk + h) * 4 * KS * NP * 64;
         const S* kp = k + (long long)ch.tok0 * a.kt + h * a.kh;
         const S* qp = q + (long long)ch.tok0 * a.qt + h * a.qh;
-        for (int f = wv; f < 4 * KS; f += 4) {  // rows are tokens
-            const int row = 16 * (f / KS) + col, ks = f % KS;
-            const int c0 = place_of(ks, grp, 0), c1 = place_of(ks, grp, 4);
-            float x[8];
-            u32x4 p[NP];
-            load8<TY>(kp + row * a.kt, c0, c1, a.dk, row < ch.n, a.kvec, x);
-            split8<NP>(x, p);
-#pragma unroll
-            for (int n = 0; n < NP; ++n) w.kf[((ks0 * 4 * KS + f) * NP + n) * 64 + lane] = p[n];
-            load8<TY>(qp + row * a.qt, c0, c1, a.dk, row < ch.n, a.qvec, x);
-            split8<NP>(x, p);
-#pragma unroll
-            for (int n = 0; n < NP; ++n) w.qf[((ks0 * 4 * KS + f) * NP + n) * 64 + lane] = p[n];
-        }
-        for (int f = wv; f < 4 * KS; f += 4) {  // rows are places of dim_k: two row tiles of 16 for each ks
-            const int row = 16 * (f >> 1) + col, ts = f & 1;
-            const bool ok = row < a.dk;
-            float x[8];
-            u32x4 p[NP];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int tok = place_of(ts, grp, j);
-                x[j] = ok && tok < ch.n ? TY::load(kp[tok * a.kt + row]) : 0.0f;
-            }
-            split8<NP>(x, p);
-#pragma unroll
-            for (int n = 0; n < NP; ++n) w.kt[((ks0 * 4 * KS + f) * NP + n) * 64 + lane] = p[n];
-            if (GRAD) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int tok = place_of(ts, grp, j);
-                    x[j] = ok && tok < ch.n ? TY::load(qp[tok * a.qt + row]) : 0.0f;
-                }
-                split8<NP>(x, p);
-#pragma unroll
-                for (int n = 0; n < NP; ++n) w.qt[((ks0 * 4 * KS + f) * NP + n) * 64 + lane] = p[n];
-            }
+        for (int f = wv; f < 2 * KS; f += 4) {
+            if (f < KS)
+                key_operands<TY, KS, true>(kp, a.kt, ch.n, a.dk, a.kvec, f, lane, w.kf + at, w.kt + at);
+            else
+                key_operands<TY, KS, GRAD>(qp, a.qt, ch.n, a.dk, a.qvec, f - KS, lane, w.qf + at, w.qt + at);
         }
         return;
     }
 
-    __shared__ double G[kC];
+    __shared__ double G[kC];  // in powers of two: sums of g log2(e)
     __shared__ float Bt[kC];
-    __shared__ __align__(16) float L[kC][kC + 4];
-    __shared__ __align__(16) float X[kC][kC + 4];
-    __shared__ __align__(16) float Mx[kC][kC + 4];
+    __shared__ __align__(16) float L[kC][kC + 4];  // L, then M
+    __shared__ __align__(16) float X[kC][kC + 4];  // T
     const int h = blockIdx.y;
     const int hk = h / (a.hv / a.hk);
     const long long vs = slot * a.hv + h;
     if (wv == 0) {
         const long long at = (long long)(ch.tok0 + lane) * a.hv + h;
         const float gv = lane < ch.n ? g[at] : 0.0f;
-        double G0 = gv < kMinDecay ? kMinDecay : gv;
+        double G0 = (double)(gv < kMinDecay ? kMinDecay : gv) * 1.4426950408889634;
         for (int off = 1; off < 64; off <<= 1) {
             const double o = __shfl_up(G0, off);
             if (lane >= off) G0 += o;
@@ -323,8 +351,8 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
         Bt[lane] = b;
         Gates& ga = w.gates[vs];
         ga.G[lane] = G0;
-        ga.gamma[lane] = exp_of(G0);
-        ga.e[lane] = exp_of(last - G0);
+        ga.gamma[lane] = exp2_of(G0);
+        ga.e[lane] = exp2_of(last - G0);
         ga.beta[lane] = b;
     }
     // k.k and q.k: wave wv has row tile wv of k.k and row tile 3 - wv of q.k, five
@@ -339,47 +367,65 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
     for (int ks = 0; ks < KS; ++ks) {
         const int c0 = place_of(ks, grp, 0), c1 = place_of(ks, grp, 4);
         u32x4 qa[NP], ka[NP];
-        float x[8];
-        load8<TY>(qp + (16 * qrow + col) * a.qt, c0, c1, a.dk, 16 * qrow + col < ch.n, a.qvec, x);
-        split8<NP>(x, qa);
-        load8<TY>(kp + (16 * wv + col) * a.kt, c0, c1, a.dk, 16 * wv + col < ch.n, a.kvec, x);
-        split8<NP>(x, ka);
+        load_parts<TY>(qp + (16 * qrow + col) * a.qt, c0, c1, a.dk, 16 * qrow + col < ch.n, a.qvec, qa);
+        load_parts<TY>(kp + (16 * wv + col) * a.kt, c0, c1, a.dk, 16 * wv + col < ch.n, a.kvec, ka);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i > wv && i > qrow) continue;
             u32x4 kb[NP];
-            load8<TY>(kp + (16 * i + col) * a.kt, c0, c1, a.dk, 16 * i + col < ch.n, a.kvec, x);
-            split8<NP>(x, kb);
+            load_parts<TY>(kp + (16 * i + col) * a.kt, c0, c1, a.dk, 16 * i + col < ch.n, a.kvec, kb);
             if (i <= wv) mma<3>(ka, kb, kk[i]);
             if (i <= qrow) mma<3>(qa, kb, qk[i]);
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    {
+        double Gk[4], Gq[4];
+        float bk[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
+            Gk[r] = G[16 * wv + 4 * grp + r];
+            Gq[r] = G[16 * qrow + 4 * grp + r];
+            bk[r] = Bt[16 * wv + 4 * grp + r];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             const int c = 16 * i + col;
+            const double Gc = G[c];
             if (i <= wv) {
-                const int row = 16 * wv + 4 * grp + r;
-                L[row][c] = c < row ? Bt[row] * exp_of(G[row] - G[c]) * kk[i][r] : 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * wv + 4 * grp + r;
+                    L[row][c] = c < row ? bk[r] * exp2_of(Gk[r] - Gc) * kk[i][r] : 0.0f;
+                }
             }
-            const int row = 16 * qrow + 4 * grp + r;
-            Mx[row][c] = c <= row ? a.scale * exp_of(G[row] - G[c]) * qk[i][r] : 0.0f;
+            if (i <= qrow) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * qrow + 4 * grp + r;
+                    qk[i][r] = c <= row ? a.scale * exp2_of(Gq[r] - Gc) * qk[i][r] : 0.0f;
+                }
+            }
         }
     }
     __syncthreads();
     // The 16 x 16 blocks on the diagonal, one for each wave: column `col` of
-    // (I + L)^-1 by substitution, the updates of all later rows at once.
+    // (I + L)^-1 by substitution.
     {
         const int r0 = 16 * wv;
         float x[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = i == col ? 1.0f : 0.0f;
+        for (int i = 0; i < 16; ++i) {
+            float even = i == col ? 1.0f : 0.0f, odd = 0.0f;
 #pragma unroll
-        for (int m = 0; m < 15; ++m)
+            for (int m4 = 0; m4 < i; m4 += 4) {
+                const f32x4 l = *reinterpret_cast<const f32x4*>(&L[r0 + i][r0 + m4]);
 #pragma unroll
-            for (int i = m + 1; i < 16; ++i) x[i] -= L[r0 + i][r0 + m] * x[m];
+                for (int j = 0; j < 4; ++j)
+                    if (m4 + j < i) (j & 1 ? odd : even) -= l[j] * x[m4 + j];
+            }
+            x[i] = even + odd;
+        }
         if (grp == 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) X[r0 + i][r0 + col] = x[i];
@@ -418,6 +464,12 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
         }
     }
     __syncthreads();
+    // M in L's place
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) L[16 * qrow + 4 * grp + r][16 * i + col] = i <= qrow ? qk[i][r] : 0.0f;
+    __syncthreads();
     // Operands, row tile rt and half ts of the summed tokens; those that are zero
     // (above the diagonal, below it in the transposed ones) are not stored.
     for (int f = wv; f < 8; f += 4) {
@@ -433,7 +485,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
             if (!GRAD) {
                 u32x4 pm[NM];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = Mx[row][place_of(ts, grp, j)];
+                for (int j = 0; j < 8; ++j) x[j] = L[row][place_of(ts, grp, j)];
                 split8<NM>(x, pm);
 #pragma unroll
                 for (int n = 0; n < NM; ++n) w.m[((vs * 8 + f) * NM + n) * 64 + lane] = pm[n];
@@ -447,7 +499,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
 #pragma unroll
             for (int n = 0; n < 3; ++n) w.tt[((vs * 8 + f) * 3 + n) * 64 + lane] = p[n];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = Mx[place_of(ts, grp, j)][row];
+            for (int j = 0; j < 8; ++j) x[j] = L[place_of(ts, grp, j)][row];
             split8<3>(x, p);
 #pragma unroll
             for (int n = 0; n < 3; ++n) w.mt[((vs * 8 + f) * 3 + n) * 64 + lane] = p[n];
@@ -459,7 +511,19 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
 // A workgroup has a head's tile of 16 NCT columns of dim_v; wave wv has token tile
 // wv of the chunk and KS / 2 row tiles of the state, which stays in its registers
 // in 32 bits.  What all waves need of each other (parts of S, of the bracket
-// before T, of U) goes through LDS in operand order.
+// before T, of U) goes through LDS in operand order, three exchanges a chunk.
+//
+// With one wave a SIMD nothing hides a latency but the wave itself.  So a chunk's
+// operands have two register sets, and each operand is loaded again as soon as
+// its last product has read it, two chunks ahead: a miss to HBM is shorter than
+// that.  All loads and stores are unconditional (bounds are the buffer
+// descriptors'), so that the compiler's counts of what is in flight stay exact and
+// no load waits for a store.  Operands of many parts (fp16 and float32 at 128 keys)
+// leave room for one set only, loaded one chunk ahead.  LDS reads are issued together behind each barrier,
+// and the products that the chain does not wait for (Q S, and M U with the stores
+// of o, one chunk later) run in their latency.
+constexpr int sets_of(int np, int ks) { return np * ks >= 8 ? 1 : 2; }
+
 template <int N, int NCT, int KSN>
 struct Exchange {  // [part][ks][column tile][lane]
     u32x4 v[N][KSN][NCT][64];
@@ -468,84 +532,112 @@ struct Exchange {  // [part][ks][column tile][lane]
 #pragma unroll
         for (int n = 0; n < N; ++n) reinterpret_cast<u32x2*>(&v[n][rt >> 1][ct][lane])[rt & 1] = p[n];
     }
-    __device__ __forceinline__ void get(int ks, int ct, int lane, u32x4 (&p)[N]) const {
+    __device__ __forceinline__ void get(int lane, u32x4 (&p)[KSN][NCT][N]) const {
 #pragma unroll
-        for (int n = 0; n < N; ++n) p[n] = v[n][ks][ct][lane];
+        for (int ks = 0; ks < KSN; ++ks)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int n = 0; n < N; ++n) p[ks][ct][n] = v[n][ks][ct][lane];
     }
 };
+__device__ __forceinline__ void reads_first() { __builtin_amdgcn_sched_barrier(0); }
 
-template <int A, int B>
-__device__ __forceinline__ void copy(u32x4 (&to)[A][B], const u32x4 (&from)[A][B]) {
-#pragma unroll
-    for (int i = 0; i < A; ++i)
-#pragma unroll
-        for (int j = 0; j < B; ++j) to[i][j] = from[i][j];
-}
-
-template <class TY, int KS, bool GRAD>
-struct ChainOps {  // a chunk's operands of one wave
-    static constexpr int NP = TY::NP, NM = NP == 3 ? 3 : 2;
-    u32x4 kf[KS][NP], qf[GRAD ? 1 : KS][NP], kt[KS / 2][2][NP], t[2][3], m[GRAD ? 1 : 2][NM];
-    f32x4 gamma, e, beta;
-    float last;
-    __device__ __forceinline__ void load(const Space& w, long long ks0, long long vs, int wv, int lane) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                kf[ks][n] = w.kf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
-                if constexpr (!GRAD) qf[ks][n] = w.qf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
-            }
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i)
-#pragma unroll
-            for (int ts = 0; ts < 2; ++ts)
-#pragma unroll
-                for (int n = 0; n < NP; ++n)
-                    kt[i][ts][n] = w.kt[((ks0 * 4 * KS + (wv * (KS / 2) + i) * 2 + ts) * NP + n) * 64 + lane];
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts)
-            if (ts <= (wv >> 1)) {
-#pragma unroll
-                for (int n = 0; n < 3; ++n) t[ts][n] = w.t[((vs * 8 + wv * 2 + ts) * 3 + n) * 64 + lane];
-                if constexpr (!GRAD) {
-#pragma unroll
-                    for (int n = 0; n < NM; ++n) m[ts][n] = w.m[((vs * 8 + wv * 2 + ts) * NM + n) * 64 + lane];
-                }
-            }
-        const Gates& ga = w.gates[vs];
-        const int r = 16 * wv + 4 * (lane >> 4);
-        gamma = *reinterpret_cast<const f32x4*>(&ga.gamma[r]);
-        e = *reinterpret_cast<const f32x4*>(&ga.e[r]);
-        beta = *reinterpret_cast<const f32x4*>(&ga.beta[r]);
-        last = ga.gamma[kC - 1];
-    }
-    __device__ __forceinline__ void take(const ChainOps& x) {
-        copy(kf, x.kf);
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i) copy(kt[i], x.kt[i]);
-        copy(t, x.t);
-        if constexpr (!GRAD) {
-            copy(qf, x.qf);
-            copy(m, x.m);
-        }
-        gamma = x.gamma, e = x.e, beta = x.beta, last = x.last;
-    }
-};
-
-// Values of token tile wv at columns n0 + 16 ct + (lane & 15), as a result lies.
+// A tile of token rows in global memory, as a result lies in registers (row 16 wv +
+// 4 grp + r, column n0 + 16 ct + col): byte offsets from the chunk's first row.
+constexpr uint32_t kNowhere = 0x80000000u;  // behind every descriptor's end
 template <class TY, int NCT>
-__device__ __forceinline__ void load_tile(const typename TY::S* p, long long stride, int n, int n0, int D, int wv,
-                                          int lane, typename TY::S (&x)[NCT][4]) {
+struct Tile {
+    using S = typename TY::S;
+    uint32_t at[NCT], step;  // of row r: at + r step
+    __device__ __forceinline__ Tile(long long stride, int n0, int D, int wv, int lane) {
+        step = (uint32_t)(stride * sizeof(S));
 #pragma unroll
-    for (int ct = 0; ct < NCT; ++ct) {
-        const int c = n0 + 16 * ct + (lane & 15);
+        for (int ct = 0; ct < NCT; ++ct) {
+            const int c = n0 + 16 * ct + (lane & 15);
+            at[ct] = c < D ? (uint32_t)(16 * wv + 4 * (lane >> 4)) * step + c * (uint32_t)sizeof(S) : kNowhere;
+        }
+    }
+    // the descriptor of n rows (none: every access is dropped)
+    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const S* p, long long stride, int n, int D) {
+        const long long bytes = n > 0 ? ((long long)(min(n, kC) - 1) * stride + D) * (long long)sizeof(S) : 0;
+        return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, S (&x)[NCT][4]) const {
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (sizeof(S) == 4)
+                    x[ct][r] = __builtin_bit_cast(S, __builtin_amdgcn_raw_buffer_load_b32(b, at[ct] + r * step, 0, 0));
+                else
+                    x[ct][r] = __builtin_bit_cast(S, __builtin_amdgcn_raw_buffer_load_b16(b, at[ct] + r * step, 0, 0));
+            }
+    }
+    __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, int ct, f32x4 x) const {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int row = 16 * wv + 4 * (lane >> 4) + r;
-            x[ct][r] = row < n && c < D ? p[row * stride + c] : (typename TY::S)0;
+            const S y = TY::store(x[r]);
+            if constexpr (sizeof(S) == 4)
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y), b, at[ct] + r * step, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, y), b, at[ct] + r * step, 0, 0);
         }
     }
+};
+
+// One wave's operands of a key or value head's chunk, from the workspace.
+template <int KS, int NP>
+__device__ __forceinline__ void load_rows(const u32x4* f, long long ks0, int wv, int lane, u32x4 (&x)[KS][NP]) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int n = 0; n < NP; ++n) x[ks][n] = f[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
+}
+template <int KS, int NP>
+__device__ __forceinline__ void load_columns(const u32x4* f, long long ks0, int wv, int lane,
+                                             u32x4 (&x)[KS / 2][2][NP]) {
+#pragma unroll
+    for (int i = 0; i < KS / 2; ++i)
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+            for (int n = 0; n < NP; ++n)
+                x[i][ts][n] = f[((ks0 * 4 * KS + (wv * (KS / 2) + i) * 2 + ts) * NP + n) * 64 + lane];
+}
+// Of a triangle: half 0 of the tokens, and half 1 where the wave's row tile has it
+// (UPPER: the other way round); the half that is zero is loaded as the other one's
+// copy and not used.
+template <int N, bool UPPER>
+__device__ __forceinline__ void load_triangle(const u32x4* f, long long vs, int wv, int lane, u32x4 (&x)[2][N]) {
+#pragma unroll
+    for (int ts = 0; ts < 2; ++ts) {
+        const int from = UPPER ? max(ts, wv >> 1) : min(ts, wv >> 1);
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[ts][n] = f[((vs * 8 + wv * 2 + from) * N + n) * 64 + lane];
+    }
+}
+struct RowGates {
+    f32x4 gamma, e, beta;
+    float last;
+    __device__ __forceinline__ void load(const Gates* g, long long vs, int wv, int lane) {
+        const int r = 16 * wv + 4 * (lane >> 4);
+        gamma = *reinterpret_cast<const f32x4*>(&g[vs].gamma[r]);
+        e = *reinterpret_cast<const f32x4*>(&g[vs].e[r]);
+        beta = *reinterpret_cast<const f32x4*>(&g[vs].beta[r]);
+        last = g[vs].gamma[kC - 1];
+    }
+};
+// A state's rows and columns of this lane.
+template <int NR, int NCT, class F>
+__device__ __forceinline__ void each_of_state(int wv, int lane, int n0, F f) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                f(i, ct, r, 16 * (wv * NR + i) + 4 * (lane >> 4) + r, n0 + 16 * ct + (lane & 15));
 }
 
 template <class TY, int KS, int NCT, bool GRAD>
@@ -553,8 +645,7 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
                                                                const float* initial, typename TY::S* __restrict__ o,
                                                                float* final_state) {
     using S = typename TY::S;
-    using Ops = ChainOps<TY, KS, GRAD>;
-    constexpr int NP = TY::NP, NM = Ops::NM, NR = KS / 2;
+    constexpr int NP = TY::NP, NM = NP == 3 ? 3 : 2, NR = KS / 2, SETS = sets_of(NP, KS);
     constexpr int ORDO = NP == 3 ? 3 : 2;  // o is rounded to 16 bits or to 32
     __shared__ Exchange<3, NCT, KS> xs;
     __shared__ Exchange<3, NCT, 2> xp, xe;
@@ -570,30 +661,33 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
     const int lane = threadIdx.x & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
     int tok0, len;
     span_of(a, s, tok0, len);
+    tok0 = __builtin_amdgcn_readfirstlane(tok0);
+    len = __builtin_amdgcn_readfirstlane(len);
     const int chunks = (int)(((long long)len + kC - 1) / kC);
     const long long base = base_of(a, s);
 
     f32x4 st[NR][NCT];
     const long long sbase = sh * a.dk * a.dv;
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * (wv * NR + i) + 4 * grp + r, c = n0 + 16 * ct + col;
-                st[i][ct][r] = initial && row < a.dk && c < a.dv ? initial[sbase + (long long)row * a.dv + c] : 0.0f;
-            }
-    Ops cur;
-    S vc[NCT][4];
-    if (chunks > 0) {
-        cur.load(w, base * a.hk + hk, base * a.hv + h, wv, lane);
-        load_tile<TY, NCT>(v + (long long)tok0 * a.vt + h * a.vh, a.vt, len, n0, a.dv, wv, lane, vc);
-    }
-    for (int c = 0; c < chunks; ++c) {
-        const int n = min(kC, len - c * kC);
-        const long long vs = (base + c) * a.hv + h;
-        // the state's parts, for all waves
+    each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int c) {
+        st[i][ct][r] = initial && row < a.dk && c < a.dv ? initial[sbase + (long long)row * a.dv + c] : 0.0f;
+    });
+
+    struct Set {
+        u32x4 kf[KS][NP], qf[GRAD ? 1 : KS][NP], kt[NR][2][NP], t[2][3], m[2][GRAD ? 1 : NM];
+        S v[NCT][4];
+        RowGates g;
+    };
+    const Tile<TY, NCT> vt(a.vt, n0, a.dv, wv, lane);
+    const Tile<TY, NCT> ot((long long)a.hv * a.dv, n0, a.dv, wv, lane);
+    const S* const v0 = v + (long long)tok0 * a.vt + h * a.vh;
+    S* const o0 = o + ((long long)tok0 * a.hv + h) * a.dv;
+    auto kslot = [&](int c) { return (base + min(c, chunks - 1)) * a.hk + hk; };
+    auto vslot = [&](int c) { return (base + min(c, chunks - 1)) * a.hv + h; };
+    auto load_v = [&](Set& x, int c) {
+        c = min(c, chunks - 1);
+        vt.load(vt.rows(v0 + (long long)c * kC * a.vt, a.vt, len - c * kC, a.dv), x.v);
+    };
+    auto put_state = [&]() {
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -601,57 +695,88 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
                 u32x2 p[3];
                 split4<3>(st[i][ct], p);
                 xs.put(wv * NR + i, ct, lane, p);
-                if (GRAD) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        w.s0[(vs * 32 * KS + 16 * (wv * NR + i) + 4 * grp + r) * w.dvp + n0 + 16 * ct + col] =
-                            st[i][ct][r];
-                }
             }
-        Ops nxt;
-        S vn[NCT][4];
-        {  // the next chunk's operands (the last one's again, at the end)
-            const int cn = min(c + 1, chunks - 1);
-            nxt.load(w, (base + cn) * a.hk + hk, (base + cn) * a.hv + h, wv, lane);
-            load_tile<TY, NCT>(v + (long long)(tok0 + cn * kC) * a.vt + h * a.vh, a.vt, len - cn * kC, n0, a.dv, wv,
-                               lane, vn);
-        }
-        __syncthreads();
-        f32x4 ks_[NCT], qs[NCT];
+    };
+    f32x4 qs[NCT];
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) ks_[ct] = f32x4{0, 0, 0, 0}, qs[ct] = f32x4{0, 0, 0, 0};
+    for (int ct = 0; ct < NCT; ++ct) qs[ct] = f32x4{0, 0, 0, 0};
+    // o of chunk c: what Q S gave, and M U
+    auto finish_o = [&](const Set& x, const u32x4 (&b)[2][NCT][GRAD ? 1 : NM], int c) {
+        if constexpr (!GRAD) {
+            const auto to = ot.rows(o0 + (long long)c * kC * a.hv * a.dv, (long long)a.hv * a.dv,
+                                    c >= 0 ? len - c * kC : 0, a.dv);
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) mma<ORDO>(x.m[0], b[0][ct], qs[ct]);
+            if (wv >= 2) {
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) mma<ORDO>(x.m[1], b[1][ct], qs[ct]);
+            }
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) ot.store(to, ct, qs[ct]);
+        }
+    };
+    auto step = [&](Set& x, Set& before, int c) {
+        const long long vs = vslot(c);
+        __syncthreads();
+        u32x4 b[KS][NCT][3], bu[2][NCT][GRAD ? 1 : NM];
+        xs.get(lane, b);
+        if constexpr (!GRAD) xu.get(lane, bu);
+        reads_first();
+        if constexpr (GRAD) {
+            each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int cc) {
+                w.s0[(vs * 32 * KS + row) * w.dvp + cc] = st[i][ct][r];
+            });
+        }
+        f32x4 kx[NCT];
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) kx[ct] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                u32x4 b[3];
-                xs.get(ks, ct, lane, b);
-                mma<3>(cur.kf[ks], b, ks_[ct]);
-                if constexpr (!GRAD) mma<ORDO>(cur.qf[ks], b, qs[ct]);
-            }
+            for (int ct = 0; ct < NCT; ++ct) mma<3>(x.kf[ks], b[ks][ct], kx[ct]);
+        load_rows<KS, NP>(w.kf, kslot(c + SETS), wv, lane, x.kf);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
-            f32x4 x;
+            f32x4 y;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = cur.beta[r] * (TY::load(vc[ct][r]) - cur.gamma[r] * ks_[ct][r]);
+            for (int r = 0; r < 4; ++r) y[r] = x.g.beta[r] * (TY::load(x.v[ct][r]) - x.g.gamma[r] * kx[ct][r]);
             u32x2 p[3];
-            split4<3>(x, p);
+            split4<3>(y, p);
             xp.put(wv, ct, lane, p);
         }
+        load_v(x, c + SETS);
+        if constexpr (!GRAD) {
+            finish_o(before, bu, c - 1);
+            load_triangle<NM, false>(w.m, vslot(c + SETS - 1), wv, lane, before.m);
+        }
         __syncthreads();
+        u32x4 bp[2][NCT][3];
+        xp.get(lane, bp);
+        reads_first();
+        if constexpr (!GRAD) {
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                qs[ct] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) mma<ORDO>(x.qf[ks], b[ks][ct], qs[ct]);
+            }
+            load_rows<KS, NP>(w.qf, kslot(c + SETS), wv, lane, x.qf);
+        }
         f32x4 u[NCT];
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             u[ct] = f32x4{0, 0, 0, 0};
+            mma<3>(x.t[0], bp[0][ct], u[ct]);
+        }
+        if (wv >= 2) {
 #pragma unroll
-            for (int ts = 0; ts < 2; ++ts)
-                if (ts <= (wv >> 1)) {
-                    u32x4 b[3];
-                    xp.get(ts, ct, lane, b);
-                    mma<3>(cur.t[ts], b, u[ct]);
-                }
+            for (int ct = 0; ct < NCT; ++ct) mma<3>(x.t[1], bp[1][ct], u[ct]);
+        }
+        load_triangle<3, false>(w.t, vslot(c + SETS), wv, lane, x.t);
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
             u32x2 p[3];
-            split4<3>(u[ct] * cur.e, p);
+            split4<3>(u[ct] * x.g.e, p);
             xe.put(wv, ct, lane, p);
             if constexpr (GRAD) {
 #pragma unroll
@@ -661,59 +786,61 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
                 u32x2 pu[NM];
                 split4<NM>(u[ct], pu);
                 xu.put(wv, ct, lane, pu);
+                qs[ct] = qs[ct] * x.g.gamma * a.scale;
             }
         }
         __syncthreads();
+        u32x4 be[2][NCT][3];
+        xe.get(lane, be);
+        reads_first();
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) st[i][ct] *= cur.last;
+            for (int ct = 0; ct < NCT; ++ct) st[i][ct] *= x.g.last;
+        x.g.load(w.gates, vslot(c + SETS), wv, lane);
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                u32x4 b[3];
-                xe.get(ts, ct, lane, b);
-#pragma unroll
-                for (int i = 0; i < NR; ++i) mma<3>(cur.kt[i][ts], b, st[i][ct]);
-            }
-        if constexpr (!GRAD) {
-            S* op = o + ((long long)(tok0 + c * kC) * a.hv + h) * a.dv;
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                f32x4 x = qs[ct] * cur.gamma * a.scale;
-#pragma unroll
-                for (int ts = 0; ts < 2; ++ts)
-                    if (ts <= (wv >> 1)) {
-                        u32x4 b[NM];
-                        xu.get(ts, ct, lane, b);
-                        mma<ORDO>(cur.m[ts], b, x);
-                    }
-                const int cc = n0 + 16 * ct + col;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * wv + 4 * grp + r;
-                    if (row < n && cc < a.dv) op[(long long)row * a.hv * a.dv + cc] = TY::store(x[r]);
-                }
-            }
-        }
-        cur.take(nxt);
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) vc[ct][r] = vn[ct][r];
-    }
-    if (final_state) {
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * (wv * NR + i) + 4 * grp + r, c = n0 + 16 * ct + col;
-                    if (row < a.dk && c < a.dv) final_state[sbase + (long long)row * a.dv + c] = st[i][ct][r];
-                }
+                for (int i = 0; i < NR; ++i) mma<3>(x.kt[i][ts], be[ts][ct], st[i][ct]);
+        load_columns<KS, NP>(w.kt, kslot(c + SETS), wv, lane, x.kt);
+        put_state();
+    };
+    if (chunks > 0) {
+        Set x[SETS];
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) {
+            load_rows<KS, NP>(w.kf, kslot(i), wv, lane, x[i].kf);
+            load_v(x[i], i);
+            if constexpr (!GRAD) load_rows<KS, NP>(w.qf, kslot(i), wv, lane, x[i].qf);
+            load_triangle<3, false>(w.t, vslot(i), wv, lane, x[i].t);
+            x[i].g.load(w.gates, vslot(i), wv, lane);
+            load_columns<KS, NP>(w.kt, kslot(i), wv, lane, x[i].kt);
+            if constexpr (!GRAD) load_triangle<NM, false>(w.m, vslot(0), wv, lane, x[i].m);
+        }
+        put_state();
+        int c = 0;
+        for (; c + SETS <= chunks; c += SETS) {
+            step(x[0], x[SETS - 1], c);
+            if constexpr (SETS == 2) step(x[1], x[0], c + 1);
+        }
+        const bool odd = SETS == 1 || c < chunks;  // the last chunk's set is x[0]
+        if (c < chunks) step(x[0], x[SETS - 1], c);
+        if constexpr (!GRAD) {
+            __syncthreads();
+            u32x4 bu[2][NCT][NM];
+            xu.get(lane, bu);
+            if (odd)
+                finish_o(x[0], bu, chunks - 1);
+            else
+                finish_o(x[SETS - 1], bu, chunks - 1);
+        }
     }
+    if (final_state)
+        each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int c) {
+            if (row < a.dk && c < a.dv) final_state[sbase + (long long)row * a.dv + c] = st[i][ct][r];
+        });
 }
 
 // ========================================= along a sequence: the gradients' chain
@@ -721,54 +848,8 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
 //   dU  = M^T dO + diag(e) K dS           dR = T^T dU   (of the bracket, by beta)
 //   dV  = diag(beta) dR
 //   dS0 = gamma_63 dS + scale Q^T diag(gamma) dO - K^T diag(gamma beta) dR
-// The same tiles and exchanges as the states' chain, from the last chunk on.
-template <class TY, int KS>
-struct ReverseOps {
-    static constexpr int NP = TY::NP;
-    u32x4 kf[KS][NP], kt[KS / 2][2][NP], qt[KS / 2][2][NP], tt[2][3], mt[2][3];
-    f32x4 gamma, e, beta;
-    float last;
-    __device__ __forceinline__ void load(const Space& w, long long ks0, long long vs, int wv, int lane) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-            for (int n = 0; n < NP; ++n) kf[ks][n] = w.kf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i)
-#pragma unroll
-            for (int ts = 0; ts < 2; ++ts)
-#pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    const long long f = ((ks0 * 4 * KS + (wv * (KS / 2) + i) * 2 + ts) * NP + n) * 64 + lane;
-                    kt[i][ts][n] = w.kt[f];
-                    qt[i][ts][n] = w.qt[f];
-                }
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts)
-            if (ts >= (wv >> 1)) {
-#pragma unroll
-                for (int n = 0; n < 3; ++n) {
-                    tt[ts][n] = w.tt[((vs * 8 + wv * 2 + ts) * 3 + n) * 64 + lane];
-                    mt[ts][n] = w.mt[((vs * 8 + wv * 2 + ts) * 3 + n) * 64 + lane];
-                }
-            }
-        const Gates& ga = w.gates[vs];
-        const int r = 16 * wv + 4 * (lane >> 4);
-        gamma = *reinterpret_cast<const f32x4*>(&ga.gamma[r]);
-        e = *reinterpret_cast<const f32x4*>(&ga.e[r]);
-        beta = *reinterpret_cast<const f32x4*>(&ga.beta[r]);
-        last = ga.gamma[kC - 1];
-    }
-    __device__ __forceinline__ void take(const ReverseOps& x) {
-        copy(kf, x.kf);
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i) copy(kt[i], x.kt[i]), copy(qt[i], x.qt[i]);
-        copy(tt, x.tt);
-        copy(mt, x.mt);
-        gamma = x.gamma, e = x.e, beta = x.beta, last = x.last;
-    }
-};
-
+// The same tiles, exchanges and register sets as the states' chain, from the last
+// chunk on.
 template <int NP, int NCT, int KS>
 struct ReverseLds {
     Exchange<3, NCT, KS> s;
@@ -783,7 +864,7 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
                                                                  typename TY::S* __restrict__ gv,
                                                                  float* grad_initial) {
     using S = typename TY::S;
-    constexpr int NP = TY::NP, NR = KS / 2;
+    constexpr int NP = TY::NP, NR = KS / 2, SETS = sets_of(NP, KS);
     extern __shared__ __align__(16) unsigned char lds[];
     auto& sh_ = *reinterpret_cast<ReverseLds<NP, NCT, KS>*>(lds);
     auto& xs = sh_.s;
@@ -799,32 +880,33 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
     const int lane = threadIdx.x & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
     int tok0, len;
     span_of(a, s, tok0, len);
+    tok0 = __builtin_amdgcn_readfirstlane(tok0);
+    len = __builtin_amdgcn_readfirstlane(len);
     const int chunks = (int)(((long long)len + kC - 1) / kC);
     const long long base = base_of(a, s);
 
     f32x4 st[NR][NCT];
     const long long sbase = sh * a.dk * a.dv;
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * (wv * NR + i) + 4 * grp + r, c = n0 + 16 * ct + col;
-                st[i][ct][r] =
-                    grad_final && row < a.dk && c < a.dv ? grad_final[sbase + (long long)row * a.dv + c] : 0.0f;
-            }
-    ReverseOps<TY, KS> cur;
-    S oc[NCT][4];
-    if (chunks > 0) {
-        const int c = chunks - 1;
-        cur.load(w, (base + c) * a.hk + hk, (base + c) * a.hv + h, wv, lane);
-        load_tile<TY, NCT>(go + (long long)(tok0 + c * kC) * a.gt + h * a.gh, a.gt, len - c * kC, n0, a.dv, wv, lane,
-                           oc);
-    }
-    for (int c = chunks - 1; c >= 0; --c) {
-        const int n = min(kC, len - c * kC);
-        const long long vs = (base + c) * a.hv + h;
+    each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int c) {
+        st[i][ct][r] = grad_final && row < a.dk && c < a.dv ? grad_final[sbase + (long long)row * a.dv + c] : 0.0f;
+    });
+    struct Set {
+        u32x4 kf[KS][NP], kt[NR][2][NP], qt[NR][2][NP], tt[2][3], mt[2][3];
+        S o[NCT][4];
+        RowGates g;
+    };
+    const Tile<TY, NCT> got(a.gt, n0, a.dv, wv, lane);
+    const Tile<TY, NCT> gvt((long long)a.hv * a.dv, n0, a.dv, wv, lane);
+    const S* const go0 = go + (long long)tok0 * a.gt + h * a.gh;
+    S* const gv0 = gv + ((long long)tok0 * a.hv + h) * a.dv;
+    auto kslot = [&](int c) { return (base + max(c, 0)) * a.hk + hk; };
+    auto vslot = [&](int c) { return (base + max(c, 0)) * a.hv + h; };
+    auto load_o = [&](Set& x, int c) {
+        c = max(c, 0);
+        got.load(got.rows(go0 + (long long)c * kC * a.gt, a.gt, len - c * kC, a.dv), x.o);
+    };
+    // what a chunk's first stage reads: dS, and its dO
+    auto put_first = [&](const Set& x) {
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -832,120 +914,131 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
                 u32x2 p[3];
                 split4<3>(st[i][ct], p);
                 xs.put(wv * NR + i, ct, lane, p);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    w.ds[(vs * 32 * KS + 16 * (wv * NR + i) + 4 * grp + r) * w.dvp + n0 + 16 * ct + col] =
-                        st[i][ct][r];
             }
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
-            f32x4 x;
+            f32x4 y;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = TY::load(oc[ct][r]);
+            for (int r = 0; r < 4; ++r) y[r] = TY::load(x.o[ct][r]);
             u32x2 p[NP], p3[3];
-            split4<NP>(x, p);
+            split4<NP>(y, p);
             xo.put(wv, ct, lane, p);
-            split4<3>(x * cur.gamma * a.scale, p3);
+            split4<3>(y * x.g.gamma * a.scale, p3);
             xg.put(wv, ct, lane, p3);
         }
-        ReverseOps<TY, KS> nxt;
-        S on[NCT][4];
-        {  // the chunk before (the first one's again, at the end)
-            const int cn = max(c - 1, 0);
-            nxt.load(w, (base + cn) * a.hk + hk, (base + cn) * a.hv + h, wv, lane);
-            load_tile<TY, NCT>(go + (long long)(tok0 + cn * kC) * a.gt + h * a.gh, a.gt, len - cn * kC, n0, a.dv, wv,
-                               lane, on);
-        }
+    };
+    auto step = [&](Set& x, Set& next, int c) {
+        const long long vs = vslot(c);
         __syncthreads();
-        f32x4 x[NCT];
+        u32x4 b[KS][NCT][3], bo[2][NCT][NP];
+        xs.get(lane, b);
+        xo.get(lane, bo);
+        reads_first();
+        each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int cc) {
+            w.ds[(vs * 32 * KS + row) * w.dvp + cc] = st[i][ct][r];
+        });
+        f32x4 y[NCT];
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) x[ct] = f32x4{0, 0, 0, 0};
+        for (int ct = 0; ct < NCT; ++ct) y[ct] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                u32x4 b[3];
-                xs.get(ks, ct, lane, b);
-                mma<3>(cur.kf[ks], b, x[ct]);
-            }
+            for (int ct = 0; ct < NCT; ++ct) mma<3>(x.kf[ks], b[ks][ct], y[ct]);
+        load_rows<KS, NP>(w.kf, kslot(c - SETS), wv, lane, x.kf);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
-            x[ct] *= cur.e;
+            y[ct] *= x.g.e;
+            mma<3>(x.mt[1], bo[1][ct], y[ct]);
+        }
+        if (wv < 2) {
 #pragma unroll
-            for (int ts = 0; ts < 2; ++ts)
-                if (ts >= (wv >> 1)) {
-                    u32x4 b[NP];
-                    xo.get(ts, ct, lane, b);
-                    mma<3>(cur.mt[ts], b, x[ct]);
-                }
+            for (int ct = 0; ct < NCT; ++ct) mma<3>(x.mt[0], bo[0][ct], y[ct]);
+        }
+        load_triangle<3, true>(w.mt, vslot(c - SETS), wv, lane, x.mt);
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
             u32x2 p[3];
-            split4<3>(x[ct], p);
+            split4<3>(y[ct], p);
             xu.put(wv, ct, lane, p);
         }
+        load_o(x, c - SETS);
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) st[i][ct] *= cur.last;
+        u32x4 bu[2][NCT][3], bg[2][NCT][3];
+        xu.get(lane, bu);
+        xg.get(lane, bg);
+        reads_first();
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
-            f32x4 y = {0, 0, 0, 0};
+            y[ct] = f32x4{0, 0, 0, 0};
+            mma<3>(x.tt[1], bu[1][ct], y[ct]);
+        }
+        if (wv < 2) {
 #pragma unroll
-            for (int ts = 0; ts < 2; ++ts)
-                if (ts >= (wv >> 1)) {
-                    u32x4 b[3];
-                    xu.get(ts, ct, lane, b);
-                    mma<3>(cur.tt[ts], b, y);
-                }
-            const f32x4 dv = y * cur.beta;
+            for (int ct = 0; ct < NCT; ++ct) mma<3>(x.tt[0], bu[0][ct], y[ct]);
+        }
+        load_triangle<3, true>(w.tt, vslot(c - SETS), wv, lane, x.tt);
+        const auto to = gvt.rows(gv0 + (long long)c * kC * a.hv * a.dv, (long long)a.hv * a.dv, len - c * kC, a.dv);
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            const f32x4 dv = y[ct] * x.g.beta;
             u32x2 p[3];
-            split4<3>(-(dv * cur.gamma), p);
+            split4<3>(-(dv * x.g.gamma), p);
             xr.put(wv, ct, lane, p);
-            const int cc = n0 + 16 * ct + col;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * wv + 4 * grp + r;
-                w.dr[(vs * kC + row) * w.dvp + cc] = y[r];
-                if (row < n && cc < a.dv)
-                    gv[((long long)(tok0 + c * kC + row) * a.hv + h) * a.dv + cc] = TY::store(dv[r]);
-            }
+            for (int r = 0; r < 4; ++r)
+                w.dr[(vs * kC + 16 * wv + 4 * grp + r) * w.dvp + n0 + 16 * ct + col] = y[ct][r];
+            gvt.store(to, ct, dv);
         }
 #pragma unroll
-        for (int ts = 0; ts < 2; ++ts)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                u32x4 b[3];
-                xg.get(ts, ct, lane, b);
-#pragma unroll
-                for (int i = 0; i < NR; ++i) mma<3>(cur.qt[i][ts], b, st[i][ct]);
-            }
-        __syncthreads();
-#pragma unroll
-        for (int ts = 0; ts < 2; ++ts)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                u32x4 b[3];
-                xr.get(ts, ct, lane, b);
-#pragma unroll
-                for (int i = 0; i < NR; ++i) mma<3>(cur.kt[i][ts], b, st[i][ct]);
-            }
-        cur.take(nxt);
-#pragma unroll
-        for (int ct = 0; ct < NCT; ++ct)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) oc[ct][r] = on[ct][r];
-    }
-    if (grad_initial) {
-#pragma unroll
         for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) st[i][ct] *= x.g.last;
+        x.g.load(w.gates, vslot(c - SETS), wv, lane);
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * (wv * NR + i) + 4 * grp + r, c = n0 + 16 * ct + col;
-                    if (row < a.dk && c < a.dv) grad_initial[sbase + (long long)row * a.dv + c] = st[i][ct][r];
-                }
+                for (int i = 0; i < NR; ++i) mma<3>(x.qt[i][ts], bg[ts][ct], st[i][ct]);
+        load_columns<KS, NP>(w.qt, kslot(c - SETS), wv, lane, x.qt);
+        __syncthreads();
+        u32x4 br[2][NCT][3];
+        xr.get(lane, br);
+        reads_first();
+#pragma unroll
+        for (int ts = 0; ts < 2; ++ts)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int i = 0; i < NR; ++i) mma<3>(x.kt[i][ts], br[ts][ct], st[i][ct]);
+        load_columns<KS, NP>(w.kt, kslot(c - SETS), wv, lane, x.kt);
+        put_first(next);
+    };
+    if (chunks > 0) {
+        Set x[SETS];
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) {
+            const int c = chunks - 1 - i;
+            load_o(x[i], c);
+            x[i].g.load(w.gates, vslot(c), wv, lane);
+            load_rows<KS, NP>(w.kf, kslot(c), wv, lane, x[i].kf);
+            load_triangle<3, true>(w.mt, vslot(c), wv, lane, x[i].mt);
+            load_triangle<3, true>(w.tt, vslot(c), wv, lane, x[i].tt);
+            load_columns<KS, NP>(w.qt, kslot(c), wv, lane, x[i].qt);
+            load_columns<KS, NP>(w.kt, kslot(c), wv, lane, x[i].kt);
+        }
+        put_first(x[0]);
+        int c = chunks - 1;
+        for (; c + 1 >= SETS; c -= SETS) {
+            step(x[0], x[SETS - 1], c);
+            if constexpr (SETS == 2) step(x[1], x[0], c - 1);
+        }
+        if (c == 0) step(x[0], x[SETS - 1], 0);
     }
+    if (grad_initial)
+        each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int c) {
+            if (row < a.dk && c < a.dv) grad_initial[sbase + (long long)row * a.dv + c] = st[i][ct][r];
+        });
 }
 
 // ====================================================== all chunks: the gradients
@@ -1119,7 +1212,7 @@ __global__ __launch_bounds__(kThreads) void delta_grads_kernel(
                 const int row = 16 * wv + 4 * grp + r;
                 float f = 0.0f, e = 0.0f;
                 if (i <= wv && c <= row) {
-                    const float decay = exp_of(G[row] - G[c]);
+                    const float decay = exp2_of(G[row] - G[c]);
                     f = a.scale * decay * dm[i][r];
                     if (c < row) {
                         const float x = -decay * dl[i][r];       // dL Gamma
@@ -1189,7 +1282,7 @@ __global__ __launch_bounds__(kThreads) void delta_grads_kernel(
             double x = d;
             if (lane == kC - 1) {
                 const float sum = (dotted[0] + dotted[1]) + (dotted[2] + dotted[3]);
-                x += (double)all + (double)exp_of(G[kC - 1]) * sum;
+                x += (double)all + (double)exp2_of(G[kC - 1]) * sum;
             }
             for (int off = 1; off < 64; off <<= 1) {
                 const double o = __shfl_down(x, off);
@@ -1468,6 +1561,9 @@ int check_shape(const delta_rule_shape_t* p, bool step, Shape* a) {
     a->gt = p->go_stride_t, a->gh = p->go_stride_h;
     a->chunks = dense ? (int)(((long long)p->seq_len + kC - 1) / kC) : 0;
     a->slots = dense ? (long long)a->chunks * n_seq : p->n_tokens / kC + n_seq;
+    // a chunk's rows of v, o and grad_o are addressed with 31 bits
+    for (long long st : {p->v_stride_t, p->go_stride_t, (long long)p->heads_v * p->dim_v})
+        if (!step && (st > INT_MAX || (kC * st + p->dim_v) * size_of(p->type) > INT_MAX)) return CFC_ERR_UNSUPPORTED;
     const long long tiles = (p->dim_v + 31) / 32 * 2;
     if (a->slots > kMaxBlocks || (long long)n_seq * p->heads_v > kMaxBlocks / tiles) return CFC_ERR_UNSUPPORTED;
     return CFC_OK;
