@@ -32,6 +32,9 @@ SOURCE_FLAGS = {
     # of accumulation registers first (the training-scale fused kernel then
     # issues 680 fewer copies and ran 0.7 % faster on MI355X)
     "cfc.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+    # the delta rule's results are split into parts and joined on the vector
+    # units: from 2 to 4 workgroups of its prep kernel on a CU
+    "delta_rule.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

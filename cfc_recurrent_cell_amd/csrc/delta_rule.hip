@@ -5,8 +5,8 @@
 // with G_i the sum of the chunk's decays up to token i, gamma_i = exp(G_i),
 // e_i = exp(G_63 - G_i), Gamma_ij = exp(G_i - G_j) for i >= j, the recurrence is
 //
-//   L_ij = beta_i Gamma_ij k_i.k_j  (i > j),   T = (I + L)^-1
-//   U    = T diag(beta) (V - diag(gamma) K S0)
+//   L_ij = beta_i Gamma_ij k_i.k_j  (i > j),   T = (I + L)^-1 diag(beta)
+//   U    = T (V - diag(gamma) K S0)
 //   O    = scale diag(gamma) Q S0 + M U,       M_ij = scale Gamma_ij q_i.k_j (i >= j)
 //   S1   = gamma_63 S0 + K^T diag(e) U
 //
@@ -125,6 +125,26 @@ __device__ __forceinline__ void mma(const u32x4 (&a)[NA], const u32x4 (&b)[NB], 
 // column l & 15), so a result becomes the next product's operand as it is.
 __device__ __forceinline__ int place_of(int ks, int g, int j) { return 32 * ks + (j < 4 ? 4 * g + j : 12 + 4 * g + j); }
 
+// Memory through buffer descriptors: a uniform base, a lane's 32-bit offset and a
+// uniform one cost no address arithmetic on the vector units, and what lies behind
+// the descriptor's end reads as zero and is not written, so that accesses need no
+// branches.  kNowhere is behind every end.
+constexpr uint32_t kNowhere = 0x80000000u;
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer_of(const void* p, long long bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+// The n'th operand part (64 lanes of 16 bytes) of an array of `parts`, and this lane's own of it.
+struct Parts {
+    Buffer b;
+    uint32_t at;
+    __device__ __forceinline__ Parts(const u32x4* p, long long parts_before, int parts, int lane)
+        : b(buffer_of(p + parts_before * 64, (long long)parts * 1024)), at(16 * lane) {}
+    __device__ __forceinline__ u32x4 operator[](int n) const {
+        return __builtin_amdgcn_raw_buffer_load_b128(b, at, 1024 * n, 0);
+    }
+};
+
 // Eight elements, row[c0 .. c0+3] and row[c1 .. c1+3], zero from D on and where !ok.
 template <class TY>
 __device__ __forceinline__ void load8(const typename TY::S* row, int c0, int c1, int D, bool ok, bool vec,
@@ -151,6 +171,38 @@ __device__ __forceinline__ void load8(const typename TY::S* row, int c0, int c1,
         for (int j = 0; j < 8; ++j) {
             const int c = j < 4 ? c0 + j : c1 + j - 4;
             x[j] = ok && c < D ? TY::load(row[c]) : 0.0f;
+        }
+    }
+}
+
+// The same from a buffer: columns c ... c + 7 of the row at byte `row`.
+template <class TY>
+__device__ __forceinline__ void load8(Buffer b, uint32_t row, int c, int D, bool ok, bool vec, float (&x)[8]) {
+    constexpr int Z = sizeof(typename TY::S);
+    if (vec) {  // 4 elements are one aligned load
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = ok && c + 4 * h < D ? row + (c + 4 * h) * Z : kNowhere;
+            if constexpr (Z == 4) {
+                const u32x4 y = __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[4 * h + j] = __uint_as_float(y[j]);
+            } else {
+                const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(b, at, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[4 * h + j] = TY::load(__builtin_bit_cast(
+                        typename TY::S, (uint16_t)(j & 1 ? y[j >> 1] >> 16 : y[j >> 1] & 0xffff)));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t at = ok && c + j < D ? row + (c + j) * Z : kNowhere;
+            if constexpr (Z == 4)
+                x[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0));
+            else
+                x[j] = TY::load(__builtin_bit_cast(typename TY::S, __builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0)));
         }
     }
 }
@@ -333,7 +385,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
     __shared__ double G[kC];  // in powers of two: sums of g log2(e)
     __shared__ float Bt[kC];
     __shared__ __align__(16) float L[kC][kC + 4];  // L, then M
-    __shared__ __align__(16) float X[kC][kC + 4];  // T
+    __shared__ __align__(16) float X[kC][kC + 4];  // (I + L)^-1
     const int h = blockIdx.y;
     const int hk = h / (a.hv / a.hk);
     const long long vs = slot * a.hv + h;
@@ -478,7 +530,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
         if (ts <= (rt >> 1)) {
             u32x4 p[3];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = X[row][place_of(ts, grp, j)];
+            for (int j = 0; j < 8; ++j) x[j] = X[row][place_of(ts, grp, j)] * Bt[place_of(ts, grp, j)];
             split8<3>(x, p);
 #pragma unroll
             for (int n = 0; n < 3; ++n) w.t[((vs * 8 + f) * 3 + n) * 64 + lane] = p[n];
@@ -545,7 +597,6 @@ __device__ __forceinline__ void reads_first() { __builtin_amdgcn_sched_barrier(0
 
 // A tile of token rows in global memory, as a result lies in registers (row 16 wv +
 // 4 grp + r, column n0 + 16 ct + col): byte offsets from the chunk's first row.
-constexpr uint32_t kNowhere = 0x80000000u;  // behind every descriptor's end
 template <class TY, int NCT>
 struct Tile {
     using S = typename TY::S;
@@ -559,11 +610,11 @@ struct Tile {
         }
     }
     // the descriptor of n rows (none: every access is dropped)
-    static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const S* p, long long stride, int n, int D) {
+    static __device__ __forceinline__ Buffer rows(const S* p, long long stride, int n, int D) {
         const long long bytes = n > 0 ? ((long long)(min(n, kC) - 1) * stride + D) * (long long)sizeof(S) : 0;
-        return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)bytes, 0x00020000);
+        return buffer_of(p, bytes);
     }
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t b, S (&x)[NCT][4]) const {
+    __device__ __forceinline__ void load(Buffer b, S (&x)[NCT][4]) const {
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
@@ -574,7 +625,7 @@ struct Tile {
                     x[ct][r] = __builtin_bit_cast(S, __builtin_amdgcn_raw_buffer_load_b16(b, at[ct] + r * step, 0, 0));
             }
     }
-    __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, int ct, f32x4 x) const {
+    __device__ __forceinline__ void store(Buffer b, int ct, f32x4 x) const {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const S y = TY::store(x[r]);
@@ -589,42 +640,47 @@ struct Tile {
 // One wave's operands of a key or value head's chunk, from the workspace.
 template <int KS, int NP>
 __device__ __forceinline__ void load_rows(const u32x4* f, long long ks0, int wv, int lane, u32x4 (&x)[KS][NP]) {
+    const Parts p(f, (ks0 * 4 + wv) * KS * NP, KS * NP, lane);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int n = 0; n < NP; ++n) x[ks][n] = f[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
+        for (int n = 0; n < NP; ++n) x[ks][n] = p[ks * NP + n];
 }
 template <int KS, int NP>
 __device__ __forceinline__ void load_columns(const u32x4* f, long long ks0, int wv, int lane,
                                              u32x4 (&x)[KS / 2][2][NP]) {
+    const Parts p(f, (ks0 * 4 + wv) * KS * NP, KS * NP, lane);
 #pragma unroll
     for (int i = 0; i < KS / 2; ++i)
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts)
 #pragma unroll
-            for (int n = 0; n < NP; ++n)
-                x[i][ts][n] = f[((ks0 * 4 * KS + (wv * (KS / 2) + i) * 2 + ts) * NP + n) * 64 + lane];
+            for (int n = 0; n < NP; ++n) x[i][ts][n] = p[(i * 2 + ts) * NP + n];
 }
 // Of a triangle: half 0 of the tokens, and half 1 where the wave's row tile has it
 // (UPPER: the other way round); the half that is zero is loaded as the other one's
 // copy and not used.
 template <int N, bool UPPER>
 __device__ __forceinline__ void load_triangle(const u32x4* f, long long vs, int wv, int lane, u32x4 (&x)[2][N]) {
+    const Parts p(f, (vs * 4 + wv) * 2 * N, 2 * N, lane);
 #pragma unroll
     for (int ts = 0; ts < 2; ++ts) {
         const int from = UPPER ? max(ts, wv >> 1) : min(ts, wv >> 1);
 #pragma unroll
-        for (int n = 0; n < N; ++n) x[ts][n] = f[((vs * 8 + wv * 2 + from) * N + n) * 64 + lane];
+        for (int n = 0; n < N; ++n) x[ts][n] = p[from * N + n];
     }
 }
+__device__ __forceinline__ f32x4 as_floats(u32x4 x) { return __builtin_bit_cast(f32x4, x); }
+template <bool BETA>
 struct RowGates {
     f32x4 gamma, e, beta;
     float last;
     __device__ __forceinline__ void load(const Gates* g, long long vs, int wv, int lane) {
-        const int r = 16 * wv + 4 * (lane >> 4);
-        gamma = *reinterpret_cast<const f32x4*>(&g[vs].gamma[r]);
-        e = *reinterpret_cast<const f32x4*>(&g[vs].e[r]);
-        beta = *reinterpret_cast<const f32x4*>(&g[vs].beta[r]);
+        const Buffer b = buffer_of(g + vs, sizeof(Gates));
+        const uint32_t r = 64 * wv + 16 * (lane >> 4);
+        gamma = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, r, offsetof(Gates, gamma), 0));
+        e = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, r, offsetof(Gates, e), 0));
+        if constexpr (BETA) beta = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, r, offsetof(Gates, beta), 0));
         last = g[vs].gamma[kC - 1];
     }
 };
@@ -638,6 +694,29 @@ __device__ __forceinline__ void each_of_state(int wv, int lane, int n0, F f) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 f(i, ct, r, 16 * (wv * NR + i) + 4 * (lane >> 4) + r, n0 + 16 * ct + (lane & 15));
+}
+
+// Results into the workspace's rows of dvp floats.
+template <int KS, int NCT>
+__device__ __forceinline__ void keep_state(float* to, long long vs, int dvp, int n0, int wv, int lane,
+                                           const f32x4 (&st)[KS / 2][NCT]) {
+    const Buffer b = buffer_of(to + vs * 32 * KS * dvp, (long long)128 * KS * dvp);
+    const uint32_t at = 4 * ((16 * wv * (KS / 2) + 4 * (lane >> 4)) * dvp + (lane & 15));
+#pragma unroll
+    for (int i = 0; i < KS / 2; ++i)
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(st[i][ct][r]), b, at,
+                                                      4 * ((16 * i + r) * dvp + n0 + 16 * ct), 0);
+}
+__device__ __forceinline__ void keep_rows(float* to, long long vs, int dvp, int n0, int wv, int lane, f32x4 x) {
+    const Buffer b = buffer_of(to + vs * kC * dvp, (long long)4 * kC * dvp);
+    const uint32_t at = 4 * ((16 * wv + 4 * (lane >> 4)) * dvp + (lane & 15));
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[r]), b, at, 4 * (r * dvp + n0), 0);
 }
 
 template <class TY, int KS, int NCT, bool GRAD>
@@ -675,7 +754,7 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
     struct Set {
         u32x4 kf[KS][NP], qf[GRAD ? 1 : KS][NP], kt[NR][2][NP], t[2][3], m[2][GRAD ? 1 : NM];
         S v[NCT][4];
-        RowGates g;
+        RowGates<false> g;
     };
     const Tile<TY, NCT> vt(a.vt, n0, a.dv, wv, lane);
     const Tile<TY, NCT> ot((long long)a.hv * a.dv, n0, a.dv, wv, lane);
@@ -723,9 +802,7 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
         if constexpr (!GRAD) xu.get(lane, bu);
         reads_first();
         if constexpr (GRAD) {
-            each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int cc) {
-                w.s0[(vs * 32 * KS + row) * w.dvp + cc] = st[i][ct][r];
-            });
+            keep_state<KS, NCT>(w.s0, vs, w.dvp, n0, wv, lane, st);
         }
         f32x4 kx[NCT];
 #pragma unroll
@@ -739,7 +816,7 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
         for (int ct = 0; ct < NCT; ++ct) {
             f32x4 y;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) y[r] = x.g.beta[r] * (TY::load(x.v[ct][r]) - x.g.gamma[r] * kx[ct][r]);
+            for (int r = 0; r < 4; ++r) y[r] = TY::load(x.v[ct][r]) - x.g.gamma[r] * kx[ct][r];
             u32x2 p[3];
             split4<3>(y, p);
             xp.put(wv, ct, lane, p);
@@ -779,9 +856,7 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
             split4<3>(u[ct] * x.g.e, p);
             xe.put(wv, ct, lane, p);
             if constexpr (GRAD) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    w.u[(vs * kC + 16 * wv + 4 * grp + r) * w.dvp + n0 + 16 * ct + col] = u[ct][r];
+                keep_rows(w.u, vs, w.dvp, n0 + 16 * ct, wv, lane, u[ct]);
             } else {
                 u32x2 pu[NM];
                 split4<NM>(u[ct], pu);
@@ -844,8 +919,8 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
 }
 
 // ========================================= along a sequence: the gradients' chain
-// With dS the gradient of the chunk's last state and dO that of O,
-//   dU  = M^T dO + diag(e) K dS           dR = T^T dU   (of the bracket, by beta)
+// With dS the gradient of the chunk's last state, dO that of O and R = (I + L)^-1,
+//   dU  = M^T dO + diag(e) K dS           dR = R^T dU   (of beta times the bracket)
 //   dV  = diag(beta) dR
 //   dS0 = gamma_63 dS + scale Q^T diag(gamma) dO - K^T diag(gamma beta) dR
 // The same tiles, exchanges and register sets as the states' chain, from the last
@@ -893,7 +968,7 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
     struct Set {
         u32x4 kf[KS][NP], kt[NR][2][NP], qt[NR][2][NP], tt[2][3], mt[2][3];
         S o[NCT][4];
-        RowGates g;
+        RowGates<true> g;
     };
     const Tile<TY, NCT> got(a.gt, n0, a.dv, wv, lane);
     const Tile<TY, NCT> gvt((long long)a.hv * a.dv, n0, a.dv, wv, lane);
@@ -934,9 +1009,7 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
         xs.get(lane, b);
         xo.get(lane, bo);
         reads_first();
-        each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int cc) {
-            w.ds[(vs * 32 * KS + row) * w.dvp + cc] = st[i][ct][r];
-        });
+        keep_state<KS, NCT>(w.ds, vs, w.dvp, n0, wv, lane, st);
         f32x4 y[NCT];
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) y[ct] = f32x4{0, 0, 0, 0};
@@ -984,9 +1057,7 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
             u32x2 p[3];
             split4<3>(-(dv * x.g.gamma), p);
             xr.put(wv, ct, lane, p);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                w.dr[(vs * kC + 16 * wv + 4 * grp + r) * w.dvp + n0 + 16 * ct + col] = y[ct][r];
+            keep_rows(w.dr, vs, w.dvp, n0 + 16 * ct, wv, lane, y[ct]);
             gvt.store(to, ct, dv);
         }
 #pragma unroll
@@ -1051,8 +1122,14 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
 // with D = dM M + dL L below the diagonal (on it both sums take the same) and
 // d_i = e_i k_i.(U dS^T)_i; the chunk's last token also gets sum_i d_i +
 // gamma_63 <dS, S0>; dg_i is the sum of dG over i and all later tokens.
+//
 // A workgroup has a key head of a chunk and takes its value heads in turn, adding
-// up dQ and dK in registers; wave wv has token tile wv.
+// up dQ and dK in registers; wave wv has token tile wv.  dim_v is summed in slices
+// of 32: S0 (with dO and dR as left operands), then dS (with U), are split into
+// parts once for the workgroup and shared through LDS, the next slice's loads in
+// flight under the products.  Two passes, and q and k in result order from products
+// with the identity, keep a wave within 256 registers, so that two are on a SIMD:
+// one's splitting runs beside the other's matrix instructions.
 __device__ __forceinline__ float over_columns(float x) {  // over the 16 lanes of a group
 #pragma unroll
     for (int off = 1; off < 16; off <<= 1) x += __shfl_xor(x, off);
@@ -1063,25 +1140,52 @@ __device__ __forceinline__ float over_groups(float x) {
     return x + __shfl_xor(x, 32);
 }
 
+template <int KS>
+struct GradsLds {
+    double G[kC];
+    float gamma[kC], e_[kC], beta[kC];
+    float row_d[kC], col_d[4][kC], end_d[kC], dotted[4];
+    float f[kC][kC + 4], e[kC][kC + 4];
+    u32x4 s[2 * KS][3][64];  // S0's or dS's slice
+    u32x4 u[4][3][64];       // U's
+};
+
+// Row `row` of 32 floats of the slice, 8 of them for each of 4 threads, to LDS as parts.
+__device__ __forceinline__ void put_parts(u32x4 (*to)[3][64], int row, int g8, f32x4 a, f32x4 b) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+    u32x4 p[3];
+    split8<3>(x, p);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) to[row >> 4][n][(row & 15) + 16 * g8] = p[n];
+}
+__device__ __forceinline__ void split_of(f32x4 a, f32x4 b, u32x4 (&p)[3]) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+    split8<3>(x, p);
+}
+// A row operand's 16 places `half` as a result lies: token 4 grp + r, place l & 15.
+template <int NP>
+__device__ __forceinline__ f32x4 as_result(const u32x4 (&x)[NP], int half, int lane) {
+    const int col = lane & 15, grp = lane >> 4;
+    u32x4 one[1] = {{0, 0, 0, 0}};
+    if (grp == (col >> 2)) one[0][2 * half + ((col >> 1) & 1)] = col & 1 ? 0x3f800000u : 0x3f80u;
+    f32x4 y = {0, 0, 0, 0};
+    mma<NP>(x, one, y);
+    return y;
+}
+
 template <class TY, int KS>
-__global__ __launch_bounds__(kThreads) void delta_grads_kernel(
-    Shape a, Space w, const typename TY::S* __restrict__ q, const typename TY::S* __restrict__ k,
-    const typename TY::S* __restrict__ v, const typename TY::S* __restrict__ go, typename TY::S* __restrict__ gq,
-    typename TY::S* __restrict__ gk, float* __restrict__ gg, float* __restrict__ gbeta) {
+__global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
+    Shape a, Space w, const typename TY::S* __restrict__ v, const typename TY::S* __restrict__ go,
+    typename TY::S* __restrict__ gq, typename TY::S* __restrict__ gk, float* __restrict__ gg,
+    float* __restrict__ gbeta) {
     using S = typename TY::S;
-    constexpr int NP = TY::NP, CT = 2 * KS;
-    struct Stage {
-        u32x4 s0[CT][3][64], ds[CT][3][64], u[4][3][64];
-    };
-    struct Square {
-        float f[kC][kC + 4], e[kC][kC + 4];
-    };
-    __shared__ __align__(16) unsigned char raw[sizeof(Stage) > sizeof(Square) ? sizeof(Stage) : sizeof(Square)];
-    __shared__ double G[kC];
-    __shared__ float ga[3][kC];           // gamma, e, beta
-    __shared__ float row_d[kC], col_d[4][kC], end_d[kC], dotted[4];
-    Stage& sg = *reinterpret_cast<Stage*>(raw);
-    Square& sq = *reinterpret_cast<Square*>(raw);
+    constexpr int NP = TY::NP, CT = 2 * KS, NT = KS / 2;  // NT: state rows' tasks of a thread
+    extern __shared__ __align__(16) unsigned char lds[];
+    GradsLds<KS>& sm = *reinterpret_cast<GradsLds<KS>*>(lds);
     const long long slot = blockIdx.x;
     const Chunk ch = chunk_of(a, slot);
     if (ch.n <= 0) return;
@@ -1090,173 +1194,220 @@ __global__ __launch_bounds__(kThreads) void delta_grads_kernel(
     const long long ks0 = slot * a.hk + hk;
     const int arow = 16 * wv + col;  // this lane's row as a left operand
     const bool aok = arow < ch.n;
-    const S* qp = q + (long long)ch.tok0 * a.qt + hk * a.qh;
-    const S* kp = k + (long long)ch.tok0 * a.kt + hk * a.kh;
+    const int trow = t >> 2, tg = t & 3;  // this thread's row and 8 columns of a slice
+    const uint32_t tat = 4 * (trow * w.dvp + 8 * tg), aat = 4 * (arow * w.dvp + 8 * grp);
+    const uint32_t vrow = arow * (uint32_t)(a.vt * sizeof(S)), orow = arow * (uint32_t)(a.gt * sizeof(S));
+    const Parts kf(w.kf, ks0 * 4 * KS * NP, 4 * KS * NP, lane), qf(w.qf, ks0 * 4 * KS * NP, 4 * KS * NP, lane),
+        kt(w.kt, ks0 * 4 * KS * NP, 4 * KS * NP, lane), qt(w.qt, ks0 * 4 * KS * NP, 4 * KS * NP, lane);
 
     f32x4 dq[CT], dk[CT];
 #pragma unroll
     for (int i = 0; i < CT; ++i) dq[i] = f32x4{0, 0, 0, 0}, dk[i] = f32x4{0, 0, 0, 0};
+#pragma unroll 1
     for (int hr = 0; hr < rep; ++hr) {
         const int h = hk * rep + hr;
         const long long vs = slot * a.hv + h;
+        const Buffer s0 = buffer_of(w.s0 + vs * 32 * KS * w.dvp, (long long)128 * KS * w.dvp);
+        const Buffer ds = buffer_of(w.ds + vs * 32 * KS * w.dvp, (long long)128 * KS * w.dvp);
+        const Buffer ub = buffer_of(w.u + vs * kC * w.dvp, (long long)4 * kC * w.dvp);
+        const Buffer rb = buffer_of(w.dr + vs * kC * w.dvp, (long long)4 * kC * w.dvp);
+        const Buffer ob = Tile<TY, 1>::rows(go + (long long)ch.tok0 * a.gt + h * a.gh, a.gt, ch.n, a.dv);
+        const Buffer vb = Tile<TY, 1>::rows(v + (long long)ch.tok0 * a.vt + h * a.vh, a.vt, ch.n, a.dv);
+        auto two = [](Buffer b, uint32_t at, int more, f32x4 (&x)[2]) {
+            x[0] = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, at, more, 0));
+            x[1] = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, at + 16, more, 0));
+        };
+        f32x4 xs[NT][2], xu[2], xr[2];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) two(s0, tat, 256 * i * w.dvp, xs[i]);
+        two(ub, tat, 0, xu);
+        two(rb, aat, 0, xr);
         __syncthreads();  // the last head is done with the shared arrays
         if (t < kC) {
             const Gates& gs = w.gates[vs];
-            G[t] = gs.G[t];
-            ga[0][t] = gs.gamma[t];
-            ga[1][t] = gs.e[t];
-            ga[2][t] = gs.beta[t];
+            sm.G[t] = gs.G[t];
+            sm.gamma[t] = gs.gamma[t];
+            sm.e_[t] = gs.e[t];
+            sm.beta[t] = gs.beta[t];
         }
-        f32x4 so[CT], sr[CT], ud[CT], dm[4], dl[4];
+        // ---- dO S0^T, dR S0^T, dO U^T, dR U^T
+        f32x4 so[CT], sr[CT], dm[4], dl[4];
 #pragma unroll
-        for (int i = 0; i < CT; ++i)
-            so[i] = f32x4{0, 0, 0, 0}, sr[i] = f32x4{0, 0, 0, 0}, ud[i] = f32x4{0, 0, 0, 0};
+        for (int i = 0; i < CT; ++i) so[i] = f32x4{0, 0, 0, 0}, sr[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 4; ++i) dm[i] = f32x4{0, 0, 0, 0}, dl[i] = f32x4{0, 0, 0, 0};
         float drv = 0.0f, dss = 0.0f;
-        const S* gop = go + (long long)(ch.tok0 + arow) * a.gt + h * a.gh;
-        const S* vp = v + (long long)(ch.tok0 + arow) * a.vt + h * a.vh;
+#pragma unroll 1
         for (int n0 = 0; n0 < w.dvp; n0 += 32) {
-            if (n0) __syncthreads();
-            for (int i = t; i < 32 * KS * 4; i += kThreads) {  // rows of S0 and dS, 8 columns each
-                const int row = i >> 2, g8 = i & 3, to = (row & 15) + 16 * g8;
-                const long long from = (vs * 32 * KS + row) * w.dvp + n0 + 8 * g8;
-                float x[8], y[8];
-                load8<F32>(w.s0 + from, 0, 4, 8, true, true, x);
-                load8<F32>(w.ds + from, 0, 4, 8, true, true, y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dss += x[j] * y[j];
-                u32x4 p[3];
-                split8<3>(x, p);
-#pragma unroll
-                for (int n = 0; n < 3; ++n) sg.s0[row >> 4][n][to] = p[n];
-                split8<3>(y, p);
-#pragma unroll
-                for (int n = 0; n < 3; ++n) sg.ds[row >> 4][n][to] = p[n];
-            }
+            const int next = n0 + 32 < w.dvp ? n0 + 32 : 0;
+            u32x4 oa[NP], rp[3];
             {
-                const int row = t >> 2, g8 = t & 3, to = (row & 15) + 16 * g8;
                 float x[8];
-                load8<F32>(w.u + (vs * kC + row) * w.dvp + n0 + 8 * g8, 0, 4, 8, true, true, x);
-                u32x4 p[3];
-                split8<3>(x, p);
-#pragma unroll
-                for (int n = 0; n < 3; ++n) sg.u[row >> 4][n][to] = p[n];
-            }
-            u32x4 oa[NP], ra[3], ua[3];
-            {
-                float x[8], y[8];
                 const int c0 = n0 + 8 * grp;
-                load8<F32>(w.dr + (vs * kC + arow) * w.dvp + c0, 0, 4, 8, true, true, x);
-                load8<TY>(vp, c0, c0 + 4, a.dv, aok, a.vvec, y);
+                load8<TY>(vb, vrow, c0, a.dv, aok, a.vvec, x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) drv += x[j] * y[j];
-                split8<3>(x, ra);
-                load8<TY>(gop, c0, c0 + 4, a.dv, aok, a.gvec, x);
+                for (int j = 0; j < 8; ++j) drv += x[j] * xr[j >> 2][j & 3];
+                load8<TY>(ob, orow, c0, a.dv, aok, a.gvec, x);
                 split8<NP>(x, oa);
             }
-            __syncthreads();
+            if (n0) __syncthreads();
 #pragma unroll
-            for (int n = 0; n < 3; ++n) ua[n] = sg.u[wv][n][lane];
+            for (int i = 0; i < NT; ++i) put_parts(sm.s, trow + 64 * i, tg, xs[i][0], xs[i][1]);
+            put_parts(sm.u, trow, tg, xu[0], xu[1]);
+            split_of(xr[0], xr[1], rp);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) two(s0, tat, 256 * i * w.dvp + 4 * next, xs[i]);
+            two(ub, tat, 4 * next, xu);
+            two(rb, aat, 4 * next, xr);
+            __syncthreads();
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
                 u32x4 b[3];
 #pragma unroll
-                for (int n = 0; n < 3; ++n) b[n] = sg.s0[i][n][lane];
+                for (int n = 0; n < 3; ++n) b[n] = sm.s[i][n][lane];
                 mma<3>(oa, b, so[i]);
-                mma<3>(ra, b, sr[i]);
-#pragma unroll
-                for (int n = 0; n < 3; ++n) b[n] = sg.ds[i][n][lane];
-                mma<3>(ua, b, ud[i]);
+                mma<3>(rp, b, sr[i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i <= wv) {
                     u32x4 b[3];
 #pragma unroll
-                    for (int n = 0; n < 3; ++n) b[n] = sg.u[i][n][lane];
+                    for (int n = 0; n < 3; ++n) b[n] = sm.u[i][n][lane];
                     mma<3>(oa, b, dm[i]);
-                    mma<3>(ra, b, dl[i]);
+                    mma<3>(rp, b, dl[i]);
                 }
         }
-        // k.k and q.k again, the triangles of F and E, and what the gates get of them
-        f32x4 kk[4], qk[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) kk[i] = f32x4{0, 0, 0, 0}, qk[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            u32x4 ka[NP], qa[NP];
-#pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                ka[n] = w.kf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
-                qa[n] = w.qf[(((ks0 * 4 + wv) * KS + ks) * NP + n) * 64 + lane];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i <= wv) {
-                    u32x4 b[NP];
-#pragma unroll
-                    for (int n = 0; n < NP; ++n) b[n] = w.kf[(((ks0 * 4 + i) * KS + ks) * NP + n) * 64 + lane];
-                    mma<3>(ka, b, kk[i]);
-                    mma<3>(qa, b, qk[i]);
-                }
-        }
-        __syncthreads();  // the staged slices are read; F and E take their place
+        const f32x4 gam = *reinterpret_cast<const f32x4*>(&sm.gamma[16 * wv + 4 * grp]);
+        const f32x4 end = *reinterpret_cast<const f32x4*>(&sm.e_[16 * wv + 4 * grp]);
+        const f32x4 bet = *reinterpret_cast<const f32x4*>(&sm.beta[16 * wv + 4 * grp]);
+        // ---- k.k and q.k again: the triangles of F and E, and what the gates get of them
         float dsum[4] = {0, 0, 0, 0}, bsum[4] = {0, 0, 0, 0};  // rows 16 wv + 4 grp + r
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = 16 * i + col;
             float down = 0.0f;
+            if (i <= wv) {
+                f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * wv + 4 * grp + r;
-                float f = 0.0f, e = 0.0f;
-                if (i <= wv && c <= row) {
-                    const float decay = exp2_of(G[row] - G[c]);
-                    f = a.scale * decay * dm[i][r];
-                    if (c < row) {
-                        const float x = -decay * dl[i][r];       // dL Gamma
-                        const float b = x * kk[i][r];
-                        e = ga[2][row] * x;
-                        const float d = f * qk[i][r] + ga[2][row] * b;
-                        bsum[r] += b;
-                        dsum[r] += d;
-                        down += d;
+                for (int ks = 0; ks < KS; ++ks) {
+                    u32x4 ka[NP], qa[NP], b[NP];
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) {
+                        ka[n] = kf[(wv * KS + ks) * NP + n];
+                        qa[n] = qf[(wv * KS + ks) * NP + n];
+                        b[n] = kf[(i * KS + ks) * NP + n];
                     }
+                    mma<3>(ka, b, kk);
+                    mma<3>(qa, b, qk);
                 }
-                sq.f[row][c] = f;
-                sq.e[row][c] = e;
+                const double Gc = sm.G[c];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * wv + 4 * grp + r;
+                    const float decay = c <= row ? exp2_of(sm.G[row] - Gc) : 0.0f;
+                    const float low = c < row ? decay : 0.0f;  // below the diagonal
+                    const float x = -low * dl[i][r];           // dL Gamma
+                    const float b = x * kk[r];
+                    const float d = a.scale * low * dm[i][r] * qk[r] + bet[r] * b;
+                    bsum[r] += b;
+                    dsum[r] += d;
+                    down += d;
+                    sm.f[row][c] = a.scale * decay * dm[i][r];
+                    sm.e[row][c] = bet[r] * x;
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * wv + 4 * grp + r;
+                    sm.f[row][c] = 0.0f;
+                    sm.e[row][c] = 0.0f;
+                }
             }
             down = over_groups(down);
-            if (grp == 0) col_d[wv][c] = down;
+            if (grp == 0) sm.col_d[wv][c] = down;
+        }
+        // ---- the states' parts of dQ and dK, and their products with q and k
+        float qdot[4] = {0, 0, 0, 0}, kdot[4] = {0, 0, 0, 0}, gone[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            u32x4 ka[NP], qa[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                ka[n] = kf[(wv * KS + ks) * NP + n];
+                qa[n] = qf[(wv * KS + ks) * NP + n];
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = 2 * ks + half;
+                const f32x4 qv = as_result<NP>(qa, half, lane), kv = as_result<NP>(ka, half, lane);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float x = a.scale * gam[r] * so[i][r], y = gam[r] * sr[i][r];
+                    qdot[r] += qv[r] * x;
+                    kdot[r] += kv[r] * y;
+                    dq[i][r] += x;
+                    dk[i][r] -= bet[r] * y;
+                }
+            }
+        }
+        // ---- U dS^T
+        f32x4 ud[CT], xd[NT][2];
+#pragma unroll
+        for (int i = 0; i < CT; ++i) ud[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < NT; ++i) two(ds, tat, 256 * i * w.dvp, xd[i]);
+        two(ub, aat, 0, xu);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) two(s0, tat, 256 * i * w.dvp, xs[i]);  // again, for <dS, S0>
+#pragma unroll 1
+        for (int n0 = 0; n0 < w.dvp; n0 += 32) {
+            const int next = n0 + 32 < w.dvp ? n0 + 32 : 0;
+            u32x4 up3[3];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dss += xs[i][j >> 2][j & 3] * xd[i][j >> 2][j & 3];
+                put_parts(sm.s, trow + 64 * i, tg, xd[i][0], xd[i][1]);
+            }
+            split_of(xu[0], xu[1], up3);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                two(ds, tat, 256 * i * w.dvp + 4 * next, xd[i]);
+                two(s0, tat, 256 * i * w.dvp + 4 * next, xs[i]);
+            }
+            two(ub, aat, 4 * next, xu);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                u32x4 b[3];
+#pragma unroll
+                for (int n = 0; n < 3; ++n) b[n] = sm.s[i][n][lane];
+                mma<3>(up3, b, ud[i]);
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            u32x4 ka[NP];
+#pragma unroll
+            for (int n = 0; n < NP; ++n) ka[n] = kf[(wv * KS + ks) * NP + n];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int i = 2 * ks + half;
+                const f32x4 kv = as_result<NP>(ka, half, lane);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float z = end[r] * ud[i][r];
+                    gone[r] += kv[r] * z;
+                    dk[i][r] += z;
+                }
+            }
         }
         drv = over_groups(drv);  // for row arow, in all groups
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) dss += __shfl_xor(dss, off);
-        if (lane == 0) dotted[wv] = dss;
-        // the states' parts of dQ and dK, and their products with q and k
-        float qdot[4] = {0, 0, 0, 0}, kdot[4] = {0, 0, 0, 0}, gone[4] = {0, 0, 0, 0};
-        const f32x4 gam = *reinterpret_cast<const f32x4*>(&ga[0][16 * wv + 4 * grp]);
-        const f32x4 end = *reinterpret_cast<const f32x4*>(&ga[1][16 * wv + 4 * grp]);
-        const f32x4 bet = *reinterpret_cast<const f32x4*>(&ga[2][16 * wv + 4 * grp]);
-#pragma unroll
-        for (int i = 0; i < CT; ++i) {
-            const int c = 16 * i + col;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * wv + 4 * grp + r;
-                const bool ok = row < ch.n && c < a.dk;
-                const float qv = ok ? TY::load(qp[row * a.qt + c]) : 0.0f;
-                const float kv = ok ? TY::load(kp[row * a.kt + c]) : 0.0f;
-                const float x = a.scale * gam[r] * so[i][r], y = gam[r] * sr[i][r], z = end[r] * ud[i][r];
-                qdot[r] += qv * x;
-                kdot[r] += kv * y;
-                gone[r] += kv * z;
-                dq[i][r] += x;
-                dk[i][r] += z - bet[r] * y;
-            }
-        }
-        __syncthreads();
+        if (lane == 0) sm.dotted[wv] = dss;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = 16 * wv + 4 * grp + r;
@@ -1264,25 +1415,25 @@ __global__ __launch_bounds__(kThreads) void delta_grads_kernel(
             const float x = over_columns(qdot[r]), y = over_columns(kdot[r]), z = over_columns(gone[r]);
             const float rv = __shfl(drv, 4 * grp + r);
             if (col == 0) {
-                row_d[row] = d + (x - bet[r] * y);
-                end_d[row] = z;
+                sm.row_d[row] = d + (x - bet[r] * y);
+                sm.end_d[row] = z;
                 if (row < ch.n) gbeta[(long long)(ch.tok0 + row) * a.hv + h] = rv - y + b;
             }
         }
         __syncthreads();
         if (wv == 0) {
-            const float z = end_d[lane];
+            const float z = sm.end_d[lane];
             float all = z;
 #pragma unroll
             for (int off = 1; off < 64; off <<= 1) all += __shfl_xor(all, off);
-            float d = row_d[lane] - z;
+            float d = sm.row_d[lane] - z;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i >= (lane >> 4)) d -= col_d[i][lane];
+                if (i >= (lane >> 4)) d -= sm.col_d[i][lane];
             double x = d;
             if (lane == kC - 1) {
-                const float sum = (dotted[0] + dotted[1]) + (dotted[2] + dotted[3]);
-                x += (double)all + (double)exp2_of(G[kC - 1]) * sum;
+                const float sum = (sm.dotted[0] + sm.dotted[1]) + (sm.dotted[2] + sm.dotted[3]);
+                x += (double)all + (double)exp2_of(sm.G[kC - 1]) * sum;
             }
             for (int off = 1; off < 64; off <<= 1) {
                 const double o = __shfl_down(x, off);
@@ -1290,47 +1441,62 @@ __global__ __launch_bounds__(kThreads) void delta_grads_kernel(
             }
             if (lane < ch.n) gg[(long long)(ch.tok0 + lane) * a.hv + h] = (float)x;
         }
-        // F K, F^T Q and (E + E^T) K
+        // ---- F K, F^T Q and (E + E^T) K
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts) {
-            u32x4 fa[3], fb[3], ea[3];
-            float x[8], y[8], z[8];
+            float x[8];
+            {
+                u32x4 ea[3];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = place_of(ts, grp, j);
-                x[j] = sq.f[arow][c];
-                y[j] = sq.f[c][arow];
-                z[j] = sq.e[arow][c] + sq.e[c][arow];
-            }
-            split8<3>(x, fa);
-            split8<3>(y, fb);
-            split8<3>(z, ea);
-#pragma unroll
-            for (int i = 0; i < CT; ++i) {
-                u32x4 kb[NP], qb[NP];
-#pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    kb[n] = w.kt[((ks0 * 4 * KS + i * 2 + ts) * NP + n) * 64 + lane];
-                    qb[n] = w.qt[((ks0 * 4 * KS + i * 2 + ts) * NP + n) * 64 + lane];
+                for (int j = 0; j < 8; ++j) {
+                    const int c = place_of(ts, grp, j);
+                    x[j] = sm.e[arow][c] + sm.e[c][arow];
                 }
-                if (ts <= (wv >> 1)) mma<3>(fa, kb, dq[i]);
-                if (ts >= (wv >> 1)) mma<3>(fb, qb, dk[i]);
-                mma<3>(ea, kb, dk[i]);
+                split8<3>(x, ea);
+#pragma unroll
+                for (int i = 0; i < CT; ++i) {
+                    u32x4 kb[NP];
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) kb[n] = kt[(i * 2 + ts) * NP + n];
+                    mma<3>(ea, kb, dk[i]);
+                }
+            }
+            if (ts <= (wv >> 1)) {
+                u32x4 fa[3];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = sm.f[arow][place_of(ts, grp, j)];
+                split8<3>(x, fa);
+#pragma unroll
+                for (int i = 0; i < CT; ++i) {
+                    u32x4 kb[NP];
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) kb[n] = kt[(i * 2 + ts) * NP + n];
+                    mma<3>(fa, kb, dq[i]);
+                }
+            }
+            if (ts >= (wv >> 1)) {
+                u32x4 fb[3];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = sm.f[place_of(ts, grp, j)][arow];
+                split8<3>(x, fb);
+#pragma unroll
+                for (int i = 0; i < CT; ++i) {
+                    u32x4 qb[NP];
+#pragma unroll
+                    for (int n = 0; n < NP; ++n) qb[n] = qt[(i * 2 + ts) * NP + n];
+                    mma<3>(fb, qb, dk[i]);
+                }
             }
         }
     }
+    const Tile<TY, CT> to((long long)a.hk * a.dk, 0, a.dk, wv, lane);
+    const long long first = ((long long)ch.tok0 * a.hk + hk) * a.dk;
+    const Buffer qb = Tile<TY, CT>::rows(gq + first, (long long)a.hk * a.dk, ch.n, a.dk);
+    const Buffer kb = Tile<TY, CT>::rows(gk + first, (long long)a.hk * a.dk, ch.n, a.dk);
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
-        const int c = 16 * i + col;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 16 * wv + 4 * grp + r;
-            if (row < ch.n && c < a.dk) {
-                const long long to = ((long long)(ch.tok0 + row) * a.hk + hk) * a.dk + c;
-                gq[to] = TY::store(dq[i][r]);
-                gk[to] = TY::store(dk[i][r]);
-            }
-        }
+        to.store(qb, i, dq[i]);
+        to.store(kb, i, dk[i]);
     }
 }
 
@@ -1561,9 +1727,11 @@ int check_shape(const delta_rule_shape_t* p, bool step, Shape* a) {
     a->gt = p->go_stride_t, a->gh = p->go_stride_h;
     a->chunks = dense ? (int)(((long long)p->seq_len + kC - 1) / kC) : 0;
     a->slots = dense ? (long long)a->chunks * n_seq : p->n_tokens / kC + n_seq;
-    // a chunk's rows of v, o and grad_o are addressed with 31 bits
-    for (long long st : {p->v_stride_t, p->go_stride_t, (long long)p->heads_v * p->dim_v})
-        if (!step && (st > INT_MAX || (kC * st + p->dim_v) * size_of(p->type) > INT_MAX)) return CFC_ERR_UNSUPPORTED;
+    // a chunk's rows are addressed with 31 bits
+    for (long long st : {p->q_stride_t, p->k_stride_t, p->v_stride_t, p->go_stride_t, (long long)p->heads_k * p->dim_k,
+                         (long long)p->heads_v * p->dim_v})
+        if (!step && (st > INT_MAX || (kC * st + DELTA_MAX_DIM_V) * size_of(p->type) > INT_MAX))
+            return CFC_ERR_UNSUPPORTED;
     const long long tiles = (p->dim_v + 31) / 32 * 2;
     if (a->slots > kMaxBlocks || (long long)n_seq * p->heads_v > kMaxBlocks / tiles) return CFC_ERR_UNSUPPORTED;
     return CFC_OK;
@@ -1659,9 +1827,12 @@ int run_backward(const Shape& a, const Space& w, const void* q, const void* k, c
     using S = typename TY::S;
     constexpr size_t lds = sizeof(ReverseLds<TY::NP, NCT, KS>);
     // idempotent, and 160 KB is what a gfx950 workgroup can have
-    if (lds > 64 * 1024 &&
-        hipFuncSetAttribute(reinterpret_cast<const void*>(&delta_reverse_kernel<TY, KS, NCT>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
+    auto allow = [](const void* kernel, size_t bytes) {
+        return bytes <= 64 * 1024 || hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                         (int)bytes) == hipSuccess;
+    };
+    if (!allow(reinterpret_cast<const void*>(&delta_reverse_kernel<TY, KS, NCT>), lds) ||
+        !allow(reinterpret_cast<const void*>(&delta_grads_kernel<TY, KS>), sizeof(GradsLds<KS>)))
         return CFC_ERR_HIP;
     launch_prep<TY, KS, true>(a, w, q, k, g, beta, stream);
     if (a.slots) launch_chain<TY, KS, NCT, true>(a, w, v, initial, nullptr, nullptr, stream);
@@ -1669,8 +1840,9 @@ int run_backward(const Shape& a, const Space& w, const void* q, const void* k, c
     hipLaunchKernelGGL((delta_reverse_kernel<TY, KS, NCT>), dim3(dealt(count)), dim3(kThreads), lds, stream, a, w,
                        (const S*)go, grad_final, (S*)gv, grad_initial);
     if (a.slots)
-        hipLaunchKernelGGL((delta_grads_kernel<TY, KS>), dim3((unsigned)a.slots, a.hk), dim3(kThreads), 0, stream, a,
-                           w, (const S*)q, (const S*)k, (const S*)v, (const S*)go, (S*)gq, (S*)gk, gg, gbeta);
+        hipLaunchKernelGGL((delta_grads_kernel<TY, KS>), dim3((unsigned)a.slots, a.hk), dim3(kThreads),
+                           sizeof(GradsLds<KS>), stream, a,
+                           w, (const S*)v, (const S*)go, (S*)gq, (S*)gk, gg, gbeta);
     return launch_status();
 }
 

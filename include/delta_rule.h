@@ -53,7 +53,7 @@ extern "C" {
  *   q, k [n_tokens, heads_k, dim_k], v [n_tokens, heads_v, dim_v]: row r, head h
  * at r * stride_t + h * stride_h elements (strides >= 0, so a slice of a fused
  * projection or a broadcast head can be read where it lies), the last axis
- * dense; 64 rows of v, o and grad_o are less than 2^31 bytes apart.  g, beta [n_tokens, heads_v] float32, dense: the decay's logarithm
+ * dense; 64 rows are less than 2^31 bytes (sequences' calls).  g, beta [n_tokens, heads_v] float32, dense: the decay's logarithm
  * (-inf: forget all) and the gate.  States [n_seq, heads_v, dim_k, dim_v]
  * float32, dense. */
 typedef struct delta_rule_shape {
