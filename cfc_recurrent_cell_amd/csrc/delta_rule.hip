@@ -1124,12 +1124,12 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
 // gamma_63 <dS, S0>; dg_i is the sum of dG over i and all later tokens.
 //
 // A workgroup has a key head of a chunk and takes its value heads in turn, adding
-// up dQ and dK in registers; wave wv has token tile wv.  dim_v is summed in slices
-// of 32: S0 (with dO and dR as left operands), then dS (with U), are split into
-// parts once for the workgroup and shared through LDS, the next slice's loads in
-// flight under the products.  Two passes, and q and k in result order from products
-// with the identity, keep a wave within 256 registers, so that two are on a SIMD:
-// one's splitting runs beside the other's matrix instructions.
+// up dQ and dK in registers.  Its 8 waves are 4 token tiles by 2 halves of dim_k;
+// the halves also share the triangles, the first has dM (and q.k), the second dL
+// (and k.k).  dim_v is summed in slices of 32: S0 (with dO and dR as left operands),
+// then dS (with U), are split into parts once for the workgroup and shared through
+// LDS, the next slice's loads in flight under the products.  q and k in result
+// order are products with the identity.
 __device__ __forceinline__ float over_columns(float x) {  // over the 16 lanes of a group
 #pragma unroll
     for (int off = 1; off < 16; off <<= 1) x += __shfl_xor(x, off);
@@ -1140,31 +1140,28 @@ __device__ __forceinline__ float over_groups(float x) {
     return x + __shfl_xor(x, 32);
 }
 
+constexpr int kGradThreads = 512;
 template <int KS>
 struct GradsLds {
     double G[kC];
-    float gamma[kC], e_[kC], beta[kC];
-    float row_d[kC], col_d[4][kC], end_d[kC], dotted[4];
+    float gamma[kC], e_[kC], beta[kC], drv[kC];
+    float row[2][4][kC];     // of each half: sums over a row of D, b, q and k products, d
+    float col_d[2][4][kC];   // of each half and row tile: D's column sums
+    float dotted[8];
     float f[kC][kC + 4], e[kC][kC + 4];
     u32x4 s[2 * KS][3][64];  // S0's or dS's slice
     u32x4 u[4][3][64];       // U's
 };
 
 // Row `row` of 32 floats of the slice, 8 of them for each of 4 threads, to LDS as parts.
-__device__ __forceinline__ void put_parts(u32x4 (*to)[3][64], int row, int g8, f32x4 a, f32x4 b) {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
+__device__ __forceinline__ void put_parts(u32x4 (*to)[3][64], int row, int g8, const f32x4 (&x)[2]) {
     u32x4 p[3];
-    split8<3>(x, p);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = x[j >> 2][j & 3];
+    split8<3>(y, p);
 #pragma unroll
     for (int n = 0; n < 3; ++n) to[row >> 4][n][(row & 15) + 16 * g8] = p[n];
-}
-__device__ __forceinline__ void split_of(f32x4 a, f32x4 b, u32x4 (&p)[3]) {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = a[j], x[4 + j] = b[j];
-    split8<3>(x, p);
 }
 // A row operand's 16 places `half` as a result lies: token 4 grp + r, place l & 15.
 template <int NP>
@@ -1178,27 +1175,33 @@ __device__ __forceinline__ f32x4 as_result(const u32x4 (&x)[NP], int half, int l
 }
 
 template <class TY, int KS>
-__global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
+__global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     Shape a, Space w, const typename TY::S* __restrict__ v, const typename TY::S* __restrict__ go,
     typename TY::S* __restrict__ gq, typename TY::S* __restrict__ gk, float* __restrict__ gg,
     float* __restrict__ gbeta) {
     using S = typename TY::S;
-    constexpr int NP = TY::NP, CT = 2 * KS, NT = KS / 2;  // NT: state rows' tasks of a thread
+    constexpr int NP = TY::NP, CT = KS;  // a wave's column tiles of dim_k
     extern __shared__ __align__(16) unsigned char lds[];
     GradsLds<KS>& sm = *reinterpret_cast<GradsLds<KS>*>(lds);
     const long long slot = blockIdx.x;
     const Chunk ch = chunk_of(a, slot);
     if (ch.n <= 0) return;
-    const int t = threadIdx.x, lane = t & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
+    const int t = threadIdx.x, lane = t & 63, wave = wave_of(), col = lane & 15, grp = lane >> 4;
+    const int wv = wave & 3, half = wave >> 2;
     const int hk = blockIdx.y, rep = a.hv / a.hk;
     const long long ks0 = slot * a.hk + hk;
     const int arow = 16 * wv + col;  // this lane's row as a left operand
     const bool aok = arow < ch.n;
     const int trow = t >> 2, tg = t & 3;  // this thread's row and 8 columns of a slice
+    const bool task_s = trow < 32 * KS, task_u = trow < kC;
     const uint32_t tat = 4 * (trow * w.dvp + 8 * tg), aat = 4 * (arow * w.dvp + 8 * grp);
     const uint32_t vrow = arow * (uint32_t)(a.vt * sizeof(S)), orow = arow * (uint32_t)(a.gt * sizeof(S));
     const Parts kf(w.kf, ks0 * 4 * KS * NP, 4 * KS * NP, lane), qf(w.qf, ks0 * 4 * KS * NP, 4 * KS * NP, lane),
         kt(w.kt, ks0 * 4 * KS * NP, 4 * KS * NP, lane), qt(w.qt, ks0 * 4 * KS * NP, 4 * KS * NP, lane);
+    auto two = [](Buffer b, uint32_t at, int more, f32x4 (&x)[2]) {
+        x[0] = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, at, more, 0));
+        x[1] = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, at + 16, more, 0));
+    };
 
     f32x4 dq[CT], dk[CT];
 #pragma unroll
@@ -1213,13 +1216,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
         const Buffer rb = buffer_of(w.dr + vs * kC * w.dvp, (long long)4 * kC * w.dvp);
         const Buffer ob = Tile<TY, 1>::rows(go + (long long)ch.tok0 * a.gt + h * a.gh, a.gt, ch.n, a.dv);
         const Buffer vb = Tile<TY, 1>::rows(v + (long long)ch.tok0 * a.vt + h * a.vh, a.vt, ch.n, a.dv);
-        auto two = [](Buffer b, uint32_t at, int more, f32x4 (&x)[2]) {
-            x[0] = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, at, more, 0));
-            x[1] = as_floats(__builtin_amdgcn_raw_buffer_load_b128(b, at + 16, more, 0));
-        };
-        f32x4 xs[NT][2], xu[2], xr[2];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) two(s0, tat, 256 * i * w.dvp, xs[i]);
+        f32x4 xs[2], xu[2], xr[2];
+        two(s0, tat, 0, xs);
         two(ub, tat, 0, xu);
         two(rb, aat, 0, xr);
         __syncthreads();  // the last head is done with the shared arrays
@@ -1230,12 +1228,12 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
             sm.e_[t] = gs.e[t];
             sm.beta[t] = gs.beta[t];
         }
-        // ---- dO S0^T, dR S0^T, dO U^T, dR U^T
-        f32x4 so[CT], sr[CT], dm[4], dl[4];
+        // ---- dO S0^T, dR S0^T; dO U^T or dR U^T
+        f32x4 so[CT], sr[CT], tri[4];
 #pragma unroll
         for (int i = 0; i < CT; ++i) so[i] = f32x4{0, 0, 0, 0}, sr[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dm[i] = f32x4{0, 0, 0, 0}, dl[i] = f32x4{0, 0, 0, 0};
+        for (int i = 0; i < 4; ++i) tri[i] = f32x4{0, 0, 0, 0};
         float drv = 0.0f, dss = 0.0f;
 #pragma unroll 1
         for (int n0 = 0; n0 < w.dvp; n0 += 32) {
@@ -1244,19 +1242,21 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
             {
                 float x[8];
                 const int c0 = n0 + 8 * grp;
-                load8<TY>(vb, vrow, c0, a.dv, aok, a.vvec, x);
+                if (half == 0) {
+                    load8<TY>(vb, vrow, c0, a.dv, aok, a.vvec, x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) drv += x[j] * xr[j >> 2][j & 3];
+                    for (int j = 0; j < 8; ++j) drv += x[j] * xr[j >> 2][j & 3];
+                }
                 load8<TY>(ob, orow, c0, a.dv, aok, a.gvec, x);
                 split8<NP>(x, oa);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = xr[j >> 2][j & 3];
+                split8<3>(x, rp);
             }
             if (n0) __syncthreads();
-#pragma unroll
-            for (int i = 0; i < NT; ++i) put_parts(sm.s, trow + 64 * i, tg, xs[i][0], xs[i][1]);
-            put_parts(sm.u, trow, tg, xu[0], xu[1]);
-            split_of(xr[0], xr[1], rp);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) two(s0, tat, 256 * i * w.dvp + 4 * next, xs[i]);
+            if (task_s) put_parts(sm.s, trow, tg, xs);
+            if (task_u) put_parts(sm.u, trow, tg, xu);
+            two(s0, tat, 4 * next, xs);
             two(ub, tat, 4 * next, xu);
             two(rb, aat, 4 * next, xr);
             __syncthreads();
@@ -1264,7 +1264,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
             for (int i = 0; i < CT; ++i) {
                 u32x4 b[3];
 #pragma unroll
-                for (int n = 0; n < 3; ++n) b[n] = sm.s[i][n][lane];
+                for (int n = 0; n < 3; ++n) b[n] = sm.s[half * CT + i][n][lane];
                 mma<3>(oa, b, so[i]);
                 mma<3>(rp, b, sr[i]);
             }
@@ -1274,73 +1274,77 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
                     u32x4 b[3];
 #pragma unroll
                     for (int n = 0; n < 3; ++n) b[n] = sm.u[i][n][lane];
-                    mma<3>(oa, b, dm[i]);
-                    mma<3>(rp, b, dl[i]);
+                    if (half == 0)
+                        mma<3>(oa, b, tri[i]);
+                    else
+                        mma<3>(rp, b, tri[i]);
                 }
         }
+        two(ds, tat, 0, xr);  // dS's first slice on its way
+        two(ub, aat, 0, xu);
         const f32x4 gam = *reinterpret_cast<const f32x4*>(&sm.gamma[16 * wv + 4 * grp]);
-        const f32x4 end = *reinterpret_cast<const f32x4*>(&sm.e_[16 * wv + 4 * grp]);
         const f32x4 bet = *reinterpret_cast<const f32x4*>(&sm.beta[16 * wv + 4 * grp]);
-        // ---- k.k and q.k again: the triangles of F and E, and what the gates get of them
+        // ---- q.k or k.k again: the triangle of F or E, and what the gates get of it
         float dsum[4] = {0, 0, 0, 0}, bsum[4] = {0, 0, 0, 0};  // rows 16 wv + 4 grp + r
+        const Parts own = half == 0 ? qf : kf;
+        float(*const square)[kC + 4] = half == 0 ? sm.f : sm.e;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = 16 * i + col;
             float down = 0.0f;
+            f32x4 z = {0, 0, 0, 0};
             if (i <= wv) {
-                f32x4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
+                f32x4 dot = {0, 0, 0, 0};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    u32x4 ka[NP], qa[NP], b[NP];
+                    u32x4 x[NP], b[NP];
 #pragma unroll
                     for (int n = 0; n < NP; ++n) {
-                        ka[n] = kf[(wv * KS + ks) * NP + n];
-                        qa[n] = qf[(wv * KS + ks) * NP + n];
+                        x[n] = own[(wv * KS + ks) * NP + n];
                         b[n] = kf[(i * KS + ks) * NP + n];
                     }
-                    mma<3>(ka, b, kk);
-                    mma<3>(qa, b, qk);
+                    mma<3>(x, b, dot);
                 }
                 const double Gc = sm.G[c];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = 16 * wv + 4 * grp + r;
                     const float decay = c <= row ? exp2_of(sm.G[row] - Gc) : 0.0f;
-                    const float low = c < row ? decay : 0.0f;  // below the diagonal
-                    const float x = -low * dl[i][r];           // dL Gamma
-                    const float b = x * kk[r];
-                    const float d = a.scale * low * dm[i][r] * qk[r] + bet[r] * b;
-                    bsum[r] += b;
+                    const float low = c < row ? 1.0f : 0.0f;  // below the diagonal
+                    float d;
+                    if (half == 0) {
+                        z[r] = a.scale * decay * tri[i][r];
+                        d = low * z[r] * dot[r];
+                    } else {
+                        const float x = -low * decay * tri[i][r];  // dL Gamma
+                        const float b = x * dot[r];
+                        bsum[r] += b;
+                        z[r] = bet[r] * x;
+                        d = bet[r] * b;
+                    }
                     dsum[r] += d;
                     down += d;
-                    sm.f[row][c] = a.scale * decay * dm[i][r];
-                    sm.e[row][c] = bet[r] * x;
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * wv + 4 * grp + r;
-                    sm.f[row][c] = 0.0f;
-                    sm.e[row][c] = 0.0f;
                 }
             }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) square[16 * wv + 4 * grp + r][c] = z[r];
             down = over_groups(down);
-            if (grp == 0) sm.col_d[wv][c] = down;
+            if (grp == 0) sm.col_d[half][wv][c] = down;
         }
         // ---- the states' parts of dQ and dK, and their products with q and k
         float qdot[4] = {0, 0, 0, 0}, kdot[4] = {0, 0, 0, 0}, gone[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
+        for (int ks = 0; ks < KS / 2; ++ks) {
             u32x4 ka[NP], qa[NP];
 #pragma unroll
             for (int n = 0; n < NP; ++n) {
-                ka[n] = kf[(wv * KS + ks) * NP + n];
-                qa[n] = qf[(wv * KS + ks) * NP + n];
+                ka[n] = kf[(wv * KS + half * (KS / 2) + ks) * NP + n];
+                qa[n] = qf[(wv * KS + half * (KS / 2) + ks) * NP + n];
             }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = 2 * ks + half;
-                const f32x4 qv = as_result<NP>(qa, half, lane), kv = as_result<NP>(ka, half, lane);
+            for (int p = 0; p < 2; ++p) {
+                const int i = 2 * ks + p;
+                const f32x4 qv = as_result<NP>(qa, p, lane), kv = as_result<NP>(ka, p, lane);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float x = a.scale * gam[r] * so[i][r], y = gam[r] * sr[i][r];
@@ -1352,50 +1356,46 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
             }
         }
         // ---- U dS^T
-        f32x4 ud[CT], xd[NT][2];
+        f32x4 ud[CT];
 #pragma unroll
         for (int i = 0; i < CT; ++i) ud[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < NT; ++i) two(ds, tat, 256 * i * w.dvp, xd[i]);
-        two(ub, aat, 0, xu);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) two(s0, tat, 256 * i * w.dvp, xs[i]);  // again, for <dS, S0>
+        two(s0, tat, 0, xs);  // again, for <dS, S0>
 #pragma unroll 1
         for (int n0 = 0; n0 < w.dvp; n0 += 32) {
             const int next = n0 + 32 < w.dvp ? n0 + 32 : 0;
-            u32x4 up3[3];
+            u32x4 ua[3];
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = xu[j >> 2][j & 3];
+            split8<3>(x, ua);
             __syncthreads();
+            if (task_s) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dss += xs[i][j >> 2][j & 3] * xd[i][j >> 2][j & 3];
-                put_parts(sm.s, trow + 64 * i, tg, xd[i][0], xd[i][1]);
+                for (int j = 0; j < 8; ++j) dss += xs[j >> 2][j & 3] * xr[j >> 2][j & 3];
+                put_parts(sm.s, trow, tg, xr);
             }
-            split_of(xu[0], xu[1], up3);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                two(ds, tat, 256 * i * w.dvp + 4 * next, xd[i]);
-                two(s0, tat, 256 * i * w.dvp + 4 * next, xs[i]);
-            }
+            two(ds, tat, 4 * next, xr);
+            two(s0, tat, 4 * next, xs);
             two(ub, aat, 4 * next, xu);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
                 u32x4 b[3];
 #pragma unroll
-                for (int n = 0; n < 3; ++n) b[n] = sm.s[i][n][lane];
-                mma<3>(up3, b, ud[i]);
+                for (int n = 0; n < 3; ++n) b[n] = sm.s[half * CT + i][n][lane];
+                mma<3>(ua, b, ud[i]);
             }
         }
+        const f32x4 end = *reinterpret_cast<const f32x4*>(&sm.e_[16 * wv + 4 * grp]);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
+        for (int ks = 0; ks < KS / 2; ++ks) {
             u32x4 ka[NP];
 #pragma unroll
-            for (int n = 0; n < NP; ++n) ka[n] = kf[(wv * KS + ks) * NP + n];
+            for (int n = 0; n < NP; ++n) ka[n] = kf[(wv * KS + half * (KS / 2) + ks) * NP + n];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int i = 2 * ks + half;
-                const f32x4 kv = as_result<NP>(ka, half, lane);
+            for (int p = 0; p < 2; ++p) {
+                const int i = 2 * ks + p;
+                const f32x4 kv = as_result<NP>(ka, p, lane);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float z = end[r] * ud[i][r];
@@ -1404,65 +1404,70 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
                 }
             }
         }
-        drv = over_groups(drv);  // for row arow, in all groups
+        // ---- the gates' sums, of each half
+        drv = over_groups(drv);
+        if (half == 0 && grp == 0) sm.drv[arow] = drv;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) dss += __shfl_xor(dss, off);
-        if (lane == 0) sm.dotted[wv] = dss;
+        if (lane == 0) sm.dotted[wave] = dss;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int row = 16 * wv + 4 * grp + r;
             const float d = over_columns(dsum[r]), b = over_columns(bsum[r]);
             const float x = over_columns(qdot[r]), y = over_columns(kdot[r]), z = over_columns(gone[r]);
-            const float rv = __shfl(drv, 4 * grp + r);
             if (col == 0) {
-                sm.row_d[row] = d + (x - bet[r] * y);
-                sm.end_d[row] = z;
-                if (row < ch.n) gbeta[(long long)(ch.tok0 + row) * a.hv + h] = rv - y + b;
+                sm.row[half][0][row] = d + (x - bet[r] * y);
+                sm.row[half][1][row] = b;
+                sm.row[half][2][row] = y;
+                sm.row[half][3][row] = z;
             }
         }
         __syncthreads();
-        if (wv == 0) {
-            const float z = sm.end_d[lane];
+        if (wave == 0) {
+            const float z = sm.row[0][3][lane] + sm.row[1][3][lane];
             float all = z;
 #pragma unroll
             for (int off = 1; off < 64; off <<= 1) all += __shfl_xor(all, off);
-            float d = sm.row_d[lane] - z;
+            float d = (sm.row[0][0][lane] + sm.row[1][0][lane]) - z;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i >= (lane >> 4)) d -= sm.col_d[i][lane];
+                if (i >= (lane >> 4)) d -= sm.col_d[0][i][lane] + sm.col_d[1][i][lane];
             double x = d;
             if (lane == kC - 1) {
-                const float sum = (sm.dotted[0] + sm.dotted[1]) + (sm.dotted[2] + sm.dotted[3]);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += sm.dotted[i];
                 x += (double)all + (double)exp2_of(sm.G[kC - 1]) * sum;
             }
             for (int off = 1; off < 64; off <<= 1) {
                 const double o = __shfl_down(x, off);
                 if (lane + off < 64) x += o;
             }
-            if (lane < ch.n) gg[(long long)(ch.tok0 + lane) * a.hv + h] = (float)x;
+            if (lane < ch.n) {
+                const long long to = (long long)(ch.tok0 + lane) * a.hv + h;
+                gg[to] = (float)x;
+                gbeta[to] = sm.drv[lane] - (sm.row[0][2][lane] + sm.row[1][2][lane]) + sm.row[1][1][lane];
+            }
         }
         // ---- F K, F^T Q and (E + E^T) K
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts) {
             float x[8];
-            {
-                u32x4 ea[3];
+            u32x4 fa[3];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = place_of(ts, grp, j);
-                    x[j] = sm.e[arow][c] + sm.e[c][arow];
-                }
-                split8<3>(x, ea);
+            for (int j = 0; j < 8; ++j) {
+                const int c = place_of(ts, grp, j);
+                x[j] = sm.e[arow][c] + sm.e[c][arow];
+            }
+            split8<3>(x, fa);
 #pragma unroll
-                for (int i = 0; i < CT; ++i) {
-                    u32x4 kb[NP];
+            for (int i = 0; i < CT; ++i) {
+                u32x4 kb[NP];
 #pragma unroll
-                    for (int n = 0; n < NP; ++n) kb[n] = kt[(i * 2 + ts) * NP + n];
-                    mma<3>(ea, kb, dk[i]);
-                }
+                for (int n = 0; n < NP; ++n) kb[n] = kt[((half * CT + i) * 2 + ts) * NP + n];
+                mma<3>(fa, kb, dk[i]);
             }
             if (ts <= (wv >> 1)) {
-                u32x4 fa[3];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = sm.f[arow][place_of(ts, grp, j)];
                 split8<3>(x, fa);
@@ -1470,26 +1475,25 @@ __global__ __launch_bounds__(kThreads, 2) void delta_grads_kernel(
                 for (int i = 0; i < CT; ++i) {
                     u32x4 kb[NP];
 #pragma unroll
-                    for (int n = 0; n < NP; ++n) kb[n] = kt[(i * 2 + ts) * NP + n];
+                    for (int n = 0; n < NP; ++n) kb[n] = kt[((half * CT + i) * 2 + ts) * NP + n];
                     mma<3>(fa, kb, dq[i]);
                 }
             }
             if (ts >= (wv >> 1)) {
-                u32x4 fb[3];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = sm.f[place_of(ts, grp, j)][arow];
-                split8<3>(x, fb);
+                split8<3>(x, fa);
 #pragma unroll
                 for (int i = 0; i < CT; ++i) {
                     u32x4 qb[NP];
 #pragma unroll
-                    for (int n = 0; n < NP; ++n) qb[n] = qt[(i * 2 + ts) * NP + n];
-                    mma<3>(fb, qb, dk[i]);
+                    for (int n = 0; n < NP; ++n) qb[n] = qt[((half * CT + i) * 2 + ts) * NP + n];
+                    mma<3>(fa, qb, dk[i]);
                 }
             }
         }
     }
-    const Tile<TY, CT> to((long long)a.hk * a.dk, 0, a.dk, wv, lane);
+    const Tile<TY, CT> to((long long)a.hk * a.dk, 16 * CT * half, a.dk, wv, lane);
     const long long first = ((long long)ch.tok0 * a.hk + hk) * a.dk;
     const Buffer qb = Tile<TY, CT>::rows(gq + first, (long long)a.hk * a.dk, ch.n, a.dk);
     const Buffer kb = Tile<TY, CT>::rows(gk + first, (long long)a.hk * a.dk, ch.n, a.dk);
@@ -1840,7 +1844,7 @@ int run_backward(const Shape& a, const Space& w, const void* q, const void* k, c
     hipLaunchKernelGGL((delta_reverse_kernel<TY, KS, NCT>), dim3(dealt(count)), dim3(kThreads), lds, stream, a, w,
                        (const S*)go, grad_final, (S*)gv, grad_initial);
     if (a.slots)
-        hipLaunchKernelGGL((delta_grads_kernel<TY, KS>), dim3((unsigned)a.slots, a.hk), dim3(kThreads),
+        hipLaunchKernelGGL((delta_grads_kernel<TY, KS>), dim3((unsigned)a.slots, a.hk), dim3(kGradThreads),
                            sizeof(GradsLds<KS>), stream, a,
                            w, (const S*)v, (const S*)go, (S*)gq, (S*)gk, gg, gbeta);
     return launch_status();
