@@ -1126,8 +1126,8 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
 // A workgroup has a key head of a chunk and takes its value heads in turn, adding
 // up dQ and dK in registers.  Its 8 waves are 4 token tiles by 2 halves of dim_k;
 // the halves also share the triangles, the first has dM (and q.k), the second dL
-// (and k.k).  dim_v is summed in slices of 32: S0 (with dO and dR as left operands),
-// then dS (with U), are split into parts once for the workgroup and shared through
+// (and k.k).  dim_v is summed in slices of 32: S0 (with dO and dR as left operands)
+// and dS (with U) are split into parts once for the workgroup and shared through
 // LDS, the next slice's loads in flight under the products.  q and k in result
 // order are products with the identity.
 __device__ __forceinline__ float over_columns(float x) {  // over the 16 lanes of a group
@@ -1149,8 +1149,8 @@ struct GradsLds {
     float col_d[2][4][kC];   // of each half and row tile: D's column sums
     float dotted[8];
     float f[kC][kC + 4], e[kC][kC + 4];
-    u32x4 s[2 * KS][3][64];  // S0's or dS's slice
-    u32x4 u[4][3][64];       // U's
+    u32x4 s[2 * KS][3][64], d[2 * KS][3][64];  // S0's and dS's slices
+    u32x4 u[4][3][64];                         // U's
 };
 
 // Row `row` of 32 floats of the slice, 8 of them for each of 4 threads, to LDS as parts.
@@ -1161,7 +1161,13 @@ __device__ __forceinline__ void put_parts(u32x4 (*to)[3][64], int row, int g8, c
     for (int j = 0; j < 8; ++j) y[j] = x[j >> 2][j & 3];
     split8<3>(y, p);
 #pragma unroll
-    for (int n = 0; n < 3; ++n) to[row >> 4][n][(row & 15) + 16 * g8] = p[n];
+    for (int n = 0; n < 3; ++n) to[row >> 4][n][16 * g8 + ((row & 15) ^ (4 * g8))] = p[n];
+}
+// ... from which lane l reads its operand: rows are turned by 4 places a group, so
+// that neither the writes of 4 rows nor the reads meet in a bank.
+__device__ __forceinline__ void get_parts(const u32x4 (&from)[3][64], int lane, u32x4 (&b)[3]) {
+#pragma unroll
+    for (int n = 0; n < 3; ++n) b[n] = from[n][lane ^ (4 * (lane >> 4))];
 }
 // A row operand's 16 places `half` as a result lies: token 4 grp + r, place l & 15.
 template <int NP>
@@ -1216,8 +1222,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         const Buffer rb = buffer_of(w.dr + vs * kC * w.dvp, (long long)4 * kC * w.dvp);
         const Buffer ob = Tile<TY, 1>::rows(go + (long long)ch.tok0 * a.gt + h * a.gh, a.gt, ch.n, a.dv);
         const Buffer vb = Tile<TY, 1>::rows(v + (long long)ch.tok0 * a.vt + h * a.vh, a.vt, ch.n, a.dv);
-        f32x4 xs[2], xu[2], xr[2];
+        f32x4 xs[2], xd[2], xu[2], xr[2];
         two(s0, tat, 0, xs);
+        two(ds, tat, 0, xd);
         two(ub, tat, 0, xu);
         two(rb, aat, 0, xr);
         __syncthreads();  // the last head is done with the shared arrays
@@ -1228,10 +1235,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
             sm.e_[t] = gs.e[t];
             sm.beta[t] = gs.beta[t];
         }
-        // ---- dO S0^T, dR S0^T; dO U^T or dR U^T
-        f32x4 so[CT], sr[CT], tri[4];
+        // ---- dO S0^T, dR S0^T, U dS^T; dO U^T or dR U^T
+        f32x4 so[CT], sr[CT], ud[CT], tri[4];
 #pragma unroll
-        for (int i = 0; i < CT; ++i) so[i] = f32x4{0, 0, 0, 0}, sr[i] = f32x4{0, 0, 0, 0};
+        for (int i = 0; i < CT; ++i)
+            so[i] = f32x4{0, 0, 0, 0}, sr[i] = f32x4{0, 0, 0, 0}, ud[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 4; ++i) tri[i] = f32x4{0, 0, 0, 0};
         float drv = 0.0f, dss = 0.0f;
@@ -1254,35 +1262,42 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
                 split8<3>(x, rp);
             }
             if (n0) __syncthreads();
-            if (task_s) put_parts(sm.s, trow, tg, xs);
+            if (task_s) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dss += xs[j >> 2][j & 3] * xd[j >> 2][j & 3];
+                put_parts(sm.s, trow, tg, xs);
+                put_parts(sm.d, trow, tg, xd);
+            }
             if (task_u) put_parts(sm.u, trow, tg, xu);
             two(s0, tat, 4 * next, xs);
+            two(ds, tat, 4 * next, xd);
             two(ub, tat, 4 * next, xu);
             two(rb, aat, 4 * next, xr);
             __syncthreads();
+            u32x4 ua[3];
+            get_parts(sm.u[wv], lane, ua);
 #pragma unroll
             for (int i = 0; i < CT; ++i) {
                 u32x4 b[3];
-#pragma unroll
-                for (int n = 0; n < 3; ++n) b[n] = sm.s[half * CT + i][n][lane];
+                get_parts(sm.s[half * CT + i], lane, b);
                 mma<3>(oa, b, so[i]);
                 mma<3>(rp, b, sr[i]);
+                get_parts(sm.d[half * CT + i], lane, b);
+                mma<3>(ua, b, ud[i]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i <= wv) {
                     u32x4 b[3];
-#pragma unroll
-                    for (int n = 0; n < 3; ++n) b[n] = sm.u[i][n][lane];
+                    get_parts(sm.u[i], lane, b);
                     if (half == 0)
                         mma<3>(oa, b, tri[i]);
                     else
                         mma<3>(rp, b, tri[i]);
                 }
         }
-        two(ds, tat, 0, xr);  // dS's first slice on its way
-        two(ub, aat, 0, xu);
         const f32x4 gam = *reinterpret_cast<const f32x4*>(&sm.gamma[16 * wv + 4 * grp]);
+        const f32x4 end = *reinterpret_cast<const f32x4*>(&sm.e_[16 * wv + 4 * grp]);
         const f32x4 bet = *reinterpret_cast<const f32x4*>(&sm.beta[16 * wv + 4 * grp]);
         // ---- q.k or k.k again: the triangle of F or E, and what the gates get of it
         float dsum[4] = {0, 0, 0, 0}, bsum[4] = {0, 0, 0, 0};  // rows 16 wv + 4 grp + r
@@ -1347,60 +1362,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
                 const f32x4 qv = as_result<NP>(qa, p, lane), kv = as_result<NP>(ka, p, lane);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float x = a.scale * gam[r] * so[i][r], y = gam[r] * sr[i][r];
+                    const float x = a.scale * gam[r] * so[i][r], y = gam[r] * sr[i][r], z = end[r] * ud[i][r];
                     qdot[r] += qv[r] * x;
                     kdot[r] += kv[r] * y;
-                    dq[i][r] += x;
-                    dk[i][r] -= bet[r] * y;
-                }
-            }
-        }
-        // ---- U dS^T
-        f32x4 ud[CT];
-#pragma unroll
-        for (int i = 0; i < CT; ++i) ud[i] = f32x4{0, 0, 0, 0};
-        two(s0, tat, 0, xs);  // again, for <dS, S0>
-#pragma unroll 1
-        for (int n0 = 0; n0 < w.dvp; n0 += 32) {
-            const int next = n0 + 32 < w.dvp ? n0 + 32 : 0;
-            u32x4 ua[3];
-            float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = xu[j >> 2][j & 3];
-            split8<3>(x, ua);
-            __syncthreads();
-            if (task_s) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dss += xs[j >> 2][j & 3] * xr[j >> 2][j & 3];
-                put_parts(sm.s, trow, tg, xr);
-            }
-            two(ds, tat, 4 * next, xr);
-            two(s0, tat, 4 * next, xs);
-            two(ub, aat, 4 * next, xu);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < CT; ++i) {
-                u32x4 b[3];
-#pragma unroll
-                for (int n = 0; n < 3; ++n) b[n] = sm.s[half * CT + i][n][lane];
-                mma<3>(ua, b, ud[i]);
-            }
-        }
-        const f32x4 end = *reinterpret_cast<const f32x4*>(&sm.e_[16 * wv + 4 * grp]);
-#pragma unroll
-        for (int ks = 0; ks < KS / 2; ++ks) {
-            u32x4 ka[NP];
-#pragma unroll
-            for (int n = 0; n < NP; ++n) ka[n] = kf[(wv * KS + half * (KS / 2) + ks) * NP + n];
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int i = 2 * ks + p;
-                const f32x4 kv = as_result<NP>(ka, p, lane);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float z = end[r] * ud[i][r];
                     gone[r] += kv[r] * z;
-                    dk[i][r] += z;
+                    dq[i][r] += x;
+                    dk[i][r] += z - bet[r] * y;
                 }
             }
         }
