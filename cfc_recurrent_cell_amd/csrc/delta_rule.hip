@@ -262,21 +262,25 @@ __device__ __forceinline__ void span_of(const Shape& a, int s, int& tok0, int& l
 }
 __device__ __forceinline__ Chunk chunk_of(const Shape& a, long long slot) {
     Chunk k;
-    if (a.offsets) {
-        int lo = 0, hi = a.n_seq - 1;  // the last sequence whose base is not behind the slot
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (base_of(a, mid) <= slot) lo = mid; else hi = mid - 1;
+    if (a.offsets) {  // the last sequence whose base is not behind the slot, 64 at a time
+        int lo = 0, n = a.n_seq;
+        while (n > 1) {
+            const int step = (n + 63) / 64, at = lo + (int)(threadIdx.x & 63) * step;
+            const bool before = at < lo + n && base_of(a, min(at, a.n_seq - 1)) <= slot;
+            const int more = max(__popcll(__ballot(before)) - 1, 0) * step;
+            lo += more;
+            n = min(step, n - more);
         }
-        k.s = lo;
+        k.s = __builtin_amdgcn_readfirstlane(lo);
     } else {
-        k.s = (int)(slot / a.chunks);
+        k.s = (int)((uint32_t)slot / (uint32_t)a.chunks);
     }
     k.c = (int)(slot - base_of(a, k.s));
     int tok0, len;
     span_of(a, k.s, tok0, len);
     k.n = k.c < 0 ? 0 : (int)min((long long)kC, (long long)len - (long long)k.c * kC);
-    k.tok0 = tok0 + k.c * kC;
+    k.n = __builtin_amdgcn_readfirstlane(k.n);
+    k.tok0 = __builtin_amdgcn_readfirstlane(tok0 + k.c * kC);
     return k;
 }
 
@@ -294,39 +298,68 @@ __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane
 // grid: (slots, hv + hk).  The first hv make T and M of a value head, the others
 // the operands of a key head.
 //
-// Rows (row tile, summed 32 of dim_k) of a key head's tensor as left operands.
-template <class TY>
-__device__ __forceinline__ void load_parts(const typename TY::S* row, int c0, int c1, int D, bool ok, bool vec,
-                                           u32x4 (&p)[TY::NP]) {
-    if constexpr (TY::NP == 1) {
-        if (vec) {  // the elements are the one part
-            u32x2 a = {0, 0}, b = {0, 0};
-            if (ok && c0 < D) a = *reinterpret_cast<const u32x2*>(row + c0);
-            if (ok && c1 < D) b = *reinterpret_cast<const u32x2*>(row + c1);
-            p[0] = u32x4{a[0], a[1], b[0], b[1]};
-            return;
-        }
+// A chunk's rows of a key head's tensor as operands, VEC: 4 elements at a time.
+template <class TY, bool VEC>
+struct KeyRows {
+    using S = typename TY::S;
+    Buffer b;
+    uint32_t step;
+    int n, D;
+    __device__ __forceinline__ KeyRows(const S* p, long long stride, int n_, int D_)
+        : step((uint32_t)(stride * sizeof(S))), n(n_), D(D_) {
+        b = buffer_of(p, ((long long)(n - 1) * stride + D) * (long long)sizeof(S));
     }
-    float x[8];
-    load8<TY>(row, c0, c1, D, ok, vec, x);
-    split8<TY::NP>(x, p);
-}
+    // lane's row 16 rt + col, 8 places of ks
+    __device__ __forceinline__ void load(int rt, int ks, int lane, u32x4 (&p)[TY::NP]) const {
+        constexpr uint32_t Z = sizeof(S);
+        const int row = 16 * rt + (lane & 15), grp = lane >> 4;
+        const uint32_t at = row < n ? row * step : kNowhere;
+        float x[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = place_of(ks, grp, 4 * h);
+            if constexpr (VEC && Z == 2) {
+                const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(b, c < D ? at + Z * c : kNowhere, 0, 0);
+                if constexpr (TY::NP == 1) {
+                    p[0][2 * h] = y[0], p[0][2 * h + 1] = y[1];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[4 * h + j] = TY::load(
+                            __builtin_bit_cast(S, (uint16_t)(j & 1 ? y[j >> 1] >> 16 : y[j >> 1] & 0xffff)));
+                }
+            } else if constexpr (VEC) {
+                const u32x4 y = __builtin_amdgcn_raw_buffer_load_b128(b, c < D ? at + Z * c : kNowhere, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[4 * h + j] = __uint_as_float(y[j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t to = c + j < D ? at + Z * (c + j) : kNowhere;
+                    if constexpr (Z == 4)
+                        x[4 * h + j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, to, 0, 0));
+                    else
+                        x[4 * h + j] =
+                            TY::load(__builtin_bit_cast(S, __builtin_amdgcn_raw_buffer_load_b16(b, to, 0, 0)));
+                }
+            }
+        }
+        if constexpr (!(VEC && TY::NP == 1)) split8<TY::NP>(x, p);
+    }
+};
 
 // The chunk's 64 tokens of 32 places of dim_k, as rows and, transposed, as columns.
 // The matrix cores turn them: times the identity, rows come out as a result lies
 // (token 4 grp + r, place l & 15), which is half of the operand with tokens summed;
 // ones and zeros leave every part as it is.
-template <class TY, int KS, bool TURN>
-__device__ __forceinline__ void key_operands(const typename TY::S* p, long long stride, int n, int dk, bool vec, int ks,
-                                             int lane, u32x4* rows, u32x4* columns) {
+template <class TY, int KS, bool TURN, bool VEC>
+__device__ __forceinline__ void key_operands(const KeyRows<TY, VEC>& from, int ks, int lane, u32x4* rows,
+                                             u32x4* columns) {
     constexpr int NP = TY::NP;
     const int col = lane & 15, grp = lane >> 4;
     u32x4 x[4][NP];
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-        const int row = 16 * rt + col;
-        load_parts<TY>(p + row * stride, place_of(ks, grp, 0), place_of(ks, grp, 4), dk, row < n, vec, x[rt]);
-    }
+    for (int rt = 0; rt < 4; ++rt) from.load(rt, ks, lane, x[rt]);
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
@@ -355,7 +388,7 @@ __device__ __forceinline__ void key_operands(const typename TY::S* p, long long 
     }
 }
 
-template <class TY, int KS, bool GRAD>
+template <class TY, int KS, bool GRAD, bool VEC>
 __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, const typename TY::S* __restrict__ q,
                                                               const typename TY::S* __restrict__ k,
                                                               const float* __restrict__ g,
@@ -375,9 +408,10 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
         const S* qp = q + (long long)ch.tok0 * a.qt + h * a.qh;
         for (int f = wv; f < 2 * KS; f += 4) {
             if (f < KS)
-                key_operands<TY, KS, true>(kp, a.kt, ch.n, a.dk, a.kvec, f, lane, w.kf + at, w.kt + at);
+                key_operands<TY, KS, true, VEC>(KeyRows<TY, VEC>(kp, a.kt, ch.n, a.dk), f, lane, w.kf + at, w.kt + at);
             else
-                key_operands<TY, KS, GRAD>(qp, a.qt, ch.n, a.dk, a.qvec, f - KS, lane, w.qf + at, w.qt + at);
+                key_operands<TY, KS, GRAD, VEC>(KeyRows<TY, VEC>(qp, a.qt, ch.n, a.dk), f - KS, lane, w.qf + at,
+                                                w.qt + at);
         }
         return;
     }
@@ -408,26 +442,36 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
         ga.beta[lane] = b;
     }
     // k.k and q.k: wave wv has row tile wv of k.k and row tile 3 - wv of q.k, five
-    // tiles of the lower triangle for each wave
-    const S* kp = k + (long long)ch.tok0 * a.kt + hk * a.kh;
-    const S* qp = q + (long long)ch.tok0 * a.qt + hk * a.qh;
+    // tiles of the lower triangle for each wave; all of the loads are issued first
+    const int qrow = 3 - wv;
     f32x4 kk[4], qk[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) kk[i] = f32x4{0, 0, 0, 0}, qk[i] = f32x4{0, 0, 0, 0};
-    const int qrow = 3 - wv;
+    {
+        const KeyRows<TY, VEC> kr(k + (long long)ch.tok0 * a.kt + hk * a.kh, a.kt, ch.n, a.dk);
+        const KeyRows<TY, VEC> qr(q + (long long)ch.tok0 * a.qt + hk * a.qh, a.qt, ch.n, a.dk);
+        constexpr int AT_ONCE = NP == 1 ? KS : 1;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        const int c0 = place_of(ks, grp, 0), c1 = place_of(ks, grp, 4);
-        u32x4 qa[NP], ka[NP];
-        load_parts<TY>(qp + (16 * qrow + col) * a.qt, c0, c1, a.dk, 16 * qrow + col < ch.n, a.qvec, qa);
-        load_parts<TY>(kp + (16 * wv + col) * a.kt, c0, c1, a.dk, 16 * wv + col < ch.n, a.kvec, ka);
+        for (int k0 = 0; k0 < KS; k0 += AT_ONCE) {
+            u32x4 ka[AT_ONCE][NP], qa[AT_ONCE][NP], kb[AT_ONCE][4][NP];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i > wv && i > qrow) continue;
-            u32x4 kb[NP];
-            load_parts<TY>(kp + (16 * i + col) * a.kt, c0, c1, a.dk, 16 * i + col < ch.n, a.kvec, kb);
-            if (i <= wv) mma<3>(ka, kb, kk[i]);
-            if (i <= qrow) mma<3>(qa, kb, qk[i]);
+            for (int ks = 0; ks < AT_ONCE; ++ks) {
+                kr.load(wv, k0 + ks, lane, ka[ks]);
+                qr.load(qrow, k0 + ks, lane, qa[ks]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kr.load(i, k0 + ks, lane, kb[ks][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i <= wv) {
+#pragma unroll
+                    for (int ks = 0; ks < AT_ONCE; ++ks) mma<3>(ka[ks], kb[ks][i], kk[i]);
+                }
+                if (i <= qrow) {
+#pragma unroll
+                    for (int ks = 0; ks < AT_ONCE; ++ks) mma<3>(qa[ks], kb[ks][i], qk[i]);
+                }
+            }
         }
     }
     __syncthreads();
@@ -1126,14 +1170,20 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
 // A workgroup has a key head of a chunk and takes its value heads in turn, adding
 // up dQ and dK in registers.  Its 8 waves are 4 token tiles by 2 halves of dim_k;
 // the halves also share the triangles, the first has dM (and q.k), the second dL
-// (and k.k).  dim_v is summed in slices of 32: S0 (with dO and dR as left operands)
+// (and k.k).  Wave w shares its SIMD with wave w + 4: that one has token tile 3 - w,
+// so that the triangles are even.  dim_v is summed in slices of 32: S0 (with dO and dR as left operands)
 // and dS (with U) are split into parts once for the workgroup and shared through
 // LDS, the next slice's loads in flight under the products.  q and k in result
 // order are products with the identity.
+template <int N>
+__device__ __forceinline__ float from_lane_behind(float x) {  // N lanes on, within the 16 of a group
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + N, 0xf, 0xf, true));
+}
 __device__ __forceinline__ float over_columns(float x) {  // over the 16 lanes of a group
-#pragma unroll
-    for (int off = 1; off < 16; off <<= 1) x += __shfl_xor(x, off);
-    return x;
+    x += from_lane_behind<8>(x);
+    x += from_lane_behind<4>(x);
+    x += from_lane_behind<2>(x);
+    return x + from_lane_behind<1>(x);
 }
 __device__ __forceinline__ float over_groups(float x) {
     x += __shfl_xor(x, 16);
@@ -1161,13 +1211,13 @@ __device__ __forceinline__ void put_parts(u32x4 (*to)[3][64], int row, int g8, c
     for (int j = 0; j < 8; ++j) y[j] = x[j >> 2][j & 3];
     split8<3>(y, p);
 #pragma unroll
-    for (int n = 0; n < 3; ++n) to[row >> 4][n][16 * g8 + ((row & 15) ^ (4 * g8))] = p[n];
+    for (int n = 0; n < 3; ++n) to[row >> 4][n][16 * g8 + ((row & 15) ^ (2 * g8))] = p[n];
 }
-// ... from which lane l reads its operand: rows are turned by 4 places a group, so
-// that neither the writes of 4 rows nor the reads meet in a bank.
+// ... from which lane l reads its operand: rows are turned by 2 places a group, so
+// that of 8 lanes neither the writes (of 2 rows) nor the reads meet in a bank.
 __device__ __forceinline__ void get_parts(const u32x4 (&from)[3][64], int lane, u32x4 (&b)[3]) {
 #pragma unroll
-    for (int n = 0; n < 3; ++n) b[n] = from[n][lane ^ (4 * (lane >> 4))];
+    for (int n = 0; n < 3; ++n) b[n] = from[n][lane ^ (2 * (lane >> 4))];
 }
 // A row operand's 16 places `half` as a result lies: token 4 grp + r, place l & 15.
 template <int NP>
@@ -1193,7 +1243,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     const Chunk ch = chunk_of(a, slot);
     if (ch.n <= 0) return;
     const int t = threadIdx.x, lane = t & 63, wave = wave_of(), col = lane & 15, grp = lane >> 4;
-    const int wv = wave & 3, half = wave >> 2;
+    const int half = wave >> 2, wv = half ? 7 - wave : wave;
     const int hk = blockIdx.y, rep = a.hv / a.hk;
     const long long ks0 = slot * a.hk + hk;
     const int arow = 16 * wv + col;  // this lane's row as a left operand
@@ -1768,8 +1818,9 @@ void launch_prep(const Shape& a, const Space& w, const void* q, const void* k, c
                  hipStream_t stream) {
     using S = typename TY::S;
     if (a.slots == 0) return;
-    hipLaunchKernelGGL((delta_prep_kernel<TY, KS, GRAD>), dim3((unsigned)a.slots, a.hv + a.hk), dim3(kThreads), 0,
-                       stream, a, w, (const S*)q, (const S*)k, g, beta);
+    const auto kernel = a.qvec && a.kvec ? delta_prep_kernel<TY, KS, GRAD, true> : delta_prep_kernel<TY, KS, GRAD, false>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)a.slots, a.hv + a.hk), dim3(kThreads), 0, stream, a, w, (const S*)q,
+                       (const S*)k, g, beta);
 }
 template <class TY, int KS, int NCT, bool GRAD>
 void launch_chain(const Shape& a, const Space& w, const void* v, const float* initial, void* o, float* final_state,
