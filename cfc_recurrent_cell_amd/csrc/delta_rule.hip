@@ -216,6 +216,12 @@ __device__ __forceinline__ float exp2_of(double d) {
     return __builtin_amdgcn_exp2f(x) * fmaf((float)(d - (double)x), 0.69314718f, 1.0f);
 }
 
+// 2^((h1 + l1) - (h2 + l2)) of sums held in two floats: the difference is off by half
+// a step, so what it gives by |difference| 2^-25, of a result that is 2^difference.
+__device__ __forceinline__ float exp2_of(float h1, float l1, float h2, float l2) {
+    return __builtin_amdgcn_exp2f((h1 - h2) + (l1 - l2));
+}
+
 // --------------------------------------------------------------- arguments
 struct Shape {
     int n_seq, seq_len, n_tokens;
@@ -416,13 +422,38 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
         return;
     }
 
-    __shared__ double G[kC];  // in powers of two: sums of g log2(e)
+    __shared__ float Gh[kC], Gl[kC];  // sums of g log2(e), each in two floats
     __shared__ float Bt[kC];
-    __shared__ __align__(16) float L[kC][kC + 4];  // L, then M
-    __shared__ __align__(16) float X[kC][kC + 4];  // (I + L)^-1
+    __shared__ __align__(16) float L[kC][kC + 4];  // k's rows, then L, then M
+    __shared__ __align__(16) float X[kC][kC + 4];  // q's rows, then (I + L)^-1
     const int h = blockIdx.y;
     const int hk = h / (a.hv / a.hk);
     const long long vs = slot * a.hv + h;
+    const S* const kp = k + (long long)ch.tok0 * a.kt + hk * a.kh;
+    const S* const qp = q + (long long)ch.tok0 * a.qt + hk * a.qh;
+    // One part and aligned rows: through LDS, loaded once and 16 bytes a lane.  (As
+    // operands straight from memory they cost 4 times the cache lookups: 7000 cycles
+    // of a workgroup's 21000.)
+    constexpr bool STAGED = VEC && NP == 1;
+    if constexpr (STAGED) {
+        constexpr int CH = 4 * KS, AT = kThreads / CH;  // 16-byte pieces of a row, rows at once
+        const int row = t / CH, c = t % CH;
+        const KeyRows<TY, VEC> kr(kp, a.kt, ch.n, a.dk), qr(qp, a.qt, ch.n, a.dk);
+        u32x4 x[kC / AT], y[kC / AT];
+#pragma unroll
+        for (int i = 0; i < kC / AT; ++i) {
+            const int r = row + i * AT;
+            const bool in = r < ch.n && 8 * c < a.dk;
+            x[i] = __builtin_amdgcn_raw_buffer_load_b128(kr.b, in ? r * kr.step + 16 * c : kNowhere, 0, 0);
+            y[i] = __builtin_amdgcn_raw_buffer_load_b128(qr.b, in ? r * qr.step + 16 * c : kNowhere, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kC / AT; ++i) {
+            *reinterpret_cast<u32x4*>(&L[row + i * AT][4 * c]) = x[i];
+            *reinterpret_cast<u32x4*>(&X[row + i * AT][4 * c]) = y[i];
+        }
+    }
+    double G_own = 0.0;
     if (wv == 0) {
         const long long at = (long long)(ch.tok0 + lane) * a.hv + h;
         const float gv = lane < ch.n ? g[at] : 0.0f;
@@ -431,25 +462,37 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
             const double o = __shfl_up(G0, off);
             if (lane >= off) G0 += o;
         }
-        const double last = __shfl(G0, 63);
-        const float b = lane < ch.n ? beta[at] : 0.0f;
-        G[lane] = G0;
-        Bt[lane] = b;
-        Gates& ga = w.gates[vs];
-        ga.G[lane] = G0;
-        ga.gamma[lane] = exp2_of(G0);
-        ga.e[lane] = exp2_of(last - G0);
-        ga.beta[lane] = b;
+        G_own = G0;
+        Gh[lane] = (float)G0;
+        Gl[lane] = (float)(G0 - (double)(float)G0);
+        Bt[lane] = lane < ch.n ? beta[at] : 0.0f;
     }
     // k.k and q.k: wave wv has row tile wv of k.k and row tile 3 - wv of q.k, five
-    // tiles of the lower triangle for each wave; all of the loads are issued first
+    // tiles of the lower triangle for each wave
     const int qrow = 3 - wv;
     f32x4 kk[4], qk[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) kk[i] = f32x4{0, 0, 0, 0}, qk[i] = f32x4{0, 0, 0, 0};
-    {
-        const KeyRows<TY, VEC> kr(k + (long long)ch.tok0 * a.kt + hk * a.kh, a.kt, ch.n, a.dk);
-        const KeyRows<TY, VEC> qr(q + (long long)ch.tok0 * a.qt + hk * a.qh, a.qt, ch.n, a.dk);
+    if constexpr (STAGED) {
+        __syncthreads();
+        auto part = [&](const float (*rows)[kC + 4], int rt, int ks, u32x4 (&p)[NP]) {
+            p[0] = *reinterpret_cast<const u32x4*>(&rows[16 * rt + col][16 * ks + 4 * grp]);
+        };
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            u32x4 ka[NP], qa[NP], kb[NP];
+            part(L, wv, ks, ka);
+            part(X, qrow, ks, qa);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i > wv && i > qrow) continue;
+                part(L, i, ks, kb);
+                if (i <= wv) mma<3>(ka, kb, kk[i]);
+                if (i <= qrow) mma<3>(qa, kb, qk[i]);
+            }
+        }
+    } else {
+        const KeyRows<TY, VEC> kr(kp, a.kt, ch.n, a.dk), qr(qp, a.qt, ch.n, a.dk);
         constexpr int AT_ONCE = NP == 1 ? KS : 1;
 #pragma unroll
         for (int k0 = 0; k0 < KS; k0 += AT_ONCE) {
@@ -476,33 +519,40 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
     }
     __syncthreads();
     {
-        double Gk[4], Gq[4];
-        float bk[4];
+        float kh[4], kl[4], qh[4], ql[4], bk[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            Gk[r] = G[16 * wv + 4 * grp + r];
-            Gq[r] = G[16 * qrow + 4 * grp + r];
+            kh[r] = Gh[16 * wv + 4 * grp + r], kl[r] = Gl[16 * wv + 4 * grp + r];
+            qh[r] = Gh[16 * qrow + 4 * grp + r], ql[r] = Gl[16 * qrow + 4 * grp + r];
             bk[r] = Bt[16 * wv + 4 * grp + r];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = 16 * i + col;
-            const double Gc = G[c];
+            const float ch_ = Gh[c], cl = Gl[c];
             if (i <= wv) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = 16 * wv + 4 * grp + r;
-                    L[row][c] = c < row ? bk[r] * exp2_of(Gk[r] - Gc) * kk[i][r] : 0.0f;
+                    L[row][c] = c < row ? bk[r] * exp2_of(kh[r], kl[r], ch_, cl) * kk[i][r] : 0.0f;
                 }
             }
             if (i <= qrow) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = 16 * qrow + 4 * grp + r;
-                    qk[i][r] = c <= row ? a.scale * exp2_of(Gq[r] - Gc) * qk[i][r] : 0.0f;
+                    qk[i][r] = c <= row ? a.scale * exp2_of(qh[r], ql[r], ch_, cl) * qk[i][r] : 0.0f;
                 }
             }
         }
+    }
+    if (wv == 0) {
+        const double last = __shfl(G_own, 63);
+        Gates& ga = w.gates[vs];
+        ga.G[lane] = G_own;
+        ga.gamma[lane] = exp2_of(G_own);
+        ga.e[lane] = exp2_of(last - G_own);
+        ga.beta[lane] = Bt[lane];
     }
     __syncthreads();
     // The 16 x 16 blocks on the diagonal, one for each wave: column `col` of
@@ -1813,12 +1863,18 @@ inline int chain_tiles(const Shape& a) {
     return wide >= 256 && a.dv > 16 ? 2 : 1;
 }
 
+// Eight elements of a 16-bit row are one aligned load.
+inline bool eights(const void* p, long long st, long long sh, int dim) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && st % 8 == 0 && sh % 8 == 0 && dim % 8 == 0;
+}
+
 template <class TY, int KS, bool GRAD>
 void launch_prep(const Shape& a, const Space& w, const void* q, const void* k, const float* g, const float* beta,
                  hipStream_t stream) {
     using S = typename TY::S;
     if (a.slots == 0) return;
-    const auto kernel = a.qvec && a.kvec ? delta_prep_kernel<TY, KS, GRAD, true> : delta_prep_kernel<TY, KS, GRAD, false>;
+    const bool vec = sizeof(S) == 4 ? a.qvec && a.kvec : eights(q, a.qt, a.qh, a.dk) && eights(k, a.kt, a.kh, a.dk);
+    const auto kernel = vec ? delta_prep_kernel<TY, KS, GRAD, true> : delta_prep_kernel<TY, KS, GRAD, false>;
     hipLaunchKernelGGL(kernel, dim3((unsigned)a.slots, a.hv + a.hk), dim3(kThreads), 0, stream, a, w, (const S*)q,
                        (const S*)k, g, beta);
 }
