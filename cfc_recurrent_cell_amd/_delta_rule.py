@@ -1,79 +1,62 @@
 """Tensor checks and pointer marshalling of the gated delta rule (include/delta_rule.h)."""
 from __future__ import annotations
 
-import ctypes
+from ctypes import byref
 from typing import Optional, Tuple
 
-from ._lib import DeltaRuleShape, _check, _on_device, _stream_ptr, element_type, load_library
+import torch
+
+from ._lib import DeltaRuleShape, _check, load_library
+from ._tensors import F32, check, element_type, given_or_new, on_device, ptr, space, stream_ptr
 
 
-def _tensor(t, name, dtype, device, shape):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device or 'a GPU'} "
-                         f"(got {t.dtype}, {t.device}, contiguous={t.is_contiguous()})")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
-
-
-def _rows(t, name, lead, like=None, shape=None):
+def _rows(t, name, lead, dtype, device, shape=None):
     """(token stride, head stride) of t [*lead, heads, dim], rows numbered along its leading axes."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dim() != lead + 2 or (like is not None and (t.dtype != like.dtype or t.device != like.device)):
+    if not t.is_cuda or t.dim() != lead + 2 or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be a {lead + 2}-dimensional tensor on a GPU, of q's type and device "
                          f"(got {t.dim()} dimensions, {t.dtype}, {t.device})")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    st = t.stride()
     n = t.shape
-    if t.numel() == 0:
-        return 0, 0
-    if n[-1] > 1 and st[-1] != 1:
+    if shape is not None and n != shape:
+        raise ValueError(f"{name} has shape {tuple(n)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and n[-1] > 1 and t.numel():
         raise ValueError(f"{name}'s last axis must be dense (its stride is {st[-1]})")
     if lead == 1:
         return st[0], st[1]
     if n[1] == 1:
         return st[0], st[2]
-    if n[0] > 1 and n[1] > 1 and st[0] != n[1] * st[1]:
+    if st[0] != n[1] * st[1] and n[0] > 1 and t.numel():
         raise ValueError(f"{name}'s sequences must lie one behind the other (strides {st}): make it contiguous")
     return st[1], st[2]
 
 
 def _shape(q, k, v, g, beta, scale, offsets, lead, grad_o=None):
-    import torch
-    s = DeltaRuleShape()
-    s.q_stride_t, s.q_stride_h = _rows(q, "q", lead)
-    s.type = element_type(q, "q")
-    s.k_stride_t, s.k_stride_h = _rows(k, "k", lead, q, q.shape)
-    s.v_stride_t, s.v_stride_h = _rows(v, "v", lead, q)
-    n = q.shape
-    if v.shape[:lead] != n[:lead]:
-        raise ValueError(f"v has shape {tuple(v.shape)}, expected {tuple(n[:lead])} tokens as q has")
-    if grad_o is not None:
-        s.go_stride_t, s.go_stride_h = _rows(grad_o, "grad_o", lead, q, v.shape)
-    s.heads_k, s.dim_k = n[lead:]
-    s.heads_v, s.dim_v = v.shape[lead:]
-    if s.heads_k < 1 or s.heads_v % s.heads_k:
-        raise ValueError(f"v's {s.heads_v} heads are no multiple of q's {s.heads_k}")
-    gates = v.shape[:lead + 1]
-    _tensor(g, "g", torch.float32, q.device, gates)
-    _tensor(beta, "beta", torch.float32, q.device, gates)
-    s.scale = s.dim_k ** -0.5 if scale is None else float(scale)
-    s.n_tokens = n[0] if lead == 1 else n[0] * n[1]
+    kind, dtype, dev, n = element_type(q, "q"), q.dtype, q.device, q.shape
+    qs = _rows(q, "q", lead, dtype, dev)
+    ks = _rows(k, "k", lead, dtype, dev, n)
+    vs = _rows(v, "v", lead, dtype, dev)
+    nv = v.shape
+    if nv[:lead] != n[:lead]:
+        raise ValueError(f"v has shape {tuple(nv)}, expected {tuple(n[:lead])} tokens as q has")
+    gs = (0, 0) if grad_o is None else _rows(grad_o, "grad_o", lead, dtype, dev, nv)
+    heads_k, dim_k, heads_v, dim_v = n[-2], n[-1], nv[-2], nv[-1]
+    if heads_k < 1 or heads_v % heads_k:
+        raise ValueError(f"v's {heads_v} heads are no multiple of q's {heads_k}")
+    gates = nv[:-1]
+    check(g, "g", F32, dev, gates)
+    check(beta, "beta", F32, dev, gates)
+    tokens, count, length, at = n[0] if lead == 1 else n[0] * n[1], 0, 0, None
     if offsets is not None:
+        check(offsets, "offsets", torch.int32, dev)
         if offsets.dim() != 1 or offsets.numel() < 1:
             raise ValueError("offsets must be a vector of the sequences' beginnings and the last one's end")
-        _tensor(offsets, "offsets", torch.int32, q.device, offsets.shape)
-        s.n_seq = offsets.numel() - 1
-        s.offsets = offsets.data_ptr()
+        count, at = offsets.numel() - 1, offsets.data_ptr()
     elif lead == 2:
-        s.n_seq, s.seq_len = n[0], n[1]
-    return s
+        count, length = n[0], n[1]
+    return DeltaRuleShape(kind, count, length, tokens, at, heads_k, heads_v, dim_k, dim_v,
+                          dim_k ** -0.5 if scale is None else scale, *qs, *ks, *vs, *gs)
 
 
 def _lead(q, offsets):
@@ -84,19 +67,10 @@ def _lead(q, offsets):
     return 2 if offsets is None else 1
 
 
-def _space(need, workspace, device, what):
-    import torch
+def _size(need: int) -> int:
     if need < 0:
-        raise ValueError(f"{what}: a size is beyond what the library takes (dim_k <= 128, dim_v <= 256)")
-    if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _ptr(t):
-    return t.data_ptr() if t is not None else None
+        raise ValueError("a size is beyond what the library takes (dim_k <= 128, dim_v <= 256)")
+    return need
 
 
 def delta_rule_workspace(q, k, v, g, beta, offsets=None, backward: bool = False) -> int:
@@ -104,10 +78,7 @@ def delta_rule_workspace(q, k, v, g, beta, offsets=None, backward: bool = False)
     these tensors; it depends on their sizes alone."""
     lib = load_library()
     s = _shape(q, k, v, g, beta, 1.0, offsets, _lead(q, offsets))
-    n = int((lib.delta_rule_backward_workspace if backward else lib.delta_rule_forward_workspace)(ctypes.byref(s)))
-    if n < 0:
-        raise ValueError("a size is beyond what the library takes (dim_k <= 128, dim_v <= 256)")
-    return n
+    return _size((lib.delta_rule_backward_workspace if backward else lib.delta_rule_forward_workspace)(byref(s)))
 
 
 def delta_rule_forward(q, k, v, g, beta, initial_state=None, scale: Optional[float] = None, offsets=None, o=None,
@@ -129,27 +100,20 @@ def delta_rule_forward(q, k, v, g, beta, initial_state=None, scale: Optional[flo
     offsets[s + 1] - 1; rows behind the last one's end keep what ``o`` held.
     ``final_state`` may be ``initial_state`` itself; ``want_final=False`` leaves
     it out (None).  The workspace is allocated here unless given."""
-    import torch
     lib = load_library()
-    lead = _lead(q, offsets)
-    s = _shape(q, k, v, g, beta, scale, offsets, lead)
+    s = _shape(q, k, v, g, beta, scale, offsets, _lead(q, offsets))
     states = (s.n_seq, s.heads_v, s.dim_k, s.dim_v)
     dev = q.device
-    with _on_device(dev, stream):
+    with on_device(dev, stream):
         if initial_state is not None:
-            _tensor(initial_state, "initial_state", torch.float32, dev, states)
-        if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
-        _tensor(o, "o", q.dtype, dev, v.shape)
-        if final_state is None and want_final:
-            final_state = torch.empty(states, dtype=torch.float32, device=dev)
-        if final_state is not None:
-            _tensor(final_state, "final_state", torch.float32, dev, states)
-        ws, ws_bytes, keep = _space(int(lib.delta_rule_forward_workspace(ctypes.byref(s))), workspace, dev,
-                                    "delta_rule_forward")
+            check(initial_state, "initial_state", F32, dev, states)
+        o = given_or_new(o, "o", q.dtype, dev, v.shape)
+        if final_state is not None or want_final:
+            final_state = given_or_new(final_state, "final_state", F32, dev, states)
+        at, size, keep = space(_size(lib.delta_rule_forward_workspace(byref(s))), workspace, dev)
         _check("delta_rule_forward", lib.delta_rule_forward(
-            ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-            _ptr(initial_state), o.data_ptr(), _ptr(final_state), ws, ws_bytes, _stream_ptr(dev, stream)))
+            byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), ptr(initial_state),
+            o.data_ptr(), ptr(final_state), at, size, stream_ptr(dev, stream)))
     return o, final_state
 
 
@@ -164,38 +128,32 @@ def delta_rule_backward(q, k, v, g, beta, grad_o, initial_state=None, grad_final
     ``grad_final_state`` None means zeros.  Value heads that share a query and
     key head add up in grad_q and grad_k.  ``grad_initial_state`` is None where
     there is no initial state and no buffer is given for it."""
-    import torch
     lib = load_library()
-    lead = _lead(q, offsets)
-    s = _shape(q, k, v, g, beta, scale, offsets, lead, grad_o)
+    s = _shape(q, k, v, g, beta, scale, offsets, _lead(q, offsets), grad_o)
     states = (s.n_seq, s.heads_v, s.dim_k, s.dim_v)
-    dev = q.device
-    with _on_device(dev, stream):
-        for t, name in ((initial_state, "initial_state"), (grad_final_state, "grad_final_state")):
-            if t is not None:
-                _tensor(t, name, torch.float32, dev, states)
+    dev, dtype = q.device, q.dtype
+    with on_device(dev, stream):
+        if initial_state is not None:
+            check(initial_state, "initial_state", F32, dev, states)
+        if grad_final_state is not None:
+            check(grad_final_state, "grad_final_state", F32, dev, states)
 
-        def out(t, name, shape, dtype):
+        def rows(t, name, kind, like):
             # rows behind the last sequence have no gradient, and keep what a given buffer holds
-            if t is None:
-                make = torch.empty if offsets is None or name == "grad_initial_state" else torch.zeros
-                return make(shape, dtype=dtype, device=dev)
-            return _tensor(t, name, dtype, dev, shape)
+            if t is None and offsets is not None:
+                return torch.zeros(like.shape, dtype=kind, device=dev)
+            return given_or_new(t, name, kind, dev, like.shape)
 
-        grad_q = out(grad_q, "grad_q", q.shape, q.dtype)
-        grad_k = out(grad_k, "grad_k", k.shape, q.dtype)
-        grad_v = out(grad_v, "grad_v", v.shape, q.dtype)
-        grad_g = out(grad_g, "grad_g", g.shape, torch.float32)
-        grad_beta = out(grad_beta, "grad_beta", g.shape, torch.float32)
+        grad_q, grad_k = rows(grad_q, "grad_q", dtype, q), rows(grad_k, "grad_k", dtype, k)
+        grad_v = rows(grad_v, "grad_v", dtype, v)
+        grad_g, grad_beta = rows(grad_g, "grad_g", F32, g), rows(grad_beta, "grad_beta", F32, g)
         if grad_initial_state is not None or initial_state is not None:
-            grad_initial_state = out(grad_initial_state, "grad_initial_state", states, torch.float32)
-        ws, ws_bytes, keep = _space(int(lib.delta_rule_backward_workspace(ctypes.byref(s))), workspace, dev,
-                                    "delta_rule_backward")
+            grad_initial_state = given_or_new(grad_initial_state, "grad_initial_state", F32, dev, states)
+        at, size, keep = space(_size(lib.delta_rule_backward_workspace(byref(s))), workspace, dev)
         _check("delta_rule_backward", lib.delta_rule_backward(
-            ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-            _ptr(initial_state), grad_o.data_ptr(), _ptr(grad_final_state), grad_q.data_ptr(), grad_k.data_ptr(),
-            grad_v.data_ptr(), grad_g.data_ptr(), grad_beta.data_ptr(), _ptr(grad_initial_state), ws, ws_bytes,
-            _stream_ptr(dev, stream)))
+            byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), ptr(initial_state),
+            grad_o.data_ptr(), ptr(grad_final_state), grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(),
+            grad_g.data_ptr(), grad_beta.data_ptr(), ptr(grad_initial_state), at, size, stream_ptr(dev, stream)))
     return grad_q, grad_k, grad_v, grad_g, grad_beta, grad_initial_state
 
 
@@ -207,25 +165,22 @@ def delta_rule_step(q, k, v, g, beta, states, slots=None, scale: Optional[float]
     states[slots[b]] (int32 on the GPU), or states[b] without ``slots``.  A slot
     outside the pool (such as -1) makes the row idle: its o is zeros.  Rows that
     name one slot are taken one after the other, in the order of the rows."""
-    import torch
     lib = load_library()
     if q.dim() != 3:
         raise ValueError(f"q must be [batch, heads, dim], got {q.dim()} dimensions")
     s = _shape(q, k, v, g, beta, scale, None, 1)
-    dev = q.device
+    dev, rows = q.device, q.shape[0]
     if not isinstance(states, torch.Tensor) or states.dim() != 4:
         raise ValueError("states must be a tensor [pool, heads_v, dim_k, dim_v]")
     pool = states.shape[0]
-    _tensor(states, "states", torch.float32, dev, (pool, s.heads_v, s.dim_k, s.dim_v))
+    check(states, "states", F32, dev, (pool, s.heads_v, s.dim_k, s.dim_v))
     if slots is not None:
-        _tensor(slots, "slots", torch.int32, dev, (s.n_tokens,))
-    elif pool < s.n_tokens:
-        raise ValueError(f"{s.n_tokens} rows need as many states, got {pool}")
-    with _on_device(dev, stream):
-        if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
-        _tensor(o, "o", q.dtype, dev, v.shape)
+        check(slots, "slots", torch.int32, dev, (rows,))
+    elif pool < rows:
+        raise ValueError(f"{rows} rows need as many states, got {pool}")
+    with on_device(dev, stream):
+        o = given_or_new(o, "o", q.dtype, dev, v.shape)
         _check("delta_rule_step", lib.delta_rule_step(
-            ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-            states.data_ptr(), pool, _ptr(slots), o.data_ptr(), _stream_ptr(dev, stream)))
+            byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), states.data_ptr(), pool,
+            ptr(slots), o.data_ptr(), stream_ptr(dev, stream)))
     return o

@@ -49,42 +49,6 @@ class DeltaRuleShape(ctypes.Structure):
                     (f"{n}_stride_{a}", ctypes.c_longlong) for n in ("q", "k", "v", "go") for a in ("t", "h")]
 
 
-def element_type(t, name: str) -> int:
-    """The library's CFC_TYPE_* of a tensor's elements."""
-    import torch
-    types = {torch.float32: CFC_TYPE_F32, torch.bfloat16: CFC_TYPE_BF16, torch.float16: CFC_TYPE_F16}
-    if t.dtype not in types:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return types[t.dtype]
-
-
-def _stream_ptr(device, stream):
-    import torch
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-
-class _on_device:
-    """Makes ``device`` current, and ``stream`` too where one is given: what is
-    allocated inside belongs to that stream, so memory freed while its kernels
-    still run is not handed to another one."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.contexts = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(device))
-        if stream is not None:
-            self.contexts.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-
-    def __exit__(self, *why):
-        for c in reversed(self.contexts):
-            c.__exit__(*why)
-
-
 class CfcError(RuntimeError):
     def __init__(self, fn: str, code: int, text: str):
         super().__init__(f"{fn} failed with status {code}: {text}")
