@@ -317,14 +317,17 @@ int check_sizes(int type, int stream_type, long long rows, long long width) {
     return CFC_OK;
 }
 
-// Threads and 8-column vectors of a row: the rule on the width alone.
-template <class F>
+// Threads and 8-column vectors of a row: the rule on the width alone.  The backward,
+// which keeps three rows' values and the weight gradient in registers, has more
+// threads and one vector each: 16384 x 4096 with 256 x 2 162 us, with 512 x 1 109 us.
+// The forward is at the rate of a copy with either.
+template <bool BACK, class F>
 int with_tiling(long long width, F f) {
     if (width <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
     if (width <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
     if (width <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-    if (width <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-    if (width <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+    if (width <= 4096) return f(std::integral_constant<int, BACK ? 512 : 256>{}, std::integral_constant<int, BACK ? 1 : 2>{});
+    if (width <= 8192) return f(std::integral_constant<int, BACK ? 1024 : 512>{}, std::integral_constant<int, BACK ? 1 : 2>{});
     return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
 }
 inline long long rows_at_once(long long width) { return width <= 128 ? 16 : width <= 512 ? 4 : 1; }
@@ -362,7 +365,7 @@ int run_forward(int type, int stream_type, long long rows, long long width, cons
     if (!outputs_disjoint(outs, 4, ins, 3)) return CFC_ERR_OVERLAP;
     const bool vec = width % 8 == 0 && aligned({x, residual, weight, y, h});
     return with_types(type, stream_type, [&](auto tx, auto th) {
-        return with_tiling(width, [&](auto tpr, auto nv) {
+        return with_tiling<false>(width, [&](auto tpr, auto nv) {
             using TX = decltype(tx);
             using TH = decltype(th);
             constexpr int T = decltype(tpr)::value, V = decltype(nv)::value;
@@ -379,7 +382,9 @@ int run_forward(int type, int stream_type, long long rows, long long width, cons
 // Workgroups of the backward, each with a row of partial weight gradients.
 inline long long parts_of(long long rows, long long width) {
     const long long need = (rows + rows_at_once(width) - 1) / rows_at_once(width);
-    return std::min(need, 512LL);
+    // narrow rows' partial sums are small, and more workgroups hide more of the loads:
+    // 99991 x 128 with 512 21.6 us, with 1024 20.0; 16384 x 4096 with 1024 121 us for 109
+    return std::min(need, width <= 512 ? 1024LL : 512LL);
 }
 
 }  // namespace
@@ -423,7 +428,7 @@ extern "C" int rms_norm_backward(int type, int stream_type, long long rows, long
     const bool vec = width % 8 == 0 && aligned({grad_y, h, weight, grad_h, grad_x});
     float* part = static_cast<float*>(workspace);
     const int e = with_types(type, stream_type, [&](auto tx, auto th) {
-        return with_tiling(width, [&](auto tpr, auto nv) {
+        return with_tiling<true>(width, [&](auto tpr, auto nv) {
             using TX = decltype(tx);
             using TH = decltype(th);
             constexpr int T = decltype(tpr)::value, V = decltype(nv)::value;

@@ -7,7 +7,7 @@ value, and the arithmetic's own error.  rstd is off by the sum of squares'
 difference (grad_x) has the error of its largest term, a sum over rows
 (grad_weight) that of its terms' magnitudes' sum, with rows / parts + log2 ...
 additions: at most 64 roundings of 2^-24 are allowed everywhere below, which
-holds for every size here (512 workgroups, at most 32 rows each).  An e4m3
+holds for every size here (at most 32 rows for a workgroup's slot).  An e4m3
 value is the nearest one or, where a tie is within the arithmetic's error, its
 neighbour: off by half a step (2^-4 of the value, or 2^-10 where e4m3 is
 subnormal) and that error."""
