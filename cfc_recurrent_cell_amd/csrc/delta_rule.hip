@@ -28,9 +28,9 @@
 //       gradients) and the parts of K, Q, K^T, Q^T, all stored in the order in
 //       which the matrix cores' operands lie in a wave's registers, so that the
 //       chain below loads them 16 bytes a lane, without masks
-//   delta_chain_kernel     along each sequence, for a tile of dim_v: O and the
-//       states (forward), or U and every chunk's S0 (for the gradients)
-//   delta_reverse_kernel   the gradients' chain from the last chunk to the first
+//   delta_chain_kernel     along each sequence, for a tile of dim_v: O and the states
+//   delta_chains_kernel    for the gradients: the states' chain again, keeping U and
+//       every chunk's S0, and the gradients' chain from the last chunk to the first
 //   delta_grads_kernel     for all chunks at once: grad_q, grad_k, grad_g, grad_beta
 //   delta_token_kernel     the recurrence token by token (a decode step, and
 //       sequences too short for chunks)
@@ -813,21 +813,29 @@ __device__ __forceinline__ void keep_rows(float* to, long long vs, int dvp, int 
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[r]), b, at, 4 * (r * dvp + n0), 0);
 }
 
-template <class TY, int KS, int NCT, bool GRAD>
-__global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w, const typename TY::S* __restrict__ v,
-                                                               const float* initial, typename TY::S* __restrict__ o,
-                                                               float* final_state) {
+template <int NP, int NCT, int KS, bool GRAD>
+struct ChainLds {
+    Exchange<3, NCT, KS> s;
+    Exchange<3, NCT, 2> p, e;
+    Exchange<GRAD || NP < 3 ? (GRAD ? 1 : 2) : 3, GRAD ? 1 : NCT, 2> u;
+};
+
+template <class TY, int KS, int NCT, bool GRAD, int SETS>
+__device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shape& a, const Space& w,
+                                           const typename TY::S* __restrict__ v, const float* initial,
+                                           typename TY::S* __restrict__ o, float* final_state) {
     using S = typename TY::S;
-    constexpr int NP = TY::NP, NM = NP == 3 ? 3 : 2, NR = KS / 2, SETS = sets_of(NP, KS);
+    constexpr int NP = TY::NP, NM = NP == 3 ? 3 : 2, NR = KS / 2;
     constexpr int ORDO = NP == 3 ? 3 : 2;  // o is rounded to 16 bits or to 32
-    __shared__ Exchange<3, NCT, KS> xs;
-    __shared__ Exchange<3, NCT, 2> xp, xe;
-    __shared__ Exchange<GRAD ? 1 : NM, GRAD ? 1 : NCT, 2> xu;
+    auto& sm = *static_cast<ChainLds<NP, NCT, KS, GRAD>*>(lds);
+    auto& xs = sm.s;
+    auto &xp = sm.p, &xe = sm.e;
+    auto& xu = sm.u;
     // for the gradients all of the padded columns: the workspace's rows are read whole
     const int tiles = ((GRAD ? w.dvp : a.dv) + 16 * NCT - 1) / (16 * NCT);
     const long long count = (long long)a.n_seq * a.hv * tiles;
-    const long long at = on_die(blockIdx.x, count);
-    if (at >= count || blockIdx.x / 8 >= (count + 7) / 8) return;
+    const long long at = on_die(block, count);
+    if (at >= count || block / 8 >= (count + 7) / 8) return;
     const int n0 = (int)(at % tiles) * 16 * NCT;
     const long long sh = at / tiles;
     const int h = (int)(sh % a.hv), s = (int)(sh / a.hv), hk = h / (a.hv / a.hk);
@@ -1019,6 +1027,14 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
 //   dS0 = gamma_63 dS + scale Q^T diag(gamma) dO - K^T diag(gamma beta) dR
 // The same tiles, exchanges and register sets as the states' chain, from the last
 // chunk on.
+template <class TY, int KS, int NCT, bool GRAD>
+__global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w, const typename TY::S* __restrict__ v,
+                                                               const float* initial, typename TY::S* __restrict__ o,
+                                                               float* final_state) {
+    __shared__ __align__(16) ChainLds<TY::NP, NCT, KS, GRAD> sm;
+    chain_task<TY, KS, NCT, GRAD, sets_of(TY::NP, KS)>(blockIdx.x, &sm, a, w, v, initial, o, final_state);
+}
+
 template <int NP, int NCT, int KS>
 struct ReverseLds {
     Exchange<3, NCT, KS> s;
@@ -1026,23 +1042,20 @@ struct ReverseLds {
     Exchange<3, NCT, 2> g, u, r;  // scale gamma dO; dU; -gamma beta dR
 };
 
-template <class TY, int KS, int NCT>
-__global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space w,
-                                                                 const typename TY::S* __restrict__ go,
-                                                                 const float* grad_final,
-                                                                 typename TY::S* __restrict__ gv,
-                                                                 float* grad_initial) {
+template <class TY, int KS, int NCT, int SETS>
+__device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Shape& a, const Space& w,
+                                             const typename TY::S* __restrict__ go, const float* grad_final,
+                                             typename TY::S* __restrict__ gv, float* grad_initial) {
     using S = typename TY::S;
-    constexpr int NP = TY::NP, NR = KS / 2, SETS = sets_of(NP, KS);
-    extern __shared__ __align__(16) unsigned char lds[];
-    auto& sh_ = *reinterpret_cast<ReverseLds<NP, NCT, KS>*>(lds);
+    constexpr int NP = TY::NP, NR = KS / 2;
+    auto& sh_ = *static_cast<ReverseLds<NP, NCT, KS>*>(lds);
     auto& xs = sh_.s;
     auto& xo = sh_.o;
     auto &xg = sh_.g, &xu = sh_.u, &xr = sh_.r;
     const int tiles = w.dvp / (16 * NCT);
     const long long count = (long long)a.n_seq * a.hv * tiles;
-    const long long at = on_die(blockIdx.x, count);
-    if (at >= count || blockIdx.x / 8 >= (count + 7) / 8) return;
+    const long long at = on_die(block, count);
+    if (at >= count || block / 8 >= (count + 7) / 8) return;
     const int n0 = (int)(at % tiles) * 16 * NCT;
     const long long sh = at / tiles;
     const int h = (int)(sh % a.hv), s = (int)(sh / a.hv), hk = h / (a.hv / a.hk);
@@ -1204,6 +1217,38 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
         each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int c) {
             if (row < a.dk && c < a.dv) grad_initial[sbase + (long long)row * a.dv + c] = st[i][ct][r];
         });
+}
+
+template <class TY, int KS, int NCT>
+__global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space w,
+                                                                 const typename TY::S* __restrict__ go,
+                                                                 const float* grad_final,
+                                                                 typename TY::S* __restrict__ gv,
+                                                                 float* grad_initial) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    reverse_task<TY, KS, NCT, sets_of(TY::NP, KS)>(blockIdx.x, lds, a, w, go, grad_final, gv, grad_initial);
+}
+
+// Both chains of the gradients in one launch: neither reads what the other writes, and
+// with one of each on a CU two waves share a SIMD, each running where the other waits.
+// The longer one's workgroups come first, so that a CU gets one of each.  Half of the
+// registers have to do for that.  Narrow tiles of 16-bit types fit: 324 narrow
+// tiles of 9 sequences of up to 1000 tokens take 50 us instead of 28 + 51.  Wide ones and
+// those of fp32 with dim_k over 64 do not: 282 us instead of 102 + 134 (256 wide tiles of
+// 2048 tokens, bf16), 117 instead of 78 (1024 narrow tiles of 256 tokens, fp32).
+template <class TY, int KS>
+constexpr bool kJoined = TY::NP < 3 || KS == 2;
+
+template <class TY, int KS>
+__global__ __launch_bounds__(kThreads, 2) void delta_chains_kernel(
+    Shape a, Space w, unsigned each, const typename TY::S* __restrict__ v, const float* initial,
+    const typename TY::S* __restrict__ go, const float* grad_final, typename TY::S* __restrict__ gv,
+    float* grad_initial) {
+    extern __shared__ __align__(16) unsigned char lds[];
+    if (blockIdx.x < each)
+        reverse_task<TY, KS, 1, 1>(blockIdx.x, lds, a, w, go, grad_final, gv, grad_initial);
+    else
+        chain_task<TY, KS, 1, true, 1>(blockIdx.x - each, lds, a, w, v, initial, nullptr, nullptr);
 }
 
 // ====================================================== all chunks: the gradients
@@ -1817,7 +1862,7 @@ int check_shape(const delta_rule_shape_t* p, bool step, Shape* a) {
         if (!step && (st > INT_MAX || (kC * st + DELTA_MAX_DIM_V) * size_of(p->type) > INT_MAX))
             return CFC_ERR_UNSUPPORTED;
     const long long tiles = (p->dim_v + 31) / 32 * 2;
-    if (a->slots > kMaxBlocks || (long long)n_seq * p->heads_v > kMaxBlocks / tiles) return CFC_ERR_UNSUPPORTED;
+    if (a->slots > kMaxBlocks || (long long)n_seq * p->heads_v > kMaxBlocks / 2 / tiles) return CFC_ERR_UNSUPPORTED;
     return CFC_OK;
 }
 // Four elements of a row are one aligned load.
@@ -1869,11 +1914,16 @@ long long lay_out(const Shape& a, int type, bool grad, void* base, Space* w) {
 
 inline int launch_status() { return hipGetLastError() == hipSuccess ? CFC_OK : CFC_ERR_HIP; }
 
-// Columns of a chain's workgroup.  Its products are the same whatever the tile,
-// so a wide one only saves loads; narrow ones make more workgroups.
-inline int chain_tiles(const Shape& a) {
-    const long long wide = (long long)a.n_seq * a.hv * ((a.dv + 31) / 32);
-    return wide >= 256 && a.dv > 16 ? 2 : 1;
+// Sixteens of columns of a chain's workgroup.  Its products are the same whatever the
+// tile, so a wide one only saves loads; narrow ones make more workgroups, as long as
+// there is a CU for each.  1024 tokens, dims of 128, 288 | 496 narrow tiles or half as many
+// wide ones: forward in bf16 90 | 92 us narrow, 81 | 82 wide, in fp32 122 | 143 and
+// 102 | 122; gradients in fp32 338 | 466 and 309 | 405.  The joined chains, two
+// workgroups to a CU, stay narrow for longer: gradients in bf16 for 288 | 384 | 496 tiles
+// 202 | 230 | 282 us narrow, 228 | 242 | 275 wide.
+inline int chain_tiles(const Shape& a, bool joined) {
+    const long long narrow = (long long)a.n_seq * a.hv * ((a.dv + 15) / 16);
+    return narrow > (joined ? 384 : 256) && a.dv > 16 ? 2 : 1;
 }
 
 // Eight elements of a 16-bit row are one aligned load.
@@ -1895,7 +1945,8 @@ template <class TY, int KS, int NCT, bool GRAD>
 void launch_chain(const Shape& a, const Space& w, const void* v, const float* initial, void* o, float* final_state,
                   hipStream_t stream) {
     using S = typename TY::S;
-    const long long count = (long long)a.n_seq * a.hv * (((GRAD ? w.dvp : a.dv) + 16 * NCT - 1) / (16 * NCT));
+    const int dv = GRAD ? w.dvp : a.dv;
+    const long long count = (long long)a.n_seq * a.hv * ((dv + 16 * NCT - 1) / (16 * NCT));
     hipLaunchKernelGGL((delta_chain_kernel<TY, KS, NCT, GRAD>), dim3(dealt(count)), dim3(kThreads), 0, stream, a, w,
                        (const S*)v, initial, (S*)o, final_state);
 }
@@ -1904,7 +1955,7 @@ template <class TY, int KS>
 int run_forward(const Shape& a, const Space& w, const void* q, const void* k, const void* v, const float* g,
                 const float* beta, const float* initial, void* o, float* final_state, hipStream_t stream) {
     launch_prep<TY, KS, false>(a, w, q, k, g, beta, stream);
-    if (chain_tiles(a) == 2)
+    if (chain_tiles(a, false) == 2)
         launch_chain<TY, KS, 2, false>(a, w, v, initial, o, final_state, stream);
     else
         launch_chain<TY, KS, 1, false>(a, w, v, initial, o, final_state, stream);
@@ -1916,20 +1967,32 @@ int run_backward(const Shape& a, const Space& w, const void* q, const void* k, c
                  const float* beta, const float* initial, const void* go, const float* grad_final, void* gq, void* gk,
                  void* gv, float* gg, float* gbeta, float* grad_initial, hipStream_t stream) {
     using S = typename TY::S;
-    constexpr size_t lds = sizeof(ReverseLds<TY::NP, NCT, KS>);
+    constexpr bool joined = NCT == 1 && kJoined<TY, KS>;
+    constexpr size_t lds_back = sizeof(ReverseLds<TY::NP, NCT, KS>);
+    constexpr size_t lds = joined ? std::max(lds_back, sizeof(ChainLds<TY::NP, NCT, KS, true>)) : lds_back;
     // idempotent, and 160 KB is what a gfx950 workgroup can have
     auto allow = [](const void* kernel, size_t bytes) {
         return bytes <= 64 * 1024 || hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
                                                          (int)bytes) == hipSuccess;
     };
-    if (!allow(reinterpret_cast<const void*>(&delta_reverse_kernel<TY, KS, NCT>), lds) ||
+    const void* chains;
+    if constexpr (joined)
+        chains = reinterpret_cast<const void*>(&delta_chains_kernel<TY, KS>);
+    else
+        chains = reinterpret_cast<const void*>(&delta_reverse_kernel<TY, KS, NCT>);
+    if (!allow(chains, lds) ||
         !allow(reinterpret_cast<const void*>(&delta_grads_kernel<TY, KS>), sizeof(GradsLds<KS>)))
         return CFC_ERR_HIP;
     launch_prep<TY, KS, true>(a, w, q, k, g, beta, stream);
-    if (a.slots) launch_chain<TY, KS, NCT, true>(a, w, v, initial, nullptr, nullptr, stream);
-    const long long count = (long long)a.n_seq * a.hv * (w.dvp / (16 * NCT));
-    hipLaunchKernelGGL((delta_reverse_kernel<TY, KS, NCT>), dim3(dealt(count)), dim3(kThreads), lds, stream, a, w,
-                       (const S*)go, grad_final, (S*)gv, grad_initial);
+    const unsigned each = dealt((long long)a.n_seq * a.hv * (w.dvp / (16 * NCT)));
+    if constexpr (joined) {
+        hipLaunchKernelGGL((delta_chains_kernel<TY, KS>), dim3(2 * each), dim3(kThreads), lds, stream, a, w, each,
+                           (const S*)v, initial, (const S*)go, grad_final, (S*)gv, grad_initial);
+    } else {
+        launch_chain<TY, KS, NCT, true>(a, w, v, initial, nullptr, nullptr, stream);
+        hipLaunchKernelGGL((delta_reverse_kernel<TY, KS, NCT>), dim3(each), dim3(kThreads), lds, stream, a, w,
+                           (const S*)go, grad_final, (S*)gv, grad_initial);
+    }
     if (a.slots)
         hipLaunchKernelGGL((delta_grads_kernel<TY, KS>), dim3((unsigned)a.slots, a.hk), dim3(kGradThreads),
                            sizeof(GradsLds<KS>), stream, a,
@@ -2064,15 +2127,15 @@ extern "C" int delta_rule_backward(const delta_rule_shape_t* shape, const void* 
                          offsets_range(a), same(gin, gfin) ? Range{0, 0} : gfin};
     if (!outputs_disjoint(outs, 7, ins, 9)) return CFC_ERR_OVERLAP;
     set_vec(shape, &a, q, k, v, grad_o);
-    const bool wide = chain_tiles(a) == 2;
     auto go = [&](auto type) {
         using TY = decltype(type);
         auto run = [&](auto f) {
             return f(a, w, q, k, v, g, beta, initial_state, grad_o, grad_final_state, grad_q, grad_k, grad_v, grad_g,
                      grad_beta, grad_initial_state, stream);
         };
-        if (a.dk <= 64) return wide ? run(run_backward<TY, 2, 2>) : run(run_backward<TY, 2, 1>);
-        return wide ? run(run_backward<TY, 4, 2>) : run(run_backward<TY, 4, 1>);
+        if (a.dk <= 64)
+            return chain_tiles(a, kJoined<TY, 2>) == 2 ? run(run_backward<TY, 2, 2>) : run(run_backward<TY, 2, 1>);
+        return chain_tiles(a, kJoined<TY, 4>) == 2 ? run(run_backward<TY, 4, 2>) : run(run_backward<TY, 4, 1>);
     };
     switch (shape->type) {
         case CFC_TYPE_F32: return go(F32{});
