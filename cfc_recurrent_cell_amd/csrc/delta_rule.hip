@@ -40,6 +40,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "delta_rule.h"
 
@@ -145,37 +146,17 @@ struct Parts {
     }
 };
 
-// Eight elements, row[c0 .. c0+3] and row[c1 .. c1+3], zero from D on and where !ok.
+// Column c of the row at byte `row`, zero from D on and where !ok.
 template <class TY>
-__device__ __forceinline__ void load8(const typename TY::S* row, int c0, int c1, int D, bool ok, bool vec,
-                                      float (&x)[8]) {
-    if (vec) {  // 4 elements are one aligned load
-        if constexpr (sizeof(typename TY::S) == 4) {
-            f32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-            if (ok && c0 < D) a = *reinterpret_cast<const f32x4*>(row + c0);
-            if (ok && c1 < D) b = *reinterpret_cast<const f32x4*>(row + c1);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = a[j], x[j + 4] = b[j];
-        } else {
-            u32x2 a = {0, 0}, b = {0, 0};
-            if (ok && c0 < D) a = *reinterpret_cast<const u32x2*>(row + c0);
-            if (ok && c1 < D) b = *reinterpret_cast<const u32x2*>(row + c1);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t two = j < 4 ? a[j >> 1] : b[(j >> 1) & 1];
-                x[j] = TY::load(__builtin_bit_cast(typename TY::S, (uint16_t)(j & 1 ? two >> 16 : two & 0xffff)));
-            }
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = j < 4 ? c0 + j : c1 + j - 4;
-            x[j] = ok && c < D ? TY::load(row[c]) : 0.0f;
-        }
-    }
+__device__ __forceinline__ float load1(Buffer b, uint32_t row, int c, int D, bool ok) {
+    using S = typename TY::S;
+    const uint32_t at = ok && c < D ? row + c * (uint32_t)sizeof(S) : kNowhere;
+    if constexpr (sizeof(S) == 4)
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0));
+    else
+        return TY::load(__builtin_bit_cast(S, __builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0)));
 }
-
-// The same from a buffer: columns c ... c + 7 of the row at byte `row`.
+// Columns c ... c + 7 of the row at byte `row`, zero from D on and where !ok.
 template <class TY>
 __device__ __forceinline__ void load8(Buffer b, uint32_t row, int c, int D, bool ok, bool vec, float (&x)[8]) {
     constexpr int Z = sizeof(typename TY::S);
@@ -197,13 +178,7 @@ __device__ __forceinline__ void load8(Buffer b, uint32_t row, int c, int D, bool
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t at = ok && c + j < D ? row + (c + j) * Z : kNowhere;
-            if constexpr (Z == 4)
-                x[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0));
-            else
-                x[j] = TY::load(__builtin_bit_cast(typename TY::S, __builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0)));
-        }
+        for (int j = 0; j < 8; ++j) x[j] = load1<TY>(b, row, c + j, D, ok);
     }
 }
 
@@ -297,6 +272,19 @@ __device__ __forceinline__ long long on_die(long long block, long long count) {
     return (block % 8) * each + block / 8;
 }
 inline unsigned dealt(long long count) { return (unsigned)((count + 7) / 8 * 8); }
+
+// Sums over lanes that stay on the vector units.
+template <int N>
+__device__ __forceinline__ float from_lane_behind(float x) {  // N lanes on, within the 16 of a group
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + N, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float over_eights(float x) {  // over lanes l, l + 8, ... l + 56 (mod 64)
+    x += from_lane_behind<8>(x);
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
 
 __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
@@ -659,17 +647,16 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
 // in 32 bits.  What all waves need of each other (parts of S, of the bracket
 // before T, of U) goes through LDS in operand order, three exchanges a chunk.
 //
-// With one wave a SIMD nothing hides a latency but the wave itself.  So a chunk's
-// operands have two register sets, and each operand is loaded again as soon as
-// its last product has read it, two chunks ahead: a miss to HBM is shorter than
-// that.  All loads and stores are unconditional (bounds are the buffer
-// descriptors'), so that the compiler's counts of what is in flight stay exact and
-// no load waits for a store.  Operands of many parts (fp16 and float32 at 128 keys)
-// leave room for one set only, loaded one chunk ahead.  LDS reads are issued together behind each barrier,
-// and the products that the chain does not wait for (Q S, and M U with the stores
-// of o, one chunk later) run in their latency.
-constexpr int sets_of(int np, int ks) { return np * ks >= 8 ? 1 : 2; }
-
+// With one wave a SIMD nothing hides a latency but the wave itself.  So each of a
+// chunk's operands is loaded again, for the next chunk, as soon as its last product has
+// read it.  (Two register sets, loaded two chunks ahead, gave nothing with bf16: 16
+// prompts of fp16 with dim_k 64 81.5 us with two, 76.6 with one, 8192 tokens of bf16 317
+// with either; in fp32 with 128 keys they do not fit: 413 instead of 333 us for 4096 tokens
+// of 32 heads.)  All loads and stores are unconditional (bounds are the buffer
+// descriptors'), so that the compiler's counts of what is in flight stay exact and no
+// load waits for a store.  LDS reads are issued together behind each barrier, and the
+// products that the chain does not wait for (Q S, and M U with the stores of o, one
+// chunk later) run in their latency.
 template <int N, int NCT, int KSN>
 struct Exchange {  // [part][ks][column tile][lane]
     u32x4 v[N][KSN][NCT][64];
@@ -815,12 +802,12 @@ __device__ __forceinline__ void keep_rows(float* to, long long vs, int dvp, int 
 
 template <int NP, int NCT, int KS, bool GRAD>
 struct ChainLds {
-    Exchange<3, NCT, KS> s;
-    Exchange<3, NCT, 2> p, e;
-    Exchange<GRAD || NP < 3 ? (GRAD ? 1 : 2) : 3, GRAD ? 1 : NCT, 2> u;
+    Exchange<3, NCT, KS> s;     // S
+    Exchange<3, NCT, 2> p, e;   // the bracket before T; e U
+    Exchange<GRAD ? 1 : NP == 3 ? 3 : 2, GRAD ? 1 : NCT, 2> u;  // unused for the gradients
 };
 
-template <class TY, int KS, int NCT, bool GRAD, int SETS>
+template <class TY, int KS, int NCT, bool GRAD>
 __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shape& a, const Space& w,
                                            const typename TY::S* __restrict__ v, const float* initial,
                                            typename TY::S* __restrict__ o, float* final_state) {
@@ -896,7 +883,7 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
             for (int ct = 0; ct < NCT; ++ct) ot.store(to, ct, qs[ct]);
         }
     };
-    auto step = [&](Set& x, Set& before, int c) {
+    auto step = [&](Set& x, int c) {
         const long long vs = vslot(c);
         __syncthreads();
         u32x4 b[KS][NCT][3], bu[2][NCT][GRAD ? 1 : NM];
@@ -913,7 +900,7 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) mma<3>(x.kf[ks], b[ks][ct], kx[ct]);
-        load_rows<KS, NP>(w.kf, kslot(c + SETS), wv, lane, x.kf);
+        load_rows<KS, NP>(w.kf, kslot(c + 1), wv, lane, x.kf);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             f32x4 y;
@@ -923,10 +910,10 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
             split4<3>(y, p);
             xp.put(wv, ct, lane, p);
         }
-        load_v(x, c + SETS);
+        load_v(x, c + 1);
         if constexpr (!GRAD) {
-            finish_o(before, bu, c - 1);
-            load_triangle<NM, false>(w.m, vslot(c + SETS - 1), wv, lane, before.m);
+            finish_o(x, bu, c - 1);
+            load_triangle<NM, false>(w.m, vs, wv, lane, x.m);
         }
         __syncthreads();
         u32x4 bp[2][NCT][3];
@@ -939,7 +926,7 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) mma<ORDO>(x.qf[ks], b[ks][ct], qs[ct]);
             }
-            load_rows<KS, NP>(w.qf, kslot(c + SETS), wv, lane, x.qf);
+            load_rows<KS, NP>(w.qf, kslot(c + 1), wv, lane, x.qf);
         }
         f32x4 u[NCT];
 #pragma unroll
@@ -951,7 +938,7 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) mma<3>(x.t[1], bp[1][ct], u[ct]);
         }
-        load_triangle<3, false>(w.t, vslot(c + SETS), wv, lane, x.t);
+        load_triangle<3, false>(w.t, vslot(c + 1), wv, lane, x.t);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             u32x2 p[3];
@@ -974,44 +961,32 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
         for (int i = 0; i < NR; ++i)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) st[i][ct] *= x.g.last;
-        x.g.load(w.gates, vslot(c + SETS), wv, lane);
+        x.g.load(w.gates, vslot(c + 1), wv, lane);
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                 for (int i = 0; i < NR; ++i) mma<3>(x.kt[i][ts], be[ts][ct], st[i][ct]);
-        load_columns<KS, NP>(w.kt, kslot(c + SETS), wv, lane, x.kt);
+        load_columns<KS, NP>(w.kt, kslot(c + 1), wv, lane, x.kt);
         put_state();
     };
     if (chunks > 0) {
-        Set x[SETS];
-#pragma unroll
-        for (int i = 0; i < SETS; ++i) {
-            load_rows<KS, NP>(w.kf, kslot(i), wv, lane, x[i].kf);
-            load_v(x[i], i);
-            if constexpr (!GRAD) load_rows<KS, NP>(w.qf, kslot(i), wv, lane, x[i].qf);
-            load_triangle<3, false>(w.t, vslot(i), wv, lane, x[i].t);
-            x[i].g.load(w.gates, vslot(i), wv, lane);
-            load_columns<KS, NP>(w.kt, kslot(i), wv, lane, x[i].kt);
-            if constexpr (!GRAD) load_triangle<NM, false>(w.m, vslot(0), wv, lane, x[i].m);
-        }
+        Set x;
+        load_rows<KS, NP>(w.kf, kslot(0), wv, lane, x.kf);
+        load_v(x, 0);
+        if constexpr (!GRAD) load_rows<KS, NP>(w.qf, kslot(0), wv, lane, x.qf);
+        load_triangle<3, false>(w.t, vslot(0), wv, lane, x.t);
+        x.g.load(w.gates, vslot(0), wv, lane);
+        load_columns<KS, NP>(w.kt, kslot(0), wv, lane, x.kt);
+        if constexpr (!GRAD) load_triangle<NM, false>(w.m, vslot(0), wv, lane, x.m);
         put_state();
-        int c = 0;
-        for (; c + SETS <= chunks; c += SETS) {
-            step(x[0], x[SETS - 1], c);
-            if constexpr (SETS == 2) step(x[1], x[0], c + 1);
-        }
-        const bool odd = SETS == 1 || c < chunks;  // the last chunk's set is x[0]
-        if (c < chunks) step(x[0], x[SETS - 1], c);
+        for (int c = 0; c < chunks; ++c) step(x, c);
         if constexpr (!GRAD) {
             __syncthreads();
             u32x4 bu[2][NCT][NM];
             xu.get(lane, bu);
-            if (odd)
-                finish_o(x[0], bu, chunks - 1);
-            else
-                finish_o(x[SETS - 1], bu, chunks - 1);
+            finish_o(x, bu, chunks - 1);
         }
     }
     if (final_state)
@@ -1020,21 +995,21 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
         });
 }
 
-// ========================================= along a sequence: the gradients' chain
-// With dS the gradient of the chunk's last state, dO that of O and R = (I + L)^-1,
-//   dU  = M^T dO + diag(e) K dS           dR = R^T dU   (of beta times the bracket)
-//   dV  = diag(beta) dR
-//   dS0 = gamma_63 dS + scale Q^T diag(gamma) dO - K^T diag(gamma beta) dR
-// The same tiles, exchanges and register sets as the states' chain, from the last
-// chunk on.
 template <class TY, int KS, int NCT, bool GRAD>
 __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w, const typename TY::S* __restrict__ v,
                                                                const float* initial, typename TY::S* __restrict__ o,
                                                                float* final_state) {
     __shared__ __align__(16) ChainLds<TY::NP, NCT, KS, GRAD> sm;
-    chain_task<TY, KS, NCT, GRAD, sets_of(TY::NP, KS)>(blockIdx.x, &sm, a, w, v, initial, o, final_state);
+    chain_task<TY, KS, NCT, GRAD>(blockIdx.x, &sm, a, w, v, initial, o, final_state);
 }
 
+// ========================================= along a sequence: the gradients' chain
+// With dS the gradient of the chunk's last state, dO that of O and R = (I + L)^-1,
+//   dU  = M^T dO + diag(e) K dS           dR = R^T dU   (of beta times the bracket)
+//   dV  = diag(beta) dR
+//   dS0 = gamma_63 dS + scale Q^T diag(gamma) dO - K^T diag(gamma beta) dR
+// The same tiles and exchanges as the states' chain, from the last
+// chunk on.
 template <int NP, int NCT, int KS>
 struct ReverseLds {
     Exchange<3, NCT, KS> s;
@@ -1042,7 +1017,7 @@ struct ReverseLds {
     Exchange<3, NCT, 2> g, u, r;  // scale gamma dO; dU; -gamma beta dR
 };
 
-template <class TY, int KS, int NCT, int SETS>
+template <class TY, int KS, int NCT>
 __device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Shape& a, const Space& w,
                                              const typename TY::S* __restrict__ go, const float* grad_final,
                                              typename TY::S* __restrict__ gv, float* grad_initial) {
@@ -1109,7 +1084,7 @@ __device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Sh
             xg.put(wv, ct, lane, p3);
         }
     };
-    auto step = [&](Set& x, Set& next, int c) {
+    auto step = [&](Set& x, int c) {
         const long long vs = vslot(c);
         __syncthreads();
         u32x4 b[KS][NCT][3], bo[2][NCT][NP];
@@ -1124,7 +1099,7 @@ __device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Sh
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) mma<3>(x.kf[ks], b[ks][ct], y[ct]);
-        load_rows<KS, NP>(w.kf, kslot(c - SETS), wv, lane, x.kf);
+        load_rows<KS, NP>(w.kf, kslot(c - 1), wv, lane, x.kf);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             y[ct] *= x.g.e;
@@ -1134,14 +1109,14 @@ __device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Sh
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) mma<3>(x.mt[0], bo[0][ct], y[ct]);
         }
-        load_triangle<3, true>(w.mt, vslot(c - SETS), wv, lane, x.mt);
+        load_triangle<3, true>(w.mt, vslot(c - 1), wv, lane, x.mt);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             u32x2 p[3];
             split4<3>(y[ct], p);
             xu.put(wv, ct, lane, p);
         }
-        load_o(x, c - SETS);
+        load_o(x, c - 1);
         __syncthreads();
         u32x4 bu[2][NCT][3], bg[2][NCT][3];
         xu.get(lane, bu);
@@ -1156,7 +1131,7 @@ __device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Sh
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) mma<3>(x.tt[0], bu[0][ct], y[ct]);
         }
-        load_triangle<3, true>(w.tt, vslot(c - SETS), wv, lane, x.tt);
+        load_triangle<3, true>(w.tt, vslot(c - 1), wv, lane, x.tt);
         const auto to = gvt.rows(gv0 + (long long)c * kC * a.hv * a.dv, (long long)a.hv * a.dv, len - c * kC, a.dv);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
@@ -1171,14 +1146,14 @@ __device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Sh
         for (int i = 0; i < NR; ++i)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) st[i][ct] *= x.g.last;
-        x.g.load(w.gates, vslot(c - SETS), wv, lane);
+        x.g.load(w.gates, vslot(c - 1), wv, lane);
 #pragma unroll
         for (int ts = 0; ts < 2; ++ts)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                 for (int i = 0; i < NR; ++i) mma<3>(x.qt[i][ts], bg[ts][ct], st[i][ct]);
-        load_columns<KS, NP>(w.qt, kslot(c - SETS), wv, lane, x.qt);
+        load_columns<KS, NP>(w.qt, kslot(c - 1), wv, lane, x.qt);
         __syncthreads();
         u32x4 br[2][NCT][3];
         xr.get(lane, br);
@@ -1189,29 +1164,21 @@ __device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Sh
             for (int ct = 0; ct < NCT; ++ct)
 #pragma unroll
                 for (int i = 0; i < NR; ++i) mma<3>(x.kt[i][ts], br[ts][ct], st[i][ct]);
-        load_columns<KS, NP>(w.kt, kslot(c - SETS), wv, lane, x.kt);
-        put_first(next);
+        load_columns<KS, NP>(w.kt, kslot(c - 1), wv, lane, x.kt);
+        put_first(x);
     };
     if (chunks > 0) {
-        Set x[SETS];
-#pragma unroll
-        for (int i = 0; i < SETS; ++i) {
-            const int c = chunks - 1 - i;
-            load_o(x[i], c);
-            x[i].g.load(w.gates, vslot(c), wv, lane);
-            load_rows<KS, NP>(w.kf, kslot(c), wv, lane, x[i].kf);
-            load_triangle<3, true>(w.mt, vslot(c), wv, lane, x[i].mt);
-            load_triangle<3, true>(w.tt, vslot(c), wv, lane, x[i].tt);
-            load_columns<KS, NP>(w.qt, kslot(c), wv, lane, x[i].qt);
-            load_columns<KS, NP>(w.kt, kslot(c), wv, lane, x[i].kt);
-        }
-        put_first(x[0]);
-        int c = chunks - 1;
-        for (; c + 1 >= SETS; c -= SETS) {
-            step(x[0], x[SETS - 1], c);
-            if constexpr (SETS == 2) step(x[1], x[0], c - 1);
-        }
-        if (c == 0) step(x[0], x[SETS - 1], 0);
+        Set x;
+        const int last = chunks - 1;
+        load_o(x, last);
+        x.g.load(w.gates, vslot(last), wv, lane);
+        load_rows<KS, NP>(w.kf, kslot(last), wv, lane, x.kf);
+        load_triangle<3, true>(w.mt, vslot(last), wv, lane, x.mt);
+        load_triangle<3, true>(w.tt, vslot(last), wv, lane, x.tt);
+        load_columns<KS, NP>(w.qt, kslot(last), wv, lane, x.qt);
+        load_columns<KS, NP>(w.kt, kslot(last), wv, lane, x.kt);
+        put_first(x);
+        for (int c = last; c >= 0; --c) step(x, c);
     }
     if (grad_initial)
         each_of_state<NR, NCT>(wv, lane, n0, [&](int i, int ct, int r, int row, int c) {
@@ -1226,7 +1193,7 @@ __global__ __launch_bounds__(kThreads) void delta_reverse_kernel(Shape a, Space 
                                                                  typename TY::S* __restrict__ gv,
                                                                  float* grad_initial) {
     extern __shared__ __align__(16) unsigned char lds[];
-    reverse_task<TY, KS, NCT, sets_of(TY::NP, KS)>(blockIdx.x, lds, a, w, go, grad_final, gv, grad_initial);
+    reverse_task<TY, KS, NCT>(blockIdx.x, lds, a, w, go, grad_final, gv, grad_initial);
 }
 
 // Both chains of the gradients in one launch: neither reads what the other writes, and
@@ -1246,9 +1213,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chains_kernel(
     float* grad_initial) {
     extern __shared__ __align__(16) unsigned char lds[];
     if (blockIdx.x < each)
-        reverse_task<TY, KS, 1, 1>(blockIdx.x, lds, a, w, go, grad_final, gv, grad_initial);
+        reverse_task<TY, KS, 1>(blockIdx.x, lds, a, w, go, grad_final, gv, grad_initial);
     else
-        chain_task<TY, KS, 1, true, 1>(blockIdx.x - each, lds, a, w, v, initial, nullptr, nullptr);
+        chain_task<TY, KS, 1, true>(blockIdx.x - each, lds, a, w, v, initial, nullptr, nullptr);
 }
 
 // ====================================================== all chunks: the gradients
@@ -1270,10 +1237,6 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chains_kernel(
 // and dS (with U) are split into parts once for the workgroup and shared through
 // LDS, the next slice's loads in flight under the products.  q and k in result
 // order are products with the identity.
-template <int N>
-__device__ __forceinline__ float from_lane_behind(float x) {  // N lanes on, within the 16 of a group
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x120 + N, 0xf, 0xf, true));
-}
 __device__ __forceinline__ float over_columns(float x) {  // over the 16 lanes of a group
     x += from_lane_behind<8>(x);
     x += from_lane_behind<4>(x);
@@ -1631,11 +1594,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 // states of other layers having passed between; the same 134 MB again and again, which
 // stay cached: 54 without, 60 with.  So from 192 MB on.
 constexpr long long kPastCache = 192LL << 20;
-template <class TY, int NR, bool PAST>
-__global__ __launch_bounds__(kThreads) void delta_token_kernel(
+template <class TY, int NR, bool STEP, bool PAST>
+__global__ __launch_bounds__(kThreads, STEP && NR == 16 ? 3 : 1) void delta_token_kernel(
     Shape a, const typename TY::S* __restrict__ q, const typename TY::S* __restrict__ k,
     const typename TY::S* __restrict__ v, const float* __restrict__ g, const float* __restrict__ beta,
-    const float* in, float* out, typename TY::S* __restrict__ o, int step, const int* __restrict__ slots, int pool,
+    const float* in, float* out, typename TY::S* __restrict__ o, const int* __restrict__ slots, int pool,
     bool vec) {
     using S = typename TY::S;
     const int tiles = (a.dv + 31) / 32;
@@ -1650,7 +1613,7 @@ __global__ __launch_bounds__(kThreads) void delta_token_kernel(
     const int h = (int)(sh % a.hv), hk = h / (a.hv / a.hk), r0 = NR * rg;
     int b = (int)(sh / a.hv), tok, end;
     long long state = b;
-    if (step) {
+    if constexpr (STEP) {
         tok = b;
         end = b + 1;
         if (slots) {
@@ -1666,7 +1629,8 @@ __global__ __launch_bounds__(kThreads) void delta_token_kernel(
     } else {
         int len;
         span_of(a, b, tok, len);
-        end = tok + len;
+        tok = __builtin_amdgcn_readfirstlane(tok);
+        end = tok + __builtin_amdgcn_readfirstlane(len);
     }
     const long long sbase = (state * a.hv + h) * a.dk * a.dv + c0;
     f32x4 s[NR];
@@ -1687,76 +1651,91 @@ __global__ __launch_bounds__(kThreads) void delta_token_kernel(
             }
         }
     }
-    if (step && slots)  // rows of one slot: the first of them takes all
+    if (STEP && slots)  // rows of one slot: the first of them takes all
         for (int j0 = 0; j0 < b; j0 += 64)
             if (__ballot(j0 + lane < b && slots[j0 + lane] == (int)state)) return;
-    while (tok < end) {
-        const S* qr = q + (long long)tok * a.qt + hk * a.qh + r0;
-        const S* kr = k + (long long)tok * a.kt + hk * a.kh + r0;
-        const S* vr = v + (long long)tok * a.vt + h * a.vh + c0;
-        const long long gi = (long long)tok * a.hv + h;
-        float kx[NR], qx[NR];
-        f32x4 x = {0, 0, 0, 0};
-        const float al = expf(g[gi]), be = beta[gi];
+    struct Row {
+        float k[NR], q[NR], g, beta;
+        f32x4 v;
+    };
+    // Without branches between the loads, so that all are in flight at once.
+    auto fetch_as = [&](int t, Row& x, bool four) {
+        constexpr int Z = sizeof(S);
+        const Buffer kb = buffer_of(k + (long long)t * a.kt + hk * a.kh, a.dk * Z);
+        const Buffer qb = buffer_of(q + (long long)t * a.qt + hk * a.qh, a.dk * Z);
+        const Buffer vb = buffer_of(v + (long long)t * a.vt + h * a.vh, a.dv * Z);
+        x.g = g[(long long)t * a.hv + h], x.beta = beta[(long long)t * a.hv + h];
         if constexpr (NR >= 8) {
 #pragma unroll
             for (int i = 0; i < NR; i += 8) {
-                float e[8];
-                load8<TY>(kr, i, i + 4, a.dk - r0, true, a.kvec, e);
+                float e[8], f[8];
+                load8<TY>(kb, 0, r0 + i, a.dk, true, four, e);
+                load8<TY>(qb, 0, r0 + i, a.dk, true, four, f);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) kx[i + j] = e[j];
-                load8<TY>(qr, i, i + 4, a.dk - r0, true, a.qvec, e);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) qx[i + j] = e[j];
+                for (int j = 0; j < 8; ++j) x.k[i + j] = e[j], x.q[i + j] = f[j];
             }
         } else {
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                kx[i] = r0 + i < a.dk ? TY::load(kr[i]) : 0.0f;
-                qx[i] = r0 + i < a.dk ? TY::load(qr[i]) : 0.0f;
+                x.k[i] = load1<TY>(kb, 0, r0 + i, a.dk, true);
+                x.q[i] = load1<TY>(qb, 0, r0 + i, a.dk, true);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c0 + j < a.dv) x[j] = TY::load(vr[j]);
+        for (int j = 0; j < 4; ++j) x.v[j] = load1<TY>(vb, 0, c0 + j, a.dv, true);
+    };
+    auto fetch = [&](int t, Row& x) {
+        if (a.kvec && a.qvec)
+            fetch_as(t, x, true);
+        else
+            fetch_as(t, x, false);
+    };
+    Row x;
+    if (tok < end) fetch(tok, x);
+    while (tok < end) {
+        int next = tok + 1;
+        if constexpr (STEP) {
+            if (slots) {  // the next row of the same slot
+                end = next;
+                for (int j0 = next; j0 < a.n_seq; j0 += 64) {
+                    const unsigned long long m = __ballot(j0 + lane < a.n_seq && slots[j0 + lane] == (int)state);
+                    if (m) {
+                        next = j0 + __builtin_ctzll(m);
+                        end = next + 1;
+                        break;
+                    }
+                }
+            }
+        }
+        Row then = x;
+        if (!STEP && next < end) fetch(next, then);  // in flight while this token is worked on
+        const float al = expf(x.g);
         f32x4 pk = {0, 0, 0, 0}, pq = {0, 0, 0, 0};
         float kq = 0.0f;
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             s[i] *= al;
-            pk += s[i] * kx[i];
-            pq += s[i] * qx[i];
-            kq += kx[i] * qx[i];
+            pk += s[i] * x.k[i];
+            pq += s[i] * x.q[i];
+            kq += x.k[i] * x.q[i];
         }
 #pragma unroll
-        for (int off = 8; off < 64; off <<= 1) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                pk[j] += __shfl_xor(pk[j], off);
-                pq[j] += __shfl_xor(pq[j], off);
-            }
-            kq += __shfl_xor(kq, off);
-        }
-        const f32x4 u = (x - pk) * be;
+        for (int j = 0; j < 4; ++j) pk[j] = over_eights(pk[j]), pq[j] = over_eights(pq[j]);
+        kq = over_eights(kq);
+        const f32x4 u = (x.v - pk) * x.beta;
         const f32x4 y = (pq + u * kq) * a.scale;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) s[i] += u * kx[i];
+        for (int i = 0; i < NR; ++i) s[i] += u * x.k[i];
         if (rg == 0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (c0 + j < a.dv) o[gi * a.dv + c0 + j] = TY::store(y[j]);
+                if (c0 + j < a.dv) o[((long long)tok * a.hv + h) * a.dv + c0 + j] = TY::store(y[j]);
         }
-        ++tok;
-        if (step && slots) {  // the next row of the same slot
-            end = tok;
-            for (int j0 = tok; j0 < a.n_seq; j0 += 64) {
-                const unsigned long long m = __ballot(j0 + lane < a.n_seq && slots[j0 + lane] == (int)state);
-                if (m) {
-                    tok = j0 + __builtin_ctzll(m);
-                    end = tok + 1;
-                    break;
-                }
-            }
+        tok = next;
+        if constexpr (STEP) {
+            if (tok < end) fetch(tok, x);
+        } else {
+            x = then;
         }
     }
     if (!out) return;
@@ -1819,7 +1798,7 @@ inline bool extent(long long tokens, int heads, int dim, long long st, long long
     return mul_ok(x + y + dim, size, r);
 }
 
-constexpr long long kMaxBlocks = (1LL << 32) / kThreads - 8;  // a grid has fewer than 2^32 work-items
+constexpr long long kMaxBlocks = (1LL << 32) / kGradThreads - 8;  // a grid has fewer than 2^32 work-items
 
 // Chunks that sequences of at most so many tokens are run without.
 constexpr int kShort = 16;
@@ -2000,26 +1979,33 @@ int run_backward(const Shape& a, const Space& w, const void* q, const void* k, c
     return launch_status();
 }
 
-template <class TY>
+template <class TY, bool STEP>
 int run_tokens(const Shape& a, const void* q, const void* k, const void* v, const float* g, const float* beta,
-               const float* in, float* out, void* o, int step, const int* slots, int pool, hipStream_t stream) {
+               const float* in, float* out, void* o, const int* slots, int pool, hipStream_t stream) {
     using S = typename TY::S;
     const long long count = (long long)a.n_seq * a.hv * ((a.dv + 31) / 32);
     const bool vec = a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(in) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(out) % 16 == 0;
     auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(dealt((count + 3) / 4)), dim3(kThreads), 0, stream, a, (const S*)q,
-                           (const S*)k, (const S*)v, g, beta, in, out, (S*)o, step, slots, pool, vec);
+                           (const S*)k, (const S*)v, g, beta, in, out, (S*)o, slots, pool, vec);
     };
     const bool past = (long long)a.n_seq * a.hv * a.dk * a.dv * 4 >= kPastCache;
+    auto rows = [&](auto n) {
+        constexpr int NR = decltype(n)::value;
+        if constexpr (STEP) {
+            if (past) return go(delta_token_kernel<TY, NR, true, true>);
+        }
+        go(delta_token_kernel<TY, NR, STEP, false>);
+    };
     if (a.dk <= 16)
-        past ? go(delta_token_kernel<TY, 2, true>) : go(delta_token_kernel<TY, 2, false>);
+        rows(std::integral_constant<int, 2>{});
     else if (a.dk <= 32)
-        past ? go(delta_token_kernel<TY, 4, true>) : go(delta_token_kernel<TY, 4, false>);
+        rows(std::integral_constant<int, 4>{});
     else if (a.dk <= 64)
-        past ? go(delta_token_kernel<TY, 8, true>) : go(delta_token_kernel<TY, 8, false>);
+        rows(std::integral_constant<int, 8>{});
     else
-        past ? go(delta_token_kernel<TY, 16, true>) : go(delta_token_kernel<TY, 16, false>);
+        rows(std::integral_constant<int, 16>{});
     return launch_status();
 }
 
@@ -2083,9 +2069,9 @@ extern "C" int delta_rule_forward(const delta_rule_shape_t* shape, const void* q
     set_vec(shape, &a, q, k, v, nullptr);
     if (brief) {
         switch (shape->type) {
-            case CFC_TYPE_F32: return run_tokens<F32>(a, q, k, v, g, beta, initial_state, final_state, o, 0, nullptr, 0, stream);
-            case CFC_TYPE_BF16: return run_tokens<BF16>(a, q, k, v, g, beta, initial_state, final_state, o, 0, nullptr, 0, stream);
-            default: return run_tokens<F16>(a, q, k, v, g, beta, initial_state, final_state, o, 0, nullptr, 0, stream);
+            case CFC_TYPE_F32: return run_tokens<F32, false>(a, q, k, v, g, beta, initial_state, final_state, o, nullptr, 0, stream);
+            case CFC_TYPE_BF16: return run_tokens<BF16, false>(a, q, k, v, g, beta, initial_state, final_state, o, nullptr, 0, stream);
+            default: return run_tokens<F16, false>(a, q, k, v, g, beta, initial_state, final_state, o, nullptr, 0, stream);
         }
     }
     auto go = [&](auto type) {
@@ -2162,8 +2148,8 @@ extern "C" int delta_rule_step(const delta_rule_shape_t* shape, const void* q, c
     if (!outputs_disjoint(outs, 2, ins, 6)) return CFC_ERR_OVERLAP;
     set_vec(shape, &a, q, k, v, nullptr);
     switch (shape->type) {
-        case CFC_TYPE_F32: return run_tokens<F32>(a, q, k, v, g, beta, states, states, o, 1, slots, pool, stream);
-        case CFC_TYPE_BF16: return run_tokens<BF16>(a, q, k, v, g, beta, states, states, o, 1, slots, pool, stream);
-        default: return run_tokens<F16>(a, q, k, v, g, beta, states, states, o, 1, slots, pool, stream);
+        case CFC_TYPE_F32: return run_tokens<F32, true>(a, q, k, v, g, beta, states, states, o, slots, pool, stream);
+        case CFC_TYPE_BF16: return run_tokens<BF16, true>(a, q, k, v, g, beta, states, states, o, slots, pool, stream);
+        default: return run_tokens<F16, true>(a, q, k, v, g, beta, states, states, o, slots, pool, stream);
     }
 }

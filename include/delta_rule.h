@@ -53,14 +53,14 @@ extern "C" {
  *   q, k [n_tokens, heads_k, dim_k], v [n_tokens, heads_v, dim_v]: row r, head h
  * at r * stride_t + h * stride_h elements (strides >= 0, so a slice of a fused
  * projection or a broadcast head can be read where it lies), the last axis
- * dense; 64 rows are less than 2^31 bytes (sequences' calls).  g, beta [n_tokens, heads_v] float32, dense: the decay's logarithm
- * (-inf: forget all) and the gate.  States [n_seq, heads_v, dim_k, dim_v]
- * float32, dense. */
+ * dense; 64 rows are less than 2^31 bytes (sequences' calls).  g, beta
+ * [n_tokens, heads_v] float32, dense: the decay's logarithm (-inf: forget all)
+ * and the gate.  States [n_seq, heads_v, dim_k, dim_v] float32, dense. */
 typedef struct delta_rule_shape {
     int type;             /* CFC_TYPE_* of q, k, v, o, grad_o, grad_q, grad_k, grad_v */
     int n_seq;            /* >= 0 */
     int seq_len;          /* read where offsets is NULL */
-    long long n_tokens;   /* < 2^31 */
+    long long n_tokens;   /* < 2^31; for the sequences' calls at most 2^23 groups of 64 */
     const int *offsets;
     int heads_k, heads_v; /* heads_v a multiple of heads_k */
     int dim_k, dim_v;     /* 1 ... DELTA_MAX_DIM_K, 1 ... DELTA_MAX_DIM_V */
@@ -80,7 +80,8 @@ long long delta_rule_backward_workspace(const delta_rule_shape_t *shape);
  * unspecified; it must not overlap any other argument, and calls that may run
  * at the same time need one each.
  * A value that is not finite in q, k, v, g or beta makes the outputs of its own
- * sequence undefined from the beginning of its group of 64 tokens on. */
+ * sequence undefined from the beginning of its group of 64 tokens on, and all
+ * gradients of that sequence. */
 int delta_rule_forward(const delta_rule_shape_t *shape, const void *q, const void *k, const void *v,
                        const float *g, const float *beta, const float *initial_state, void *o,
                        float *final_state, void *workspace, long long workspace_bytes,
