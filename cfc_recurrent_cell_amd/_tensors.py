@@ -74,5 +74,7 @@ def on_device(device, stream):
     is allocated inside belongs to that stream, so memory freed while its kernels
     still run is not handed to another one."""
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)  # makes the stream's device current
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)

@@ -1800,9 +1800,6 @@ inline bool extent(long long tokens, int heads, int dim, long long st, long long
 
 constexpr long long kMaxBlocks = (1LL << 32) / kGradThreads - 8;  // a grid has fewer than 2^32 work-items
 
-// Chunks that sequences of at most so many tokens are run without.
-constexpr int kShort = 16;
-
 int check_shape(const delta_rule_shape_t* p, bool step, Shape* a) {
     if (!p) return CFC_ERR_NULL;
     const int n_seq = step ? (int)std::min(p->n_tokens, (long long)INT_MAX) : p->n_seq;
@@ -1858,7 +1855,15 @@ inline void set_vec(const delta_rule_shape_t* p, Shape* a, const void* q, const 
     a->gvec = go && fours(go, a->gt, a->gh, a->dv, z);
 }
 
-inline bool is_short(const Shape& a) { return (a.offsets ? a.n_tokens : a.seq_len) <= kShort; }
+// Sequences so short that they are run token by token: 10 us and 1.2 a token for up to
+// 256 heads' states (8 tokens 18.4 us, 32 47), while the chunks' two kernels take 18.5
+// for 32 heads, 31 for 128, 44 for 256, 79 for 512, whatever the length up to 64 (32
+// heads x 1, 4, 8 and 16 sequences, dims of 128, bf16): they are even at 8, 17, 28 and 40
+// tokens, and at 36 to 40 for more sequences.
+inline bool is_short(const Shape& a) {
+    const long long most = 8 + std::min((long long)a.n_seq * a.hv / 16, 24LL);
+    return (a.offsets ? a.n_tokens : a.seq_len) <= most;
+}
 
 // The workspace's arrays, one behind the other; returns its bytes.
 long long lay_out(const Shape& a, int type, bool grad, void* base, Space* w) {

@@ -146,3 +146,29 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         C.delta_rule_backward(q, q, q, g, g, q, offsets=torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError, match="batch, heads, dim"):
         C.delta_rule_step(q, q, q, g, g, torch.zeros(1, 2, 8, 8))
+
+
+def test_more_chunks_than_a_launch_has(lib):
+    """The gradients' last kernel has 512 threads a chunk, and a launch fewer than 2^32."""
+    for n, ok in ((1 << 28, True), ((1 << 29) - 64 * 8, True), (1 << 29, False), (3 << 28, False)):
+        s = shape(n_seq=1, seq_len=n, hk=1, hv=1, dk=1, dv=1)
+        for size in (lib.delta_rule_forward_workspace, lib.delta_rule_backward_workspace):
+            assert (size(ctypes.byref(s)) > 0) == ok, n
+        if not ok:
+            assert fwd(lib, s) == C.CFC_ERR_UNSUPPORTED and bwd(lib, s) == C.CFC_ERR_UNSUPPORTED
+
+
+def test_a_stream_of_another_device_is_refused():
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+
+    from cfc_recurrent_cell_amd._tensors import on_device
+    with pytest.raises(ValueError, match="cuda:1"):
+        on_device(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+@pytest.mark.parametrize("seqs,heads,longest", [(1, 1, 8), (1, 32, 10), (4, 32, 16), (16, 32, 32), (64, 64, 32)])
+def test_short_sequences_need_no_workspace(lib, seqs, heads, longest):
+    need = [lib.delta_rule_forward_workspace(ctypes.byref(shape(n_seq=seqs, seq_len=n, hk=1, hv=heads)))
+            for n in (longest, longest + 1)]
+    assert need[0] == 0 < need[1]

@@ -149,6 +149,16 @@ def test_lengths_dense(length, state):
     c.check_backward(c.backward())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("length", [8, 9, 31, 32, 33])
+def test_token_by_token_up_to_32_with_many_heads(kind, length):
+    """With 384 heads' states the token kernel takes 32 tokens and the chunks 33; of one head 8 and 9."""
+    for batch, hv, dims in ((8, 48, (16, 8)), (1, 1, (100, 36)), (96, 4, (30, 5))):
+        say(f"[delta] short {kind} {length} x {batch} x {hv}")
+        c = Case(14 + length, kind, batch=batch, length=length, hk=hv // 2 or 1, hv=hv, dk=dims[0], dv=dims[1])
+        c.check_forward(*c.forward())
+
+
 @pytest.mark.parametrize("kind,dk,dv", [("bf16", 64, 64), ("fp16", 40, 24), ("fp32", 128, 36), ("bf16", 33, 7)])
 def test_slices_of_one_projection(kind, dk, dv):
     """q, k and v as slices (strided, at odd sizes not aligned) give the bits that contiguous ones give."""
