@@ -6,7 +6,10 @@
 // written from the registers.  TPR threads have a row: 16 lanes up to 128
 // columns (four rows a wave), a wave up to 512, several waves beyond, which join
 // their sums through LDS.  Workgroups stride over the rows with the weight in
-// registers.
+// registers.  In bf16, where a large copy reaches 4.7 TB/s: 16384 x 4096 with a residual,
+// 537 MB, in 113 us, 4.8 TB/s; its backward (with grad_h, 537 MB) in 107 us, 5.0 TB/s;
+// the backward of 99991 x 128 (77 MB) in 19.5 us, 3.9 TB/s; 32 rows of 4096 to e4m3 in
+// 5 us on the GPU, a launch's time.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -96,9 +99,10 @@ __device__ __forceinline__ float over_row(float x, F join, float (*red)[16], int
     if constexpr (TPR > 64) {
         if ((threadIdx.x & 63) == 0) red[turn][threadIdx.x >> 6] = x;
         __syncthreads();
-        x = red[turn][0];
+        const int first = threadIdx.x / TPR * (TPR / 64);
+        x = red[turn][first];
 #pragma unroll
-        for (int i = 1; i < TPR / 64; ++i) x = join(x, red[turn][i]);
+        for (int i = 1; i < TPR / 64; ++i) x = join(x, red[turn][first + i]);
     }
     return x;
 }
@@ -317,20 +321,24 @@ int check_sizes(int type, int stream_type, long long rows, long long width) {
     return CFC_OK;
 }
 
-// Threads and 8-column vectors of a row: the rule on the width alone.  The backward,
-// which keeps three rows' values and the weight gradient in registers, has more
-// threads and one vector each: 16384 x 4096 with 256 x 2 162 us, with 512 x 1 109 us.
-// The forward is at the rate of a copy with either.
-template <bool BACK, class F>
+// Threads and 8-column vectors of a row: the rule on the width alone, as few threads as
+// hold the row with one vector each.  More leave lanes idle (forward | backward in us,
+// bf16): 300000 x 128 with 16 lanes a row 27 | 44, with 64 62 | 98; 100000 x 512 with 64
+// 34 | 63, with 256 76 | 173; 65536 x 1024 with 128 47 | 85, with 256 60 | 226.  Fewer, with
+// two vectors, leave less in flight: 16384 x 4096 with 512 threads 45 | 86, with 256
+// 48 | 137.  Beyond 8192 columns a workgroup has no more threads.
+template <class F>
 int with_tiling(long long width, F f) {
-    if (width <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-    if (width <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-    if (width <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-    if (width <= 4096) return f(std::integral_constant<int, BACK ? 512 : 256>{}, std::integral_constant<int, BACK ? 1 : 2>{});
-    if (width <= 8192) return f(std::integral_constant<int, BACK ? 1024 : 512>{}, std::integral_constant<int, BACK ? 1 : 2>{});
+    const std::integral_constant<int, 1> one;
+    if (width <= 128) return f(std::integral_constant<int, 16>{}, one);
+    if (width <= 512) return f(std::integral_constant<int, 64>{}, one);
+    if (width <= 1024) return f(std::integral_constant<int, 128>{}, one);
+    if (width <= 2048) return f(std::integral_constant<int, 256>{}, one);
+    if (width <= 4096) return f(std::integral_constant<int, 512>{}, one);
+    if (width <= 8192) return f(std::integral_constant<int, 1024>{}, one);
     return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
 }
-inline long long rows_at_once(long long width) { return width <= 128 ? 16 : width <= 512 ? 4 : 1; }
+inline long long rows_at_once(long long width) { return width <= 128 ? 16 : width <= 512 ? 4 : width <= 1024 ? 2 : 1; }
 
 template <class F>
 int with_types(int type, int stream_type, F f) {
@@ -365,7 +373,7 @@ int run_forward(int type, int stream_type, long long rows, long long width, cons
     if (!outputs_disjoint(outs, 4, ins, 3)) return CFC_ERR_OVERLAP;
     const bool vec = width % 8 == 0 && aligned({x, residual, weight, y, h});
     return with_types(type, stream_type, [&](auto tx, auto th) {
-        return with_tiling<false>(width, [&](auto tpr, auto nv) {
+        return with_tiling(width, [&](auto tpr, auto nv) {
             using TX = decltype(tx);
             using TH = decltype(th);
             constexpr int T = decltype(tpr)::value, V = decltype(nv)::value;
@@ -383,8 +391,9 @@ int run_forward(int type, int stream_type, long long rows, long long width, cons
 inline long long parts_of(long long rows, long long width) {
     const long long need = (rows + rows_at_once(width) - 1) / rows_at_once(width);
     // narrow rows' partial sums are small, and more workgroups hide more of the loads:
-    // 99991 x 128 with 512 21.6 us, with 1024 20.0; 16384 x 4096 with 1024 121 us for 109
-    return std::min(need, width <= 512 ? 1024LL : 512LL);
+    // 99991 x 128 with 512 21.6 us, with 1024 20.0; 32768 x 2048 133 and 85, with 2048 99;
+    // 16384 x 4096 with 1024 121 us for 109
+    return std::min(need, width <= 2048 ? 1024LL : 512LL);
 }
 
 }  // namespace
@@ -428,7 +437,7 @@ extern "C" int rms_norm_backward(int type, int stream_type, long long rows, long
     const bool vec = width % 8 == 0 && aligned({grad_y, h, weight, grad_h, grad_x});
     float* part = static_cast<float*>(workspace);
     const int e = with_types(type, stream_type, [&](auto tx, auto th) {
-        return with_tiling<true>(width, [&](auto tpr, auto nv) {
+        return with_tiling(width, [&](auto tpr, auto nv) {
             using TX = decltype(tx);
             using TH = decltype(th);
             constexpr int T = decltype(tpr)::value, V = decltype(nv)::value;
