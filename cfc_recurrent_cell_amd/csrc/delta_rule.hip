@@ -290,7 +290,12 @@ __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane
 
 // =========================================================== all chunks: prep
 // grid: (slots, hv + hk).  The first hv make T and M of a value head, the others
-// the operands of a key head.
+// the operands of a key head.  M's triangle and the inverse's 16 x 16 blocks are worked
+// on by one wave each, the inverse on the 32-bit matrix cores: its products are 1/50 of
+// the chunk's and wait for each other, so parts would only make them longer.  Bound by
+// the chunk's chain of latencies (products, decays, inverse, each behind a barrier)
+// with 4 workgroups a CU: 128 chunks of 32 + 16 heads (bf16, dim_k 128) in 87 us; for the
+// gradients 128 of 16 + 8 in 52.
 //
 // A chunk's rows of a key head's tensor as operands, VEC: 4 elements at a time.
 template <class TY, bool VEC>
@@ -657,6 +662,14 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
 // load waits for a store.  LDS reads are issued together behind each barrier, and the
 // products that the chain does not wait for (Q S, and M U with the stores of o, one
 // chunk later) run in their latency.
+//
+// Bound by one wave's instructions: a chunk is 4300 cycles of matrix and vector
+// instructions that a SIMD's only wave issues one after the other.  1 x 8192 tokens, 32
+// heads, bf16, dims of 128: 256 workgroups, 128 chunks, 231 us, 1.8 us a chunk.  16
+// packed fp16 prompts (of 8 heads, dim_k 64) 56 us; the states' chain for the
+// gradients of 4 x 2048 (64 heads in all, wide tiles) 100 us.  Left alone: no LDS and a
+// wave for each tile (365 us instead of 237, each wave splits S by itself), scalar
+// cursors instead of multiplied slots (253 instead of 230).
 template <int N, int NCT, int KSN>
 struct Exchange {  // [part][ks][column tile][lane]
     u32x4 v[N][KSN][NCT][64];
@@ -1009,7 +1022,8 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w,
 //   dV  = diag(beta) dR
 //   dS0 = gamma_63 dS + scale Q^T diag(gamma) dO - K^T diag(gamma beta) dR
 // The same tiles and exchanges as the states' chain, from the last
-// chunk on.
+// chunk on, and bound alike: 4 x 2048 tokens of 16 heads each in 135 us, 4.2 us a chunk
+// of a wide tile with one more state-sized product than the states' chain.
 template <int NP, int NCT, int KS>
 struct ReverseLds {
     Exchange<3, NCT, KS> s;
@@ -1233,10 +1247,18 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chains_kernel(
 // up dQ and dK in registers.  Its 8 waves are 4 token tiles by 2 halves of dim_k;
 // the halves also share the triangles, the first has dM (and q.k), the second dL
 // (and k.k).  Wave w shares its SIMD with wave w + 4: that one has token tile 3 - w,
-// so that the triangles are even.  dim_v is summed in slices of 32: S0 (with dO and dR as left operands)
-// and dS (with U) are split into parts once for the workgroup and shared through
-// LDS, the next slice's loads in flight under the products.  q and k in result
+// so that the triangles are even.  dim_v is summed in slices of 32: S0 (with dO and dR as
+// left operands) and dS (with U) are split into parts once for the workgroup and shared
+// through LDS, the next slice's loads in flight under the products.  q and k in result
 // order are products with the identity.
+//
+// Bound by latency: 99 KB of LDS leave one workgroup (two waves a SIMD) a CU, and a
+// slice's loads, split, barrier and products follow each other.  4 x 2048 tokens, 8 key
+// and 16 value heads, bf16, dims of 128: 238 us, 75000 cycles for a chunk's value head,
+// of which 5000 to 10000 are each of the 4 slices; 0.54 GB of states
+// and rows, 2.3 TB/s.  Slices
+// in two LDS buffers, or v and dO loaded ahead too, need more registers than there are
+// (510 us).
 __device__ __forceinline__ float over_columns(float x) {  // over the 16 lanes of a group
     x += from_lane_behind<8>(x);
     x += from_lane_behind<4>(x);
@@ -1586,8 +1608,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 // in-lane and then over 8 lanes.  S'^T k and S'^T q are summed together, and
 // o = S'^T q + u (k.q), so a token is one pass over the state.
 //
-// As a decode step (`slots`, or all rows in order) and as the sequence form of
-// short sequences.
+// STEP: a decode step (`slots`, or all rows in order); otherwise the sequence form of
+// short sequences, the next token's rows in flight while one is worked on.  A step is
+// bound by reading and writing the states: 256 rows x 16 heads of 128 x 128 (537 MB) in 111
+// us, 4.8 TB/s, the rate of a large copy; 32 heads of one row in 7 us, latency.  It keeps
+// 3 waves a SIMD at 128 keys: with 2, where the compiler would leave it, 129 us.
 //
 // PAST: states beyond what the last-level cache holds pass it by (non-temporal loads
 // and stores).  256 rows x 16 heads, 268 MB each way: 145 us without, 122 with, the
@@ -2073,10 +2098,14 @@ extern "C" int delta_rule_forward(const delta_rule_shape_t* shape, const void* q
         (overlap(outs[0], ini) || overlap(outs[2], ini))) return CFC_ERR_OVERLAP;
     set_vec(shape, &a, q, k, v, nullptr);
     if (brief) {
+        auto tokens = [&](auto type) {
+            return run_tokens<decltype(type), false>(a, q, k, v, g, beta, initial_state, final_state, o, nullptr, 0,
+                                                     stream);
+        };
         switch (shape->type) {
-            case CFC_TYPE_F32: return run_tokens<F32, false>(a, q, k, v, g, beta, initial_state, final_state, o, nullptr, 0, stream);
-            case CFC_TYPE_BF16: return run_tokens<BF16, false>(a, q, k, v, g, beta, initial_state, final_state, o, nullptr, 0, stream);
-            default: return run_tokens<F16, false>(a, q, k, v, g, beta, initial_state, final_state, o, nullptr, 0, stream);
+            case CFC_TYPE_F32: return tokens(F32{});
+            case CFC_TYPE_BF16: return tokens(BF16{});
+            default: return tokens(F16{});
         }
     }
     auto go = [&](auto type) {
