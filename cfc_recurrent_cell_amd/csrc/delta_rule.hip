@@ -1255,10 +1255,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chains_kernel(
 // Bound by latency: 99 KB of LDS leave one workgroup (two waves a SIMD) a CU, and a
 // slice's loads, split, barrier and products follow each other.  4 x 2048 tokens, 8 key
 // and 16 value heads, bf16, dims of 128: 238 us, 75000 cycles for a chunk's value head,
-// of which 5000 to 10000 are each of the 4 slices; 0.54 GB of states
-// and rows, 2.3 TB/s.  Slices
-// in two LDS buffers, or v and dO loaded ahead too, need more registers than there are
-// (510 us).
+// of which 5000 to 10000 are each of the 4 slices; 0.54 GB of states and rows, 2.3 TB/s.
+// Slices in two LDS buffers, or v and dO loaded ahead too, need more registers than there
+// are (510 us).
 __device__ __forceinline__ float over_columns(float x) {  // over the 16 lanes of a group
     x += from_lane_behind<8>(x);
     x += from_lane_behind<4>(x);
