@@ -663,8 +663,9 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
 // products that the chain does not wait for (Q S, and M U with the stores of o, one
 // chunk later) run in their latency.
 //
-// Bound by one wave's instructions: a chunk is 4300 cycles of matrix and vector
-// instructions that a SIMD's only wave issues one after the other.  1 x 8192 tokens, 32
+// Bound by the way from one state to the next: a chunk is 4300 cycles of three
+// exchanges, each a split, an LDS write, a barrier, an LDS read and a product (four
+// more waves that make o beside it change nothing: 321 us instead of 319).  1 x 8192 tokens, 32
 // heads, bf16, dims of 128: 256 workgroups, 128 chunks, 231 us, 1.8 us a chunk.  16
 // packed fp16 prompts (of 8 heads, dim_k 64) 56 us; the states' chain for the
 // gradients of 4 x 2048 (64 heads in all, wide tiles) 100 us.  Left alone: no LDS and a
