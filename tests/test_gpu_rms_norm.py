@@ -60,7 +60,8 @@ def floor_of(t):
 
 
 SIZES = [(1, 1), (3, 7), (17, 16), (5, 127), (1000, 128), (33, 129), (9, 512), (7, 513), (20, 1000), (3, 2048),
-         (2, 2049), (5, 4096), (3, 4104), (2, 8192), (1, 8193), (2, 16384), (600, 33), (5000, 64)]
+         (2, 2049), (5, 4096), (3, 4104), (2, 8192), (1, 8193), (2, 16384), (600, 33), (5000, 64),
+         (9001, 600), (2100, 1500)]  # the last two: more rows than a launch has workgroups
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
