@@ -403,3 +403,45 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+def test_offsets_past_32_bits():
+    """Rows 16 MB apart (5 GB of them) and a pool of 9 GB give the bits that small ones give."""
+    import cfc_recurrent_cell_amd as C
+    n, step = 300, 1 << 23
+    c = Case(61, "bf16", batch=1, length=n, hk=1, hv=1, dk=128, dv=128)
+    wide = torch.empty(n, step, dtype=torch.bfloat16, device="cuda")
+    far = {}
+    for i, name in enumerate(("q", "k", "v", "go")):
+        far[name] = wide[:, 128 * i:128 * (i + 1)].view(1, n, 1, 128)
+        far[name].copy_(c.d[name])
+    want = (*c.forward(), *c.backward())
+    c.d.update(far)
+    for x, y in zip((*c.forward(), *c.backward()), want):
+        assert torch.equal(x, y)
+    del wide, far
+    c = Case(62, "bf16", batch=3, length=1, hk=1, hv=2, dk=128, dv=128)
+    args = [c.d[m][:, 0].contiguous() for m in ("q", "k", "v", "g", "beta")]
+    pool, slots = 70000, torch.tensor([69999, 4, 40000], dtype=torch.int32, device="cuda")
+    states = torch.empty(pool, 2, 128, 128, device="cuda")
+    few = c.d["s0"].clone()
+    states[slots.long()] = few
+    o = C.delta_rule_step(*args, states, slots)
+    assert torch.equal(o, C.delta_rule_step(*args, few))
+    assert torch.equal(states[slots.long()], few)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, a workspace each, while both run."""
+    a = Case(63, "bf16", batch=2, length=900, hk=2, hv=4, dk=128, dv=128)
+    b = Case(64, "bf16", lens=[700, 3, 250], hk=1, hv=2, dk=128, dv=64)
+    want = [(*c.forward(), *c.backward()) for c in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [None, None]
+        for i, c in enumerate((a, b)):
+            got[i] = (*c.forward(stream=streams[i]), *c.backward(stream=streams[i]))
+        torch.cuda.synchronize()
+        for x, y in zip(sum(got, ()), sum(want, ())):
+            assert torch.equal(x, y)

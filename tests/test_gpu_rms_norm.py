@@ -237,3 +237,24 @@ def test_equal_bits_side_stream_and_capture():
         got = [t.clone() for t in out]
         for a, b in zip(all_of(), got):
             assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    import cfc_recurrent_cell_amd as C
+    rows, width = 140000, 16384
+    x, w, _ = make(14, "bf16", 3, width, "none")
+    gy, _, gh = make(15, "bf16", 3, width, "same")
+    y, h, rstd = C.rms_norm_forward(x, w, EPS)
+    gx, gw = C.rms_norm_backward(gy, h, w, rstd)
+    many = torch.zeros(rows, width, dtype=x.dtype, device="cuda")
+    many[-3:] = x
+    y2, _, rstd2 = C.rms_norm_forward(many, w, EPS)
+    assert torch.equal(y2[-3:], y) and torch.equal(rstd2[-3:], rstd) and not y2[:-3].any()
+    y2.zero_()
+    y2[-3:] = gy
+    gx2, gw2 = C.rms_norm_backward(y2, many, w, rstd2)
+    assert torch.equal(gx2[-3:], gx) and not gx2[:-3].any()
+    near(gw2, gw.double(), 0.0, size=(gy.double() * h.double() * rstd.double()[:, None]).abs().sum(0))
+    q, s, _ = C.rms_norm_forward_e4m3(many, w, EPS, group=128)
+    q3, s3, _ = C.rms_norm_forward_e4m3(x, w, EPS, group=128)
+    assert torch.equal(q[-3:].view(torch.uint8), q3.view(torch.uint8)) and torch.equal(s[-3:], s3)
