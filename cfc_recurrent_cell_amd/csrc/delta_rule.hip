@@ -20,8 +20,9 @@
 // rounded, so the sum is exact), and a product takes the six pairs of parts that
 // reach above 2^-24.  bf16 inputs are one part, fp16 two, float32 three.  The
 // matrix cores' own 32-bit form has 1/16 of the rate of bf16, so even six
-// products of parts are 2.7 times faster.  Only M U, which is rounded to 16 bits
-// with o, takes two parts of each where o is bf16 or fp16.
+// products of parts are 2.7 times faster.  That holds for o of 16-bit types too: Q S0
+// and M U can be far larger than their sum (a key's old value is taken back), so two
+// parts of each are not enough for it.
 //
 // Kernels
 //   delta_prep_kernel      for all chunks at once: T, M (transposed for the
@@ -394,7 +395,6 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
                                                               const float* __restrict__ beta) {
     using S = typename TY::S;
     constexpr int NP = TY::NP;
-    constexpr int NM = GRAD || NP == 3 ? 3 : 2;  // parts of M
     const long long slot = blockIdx.x;
     const Chunk ch = chunk_of(a, slot);
     if (ch.n <= 0) return;
@@ -622,12 +622,11 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
 #pragma unroll
             for (int n = 0; n < 3; ++n) w.t[((vs * 8 + f) * 3 + n) * 64 + lane] = p[n];
             if (!GRAD) {
-                u32x4 pm[NM];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[j] = L[row][place_of(ts, grp, j)];
-                split8<NM>(x, pm);
+                split8<3>(x, p);
 #pragma unroll
-                for (int n = 0; n < NM; ++n) w.m[((vs * 8 + f) * NM + n) * 64 + lane] = pm[n];
+                for (int n = 0; n < 3; ++n) w.m[((vs * 8 + f) * 3 + n) * 64 + lane] = p[n];
             }
         }
         if (GRAD && ts >= (rt >> 1)) {
@@ -814,11 +813,11 @@ __device__ __forceinline__ void keep_rows(float* to, long long vs, int dvp, int 
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[r]), b, at, 4 * (r * dvp + n0), 0);
 }
 
-template <int NP, int NCT, int KS, bool GRAD>
+template <int NCT, int KS, bool GRAD>
 struct ChainLds {
     Exchange<3, NCT, KS> s;     // S
     Exchange<3, NCT, 2> p, e;   // the bracket before T; e U
-    Exchange<GRAD ? 1 : NP == 3 ? 3 : 2, GRAD ? 1 : NCT, 2> u;  // unused for the gradients
+    Exchange<GRAD ? 1 : 3, GRAD ? 1 : NCT, 2> u;  // U; unused for the gradients
 };
 
 template <class TY, int KS, int NCT, bool GRAD>
@@ -826,9 +825,8 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
                                            const typename TY::S* __restrict__ v, const float* initial,
                                            typename TY::S* __restrict__ o, float* final_state) {
     using S = typename TY::S;
-    constexpr int NP = TY::NP, NM = NP == 3 ? 3 : 2, NR = KS / 2;
-    constexpr int ORDO = NP == 3 ? 3 : 2;  // o is rounded to 16 bits or to 32
-    auto& sm = *static_cast<ChainLds<NP, NCT, KS, GRAD>*>(lds);
+    constexpr int NP = TY::NP, NR = KS / 2;
+    auto& sm = *static_cast<ChainLds<NCT, KS, GRAD>*>(lds);
     auto& xs = sm.s;
     auto &xp = sm.p, &xe = sm.e;
     auto& xu = sm.u;
@@ -855,7 +853,7 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
     });
 
     struct Set {
-        u32x4 kf[KS][NP], qf[GRAD ? 1 : KS][NP], kt[NR][2][NP], t[2][3], m[2][GRAD ? 1 : NM];
+        u32x4 kf[KS][NP], qf[GRAD ? 1 : KS][NP], kt[NR][2][NP], t[2][3], m[2][GRAD ? 1 : 3];
         S v[NCT][4];
         RowGates<false> g;
     };
@@ -883,15 +881,15 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
 #pragma unroll
     for (int ct = 0; ct < NCT; ++ct) qs[ct] = f32x4{0, 0, 0, 0};
     // o of chunk c: what Q S gave, and M U
-    auto finish_o = [&](const Set& x, const u32x4 (&b)[2][NCT][GRAD ? 1 : NM], int c) {
+    auto finish_o = [&](const Set& x, const u32x4 (&b)[2][NCT][GRAD ? 1 : 3], int c) {
         if constexpr (!GRAD) {
             const auto to = ot.rows(o0 + (long long)c * kC * a.hv * a.dv, (long long)a.hv * a.dv,
                                     c >= 0 ? len - c * kC : 0, a.dv);
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) mma<ORDO>(x.m[0], b[0][ct], qs[ct]);
+            for (int ct = 0; ct < NCT; ++ct) mma<3>(x.m[0], b[0][ct], qs[ct]);
             if (wv >= 2) {
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) mma<ORDO>(x.m[1], b[1][ct], qs[ct]);
+                for (int ct = 0; ct < NCT; ++ct) mma<3>(x.m[1], b[1][ct], qs[ct]);
             }
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) ot.store(to, ct, qs[ct]);
@@ -900,7 +898,7 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
     auto step = [&](Set& x, int c) {
         const long long vs = vslot(c);
         __syncthreads();
-        u32x4 b[KS][NCT][3], bu[2][NCT][GRAD ? 1 : NM];
+        u32x4 b[KS][NCT][3], bu[2][NCT][GRAD ? 1 : 3];
         xs.get(lane, b);
         if constexpr (!GRAD) xu.get(lane, bu);
         reads_first();
@@ -927,7 +925,7 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
         load_v(x, c + 1);
         if constexpr (!GRAD) {
             finish_o(x, bu, c - 1);
-            load_triangle<NM, false>(w.m, vs, wv, lane, x.m);
+            load_triangle<3, false>(w.m, vs, wv, lane, x.m);
         }
         __syncthreads();
         u32x4 bp[2][NCT][3];
@@ -938,7 +936,7 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
             for (int ct = 0; ct < NCT; ++ct) {
                 qs[ct] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) mma<ORDO>(x.qf[ks], b[ks][ct], qs[ct]);
+                for (int ks = 0; ks < KS; ++ks) mma<3>(x.qf[ks], b[ks][ct], qs[ct]);
             }
             load_rows<KS, NP>(w.qf, kslot(c + 1), wv, lane, x.qf);
         }
@@ -961,8 +959,8 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
             if constexpr (GRAD) {
                 keep_rows(w.u, vs, w.dvp, n0 + 16 * ct, wv, lane, u[ct]);
             } else {
-                u32x2 pu[NM];
-                split4<NM>(u[ct], pu);
+                u32x2 pu[3];
+                split4<3>(u[ct], pu);
                 xu.put(wv, ct, lane, pu);
                 qs[ct] = qs[ct] * x.g.gamma * a.scale;
             }
@@ -993,12 +991,12 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
         load_triangle<3, false>(w.t, vslot(0), wv, lane, x.t);
         x.g.load(w.gates, vslot(0), wv, lane);
         load_columns<KS, NP>(w.kt, kslot(0), wv, lane, x.kt);
-        if constexpr (!GRAD) load_triangle<NM, false>(w.m, vslot(0), wv, lane, x.m);
+        if constexpr (!GRAD) load_triangle<3, false>(w.m, vslot(0), wv, lane, x.m);
         put_state();
         for (int c = 0; c < chunks; ++c) step(x, c);
         if constexpr (!GRAD) {
             __syncthreads();
-            u32x4 bu[2][NCT][NM];
+            u32x4 bu[2][NCT][3];
             xu.get(lane, bu);
             finish_o(x, bu, chunks - 1);
         }
@@ -1009,11 +1007,13 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
         });
 }
 
+// With fp16 and dim_k <= 64 two workgroups share a CU where the compiler would take 6
+// registers too many for that: 16 packed prompts 85.5 us, with one 88.3.
 template <class TY, int KS, int NCT, bool GRAD>
-__global__ __launch_bounds__(kThreads) void delta_chain_kernel(Shape a, Space w, const typename TY::S* __restrict__ v,
+__global__ __launch_bounds__(kThreads, TY::NP == 2 && KS == 2 ? 2 : 1) void delta_chain_kernel(Shape a, Space w, const typename TY::S* __restrict__ v,
                                                                const float* initial, typename TY::S* __restrict__ o,
                                                                float* final_state) {
-    __shared__ __align__(16) ChainLds<TY::NP, NCT, KS, GRAD> sm;
+    __shared__ __align__(16) ChainLds<NCT, KS, GRAD> sm;
     chain_task<TY, KS, NCT, GRAD>(blockIdx.x, &sm, a, w, v, initial, o, final_state);
 }
 
@@ -1893,7 +1893,7 @@ inline bool is_short(const Shape& a) {
 // The workspace's arrays, one behind the other; returns its bytes.
 long long lay_out(const Shape& a, int type, bool grad, void* base, Space* w) {
     const int np = type == CFC_TYPE_BF16 ? 1 : type == CFC_TYPE_F16 ? 2 : 3;
-    const int ks = a.dk <= 64 ? 2 : 4, nm = grad || np == 3 ? 3 : 2;
+    const int ks = a.dk <= 64 ? 2 : 4;
     const long long kslots = a.slots * a.hk, vslots = a.slots * a.hv;
     char* at = static_cast<char*>(base);
     long long total = 0;
@@ -1910,7 +1910,7 @@ long long lay_out(const Shape& a, int type, bool grad, void* base, Space* w) {
     w->kt = (u32x4*)take(kb);
     w->qt = (u32x4*)take(grad ? kb : 0);
     w->t = (u32x4*)take(vslots * 8 * 3 * 1024);
-    w->m = (u32x4*)take(grad ? 0 : vslots * 8 * nm * 1024);
+    w->m = (u32x4*)take(grad ? 0 : vslots * 8 * 3 * 1024);
     w->tt = (u32x4*)take(grad ? vslots * 8 * 3 * 1024 : 0);
     w->mt = (u32x4*)take(grad ? vslots * 8 * 3 * 1024 : 0);
     w->gates = (Gates*)take(vslots * (long long)sizeof(Gates));
@@ -1978,7 +1978,7 @@ int run_backward(const Shape& a, const Space& w, const void* q, const void* k, c
     using S = typename TY::S;
     constexpr bool joined = NCT == 1 && kJoined<TY, KS>;
     constexpr size_t lds_back = sizeof(ReverseLds<TY::NP, NCT, KS>);
-    constexpr size_t lds = joined ? std::max(lds_back, sizeof(ChainLds<TY::NP, NCT, KS, true>)) : lds_back;
+    constexpr size_t lds = joined ? std::max(lds_back, sizeof(ChainLds<NCT, KS, true>)) : lds_back;
     // idempotent, and 160 KB is what a gfx950 workgroup can have
     auto allow = [](const void* kernel, size_t bytes) {
         return bytes <= 64 * 1024 || hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
