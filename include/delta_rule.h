@@ -81,7 +81,8 @@ long long delta_rule_backward_workspace(const delta_rule_shape_t *shape);
  * at the same time need one each.
  * A value that is not finite in q, k, v, g or beta makes the outputs of its own
  * sequence undefined from the beginning of its group of 64 tokens on, and all
- * gradients of that sequence. */
+ * gradients of that sequence; so does a 32-bit one that rounds to infinity in bf16
+ * (from 2^128 - 2^119 on). */
 int delta_rule_forward(const delta_rule_shape_t *shape, const void *q, const void *k, const void *v,
                        const float *g, const float *beta, const float *initial_state, void *o,
                        float *final_state, void *workspace, long long workspace_bytes,

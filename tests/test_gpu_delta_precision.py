@@ -49,3 +49,25 @@ def test_o_where_a_large_value_is_taken_back(gpu, kind, batch, heads, dk, dv):
     bound = ((2 * dk + 160) / 3) ** 0.5 * 2.0 ** -24 * size + 2 * 2.0 ** -22 * size + step
     err = rms(o.double() - v.double())
     assert err <= bound, f"{err:.3e} of {bound:.3e}"
+
+
+@pytest.mark.parametrize("batch,heads", [(1, 4), (4, 16)])
+def test_parts_leave_nothing_out_on_one_side(gpu, batch, heads):
+    """o = Q S0 of positive values (a gate of 0 adds nothing), 128 terms a sum, in fp32.  Parts
+    that were cut off would leave out 2^-8 2^-16 of each product twice, half of it on average
+    and always of one sign: -2^-24.  Rounded parts leave out as much of either sign, and the
+    sum's roundings are even, so the mean over more than 2^15 outputs is held to a
+    quarter of that; a single value to the roundings of 128 terms."""
+    say(f"[delta] parts {batch} {heads}")
+    gen = torch.Generator().manual_seed(72)
+    length, dim = 64, 128
+    q = torch.rand(batch, length, heads, dim, generator=gen) + 0.1
+    s0 = torch.rand(batch, heads, dim, dim, generator=gen) + 0.1
+    want = (q.double().transpose(1, 2).contiguous() @ s0.double()).transpose(1, 2)
+    g = torch.zeros(batch, length, heads, device="cuda")
+    o, final = gpu.delta_rule_forward(q.cuda(), q.cuda() / 16, torch.randn(q.shape, generator=gen).cuda(), g, g,
+                                      initial_state=s0.cuda(), scale=1.0)
+    off = o.double().cpu() / want - 1
+    assert abs(off.mean().item()) <= 2.0 ** -26, f"mean {off.mean().item():.3e}"
+    assert off.abs().max() <= 128 * 2.0 ** -24
+    assert torch.equal(final.cpu(), s0)
