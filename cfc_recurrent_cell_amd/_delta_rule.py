@@ -69,7 +69,8 @@ def _lead(q, offsets):
 
 def _size(need: int) -> int:
     if need < 0:
-        raise ValueError("a size is beyond what the library takes (dim_k <= 128, dim_v <= 256)")
+        raise ValueError("a size is beyond what the library takes (dim_k <= 128, dim_v <= 256, 64 tokens' rows of "
+                         "any argument less than 2^31 bytes from the first to the last, 2^23 groups of 64 tokens)")
     return need
 
 
@@ -92,7 +93,8 @@ def delta_rule_forward(q, k, v, g, beta, initial_state=None, scale: Optional[flo
 
     ``q``, ``k`` [B, T, heads_k, dim_k] and ``v`` [B, T, heads_v, dim_v] are
     float32, bfloat16 or float16, of any token and head strides with a dense
-    last axis (slices of one projection are read where they lie); ``g`` (the
+    last axis and, where B > 1, the sequences one behind the other (slices of one
+    projection are read where they lie); ``g`` (the
     decay's logarithm) and ``beta`` [B, T, heads_v] and the states
     [B, heads_v, dim_k, dim_v] are contiguous float32.  ``scale`` is
     dim_k ** -0.5 by default.  With ``offsets`` (int32 on the GPU, [S + 1]) the

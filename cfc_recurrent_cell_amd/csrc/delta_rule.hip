@@ -698,7 +698,8 @@ struct Tile {
     using S = typename TY::S;
     uint32_t at[NCT], step;  // of row r: at + r step
     __device__ __forceinline__ Tile(long long stride, int n0, int D, int wv, int lane) {
-        step = (uint32_t)(stride * sizeof(S));
+        // (only where a chunk has no second row is the stride larger: any then puts it behind the end)
+        step = (uint32_t)min(stride * (long long)sizeof(S), 1LL << 25);
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
             const int c = n0 + 16 * ct + (lane & 15);
@@ -1859,14 +1860,18 @@ int check_shape(const delta_rule_shape_t* p, bool step, Shape* a) {
     a->gt = p->go_stride_t, a->gh = p->go_stride_h;
     a->chunks = dense ? (int)(((long long)p->seq_len + kC - 1) / kC) : 0;
     a->slots = dense ? (long long)a->chunks * n_seq : p->n_tokens / kC + n_seq;
-    // a chunk's rows are addressed with 31 bits
-    for (long long st : {p->q_stride_t, p->k_stride_t, p->v_stride_t, p->go_stride_t, (long long)p->heads_k * p->dim_k,
-                         (long long)p->heads_v * p->dim_v})
-        if (!step && (st > INT_MAX || (kC * st + DELTA_MAX_DIM_V) * size_of(p->type) > INT_MAX))
-            return CFC_ERR_UNSUPPORTED;
     const long long tiles = (p->dim_v + 31) / 32 * 2;
     if (a->slots > kMaxBlocks || (long long)n_seq * p->heads_v > kMaxBlocks / 2 / tiles) return CFC_ERR_UNSUPPORTED;
     return CFC_OK;
+}
+// The chunks' kernels address a chunk's rows with 31 bits.  (Where a chunk has one row its
+// stride is not used, and the token kernel's rows have 64.)
+bool rows_fit(const delta_rule_shape_t* p) {
+    if ((p->offsets ? p->n_tokens : p->seq_len) <= 1) return true;
+    for (long long st : {p->q_stride_t, p->k_stride_t, p->v_stride_t, p->go_stride_t, (long long)p->heads_k * p->dim_k,
+                         (long long)p->heads_v * p->dim_v})
+        if (st > INT_MAX || (kC * st + DELTA_MAX_DIM_V) * size_of(p->type) > INT_MAX) return false;
+    return true;
 }
 // Four elements of a row are one aligned load.
 inline bool fours(const void* p, long long st, long long sh, int dim, int size) {
@@ -2064,13 +2069,14 @@ extern "C" long long delta_rule_forward_workspace(const delta_rule_shape_t* shap
     Shape a;
     Space w;
     if (check_shape(shape, false, &a) != CFC_OK) return -1;
-    return is_short(a) ? 0 : lay_out(a, shape->type, false, nullptr, &w);
+    if (is_short(a)) return 0;
+    return rows_fit(shape) ? lay_out(a, shape->type, false, nullptr, &w) : -1;
 }
 
 extern "C" long long delta_rule_backward_workspace(const delta_rule_shape_t* shape) {
     Shape a;
     Space w;
-    if (check_shape(shape, false, &a) != CFC_OK) return -1;
+    if (check_shape(shape, false, &a) != CFC_OK || !rows_fit(shape)) return -1;
     return lay_out(a, shape->type, true, nullptr, &w);
 }
 
@@ -2080,11 +2086,12 @@ extern "C" int delta_rule_forward(const delta_rule_shape_t* shape, const void* q
                                   hipStream_t stream) {
     Shape a;
     if (const int e = check_shape(shape, false, &a)) return e;
+    const bool brief = is_short(a);
+    if (!brief && !rows_fit(shape)) return CFC_ERR_UNSUPPORTED;
     Sizes z;
     if (!sizes_of(shape, a, &z)) return CFC_ERR_DIM;
     if (a.n_seq == 0) return CFC_OK;
     if (a.n_tokens && (!q || !k || !v || !g || !beta || !o)) return CFC_ERR_NULL;
-    const bool brief = is_short(a);
     Space w{};
     const long long need = brief ? 0 : lay_out(a, shape->type, false, workspace, &w);
     if (need) {
@@ -2129,6 +2136,7 @@ extern "C" int delta_rule_backward(const delta_rule_shape_t* shape, const void* 
                                    void* workspace, long long workspace_bytes, hipStream_t stream) {
     Shape a;
     if (const int e = check_shape(shape, false, &a)) return e;
+    if (!rows_fit(shape)) return CFC_ERR_UNSUPPORTED;
     Sizes z;
     if (!sizes_of(shape, a, &z)) return CFC_ERR_DIM;
     if (a.n_seq == 0) return CFC_OK;

@@ -53,7 +53,8 @@ extern "C" {
  *   q, k [n_tokens, heads_k, dim_k], v [n_tokens, heads_v, dim_v]: row r, head h
  * at r * stride_t + h * stride_h elements (strides >= 0, so a slice of a fused
  * projection or a broadcast head can be read where it lies), the last axis
- * dense; 64 rows are less than 2^31 bytes (sequences' calls).  g, beta
+ * dense; 64 rows are less than 2^31 bytes (except for a step, a forward of sequences
+ * so short that it takes no workspace, and sequences of one row).  g, beta
  * [n_tokens, heads_v] float32, dense: the decay's logarithm (-inf: forget all)
  * and the gate.  States [n_seq, heads_v, dim_k, dim_v] float32, dense. */
 typedef struct delta_rule_shape {

@@ -172,3 +172,27 @@ def test_short_sequences_need_no_workspace(lib, seqs, heads, longest):
     need = [lib.delta_rule_forward_workspace(ctypes.byref(shape(n_seq=seqs, seq_len=n, hk=1, hv=heads)))
             for n in (longest, longest + 1)]
     assert need[0] == 0 < need[1]
+
+
+def test_row_strides_count_only_where_chunks_have_rows(lib):
+    """One-token and few-token slices of a long tensor: rows 2^24 elements (of 64, 2^31 bytes) apart."""
+    def needs(**sizes):
+        s = shape(hk=16, hv=16, dk=128, dv=128, **{n: 1 << 24 for n in ("q_t", "k_t", "v_t", "go_t")}, **sizes)
+        return [f(ctypes.byref(s)) for f in (lib.delta_rule_forward_workspace, lib.delta_rule_backward_workspace)]
+
+    for seqs in (1, 3):
+        forward, backward = needs(n_seq=seqs, seq_len=1)
+        assert forward == 0 and backward > 0
+        assert needs(n_seq=seqs, seq_len=5) == [0, -1]
+        assert needs(n_seq=seqs, seq_len=100) == [-1, -1]
+    assert needs(n_seq=1, n_tokens=5, offsets=GRADS[0]) == [0, -1]
+    assert needs(n_seq=1, n_tokens=100, offsets=GRADS[0]) == [-1, -1]
+    s = shape(seq_len=5, k_t=1 << 62)
+    assert fwd(lib, s) == C.CFC_ERR_DIM      # the array's end is past 64 bits
+    assert bwd(lib, s) == C.CFC_ERR_UNSUPPORTED
+
+
+def test_the_stride_limit_is_named():
+    from cfc_recurrent_cell_amd._delta_rule import _size
+    with pytest.raises(ValueError, match="2\\^31 bytes"):
+        _size(-1)
