@@ -32,6 +32,11 @@ def _rows(t, name, lead, dtype, device, shape=None):
     return st[1], st[2]
 
 
+def _ints(*sizes):
+    if max(sizes) > 0x7fffffff:  # ctypes would pass their low 32 bits
+        raise ValueError(f"sizes {sizes} do not fit 32 bits")
+
+
 def _shape(q, k, v, g, beta, scale, offsets, lead, grad_o=None):
     kind, dtype, dev, n = element_type(q, "q"), q.dtype, q.device, q.shape
     qs = _rows(q, "q", lead, dtype, dev)
@@ -42,7 +47,9 @@ def _shape(q, k, v, g, beta, scale, offsets, lead, grad_o=None):
         raise ValueError(f"v has shape {tuple(nv)}, expected {tuple(n[:lead])} tokens as q has")
     gs = (0, 0) if grad_o is None else _rows(grad_o, "grad_o", lead, dtype, dev, nv)
     heads_k, dim_k, heads_v, dim_v = n[-2], n[-1], nv[-2], nv[-1]
-    if heads_k < 1 or heads_v % heads_k:
+    if dim_k < 1 or dim_v < 1:
+        raise ValueError(f"q and v have heads of {dim_k} and {dim_v} elements, expected at least 1")
+    if heads_k < 1 or heads_v < 1 or heads_v % heads_k:
         raise ValueError(f"v's {heads_v} heads are no multiple of q's {heads_k}")
     gates = nv[:-1]
     check(g, "g", F32, dev, gates)
@@ -55,6 +62,7 @@ def _shape(q, k, v, g, beta, scale, offsets, lead, grad_o=None):
         count, at = offsets.numel() - 1, offsets.data_ptr()
     elif lead == 2:
         count, length = n[0], n[1]
+    _ints(count, length, heads_v, dim_k, dim_v)
     return DeltaRuleShape(kind, count, length, tokens, at, heads_k, heads_v, dim_k, dim_v,
                           dim_k ** -0.5 if scale is None else scale, *qs, *ks, *vs, *gs)
 
@@ -175,6 +183,7 @@ def delta_rule_step(q, k, v, g, beta, states, slots=None, scale: Optional[float]
     if not isinstance(states, torch.Tensor) or states.dim() != 4:
         raise ValueError("states must be a tensor [pool, heads_v, dim_k, dim_v]")
     pool = states.shape[0]
+    _ints(pool)
     check(states, "states", F32, dev, (pool, s.heads_v, s.dim_k, s.dim_v))
     if slots is not None:
         check(slots, "slots", torch.int32, dev, (rows,))

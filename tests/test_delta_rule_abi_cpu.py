@@ -196,3 +196,10 @@ def test_the_stride_limit_is_named():
     from cfc_recurrent_cell_amd._delta_rule import _size
     with pytest.raises(ValueError, match="2\\^31 bytes"):
         _size(-1)
+
+
+def test_sizes_past_32_bits_are_refused():
+    from cfc_recurrent_cell_amd._delta_rule import _ints
+    _ints(0, 2 ** 31 - 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        _ints(4, 2 ** 32 + 4)

@@ -60,3 +60,18 @@ def test_one_token_of_a_long_tensor(gpu):
     c = t.clone(memory_format=torch.contiguous_format)
     for a, b in zip(got, (*gpu.delta_rule_forward(c, c, c, g, -g), *gpu.delta_rule_backward(c, c, c, g, -g, c)[:5])):
         assert torch.equal(a, b)
+
+
+def test_sizes_that_are_refused(gpu):
+    """Empty heads, and a pool of more states than 32 bits count (its low 32 bits would be five)."""
+    for dk, dv, heads in ((0, 8, 2), (8, 0, 2), (8, 8, 0)):
+        q, v = (torch.zeros(1, 3, h, d, device="cuda") for h, d in ((2, dk), (heads, dv)))
+        g = torch.zeros(1, 3, heads, device="cuda")
+        with pytest.raises(ValueError, match="elements|heads"):
+            gpu.delta_rule_forward(q, q, v, g, g)
+        with pytest.raises(ValueError, match="elements|heads"):
+            gpu.delta_rule_step(q[0], q[0], v[0], g[0], g[0], torch.zeros(3, heads, dk, dv, device="cuda"))
+    q, g = torch.zeros(5, 1, 1, device="cuda"), torch.zeros(5, 1, device="cuda")
+    many = torch.empty((1 << 32) + 5, 1, 1, 1, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        gpu.delta_rule_step(q, q, q, g, g, many)
