@@ -15,7 +15,7 @@
  * allocated, synchronised or copied to the host, kernels only enqueued on
  * `stream` (capturable), argument errors before anything is enqueued, no atomics
  * and fixed summation orders, 64-bit offsets.  Arithmetic and sums are those of
- * 32-bit floats; the weight gradient's last sum is reduce_axis0's.  The norm is
+ * 32-bit floats; the weight gradient's terms are summed in 64 bits.  The norm is
  * that of the rounded h, so that the backward, which reads the rounded h, is the
  * gradient of what the forward computed.
  */
