@@ -837,11 +837,11 @@ __device__ __forceinline__ void chain_task(unsigned block, void* lds, const Shap
     const int tiles = ((GRAD ? w.dvp : a.dv) + 16 * NCT - 1) / (16 * NCT);
     const long long count = (long long)a.n_seq * a.hv * tiles;
     const long long at = on_die(block, count);
-    if (at >= count || block / 8 >= (count + 7) / 8) return;
+    if (at >= count) return;
     const int n0 = (int)(at % tiles) * 16 * NCT;
     const long long sh = at / tiles;
     const int h = (int)(sh % a.hv), s = (int)(sh / a.hv), hk = h / (a.hv / a.hk);
-    const int lane = threadIdx.x & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
+    const int lane = threadIdx.x & 63, wv = wave_of();
     int tok0, len;
     span_of(a, s, tok0, len);
     tok0 = __builtin_amdgcn_readfirstlane(tok0);
@@ -1048,11 +1048,11 @@ __device__ __forceinline__ void reverse_task(unsigned block, void* lds, const Sh
     const int tiles = w.dvp / (16 * NCT);
     const long long count = (long long)a.n_seq * a.hv * tiles;
     const long long at = on_die(block, count);
-    if (at >= count || block / 8 >= (count + 7) / 8) return;
+    if (at >= count) return;
     const int n0 = (int)(at % tiles) * 16 * NCT;
     const long long sh = at / tiles;
     const int h = (int)(sh % a.hv), s = (int)(sh / a.hv), hk = h / (a.hv / a.hk);
-    const int lane = threadIdx.x & 63, wv = wave_of(), col = lane & 15, grp = lane >> 4;
+    const int lane = threadIdx.x & 63, wv = wave_of();
     int tok0, len;
     span_of(a, s, tok0, len);
     tok0 = __builtin_amdgcn_readfirstlane(tok0);
@@ -1632,7 +1632,6 @@ __global__ __launch_bounds__(kThreads, STEP && NR == 16 ? 3 : 1) void delta_toke
     const int tiles = (a.dv + 31) / 32;
     const long long count = (long long)a.n_seq * a.hv * tiles, blocks = (count + 3) / 4;
     const long long block = on_die(blockIdx.x, blocks);
-    if (blockIdx.x / 8 >= (blocks + 7) / 8) return;
     const long long at = block * 4 + wave_of();
     if (at >= count) return;
     const int lane = threadIdx.x & 63, rg = lane >> 3;
@@ -2103,8 +2102,6 @@ extern "C" int delta_rule_forward(const delta_rule_shape_t* shape, const void* q
     const Range ins[] = {bytes_of(q, z.q),        bytes_of(k, z.k), bytes_of(v, z.v), bytes_of(g, z.gates),
                          bytes_of(beta, z.gates), offsets_range(a), same(fin, ini) ? Range{0, 0} : ini};
     if (!outputs_disjoint(outs, 3, ins, 7)) return CFC_ERR_OVERLAP;
-    if (same(fin, ini) && initial_state &&
-        (overlap(outs[0], ini) || overlap(outs[2], ini))) return CFC_ERR_OVERLAP;
     set_vec(shape, &a, q, k, v, nullptr);
     if (brief) {
         auto tokens = [&](auto type) {
