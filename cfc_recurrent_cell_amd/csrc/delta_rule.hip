@@ -46,6 +46,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "elements.h"
 #include "delta_rule.h"
 
 namespace {
@@ -59,26 +60,6 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// ------------------------------------------------------------- element types
-struct F32 {
-    using S = float;
-    static constexpr int NP = 3;  // bf16 parts that hold a value exactly
-    static __device__ __forceinline__ float load(S x) { return x; }
-    static __device__ __forceinline__ S store(float x) { return x; }
-};
-struct BF16 {
-    using S = uint16_t;
-    static constexpr int NP = 1;
-    static __device__ __forceinline__ float load(S x) { return __uint_as_float((uint32_t)x << 16); }
-    static __device__ __forceinline__ S store(float x) { return __builtin_bit_cast(S, (__bf16)x); }
-};
-struct F16 {
-    using S = _Float16;
-    static constexpr int NP = 2;
-    static __device__ __forceinline__ float load(S x) { return (float)x; }
-    static __device__ __forceinline__ S store(float x) { return (_Float16)x; }
-};
 
 // ------------------------------------------------------------------ bf16 parts
 // Two floats rounded to bf16.
@@ -1788,31 +1769,12 @@ __global__ __launch_bounds__(kThreads, STEP && NR == 16 ? 3 : 1) void delta_toke
 }
 
 // ---------------------------------------------------------- host helpers
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-inline Range bytes_of(const void* p, long long n) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + (uintptr_t)(p ? n : 0)};
-}
-inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-inline bool same(Range a, Range b) { return a.lo == b.lo && a.hi == b.hi; }
-inline bool outputs_disjoint(const Range* outs, int n_out, const Range* ins, int n_in) {
-    for (int o = 0; o < n_out; ++o) {
-        for (int i = 0; i < n_in; ++i)
-            if (overlap(outs[o], ins[i])) return false;
-        for (int p = o + 1; p < n_out; ++p)
-            if (overlap(outs[o], outs[p])) return false;
-    }
-    return true;
-}
 inline bool mul_ok(long long a, long long b, long long* r) {
     if (a < 0 || b < 0) return false;
     if (a != 0 && b > (LLONG_MAX / 16) / a) return false;
     *r = a * b;
     return true;
 }
-inline int size_of(int type) { return type == CFC_TYPE_F32 ? 4 : 2; }
 
 // Bytes from the first to the last element of a strided [tokens, heads, dim] array.
 inline bool extent(long long tokens, int heads, int dim, long long st, long long sh, int size, long long* r) {
@@ -1926,8 +1888,6 @@ long long lay_out(const Shape& a, int type, bool grad, void* base, Space* w) {
     w->dr = (float*)take(grad ? rows : 0);
     return total;
 }
-
-inline int launch_status() { return hipGetLastError() == hipSuccess ? CFC_OK : CFC_ERR_HIP; }
 
 // Sixteens of columns of a chain's workgroup.  Its products are the same whatever the
 // tile, so a wide one only saves loads; narrow ones make more workgroups, as long as

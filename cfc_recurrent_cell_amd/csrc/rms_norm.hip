@@ -17,6 +17,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "elements.h"
 #include "rms_norm.h"
 
 namespace {
@@ -24,22 +25,6 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-struct F32 {
-    using S = float;
-    static __device__ __forceinline__ float load(S x) { return x; }
-    static __device__ __forceinline__ S store(float x) { return x; }
-};
-struct BF16 {
-    using S = uint16_t;
-    static __device__ __forceinline__ float load(S x) { return __uint_as_float((uint32_t)x << 16); }
-    static __device__ __forceinline__ S store(float x) { return __builtin_bit_cast(S, (__bf16)x); }
-};
-struct F16 {
-    using S = _Float16;
-    static __device__ __forceinline__ float load(S x) { return (float)x; }
-    static __device__ __forceinline__ S store(float x) { return (_Float16)x; }
-};
 
 // Columns c ... c + 7 of a row; zero from `width` on.
 template <class TY>
@@ -298,27 +283,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void rms_norm_backward_kernel(
 }
 
 // ---------------------------------------------------------- host helpers
-struct Range {
-    uintptr_t lo, hi;
-};
-inline Range bytes_of(const void* p, long long n) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Range{lo, lo + (uintptr_t)(p ? n : 0)};
-}
-inline bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-inline bool same(Range a, Range b) { return a.lo == b.lo && a.hi == b.hi; }
-inline bool outputs_disjoint(const Range* outs, int n_out, const Range* ins, int n_in) {
-    for (int o = 0; o < n_out; ++o) {
-        for (int i = 0; i < n_in; ++i)
-            if (overlap(outs[o], ins[i])) return false;
-        for (int p = o + 1; p < n_out; ++p)
-            if (overlap(outs[o], outs[p])) return false;
-    }
-    return true;
-}
-inline int size_of(int type) { return type == CFC_TYPE_F32 ? 4 : 2; }
 inline bool is_type(int t) { return t == CFC_TYPE_F32 || t == CFC_TYPE_BF16 || t == CFC_TYPE_F16; }
-inline int launch_status() { return hipGetLastError() == hipSuccess ? CFC_OK : CFC_ERR_HIP; }
 
 int check_sizes(int type, int stream_type, long long rows, long long width) {
     if (!is_type(type) || (stream_type != type && stream_type != CFC_TYPE_F32)) return CFC_ERR_UNSUPPORTED;
