@@ -1598,11 +1598,15 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 // us, 4.8 TB/s, the rate of a large copy; 32 heads of one row in 7 us, latency.  It keeps
 // 3 waves a SIMD at 128 keys: with 2, where the compiler would leave it, 129 us.
 //
-// PAST: states beyond what the last-level cache holds pass it by (non-temporal loads
-// and stores).  256 rows x 16 heads, 268 MB each way: 145 us without, 122 with, the
-// states of other layers having passed between; the same 134 MB again and again, which
-// stay cached: 54 without, 60 with.  So from 192 MB on.
-constexpr long long kPastCache = 192LL << 20;
+// PAST: states that the 256 MB of the last-level cache will not hold until their next step
+// pass it by (non-temporal loads and stores).  Between two steps of a layer all the others'
+// run, so what counts is all layers' states: from 32 MB of one call's on, eight layers
+// fill the cache.  Steps of bf16, 16 heads of 128 x 128, with | without, us: 2 GB (at most 24
+// layers) of other states between, 64 MB 34 | 41, 128 MB 64 | 76, 190 MB 80 | 90, 256 MB 119 |
+// 145 (and 50 MB of weights between: 35 | 42, 65 | 78, 81 | 89, 120 | 141); the same states
+// again and again, which no model of more layers does, 31 | 28, 62 | 50, 80 | 68, 118 | 105.
+// At 16 MB, where fewer than 16 layers stay cached, 15 | 17 and 17 | 17.
+constexpr long long kPastCache = 32LL << 20;
 template <class TY, int NR, bool STEP, bool PAST>
 __global__ __launch_bounds__(kThreads, STEP && NR == 16 ? 3 : 1) void delta_token_kernel(
     Shape a, const typename TY::S* __restrict__ q, const typename TY::S* __restrict__ k,
