@@ -1852,11 +1852,12 @@ inline void set_vec(const delta_rule_shape_t* p, Shape* a, const void* q, const 
     a->gvec = go && fours(go, a->gt, a->gh, a->dv, z);
 }
 
-// Sequences so short that they are run token by token: 10 us and 1.2 a token for up to
-// 256 heads' states (8 tokens 18.4 us, 32 47), while the chunks' two kernels take 18.5
-// for 32 heads, 31 for 128, 44 for 256, 79 for 512, whatever the length up to 64 (32
-// heads x 1, 4, 8 and 16 sequences, dims of 128, bf16): they are even at 8, 17, 28 and 40
-// tokens, and at 36 to 40 for more sequences.
+// Sequences so short that they are run token by token: 7 to 8 us and 1.2 a token for up to
+// 256 heads' states (8 tokens 17 to 19 us, 32 45 to 48), while the chunks' two kernels take
+// 17.4 for 32 heads, 30 for 128, 44 for 256, 81 for 512, whatever the length up to 64 (32
+// heads x 1, 4, 8 and 16 sequences, dims of 128, bf16): they are even at 8, 18, 28 and 40
+// tokens, and at 36 to 40 for more sequences.  Packed sequences' lengths are not known on
+// the host; as many tokens in all are as short as that whatever their lengths.
 inline bool is_short(const Shape& a) {
     const long long most = 8 + std::min((long long)a.n_seq * a.hv / 16, 24LL);
     return (a.offsets ? a.n_tokens : a.seq_len) <= most;
@@ -1895,15 +1896,20 @@ long long lay_out(const Shape& a, int type, bool grad, void* base, Space* w) {
 
 // Sixteens of columns of a chain's workgroup.  Its products are the same whatever the
 // tile, so a wide one only saves loads; narrow ones make more workgroups, as long as
-// there is a CU for each.  1024 tokens, dims of 128, 288 | 496 narrow tiles or half as many
-// wide ones: forward in bf16 90 | 92 us narrow, 81 | 82 wide, in fp32 122 | 143 and
-// 102 | 122; gradients in fp32 338 | 466 and 309 | 405.  The joined chains, two
-// workgroups to a CU, stay narrow for longer: gradients in bf16 for 288 | 384 | 496 tiles
-// 202 | 230 | 282 us narrow, 228 | 242 | 275 wide.
-inline int chain_tiles(const Shape& a, bool joined) {
+// there is a CU for each, or half of one where the registers allow it: in bf16, and in the
+// joined chains.  1024 tokens, dims of 128, in us, narrow tiles | half as many wide ones.
+// Forward, of 288 and 496 tiles: fp16 94 | 81 and 104 | 90, fp32 107 | 86 and 124 | 102; bf16 62 | 66
+// and 69 | 71, of 528 90 | 114, of 768 99 | 121, of 1024 129 | 135, of 2048 316 | 289, and with
+// dim_k 64 of 768 76 | 77, of 896 89 | 79.  Gradients of 288 and 496 tiles: fp32 313 | 281 and
+// 433 | 372; joined, in bf16 of 288, 384 and 496 173 | 197, 197 | 210 and 262 | 254.
+inline int chain_tiles(const Shape& a, long long most) {
     const long long narrow = (long long)a.n_seq * a.hv * ((a.dv + 15) / 16);
-    return narrow > (joined ? 384 : 256) && a.dv > 16 ? 2 : 1;
+    return narrow > most && a.dv > 16 ? 2 : 1;
 }
+template <class TY>
+constexpr long long kForwardNarrow = TY::NP == 1 ? 768 : 256;
+template <class TY, int KS>
+constexpr long long kBackwardNarrow = kJoined<TY, KS> ? 384 : 256;
 
 // Eight elements of a 16-bit row are one aligned load.
 inline bool eights(const void* p, long long st, long long sh, int dim) {
@@ -1934,7 +1940,7 @@ template <class TY, int KS>
 int run_forward(const Shape& a, const Space& w, const void* q, const void* k, const void* v, const float* g,
                 const float* beta, const float* initial, void* o, float* final_state, hipStream_t stream) {
     launch_prep<TY, KS, false>(a, w, q, k, g, beta, stream);
-    if (chain_tiles(a, false) == 2)
+    if (chain_tiles(a, kForwardNarrow<TY>) == 2)
         launch_chain<TY, KS, 2, false>(a, w, v, initial, o, final_state, stream);
     else
         launch_chain<TY, KS, 1, false>(a, w, v, initial, o, final_state, stream);
@@ -2125,8 +2131,8 @@ extern "C" int delta_rule_backward(const delta_rule_shape_t* shape, const void* 
                      grad_beta, grad_initial_state, stream);
         };
         if (a.dk <= 64)
-            return chain_tiles(a, kJoined<TY, 2>) == 2 ? run(run_backward<TY, 2, 2>) : run(run_backward<TY, 2, 1>);
-        return chain_tiles(a, kJoined<TY, 4>) == 2 ? run(run_backward<TY, 4, 2>) : run(run_backward<TY, 4, 1>);
+            return chain_tiles(a, kBackwardNarrow<TY, 2>) == 2 ? run(run_backward<TY, 2, 2>) : run(run_backward<TY, 2, 1>);
+        return chain_tiles(a, kBackwardNarrow<TY, 4>) == 2 ? run(run_backward<TY, 4, 2>) : run(run_backward<TY, 4, 1>);
     };
     switch (shape->type) {
         case CFC_TYPE_F32: return go(F32{});

@@ -1,6 +1,6 @@
 """The delta rule's kernels for large calls, which a rule on the sizes chooses: wide
 tiles of dim_v (more than 256 narrow ones, 384 where the gradients' chains share a
-launch), packed batches of more sequences than a wave has lanes, steps whose states
+launch, 768 for a forward in bf16), packed batches of more sequences than a wave has lanes, steps whose states
 pass the cache by, sequences of many chunks; and keys that are not unit vectors.
 
 Tolerances are those of test_gpu_delta_rule.py, without its allowance for 16-bit o.  Along
@@ -45,9 +45,10 @@ LENS = [66, 1, 0, 64, 65, 33, 7, 70, 130, 2, 64, 9, 63]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("hk,hv,dk,dv", [(2, 4, 128, 128), (4, 4, 64, 128), (2, 4, 100, 130), (1, 4, 33, 117)])
+@pytest.mark.parametrize("hk,hv,dk,dv", [(2, 4, 128, 128), (4, 4, 64, 128), (2, 4, 100, 130), (1, 4, 33, 117),
+                                         (4, 8, 128, 128), (8, 8, 64, 128), (2, 8, 100, 130), (1, 8, 33, 117)])
 def test_wide_tiles(kind, hk, hv, dk, dv):
-    assert len(LENS) * hv * -(-dv // 16) > 384
+    assert len(LENS) * hv * -(-dv // 16) > (768 if hv == 8 else 384)
     say(f"[delta] wide {kind} {hk} {hv} {dk} {dv}")
     check(Case(101, kind, lens=LENS, hk=hk, hv=hv, dk=dk, dv=dv))
 
@@ -55,8 +56,8 @@ def test_wide_tiles(kind, hk, hv, dk, dv):
 @pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
 def test_wide_tiles_of_equal_sequences(kind):
     say(f"[delta] wide dense {kind}")
-    check(Case(102, kind, batch=26, length=70, hk=1, hv=2, dk=64, dv=128, state=False))
-    check(Case(103, kind, batch=13, length=65, hk=1, hv=2, dk=128, dv=256))
+    check(Case(102, kind, batch=49, length=70, hk=1, hv=2, dk=64, dv=128, state=False))
+    check(Case(103, kind, batch=25, length=65, hk=1, hv=2, dk=128, dv=256))
 
 
 @pytest.mark.parametrize("count", [64, 65, 200, 5000])
