@@ -278,7 +278,7 @@ __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane
 // on by one wave each, the inverse on the 32-bit matrix cores: its products are 1/50 of
 // the chunk's and wait for each other, so parts would only make them longer.  Bound by
 // the chunk's chain of latencies (products, decays, inverse, each behind a barrier)
-// with 4 workgroups a CU: 128 chunks of 32 + 16 heads (bf16, dim_k 128) in 87 us; for the
+// with 4 workgroups a CU: 128 chunks of 32 + 16 heads (bf16, dim_k 128) in 88 us; for the
 // gradients 128 of 16 + 8 in 52.
 //
 // A chunk's rows of a key head's tensor as operands, VEC: 4 elements at a time.
@@ -636,22 +636,23 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(Shape a, Space w, 
 //
 // With one wave a SIMD nothing hides a latency but the wave itself.  So each of a
 // chunk's operands is loaded again, for the next chunk, as soon as its last product has
-// read it.  (Two register sets, loaded two chunks ahead, gave nothing with bf16: 16
-// prompts of fp16 with dim_k 64 81.5 us with two, 76.6 with one, 8192 tokens of bf16 317
-// with either; in fp32 with 128 keys they do not fit: 413 instead of 333 us for 4096 tokens
+// read it.  (Two register sets, loaded two chunks ahead, gave nothing with 16-bit types,
+// o then in two parts: 16 prompts of fp16 with dim_k 64 81.5 us with two, 76.6 with one,
+// 8192 tokens of bf16 317 with either; in fp32 with 128 keys they do not fit: 413 instead of 333 us for 4096 tokens
 // of 32 heads.)  All loads and stores are unconditional (bounds are the buffer
 // descriptors'), so that the compiler's counts of what is in flight stay exact and no
 // load waits for a store.  LDS reads are issued together behind each barrier, and the
 // products that the chain does not wait for (Q S, and M U with the stores of o, one
 // chunk later) run in their latency.
 //
-// Bound by the way from one state to the next: a chunk is 4300 cycles of three
-// exchanges, each a split, an LDS write, a barrier, an LDS read and a product (four
-// more waves that make o beside it change nothing: 321 us instead of 319).  1 x 8192 tokens, 32
-// heads, bf16, dims of 128: 256 workgroups, 128 chunks, 231 us, 1.8 us a chunk.  16
-// packed fp16 prompts (of 8 heads, dim_k 64) 56 us; the states' chain for the
+// Bound by the way from one state to the next: a chunk is 4700 cycles of three
+// exchanges, each a split, an LDS write, a barrier, an LDS read and a product; o's products
+// add 20 us of 250 with three parts instead of two (four more waves that made o beside the
+// chain gave nothing: 321 us for 319, with two).  1 x 8192 tokens, 32 heads, bf16, dims of
+// 128: 256 workgroups, 128 chunks, 250 us, 1.95 us a chunk.  16
+// packed fp16 prompts (of 8 heads, dim_k 64) 62 us; the states' chain for the
 // gradients of 4 x 2048 (64 heads in all, wide tiles) 100 us.  Left alone: no LDS and a
-// wave for each tile (365 us instead of 237, each wave splits S by itself), scalar
+// wave for each tile (365 us instead of then 237, each wave splits S by itself), scalar
 // cursors instead of multiplied slots (253 instead of 230).
 template <int N, int NCT, int KSN>
 struct Exchange {  // [part][ks][column tile][lane]
@@ -1239,7 +1240,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_chains_kernel(
 //
 // Bound by latency: 99 KB of LDS leave one workgroup (two waves a SIMD) a CU, and a
 // slice's loads, split, barrier and products follow each other.  4 x 2048 tokens, 8 key
-// and 16 value heads, bf16, dims of 128: 238 us, 75000 cycles for a chunk's value head,
+// and 16 value heads, bf16, dims of 128: 240 us, 75000 cycles for a chunk's value head,
 // of which 5000 to 10000 are each of the 4 slices; 0.54 GB of states and rows, 2.3 TB/s.
 // Slices in two LDS buffers, or v and dO loaded ahead too, need more registers than there
 // are (510 us).
@@ -1594,8 +1595,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 //
 // STEP: a decode step (`slots`, or all rows in order); otherwise the sequence form of
 // short sequences, the next token's rows in flight while one is worked on.  A step is
-// bound by reading and writing the states: 256 rows x 16 heads of 128 x 128 (537 MB) in 111
-// us, 4.8 TB/s, the rate of a large copy; 32 heads of one row in 7 us, latency.  It keeps
+// bound by reading and writing the states: 256 rows x 16 heads of 128 x 128, 13 rows idle
+// (513 MB), in 113 us, 4.5 TB/s where a large copy reaches 4.7; 32 heads of one row in 7 us,
+// latency.  It keeps
 // 3 waves a SIMD at 128 keys: with 2, where the compiler would leave it, 129 us.
 //
 // PAST: states that the 256 MB of the last-level cache will not hold until their next step

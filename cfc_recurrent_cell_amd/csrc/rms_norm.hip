@@ -7,8 +7,8 @@
 // columns (four rows a wave), a wave up to 512, several waves beyond, which join
 // their sums through LDS.  Workgroups stride over the rows with the weight in
 // registers.  In bf16, where a large copy reaches 4.7 TB/s: 16384 x 4096 with a residual,
-// 537 MB, in 99 us, 5.4 TB/s; its backward (with grad_h, 537 MB) in 108 us, 5.0 TB/s;
-// the backward of 99991 x 128 (77 MB) in 19.3 us, 4.0 TB/s, 5 of them the column sum's
+// 537 MB, in 99 us, 5.4 TB/s; its backward (with grad_h, 537 MB) in 110 us, 4.9 TB/s;
+// the backward of 99991 x 128 (77 MB) in 19.8 us, 3.9 TB/s, 5 of them the column sum's
 // own launch; 32 rows of 4096 to e4m3 in 4.4 us on the GPU, a launch's time.
 #include <hip/hip_runtime.h>
 
@@ -295,10 +295,10 @@ int check_sizes(int type, int stream_type, long long rows, long long width) {
 
 // Threads and 8-column vectors of a row: the rule on the width alone, as few threads as
 // hold the row with one vector each.  More leave lanes idle (forward | backward in us,
-// bf16): 300000 x 128 with 16 lanes a row 27 | 44, with 64 62 | 98; 100000 x 512 with 64
-// 34 | 63, with 256 76 | 173; 65536 x 1024 with 128 47 | 85, with 256 60 | 226.  Fewer, with
-// two vectors, leave less in flight: 16384 x 4096 with 512 threads 45 | 86, with 256
-// 48 | 137.  Beyond 8192 columns a workgroup has no more threads.
+// bf16): 300000 x 128 with 16 lanes a row 25 | 43, with 64 61 | 106; 100000 x 512 with 64
+// 34 | 63, with 256 74 | 180; 65536 x 1024 with 128 45 | 85, with 256 56 | 139.  Fewer, with
+// two vectors, leave less in flight: 16384 x 4096 with 512 threads 43 | 86, with 256
+// 47 | 126.  Beyond 8192 columns a workgroup has no more threads.
 template <class F>
 int with_tiling(long long width, F f) {
     const std::integral_constant<int, 1> one;
@@ -363,8 +363,8 @@ int run_forward(int type, int stream_type, long long rows, long long width, cons
 inline long long parts_of(long long rows, long long width) {
     const long long need = (rows + rows_at_once(width) - 1) / rows_at_once(width);
     // narrow rows' partial sums are small, and more workgroups hide more of the loads:
-    // 99991 x 128 with 512 21.6 us, with 1024 20.0; 32768 x 2048 133 and 85, with 2048 99;
-    // 16384 x 4096 with 1024 121 us for 109
+    // 99991 x 128 with 512 23.7 us, with 1024 21.5, with 2048 25.3; 32768 x 2048 135, 86
+    // and 91; 16384 x 4096 86, 89 and 100
     return std::min(need, width <= 2048 ? 1024LL : 512LL);
 }
 
