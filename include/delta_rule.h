@@ -49,7 +49,9 @@ extern "C" {
  * offsets[s + 1] - 1.  Sequences of no rows are allowed: their final state is
  * their initial one.  Output rows behind the last sequence are left as they were.
  * Offsets are not checked on the host; ones that break the rule give undefined
- * outputs, within the arrays' bounds.
+ * outputs, within the arrays' bounds.  Packed sequences are taken in groups of 64
+ * tokens unless they have 8 to 32 in all: single tokens of many belong in
+ * delta_rule_step.
  *   q, k [n_tokens, heads_k, dim_k], v [n_tokens, heads_v, dim_v]: row r, head h
  * at r * stride_t + h * stride_h elements (strides >= 0, so a slice of a fused
  * projection or a broadcast head can be read where it lies), the last axis
