@@ -75,6 +75,15 @@ def _lead(q, offsets):
     return 2 if offsets is None else 1
 
 
+def _token_rows(t, name, dtype, device, shape, offsets):
+    """The given buffer of token rows after its checks, or a new one.  Rows behind the last packed
+    sequence keep what a given buffer holds; a new one's are zeros, so that what follows over all rows
+    (a sum over tokens) meets no stale memory."""
+    if t is None and offsets is not None:
+        return torch.zeros(shape, dtype=dtype, device=device)
+    return given_or_new(t, name, dtype, device, shape)
+
+
 def _size(need: int) -> int:
     if need < 0:
         raise ValueError("a size is beyond what the library takes (dim_k <= 128, dim_v <= 256, 64 tokens' rows of "
@@ -107,7 +116,8 @@ def delta_rule_forward(q, k, v, g, beta, initial_state=None, scale: Optional[flo
     [B, heads_v, dim_k, dim_v] are contiguous float32.  ``scale`` is
     dim_k ** -0.5 by default.  With ``offsets`` (int32 on the GPU, [S + 1]) the
     tokens are packed, [N, heads, dim] with sequence s in rows offsets[s] to
-    offsets[s + 1] - 1; rows behind the last one's end keep what ``o`` held.
+    offsets[s + 1] - 1; rows behind the last one's end keep what a given ``o``
+    holds (with ``o`` given no fill is launched) and are zeros in a new one.
     ``final_state`` may be ``initial_state`` itself; ``want_final=False`` leaves
     it out (None).  The workspace is allocated here unless given."""
     lib = load_library()
@@ -117,7 +127,7 @@ def delta_rule_forward(q, k, v, g, beta, initial_state=None, scale: Optional[flo
     with on_device(dev, stream):
         if initial_state is not None:
             check(initial_state, "initial_state", F32, dev, states)
-        o = given_or_new(o, "o", q.dtype, dev, v.shape)
+        o = _token_rows(o, "o", q.dtype, dev, v.shape, offsets)
         if final_state is not None or want_final:
             final_state = given_or_new(final_state, "final_state", F32, dev, states)
         at, size, keep = space(_size(lib.delta_rule_forward_workspace(byref(s))), workspace, dev)
@@ -147,16 +157,11 @@ def delta_rule_backward(q, k, v, g, beta, grad_o, initial_state=None, grad_final
             check(initial_state, "initial_state", F32, dev, states)
         if grad_final_state is not None:
             check(grad_final_state, "grad_final_state", F32, dev, states)
-
-        def rows(t, name, kind, like):
-            # rows behind the last sequence have no gradient, and keep what a given buffer holds
-            if t is None and offsets is not None:
-                return torch.zeros(like.shape, dtype=kind, device=dev)
-            return given_or_new(t, name, kind, dev, like.shape)
-
-        grad_q, grad_k = rows(grad_q, "grad_q", dtype, q), rows(grad_k, "grad_k", dtype, k)
-        grad_v = rows(grad_v, "grad_v", dtype, v)
-        grad_g, grad_beta = rows(grad_g, "grad_g", F32, g), rows(grad_beta, "grad_beta", F32, g)
+        grad_q = _token_rows(grad_q, "grad_q", dtype, dev, q.shape, offsets)
+        grad_k = _token_rows(grad_k, "grad_k", dtype, dev, k.shape, offsets)
+        grad_v = _token_rows(grad_v, "grad_v", dtype, dev, v.shape, offsets)
+        grad_g = _token_rows(grad_g, "grad_g", F32, dev, g.shape, offsets)
+        grad_beta = _token_rows(grad_beta, "grad_beta", F32, dev, g.shape, offsets)
         if grad_initial_state is not None or initial_state is not None:
             grad_initial_state = given_or_new(grad_initial_state, "grad_initial_state", F32, dev, states)
         at, size, keep = space(_size(lib.delta_rule_backward_workspace(byref(s))), workspace, dev)
