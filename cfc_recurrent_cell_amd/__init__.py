@@ -20,15 +20,31 @@ from ._lib import (  # noqa: F401
 from ._delta_rule import (  # noqa: F401
     delta_rule_backward, delta_rule_forward, delta_rule_step, delta_rule_workspace,
 )
+from ._grad_norm import (  # noqa: F401
+    clip_grad_norm, grad_norm, grad_norm_workspace,
+)
+from ._layer_norm import (  # noqa: F401
+    layer_norm_backward, layer_norm_backward_workspace, layer_norm_forward,
+)
 from ._rms_norm import (  # noqa: F401
     rms_norm_backward, rms_norm_backward_workspace, rms_norm_forward, rms_norm_forward_e4m3,
+)
+from ._selective_scan import (  # noqa: F401
+    selective_scan_backward, selective_scan_backward_workspace, selective_scan_forward, selective_scan_step,
+)
+from ._short_conv import (  # noqa: F401
+    short_conv_backward, short_conv_backward_workspace, short_conv_forward, short_conv_step,
 )
 
 __all__ = ["cfc_forward", "cfc_backward", "cfc_backward_window", "cfc_backward_windows",
            "cfc_backward_workspace", "cfc_forward_backward_workspace", "cfc_forward_backward", "reduce_axis0", "reduce_axis0_noalloc",
            "reduce_axis0_split_workspace", "cfc_scratch_row_len", "delta_rule_forward",
            "delta_rule_backward", "delta_rule_step", "delta_rule_workspace", "rms_norm_forward",
-           "rms_norm_forward_e4m3", "rms_norm_backward", "rms_norm_backward_workspace", "CfcError", "load_library"]
+           "rms_norm_forward_e4m3", "rms_norm_backward", "rms_norm_backward_workspace", "layer_norm_forward",
+           "layer_norm_backward", "layer_norm_backward_workspace", "short_conv_forward", "short_conv_backward",
+           "short_conv_backward_workspace", "short_conv_step", "selective_scan_forward", "selective_scan_backward",
+           "selective_scan_backward_workspace", "selective_scan_step", "grad_norm", "clip_grad_norm", "grad_norm_workspace",
+           "CfcError", "load_library"]
 
 
 def cfc_scratch_row_len(n_in: int, n_hid: int) -> int:

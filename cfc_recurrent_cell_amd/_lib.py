@@ -49,6 +49,31 @@ class DeltaRuleShape(ctypes.Structure):
                     (f"{n}_stride_{a}", ctypes.c_longlong) for n in ("q", "k", "v", "go") for a in ("t", "h")]
 
 
+class ShortConvShape(ctypes.Structure):
+    """short_conv_shape_t of include/short_conv.h."""
+    _fields_ = [("type", ctypes.c_int), ("n_seq", ctypes.c_int), ("seq_len", ctypes.c_int),
+                ("n_tokens", ctypes.c_longlong), ("offsets", ctypes.c_void_p), ("channels", ctypes.c_int),
+                ("width", ctypes.c_int), ("silu", ctypes.c_int), ("clear_rest", ctypes.c_int),
+                ("x_stride", ctypes.c_longlong),
+                ("grad_y_stride", ctypes.c_longlong)]
+
+
+class SelectiveScanShape(ctypes.Structure):
+    """selective_scan_shape_t of include/selective_scan.h."""
+    _fields_ = [("type", ctypes.c_int), ("n_seq", ctypes.c_int), ("seq_len", ctypes.c_int),
+                ("n_tokens", ctypes.c_longlong), ("offsets", ctypes.c_void_p), ("channels", ctypes.c_int),
+                ("groups", ctypes.c_int), ("state", ctypes.c_int), ("softplus", ctypes.c_int),
+                ("clear_rest", ctypes.c_int)] + [
+                    (n, ctypes.c_longlong) for n in ("x_stride", "dt_stride", "z_stride", "grad_y_stride",
+                                                     "b_stride_t", "b_stride_g", "c_stride_t", "c_stride_g")]
+
+
+class GradTensor(ctypes.Structure):
+    """grad_tensor_t of include/grad_norm.h."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_longlong),
+                ("type", ctypes.c_int)]
+
+
 class CfcError(RuntimeError):
     def __init__(self, fn: str, code: int, text: str):
         super().__init__(f"{fn} failed with status {code}: {text}")
@@ -116,6 +141,36 @@ def load_library(path: str = LIB_PATH):
     lib.rms_norm_backward_workspace.argtypes = [ll, ll]
     lib.rms_norm_backward.restype = i
     lib.rms_norm_backward.argtypes = [i, i, ll, ll] + [vp] * 8 + [ll, vp]
+    lib.layer_norm_forward.restype = i
+    lib.layer_norm_forward.argtypes = [i, i, ll, ll, vp, vp, vp, vp, f, vp, vp, vp, vp, vp]
+    lib.layer_norm_backward_workspace.restype = ll
+    lib.layer_norm_backward_workspace.argtypes = [ll, ll]
+    lib.layer_norm_backward.restype = i
+    lib.layer_norm_backward.argtypes = [i, i, ll, ll] + [vp] * 10 + [ll, vp]
+    conv = ctypes.POINTER(ShortConvShape)
+    lib.short_conv_forward.restype = i
+    lib.short_conv_forward.argtypes = [conv] + [vp] * 7
+    lib.short_conv_backward_workspace.restype = ll
+    lib.short_conv_backward_workspace.argtypes = [conv]
+    lib.short_conv_backward.restype = i
+    lib.short_conv_backward.argtypes = [conv] + [vp] * 11 + [ll, vp]
+    lib.short_conv_step.restype = i
+    lib.short_conv_step.argtypes = [conv] + [vp] * 4 + [i, vp, vp, vp]
+    scan = ctypes.POINTER(SelectiveScanShape)
+    lib.selective_scan_forward.restype = i
+    lib.selective_scan_forward.argtypes = [scan] + [vp] * 12
+    lib.selective_scan_backward_workspace.restype = ll
+    lib.selective_scan_backward_workspace.argtypes = [scan]
+    lib.selective_scan_backward.restype = i
+    lib.selective_scan_backward.argtypes = [scan] + [vp] * 21 + [ll, vp]
+    lib.selective_scan_step.restype = i
+    lib.selective_scan_step.argtypes = [scan] + [vp] * 9 + [i, vp, vp, vp]
+    lib.grad_norm_workspace.restype = ll
+    lib.grad_norm_workspace.argtypes = [i]
+    lib.grad_norm.restype = i
+    lib.grad_norm.argtypes = [vp, i, vp, vp, ll, vp]
+    lib.clip_grad_norm.restype = i
+    lib.clip_grad_norm.argtypes = [vp, i, f, vp, vp, ll, vp]
     lib.cfc_status_string.restype = ctypes.c_char_p
     lib.cfc_status_string.argtypes = [i]
     _lib = lib

@@ -1,10 +1,11 @@
-// elements.h -- element types and argument checks that delta_rule.hip and rms_norm.hip
-// share.
+// elements.h -- element types, their loads and argument checks that the kernels share
+// (all but cfc.hip's).
 #pragma once
 
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "delta_rule.h" /* CFC_TYPE_*, status codes */
 
@@ -30,6 +31,77 @@ struct F16 {
     static __device__ __forceinline__ S store(float x) { return (_Float16)x; }
 };
 
+// 16 bytes at an address that the element's size divides; the memory takes them at any.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight consecutive elements as they lie in memory.
+template <class TY>
+struct Eight {
+    uint32_t w[2 * sizeof(typename TY::S)];
+};
+
+// Columns c ... c + 7 of a row; zero from `width` on.
+template <class TY>
+__device__ __forceinline__ Eight<TY> fetch8(const typename TY::S* row, int c, int width) {
+    Eight<TY> e;
+    if (c + 8 <= width) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(e) / 16; ++i) {
+            const u32x4_any a = *reinterpret_cast<const u32x4_any*>(row + c + 4 * i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) e.w[4 * i + j] = a[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(e) / 4; ++i) e.w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < width) {
+                if constexpr (sizeof(typename TY::S) == 4)
+                    e.w[j] = __builtin_bit_cast(uint32_t, row[c + j]);
+                else
+                    e.w[j >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[c + j]) << (16 * (j & 1));
+            }
+    }
+    return e;
+}
+template <class TY>
+__device__ __forceinline__ void unpack8(const Eight<TY>& e, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(typename TY::S) == 4)
+            x[j] = __builtin_bit_cast(float, e.w[j]);
+        else
+            x[j] = TY::load(__builtin_bit_cast(typename TY::S,
+                                               (uint16_t)(j & 1 ? e.w[j >> 1] >> 16 : e.w[j >> 1] & 0xffff)));
+    }
+}
+template <class TY>
+__device__ __forceinline__ void load8(const typename TY::S* row, int c, int width, float (&x)[8]) {
+    unpack8<TY>(fetch8<TY>(row, c, width), x);
+}
+template <class TY>
+__device__ __forceinline__ void store8(typename TY::S* row, int c, int width, const float (&x)[8]) {
+    if (c + 8 <= width) {
+        if constexpr (sizeof(typename TY::S) == 4) {
+            *reinterpret_cast<f32x4_any*>(row + c) = f32x4_any{x[0], x[1], x[2], x[3]};
+            *reinterpret_cast<f32x4_any*>(row + c + 4) = f32x4_any{x[4], x[5], x[6], x[7]};
+        } else {
+            u32x4_any a;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                a[j] = (uint32_t)__builtin_bit_cast(uint16_t, TY::store(x[2 * j])) |
+                       (uint32_t)__builtin_bit_cast(uint16_t, TY::store(x[2 * j + 1])) << 16;
+            *reinterpret_cast<u32x4_any*>(row + c) = a;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (c + j < width) row[c + j] = TY::store(x[j]);
+    }
+}
+
 inline int size_of(int type) { return type == CFC_TYPE_F32 ? 4 : 2; }
 
 // An argument's bytes; none of a null pointer.
@@ -49,6 +121,13 @@ inline bool outputs_disjoint(const Range* outs, int n_out, const Range* ins, int
         for (int p = o + 1; p < n_out; ++p)
             if (overlap(outs[o], outs[p])) return false;
     }
+    return true;
+}
+
+// Whether addresses are multiples of `size` (null ones are).
+inline bool fits(std::initializer_list<const void*> ps, int size) {
+    for (const void* p : ps)
+        if (reinterpret_cast<uintptr_t>(p) % size) return false;
     return true;
 }
 

@@ -1,0 +1,41 @@
+// functions.h -- the gates' functions in 32 bits (short_conv.hip, selective_scan.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace {
+
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// exp(x) for x <= 0: the rounding of x log2(e) is put right, so that a step of a
+// thousandth, exp(-7), is as exact as one of one.
+__device__ __forceinline__ float exp_of(float x) {
+    constexpr float low = 1.92596299e-8f;  // log2(e) - kLog2e
+    x = fmaxf(x, -1000.0f);
+    const float t = x * kLog2e, e = fmaf(x, low, fmaf(x, kLog2e, -t));
+    const float p = exp2_of(t);
+    return fmaf(p, e * kLn2, p);
+}
+__device__ __forceinline__ float reciprocal(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ float sigmoid_of(float x) {
+    const float e = exp_of(-fabsf(x)), r = reciprocal(1.0f + e);
+    return x >= 0.0f ? r : e * r;
+}
+// max(x, 0) + log(1 + exp(-|x|)); the logarithm as 2 artanh(e / (2 + e)) by its series,
+// whose argument is at most a third, so that small results lose nothing.
+__device__ __forceinline__ float softplus_of(float x) {
+    const float e = exp_of(-fabsf(x)), s = e * reciprocal(2.0f + e), z = s * s;
+    float p = 1.0f / 15;
+    p = fmaf(p, z, 1.0f / 13);
+    p = fmaf(p, z, 1.0f / 11);
+    p = fmaf(p, z, 1.0f / 9);
+    p = fmaf(p, z, 1.0f / 7);
+    p = fmaf(p, z, 1.0f / 5);
+    p = fmaf(p, z, 1.0f / 3);
+    p = fmaf(p, z, 1.0f);
+    return fmaxf(x, 0.0f) + 2.0f * s * p + (x != x ? x : 0.0f);
+}
+
+}  // namespace

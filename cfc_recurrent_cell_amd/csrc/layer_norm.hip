@@ -1,0 +1,298 @@
+// layer_norm.hip -- gfx950 kernels and C ABI of the layer norm (see
+// include/layer_norm.h).
+//
+// Memory is the bound, so a row is read once into registers, 8 consecutive columns
+// a lane, and mean and variance are two sums over its lanes: the variance from the
+// differences to the mean, which loses nothing where the mean is far from zero.
+// Rows of any width and address are read in 16-byte loads (the memory takes them at
+// any alignment); only a row's last columns, fewer than 8, go one by one.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "elements.h"
+#include "layer_norm.h"
+#include "rows.h"
+
+namespace {
+
+__device__ __forceinline__ float plus(float p, float q) { return p + q; }
+
+template <class TX, class TH, int TPR, int NV>
+__global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
+    long long rows, int width, const typename TX::S* x, const typename TH::S* residual,
+    const typename TX::S* __restrict__ weight, const typename TX::S* __restrict__ bias, float eps,
+    typename TX::S* __restrict__ y, typename TH::S* h, float* __restrict__ mean, float* __restrict__ rstd) {
+    constexpr int RPW = threads_of(TPR) / TPR;
+    __shared__ float red[2][16];
+    const int sub = threadIdx.x % TPR;
+    float w[NV][8], b[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        load8<TX>(weight, 8 * (v * TPR + sub), width, w[v]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
+        if (bias) load8<TX>(bias, 8 * (v * TPR + sub), width, b[v]);
+    }
+    for (long long r0 = (long long)blockIdx.x * RPW; r0 < rows; r0 += (long long)gridDim.x * RPW) {
+        const long long row = r0 + threadIdx.x / TPR;
+        const bool in = row < rows;  // lanes of a row behind the last compute and write nothing
+        const long long at = (in ? row : rows - 1) * width;
+        float a[NV][8];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) load8<TX>(x + at, 8 * (v * TPR + sub), width, a[v]);
+        if (residual) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                float e[8];
+                const int c = 8 * (v * TPR + sub);
+                load8<TH>(residual + at, c, width, e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[v][j] = TH::load(TH::store(a[v][j] + e[j]));
+                if (h && in) store8<TH>(h + at, c, width, a[v]);
+            }
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s += a[v][j];
+        const float m = over_row<TPR>(s, plus, red, 0) / (float)width;
+        s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[v][j] -= m;
+                if (8 * (v * TPR + sub) + j < width) s += a[v][j] * a[v][j];
+            }
+        const float rs = 1.0f / sqrtf(over_row<TPR>(s, plus, red, 1) / (float)width + eps);
+        if (sub == 0 && in) {
+            if (mean) mean[row] = m;
+            if (rstd) rstd[row] = rs;
+        }
+        if (in) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[v][j] = a[v][j] * rs * w[v][j] + b[v][j];
+                store8<TX>(y + at, 8 * (v * TPR + sub), width, a[v]);
+            }
+        }
+    }
+}
+
+// The weight's and the bias's terms are summed over the workgroup's rows in registers,
+// in 64 bits, then over its row slots through LDS, into part[2 * blockIdx.x] and the
+// row behind it; column_sums_kernel sums those.
+template <class TX, class TH, int TPR, int NV>
+__global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
+    long long rows, int width, const typename TX::S* __restrict__ gy, const typename TH::S* __restrict__ h,
+    const typename TX::S* __restrict__ weight, const float* __restrict__ mean, const float* __restrict__ rstd,
+    const typename TH::S* gh, typename TH::S* gx, float* __restrict__ part) {
+    constexpr int RPW = threads_of(TPR) / TPR;
+    __shared__ float red[2][16];
+    const int sub = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    float w[NV][8];
+    double gw[NV][8], gb[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        load8<TX>(weight, 8 * (v * TPR + sub), width, w[v]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gw[v][j] = gb[v][j] = 0.0;
+    }
+    for (long long r0 = (long long)blockIdx.x * RPW; r0 < rows; r0 += (long long)gridDim.x * RPW) {
+        const long long row = r0 + slot;
+        const bool in = row < rows;
+        const long long at = (in ? row : rows - 1) * width;
+        const float rs = in ? rstd[row] : 0.0f, m = in ? mean[row] : 0.0f;
+        float n[NV][8], d[NV][8];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            load8<TH>(h + at, 8 * (v * TPR + sub), width, n[v]);
+            load8<TX>(gy + at, 8 * (v * TPR + sub), width, d[v]);
+        }
+        float s = 0.0f, sn = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                n[v][j] = (n[v][j] - m) * rs;  // columns behind the last have d = 0
+                if (in) {
+                    gw[v][j] += d[v][j] * n[v][j];
+                    gb[v][j] += d[v][j];
+                }
+                d[v][j] *= w[v][j];
+                s += d[v][j];
+                sn += d[v][j] * n[v][j];
+            }
+        s = over_row<TPR>(s, plus, red, 0) / (float)width;
+        sn = over_row<TPR>(sn, plus, red, 1) / (float)width;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = 8 * (v * TPR + sub);
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = rs * (d[v][j] - s - n[v][j] * sn);
+            if (gh) {
+                float e[8];
+                load8<TH>(gh + at, c, width, e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] += e[j];
+            }
+            if (in) store8<TH>(gx + at, c, width, o);
+        }
+    }
+    float* to = part + 2LL * blockIdx.x * width;
+    if constexpr (RPW > 1) {
+        __shared__ double sum[RPW][8 * TPR * NV + 2];
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[slot][8 * (v * TPR + sub) + j] = which ? gb[v][j] : gw[v][j];
+            __syncthreads();
+            for (int c = threadIdx.x; c < width; c += threads_of(TPR)) {
+                double x = sum[0][c];
+#pragma unroll
+                for (int i = 1; i < RPW; ++i) x += sum[i][c];
+                to[(long long)which * width + c] = (float)x;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (float)gw[v][j];
+            store8<F32>(to, 8 * (v * TPR + sub), width, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = (float)gb[v][j];
+            store8<F32>(to + width, 8 * (v * TPR + sub), width, x);
+        }
+    }
+}
+
+// Columns of part [parts, 2 width] summed in 64 bits: the first half into gw, the other
+// into gb (or nowhere).  32 columns a workgroup (a cache line of each row), 32 rows at once.
+constexpr int kSumCols = 32, kSumRows = 32;
+__global__ __launch_bounds__(kSumCols* kSumRows) void column_sums_kernel(const float* __restrict__ part, int parts,
+                                                                         int width, float* __restrict__ gw,
+                                                                         float* __restrict__ gb) {
+    __shared__ double red[kSumRows][kSumCols + 1];
+    const int sub = threadIdx.x % kSumCols, slot = threadIdx.x / kSumCols;
+    const int c = blockIdx.x * kSumCols + sub;
+    double x = 0.0;
+    if (c < 2 * width)
+#pragma unroll 4
+        for (int r = slot; r < parts; r += kSumRows) x += part[2LL * r * width + c];
+    red[slot][sub] = x;
+    __syncthreads();
+    if (slot != 0 || c >= 2 * width) return;
+#pragma unroll
+    for (int i = 1; i < kSumRows; ++i) x += red[i][sub];
+    if (c < width)
+        gw[c] = (float)x;
+    else if (gb)
+        gb[c - width] = (float)x;
+}
+
+// Workgroups of the backward, each with two rows of partial sums.
+inline long long parts_of(long long rows, long long width) {
+    const long long need = (rows + rows_at_once(width) - 1) / rows_at_once(width);
+    return std::min(need, width <= 2048 ? 1024LL : 512LL);
+}
+
+}  // namespace
+
+// ================================================================ C ABI
+extern "C" int layer_norm_forward(int type, int stream_type, long long rows, long long width, const void* x,
+                                  const void* residual, const void* weight, const void* bias, float eps, void* y,
+                                  void* h, float* mean, float* rstd, hipStream_t stream) {
+    if (const int e = check_sizes(type, stream_type, rows, width)) return e;
+    if (!std::isfinite(eps) || eps < 0.0f) return CFC_ERR_DT;
+    if (!residual && (h || stream_type != type)) return CFC_ERR_DIM;
+    if (rows == 0) return CFC_OK;
+    if (!x || !weight || !y) return CFC_ERR_NULL;
+    if (!fits({x, weight, bias, y}, size_of(type)) || !fits({residual, h}, size_of(stream_type)) ||
+        !fits({mean, rstd}, 4))
+        return CFC_ERR_DIM;
+    const long long n = rows * width;
+    const Range rx = bytes_of(x, n * size_of(type)), rr = bytes_of(residual, n * size_of(stream_type)),
+                rh = bytes_of(h, n * size_of(stream_type));
+    const bool over_x = same(rh, rx) && stream_type == type, over_r = same(rh, rr);
+    const Range outs[] = {bytes_of(y, n * size_of(type)), rh, bytes_of(mean, rows * 4), bytes_of(rstd, rows * 4)};
+    const Range ins[] = {bytes_of(weight, width * size_of(type)), bytes_of(bias, width * size_of(type)),
+                         over_x ? Range{0, 0} : rx, over_r ? Range{0, 0} : rr};
+    if (!outputs_disjoint(outs, 4, ins, 4)) return CFC_ERR_OVERLAP;
+    return with_types(type, stream_type, [&](auto tx, auto th) {
+        return with_tiling(width, [&](auto tpr, auto nv) {
+            using TX = decltype(tx);
+            using TH = decltype(th);
+            constexpr int T = decltype(tpr)::value, V = decltype(nv)::value;
+            const long long need = (rows + rows_at_once(width) - 1) / rows_at_once(width);
+            const unsigned grid = (unsigned)std::min(need, (long long)256 * 8 * 256 / threads_of(T));
+            hipLaunchKernelGGL((layer_norm_kernel<TX, TH, T, V>), dim3(grid), dim3(threads_of(T)), 0, stream, rows,
+                               (int)width, (const typename TX::S*)x, (const typename TH::S*)residual,
+                               (const typename TX::S*)weight, (const typename TX::S*)bias, eps, (typename TX::S*)y,
+                               (typename TH::S*)h, mean, rstd);
+            return launch_status();
+        });
+    });
+}
+
+extern "C" long long layer_norm_backward_workspace(long long rows, long long width) {
+    if (check_sizes(CFC_TYPE_F32, CFC_TYPE_F32, rows, width) != CFC_OK) return -1;
+    return (parts_of(rows, width) * width * 8 + 15) / 16 * 16;
+}
+
+extern "C" int layer_norm_backward(int type, int stream_type, long long rows, long long width, const void* grad_y,
+                                   const void* h, const void* weight, const float* mean, const float* rstd,
+                                   const void* grad_h, void* grad_x, float* grad_weight, float* grad_bias,
+                                   void* workspace, long long workspace_bytes, hipStream_t stream) {
+    if (const int e = check_sizes(type, stream_type, rows, width)) return e;
+    if (!grad_weight) return CFC_ERR_NULL;
+    const long long need = layer_norm_backward_workspace(rows, width), parts = parts_of(rows, width);
+    if (rows) {
+        if (!grad_y || !h || !weight || !mean || !rstd || !grad_x || !workspace) return CFC_ERR_NULL;
+        if (workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16) return CFC_ERR_DIM;
+    }
+    if (!fits({grad_y, weight}, size_of(type)) || !fits({h, grad_h, grad_x}, size_of(stream_type)) ||
+        !fits({mean, rstd, grad_weight, grad_bias}, 4))
+        return CFC_ERR_DIM;
+    const long long n = rows * width;
+    const Range rgh = bytes_of(grad_h, n * size_of(stream_type)), rgx = bytes_of(grad_x, n * size_of(stream_type));
+    const Range outs[] = {rgx, bytes_of(grad_weight, width * 4), bytes_of(grad_bias, width * 4),
+                          bytes_of(rows ? workspace : nullptr, need)};
+    const Range ins[] = {bytes_of(grad_y, n * size_of(type)),
+                         bytes_of(h, n * size_of(stream_type)),
+                         bytes_of(rows ? weight : nullptr, width * size_of(type)),
+                         bytes_of(mean, rows * 4),
+                         bytes_of(rstd, rows * 4),
+                         same(rgh, rgx) ? Range{0, 0} : rgh};
+    if (!outputs_disjoint(outs, 4, ins, 6)) return CFC_ERR_OVERLAP;
+    float* part = static_cast<float*>(workspace);
+    if (rows) {
+        const int e = with_types(type, stream_type, [&](auto tx, auto th) {
+            return with_tiling(width, [&](auto tpr, auto nv) {
+                using TX = decltype(tx);
+                using TH = decltype(th);
+                constexpr int T = decltype(tpr)::value, V = decltype(nv)::value;
+                hipLaunchKernelGGL((layer_norm_backward_kernel<TX, TH, T, V>), dim3((unsigned)parts),
+                                   dim3(threads_of(T)), 0, stream, rows, (int)width, (const typename TX::S*)grad_y,
+                                   (const typename TH::S*)h, (const typename TX::S*)weight, mean, rstd,
+                                   (const typename TH::S*)grad_h, (typename TH::S*)grad_x, part);
+                return launch_status();
+            });
+        });
+        if (e != CFC_OK) return e;
+    }
+    hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((2 * width + kSumCols - 1) / kSumCols)),
+                       dim3(kSumCols * kSumRows), 0, stream, part, (int)parts, (int)width, grad_weight, grad_bias);
+    return launch_status();
+}

@@ -1,0 +1,844 @@
+// selective_scan.hip -- gfx950 kernels and C ABI of the selective scan (see
+// include/selective_scan.h).
+//
+// h_t = a_t h_{t-1} + b_t is linear in h, so a stretch of tokens from any state h is
+// P h + h', with P the product of its a_t (one exponential of the sum of the steps) and h'
+// what it makes of zeros.  A workgroup has 16 channels of a sequence and goes along it by
+// blocks of tokens, each of its waves with T of a block's: a wave computes its P and h' with
+// its a_t and b_t kept in registers, the waves exchange P and h' through LDS, and each goes
+// over its tokens again from the state that it now knows, one multiply-add each and no
+// exponential.
+//
+// Four lanes have a channel, with S states each.  What is done once for each token and
+// channel (softplus, the gate) lane j of the four does for the tokens 4 i + j, and the
+// others take it through a lane permutation; b and c are turned to 32 bits once for all of
+// a wave's channels and read from LDS.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "elements.h"
+#include "functions.h"
+#include "selective_scan.h"
+#include "sequences.h"
+
+namespace {
+
+constexpr int kGroupCh = 16;  // channels of a workgroup
+
+// Tokens of a wave and waves of a workgroup, by the states of a lane: what is kept of a
+// token are 2 S registers.
+constexpr int tokens_of(int s) { return s <= 4 ? 8 : 4; }
+constexpr int waves_of(int s) { return s <= 8 ? 8 : 4; }
+constexpr int block_of(int s) { return tokens_of(s) * waves_of(s); }
+
+struct Scan {
+    Sequences q;
+    int channels, groups, share, state;  // share: channels of a group
+    int softplus, clear;
+    long long xt, dtt, zt, gt, bt, bg, ct, cg;
+};
+
+// ------------------------------------------------------------------- lanes
+template <int CTRL>
+__device__ __forceinline__ float quad_perm(float x) {
+    return __builtin_bit_cast(
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+// Lane J of each four lanes' value.
+template <int J>
+__device__ __forceinline__ float from(float x) {
+    return quad_perm<J * 0x55>(x);
+}
+// Lane j of each four gets the sum over them of v[j].
+__device__ __forceinline__ float over_four(const float (&v)[4]) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+    const float a = (odd ? v[1] : v[0]) + quad_perm<0xB1>(odd ? v[0] : v[1]);
+    const float b = (odd ? v[3] : v[2]) + quad_perm<0xB1>(odd ? v[2] : v[3]);
+    return (high ? b : a) + quad_perm<0x4E>(high ? a : b);
+}
+
+// A workgroup's channels: the group of b and c that they read, and the lane's own.
+struct Place {
+    int group, ch, quad, j;
+    bool in;
+};
+__device__ __forceinline__ Place place_of(const Scan& a, int index) {
+    const int parts = (a.share + kGroupCh - 1) / kGroupCh, lane = threadIdx.x & 63;
+    Place p;
+    p.group = index / parts;
+    p.quad = lane >> 2;
+    p.j = lane & 3;
+    const int at = index % parts * kGroupCh + p.quad;
+    p.in = at < a.share;
+    p.ch = p.group * a.share + min(at, a.share - 1);
+    return p;
+}
+
+// S values from `n` on of a row of `state` floats; `none` beyond.
+template <int S>
+__device__ __forceinline__ void load_states(const float* row, int n, int state, float none, float (&h)[S]) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) h[s] = n + s < state ? row[n + s] : none;
+}
+template <int S>
+__device__ __forceinline__ void store_states(float* row, int n, int state, const float (&h)[S]) {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+        if (n + s < state) row[n + s] = h[s];
+}
+
+// What a wave's lanes write to LDS for each other: its own LDS instructions go in order.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// b or c of a wave's T tokens, as 32-bit floats [T][4 S], zero behind the sequence's end.
+template <class TY, int S, int T>
+__device__ __forceinline__ void stage(const typename TY::S* p, long long st, int t0, int end, int state, float* to) {
+#pragma unroll
+    for (int i = 0; i < (T * 4 * S + 63) / 64; ++i) {
+        const int e = i * 64 + (threadIdx.x & 63), t = e / (4 * S), n = e % (4 * S);
+        if (T * 4 * S % 64 == 0 || e < T * 4 * S)
+            to[e] = t0 + t < end && n < state ? TY::load(p[(t0 + t) * st + n]) : 0.0f;
+    }
+}
+
+// -------------------------------------------------------------------- forward
+template <class TY, int S>
+__global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
+    Scan a, int channel_groups, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
+    const float* __restrict__ decay, const typename TY::S* __restrict__ b, const typename TY::S* __restrict__ c,
+    const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias,
+    const float* initial, typename TY::S* __restrict__ y, float* final) {
+    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4;
+    __shared__ float sum[2][NW][2][S][64];  // P and h' of each wave
+    __shared__ float carry[2][S][64];
+    __shared__ float bc[NW][2][T * 4 * S];
+    const Place p = place_of(a, blockIdx.x % channel_groups);
+    const int seq = blockIdx.x / channel_groups, lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = p.j * S;
+    int first, end;
+    span_of(a.q, seq, first, end);
+    float a2[S], h[S];
+    load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
+#pragma unroll
+    for (int s = 0; s < S; ++s) a2[s] *= kLog2e, h[s] = 0.0f;
+    const long long kept = ((long long)seq * a.channels + p.ch) * a.state;
+    if (initial) load_states<S>(initial + kept, n0, a.state, 0.0f, h);
+    const float skip = d ? d[p.ch] : 0.0f, bias = dt_bias ? dt_bias[p.ch] : 0.0f;
+    b += p.group * a.bg;
+    c += p.group * a.cg;
+    int turn = 0;
+    for (int block = first; block < end; block += T * NW, turn ^= 1) {
+        const int t0 = block + w * T;
+        wave_fence();
+        stage<TY, S, T>(b, a.bt, t0, end, a.state, bc[w][0]);
+        stage<TY, S, T>(c, a.ct, t0, end, a.state, bc[w][1]);
+        wave_fence();
+        float xv[Q], step[Q], u[Q], gate[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            const int t = t0 + 4 * i + p.j;
+            const bool in = t < end;
+            xv[i] = in ? TY::load(x[t * a.xt + p.ch]) : 0.0f;
+            const float pre = (in ? TY::load(dt[t * a.dtt + p.ch]) : 0.0f) + bias;
+            const float zv = in && z ? TY::load(z[t * a.zt + p.ch]) : 0.0f;
+            step[i] = in ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
+            u[i] = step[i] * xv[i];
+            gate[i] = z ? zv * sigmoid_of(zv) : 1.0f;
+        }
+        float at[T][S], add[T][S], hl[S], all = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) hl[s] = 0.0f;
+        auto one = [&](auto k, int i) {
+            constexpr int J = decltype(k)::value;
+            const int t = 4 * i + J;
+            const float dl = from<J>(step[i]), ul = from<J>(u[i]);
+            all += dl;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                at[t][s] = exp2_of(dl * a2[s]);
+                add[t][s] = ul * bc[w][0][t * 4 * S + n0 + s];
+                hl[s] = fmaf(at[t][s], hl[s], add[t][s]);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            one(std::integral_constant<int, 0>{}, i);
+            one(std::integral_constant<int, 1>{}, i);
+            one(std::integral_constant<int, 2>{}, i);
+            one(std::integral_constant<int, 3>{}, i);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            sum[turn][w][0][s][lane] = exp2_of(all * a2[s]);
+            sum[turn][w][1][s][lane] = hl[s];
+        }
+        __syncthreads();
+        if (block != first) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) h[s] = carry[turn][s][lane];
+        }
+        for (int i = 0; i < w; ++i)
+#pragma unroll
+            for (int s = 0; s < S; ++s) h[s] = fmaf(sum[turn][i][0][s][lane], h[s], sum[turn][i][1][s][lane]);
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = 4 * i + k;
+                v[k] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    h[s] = fmaf(at[t][s], h[s], add[t][s]);
+                    v[k] = fmaf(bc[w][1][t * 4 * S + n0 + s], h[s], v[k]);
+                }
+            }
+            const int t = t0 + 4 * i + p.j;
+            const float out = fmaf(skip, xv[i], over_four(v)) * gate[i];
+            if (t < end && p.in) y[(long long)t * a.channels + p.ch] = TY::store(out);
+        }
+        if (w == NW - 1) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) carry[turn ^ 1][s][lane] = h[s];
+        }
+    }
+    // (the last wave has the state behind the last block, the first one the state before any)
+    if (final && p.in && w == NW - 1) store_states<S>(final + kept, n0, a.state, h);
+    if ((a.clear & SELECTIVE_SCAN_CLEAR_Y) && seq == a.q.n_seq - 1 && p.in)
+        for (int t = end + 4 * w + p.j; t < a.q.n_tokens; t += 4 * NW)
+            y[(long long)t * a.channels + p.ch] = TY::store(0.0f);
+}
+
+// ------------------------------------------------------------------- backward
+// With G_t the gradient of h_t, and e what comes to it from behind,
+//   G_t = c_t gy_t + e,  e' = a_t G_t,
+// which is linear in e as the forward is in h, and is cut into the same stretches.
+
+// The states before each block of block_of(S) tokens, to kept[slot][channel][4 S].  The last
+// wave goes along the blocks; the others' part is their stretches.
+template <class TY, int S>
+__global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
+    Scan a, int channel_groups, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
+    const float* __restrict__ decay, const typename TY::S* __restrict__ b, const float* __restrict__ dt_bias,
+    const float* __restrict__ initial, float* __restrict__ kept) {
+    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4;
+    __shared__ float sum[2][NW][2][S][64];
+    __shared__ float bs[NW][T * 4 * S];
+    const Place p = place_of(a, blockIdx.x % channel_groups);
+    const int seq = blockIdx.x / channel_groups, lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = p.j * S;
+    int first, end;
+    span_of(a.q, seq, first, end);
+    float a2[S], h[S];
+    load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
+#pragma unroll
+    for (int s = 0; s < S; ++s) a2[s] *= kLog2e, h[s] = 0.0f;
+    if (initial) load_states<S>(initial + ((long long)seq * a.channels + p.ch) * a.state, n0, a.state, 0.0f, h);
+    const float bias = dt_bias ? dt_bias[p.ch] : 0.0f;
+    b += p.group * a.bg;
+    long long slot = first / (T * NW) + seq;
+    int turn = 0;
+    for (int block = first; block < end; block += T * NW, turn ^= 1, ++slot) {
+        if (w == NW - 1 && p.in) store_states<S>(kept + (slot * a.channels + p.ch) * (4 * S), n0, 4 * S, h);
+        const int t0 = block + w * T;
+        wave_fence();
+        stage<TY, S, T>(b, a.bt, t0, end, a.state, bs[w]);
+        wave_fence();
+        float step[Q], u[Q];
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            const int t = t0 + 4 * i + p.j;
+            const bool in = t < end;
+            const float xv = in ? TY::load(x[t * a.xt + p.ch]) : 0.0f;
+            const float pre = (in ? TY::load(dt[t * a.dtt + p.ch]) : 0.0f) + bias;
+            step[i] = in ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
+            u[i] = step[i] * xv;
+        }
+        float hl[S], all = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) hl[s] = 0.0f;
+        auto one = [&](auto k, int i) {
+            constexpr int J = decltype(k)::value;
+            const int t = 4 * i + J;
+            const float dl = from<J>(step[i]), ul = from<J>(u[i]);
+            all += dl;
+#pragma unroll
+            for (int s = 0; s < S; ++s) hl[s] = fmaf(exp2_of(dl * a2[s]), hl[s], ul * bs[w][t * 4 * S + n0 + s]);
+        };
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            one(std::integral_constant<int, 0>{}, i);
+            one(std::integral_constant<int, 1>{}, i);
+            one(std::integral_constant<int, 2>{}, i);
+            one(std::integral_constant<int, 3>{}, i);
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            sum[turn][w][0][s][lane] = exp2_of(all * a2[s]);
+            sum[turn][w][1][s][lane] = hl[s];
+        }
+        __syncthreads();
+        if (w == NW - 1)
+            for (int i = 0; i < NW; ++i)
+#pragma unroll
+                for (int s = 0; s < S; ++s) h[s] = fmaf(sum[turn][i][0][s][lane], h[s], sum[turn][i][1][s][lane]);
+    }
+}
+
+struct Grads {  // the backward's outputs and workspace
+    void *x, *dt, *z;
+    float *initial, *kept, *part_b, *part_c, *part_a, *part_d, *part_bias;
+    long long rows;  // of part_b and part_c: n_tokens * groups * state
+};
+
+// The sum of x over the lanes of the same j.
+__device__ __forceinline__ float over_quads(float x) {
+#pragma unroll
+    for (int off = 4; off < 64; off <<= 1) x += __shfl_xor(x, off);
+    return x;
+}
+
+// A workgroup has 16 channels and every parts-th sequence.
+template <class TY, int S>
+__global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
+    Scan a, int channel_groups, int parts, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
+    const float* __restrict__ decay, const typename TY::S* __restrict__ b, const typename TY::S* __restrict__ c,
+    const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias,
+    const typename TY::S* __restrict__ gy, const float* gfinal, Grads g) {
+    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4;
+    __shared__ float sum[2][NW][3][S][64];  // P, h' and e' of each wave
+    __shared__ float carry[2][S][64];
+    __shared__ float bc[NW][2][T * 4 * S];
+    const int index = blockIdx.x % channel_groups, part = blockIdx.x / channel_groups;
+    const Place p = place_of(a, index);
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = p.j * S;
+    using E = typename TY::S;
+    float a2[S];
+    double da[S], dd = 0.0, dbias = 0.0;
+    load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
+#pragma unroll
+    for (int s = 0; s < S; ++s) a2[s] *= kLog2e, da[s] = 0.0;
+    const float skip = d ? d[p.ch] : 0.0f, bias = dt_bias ? dt_bias[p.ch] : 0.0f;
+    b += p.group * a.bg;
+    c += p.group * a.cg;
+    const int in_group = index % (channel_groups / a.groups);
+    float* to_b = g.part_b + in_group * g.rows + p.group * a.state;
+    float* to_c = g.part_c + in_group * g.rows + p.group * a.state;
+    const long long row = (long long)a.groups * a.state;
+    int turn = 0;
+    for (int seq = part; seq < a.q.n_seq; seq += parts) {
+        int first, end;
+        span_of(a.q, seq, first, end);
+        const long long state_at = ((long long)seq * a.channels + p.ch) * a.state;
+        float e[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) e[s] = 0.0f;
+        if (gfinal) load_states<S>(gfinal + state_at, n0, a.state, 0.0f, e);
+        const int blocks = (end - first + T * NW - 1) / (T * NW);
+        for (int block = blocks - 1; block >= 0; --block, turn ^= 1) {
+            const int t0 = first + block * (T * NW) + w * T;
+            wave_fence();
+            stage<TY, S, T>(b, a.bt, t0, end, a.state, bc[w][0]);
+            stage<TY, S, T>(c, a.ct, t0, end, a.state, bc[w][1]);
+            wave_fence();
+            float xv[Q], pre[Q], step[Q], u[Q], gv[Q], zv[Q], gp[Q];
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const int t = t0 + 4 * i + p.j;
+                const bool in = t < end;
+                xv[i] = in ? TY::load(x[t * a.xt + p.ch]) : 0.0f;
+                pre[i] = (in ? TY::load(dt[t * a.dtt + p.ch]) : 0.0f) + bias;
+                zv[i] = in && z ? TY::load(z[t * a.zt + p.ch]) : 0.0f;
+                gv[i] = in && p.in ? TY::load(gy[t * a.gt + p.ch]) : 0.0f;
+                step[i] = in ? (a.softplus ? softplus_of(pre[i]) : pre[i]) : 0.0f;
+                u[i] = step[i] * xv[i];
+                gp[i] = z ? gv[i] * zv[i] * sigmoid_of(zv[i]) : gv[i];
+            }
+            float at[T][S], add[T][S], gl[T], hl[S], el[S], all = 0.0f;
+#pragma unroll
+            for (int s = 0; s < S; ++s) hl[s] = el[s] = 0.0f;
+            auto one = [&](auto k, int i) {
+                constexpr int J = decltype(k)::value;
+                const int t = 4 * i + J;
+                const float dl = from<J>(step[i]), ul = from<J>(u[i]);
+                gl[t] = from<J>(gp[i]);
+                all += dl;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    at[t][s] = exp2_of(dl * a2[s]);
+                    add[t][s] = ul * bc[w][0][t * 4 * S + n0 + s];
+                    hl[s] = fmaf(at[t][s], hl[s], add[t][s]);
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                one(std::integral_constant<int, 0>{}, i);
+                one(std::integral_constant<int, 1>{}, i);
+                one(std::integral_constant<int, 2>{}, i);
+                one(std::integral_constant<int, 3>{}, i);
+            }
+#pragma unroll
+            for (int t = T - 1; t >= 0; --t)
+#pragma unroll
+                for (int s = 0; s < S; ++s) el[s] = at[t][s] * fmaf(bc[w][1][t * 4 * S + n0 + s], gl[t], el[s]);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                sum[turn][w][0][s][lane] = exp2_of(all * a2[s]);
+                sum[turn][w][1][s][lane] = hl[s];
+                sum[turn][w][2][s][lane] = el[s];
+            }
+            float h[S];
+            const long long slot = first / (T * NW) + seq + block;
+            load_states<S>(g.kept + (slot * a.channels + p.ch) * (4 * S), n0, 4 * S, 0.0f, h);
+            __syncthreads();
+            if (block != blocks - 1) {
+#pragma unroll
+                for (int s = 0; s < S; ++s) e[s] = carry[turn][s][lane];
+            }
+            for (int i = 0; i < w; ++i)
+#pragma unroll
+                for (int s = 0; s < S; ++s) h[s] = fmaf(sum[turn][i][0][s][lane], h[s], sum[turn][i][1][s][lane]);
+            for (int i = NW - 1; i > w; --i)
+#pragma unroll
+                for (int s = 0; s < S; ++s) e[s] = fmaf(sum[turn][i][0][s][lane], e[s], sum[turn][i][2][s][lane]);
+            float ypre[Q], gu[Q], ga[Q], das[S];
+#pragma unroll
+            for (int s = 0; s < S; ++s) das[s] = 0.0f;
+            // forward: `add` becomes a_t h_{t-1}
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = 4 * i + k;
+                    v[k] = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        const float ah = at[t][s] * h[s];
+                        h[s] = ah + add[t][s];
+                        add[t][s] = ah;
+                        v[k] = fmaf(bc[w][1][t * 4 * S + n0 + s], h[s], v[k]);
+                        const float gc = over_quads(p.in ? gl[t] * h[s] : 0.0f);
+                        if (p.quad == 0 && t0 + t < end && n0 + s < a.state) to_c[(t0 + t) * row + n0 + s] = gc;
+                    }
+                }
+                ypre[i] = over_four(v);
+            }
+            // back
+            auto back = [&](auto k, int i, float (&v)[4], float (&r)[4]) {
+                constexpr int J = decltype(k)::value;
+                const int t = 4 * i + J;
+                const float dl = from<J>(step[i]), ul = from<J>(u[i]);
+                v[J] = r[J] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const float G = fmaf(bc[w][1][t * 4 * S + n0 + s], gl[t], e[s]);
+                    const float gb = over_quads(p.in ? G * ul : 0.0f);
+                    if (p.quad == 0 && t0 + t < end && n0 + s < a.state) to_b[(t0 + t) * row + n0 + s] = gb;
+                    v[J] = fmaf(G, bc[w][0][t * 4 * S + n0 + s], v[J]);
+                    const float q = G * add[t][s];
+                    r[J] = fmaf(q, a2[s], r[J]);
+                    das[s] = fmaf(q, dl, das[s]);
+                    e[s] = at[t][s] * G;
+                }
+            };
+#pragma unroll
+            for (int i = Q - 1; i >= 0; --i) {
+                float v[4], r[4];
+                back(std::integral_constant<int, 3>{}, i, v, r);
+                back(std::integral_constant<int, 2>{}, i, v, r);
+                back(std::integral_constant<int, 1>{}, i, v, r);
+                back(std::integral_constant<int, 0>{}, i, v, r);
+                gu[i] = over_four(v);
+                ga[i] = over_four(r);
+            }
+#pragma unroll
+            for (int s = 0; s < S; ++s) da[s] += das[s];
+            if (w == 0) {
+#pragma unroll
+                for (int s = 0; s < S; ++s) carry[turn ^ 1][s][lane] = e[s];
+            }
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                const int t = t0 + 4 * i + p.j;
+                if (t >= end || !p.in) continue;
+                const long long to = (long long)t * a.channels + p.ch;
+                const float gstep = fmaf(gu[i], xv[i], ga[i] * kLn2);
+                const float gdt = a.softplus ? gstep * sigmoid_of(pre[i]) : gstep;
+                static_cast<E*>(g.x)[to] = TY::store(fmaf(gu[i], step[i], skip * gp[i]));
+                static_cast<E*>(g.dt)[to] = TY::store(gdt);
+                if (z) {
+                    const float sig = sigmoid_of(zv[i]);
+                    static_cast<E*>(g.z)[to] = TY::store(gv[i] * fmaf(skip, xv[i], ypre[i]) * sig * (1.0f + zv[i] * (1.0f - sig)));
+                }
+                dd += gp[i] * xv[i];
+                dbias += gdt;
+            }
+        }
+        if (g.initial && p.in && w == 0) store_states<S>(g.initial + state_at, n0, a.state, e);
+        if (a.clear && seq == a.q.n_seq - 1 && p.in)
+            for (int t = end + 4 * w + p.j; t < a.q.n_tokens; t += 4 * NW) {
+                const long long to = (long long)t * a.channels + p.ch;
+                if (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_X) static_cast<E*>(g.x)[to] = TY::store(0.0f);
+                if (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_DT) static_cast<E*>(g.dt)[to] = TY::store(0.0f);
+                if (z && (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_Z)) static_cast<E*>(g.z)[to] = TY::store(0.0f);
+            }
+    }
+    // the waves' sums together
+    __syncthreads();
+    __shared__ double all[NW][64];
+#pragma unroll
+    for (int s = 0; s < S + 2; ++s) {
+        double v = s < S ? da[s < S ? s : 0] : s == S ? dd : dbias;
+        if (s >= S) {  // of the lanes' tokens
+            v += __shfl_xor(v, 1);
+            v += __shfl_xor(v, 2);
+        }
+        all[w][lane] = v;
+        __syncthreads();
+        if (w == 0 && p.in) {
+            v = all[0][lane];
+#pragma unroll
+            for (int i = 1; i < NW; ++i) v += all[i][lane];
+            if (s < S) {
+                if (n0 + s < a.state) g.part_a[((long long)part * a.channels + p.ch) * a.state + n0 + s] = (float)v;
+            } else if (p.j == 0) {
+                (s == S ? g.part_d : g.part_bias)[(long long)part * a.channels + p.ch] = (float)v;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// What the workgroups left, summed: b's and c's gradients over the channels' workgroups, a's,
+// d's and dt_bias's over the sequences' parts.  A thread has an element.
+constexpr int kSumThreads = 256;
+template <class TY>
+__global__ __launch_bounds__(kSumThreads) void scan_sums_kernel(Scan a, Grads g, int in_group, int parts,
+                                                                typename TY::S* __restrict__ gb,
+                                                                typename TY::S* __restrict__ gc, float* __restrict__ ga,
+                                                                float* __restrict__ gd, float* __restrict__ gbias) {
+    long long i = (long long)blockIdx.x * kSumThreads + threadIdx.x;
+    const long long row = (long long)a.groups * a.state;
+    if (i < 2 * g.rows) {
+        const bool is_c = i >= g.rows;
+        if (is_c) i -= g.rows;
+        const float* from = is_c ? g.part_c : g.part_b;
+        typename TY::S* to = is_c ? gc : gb;
+        const int last = a.q.offsets ? min(max(a.q.offsets[a.q.n_seq], 0), a.q.n_tokens) : a.q.n_tokens;
+        if (i / row >= last) {
+            if (a.clear & (is_c ? SELECTIVE_SCAN_CLEAR_GRAD_C : SELECTIVE_SCAN_CLEAR_GRAD_B)) to[i] = TY::store(0.0f);
+            return;
+        }
+        double v = 0.0;
+        for (int k = 0; k < in_group; ++k) v += from[k * g.rows + i];
+        to[i] = TY::store((float)v);
+        return;
+    }
+    i -= 2 * g.rows;
+    const long long na = (long long)a.channels * a.state;
+    const float* from;
+    float* to;
+    long long n;
+    if (i < na) {
+        from = g.part_a, to = ga, n = na;
+    } else if (i < na + 2LL * a.channels) {
+        i -= na;
+        const bool second = i >= a.channels;
+        if (second) i -= a.channels;
+        from = second ? g.part_bias : g.part_d, to = second ? gbias : gd, n = a.channels;
+    } else {
+        return;
+    }
+    if (!to) return;
+    double v = 0.0;
+    for (int k = 0; k < parts; ++k) v += from[k * n + i];
+    to[i] = (float)v;
+}
+
+// ----------------------------------------------------------------------- step
+constexpr int kStepThreads = 256;
+template <class TY, int S>
+__global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
+    Scan a, long long waves, int channel_groups, const typename TY::S* __restrict__ x,
+    const typename TY::S* __restrict__ dt, const float* __restrict__ decay, const typename TY::S* __restrict__ b,
+    const typename TY::S* __restrict__ c, const float* __restrict__ d, const typename TY::S* __restrict__ z,
+    const float* __restrict__ dt_bias, float* states, int pool, const int* __restrict__ slots,
+    typename TY::S* __restrict__ y) {
+    const long long wave =
+        (long long)blockIdx.x * (kStepThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= waves) return;
+    const Place p = place_of(a, (int)(wave % channel_groups));
+    const int lane = threadIdx.x & 63, n0 = p.j * S, rows = a.q.n_tokens;
+    int row = (int)(wave / channel_groups), slot = row;
+    if (slots) {
+        slot = __builtin_amdgcn_readfirstlane(slots[row]);
+        if (slot < 0 || slot >= pool) {
+            if (p.in && p.j == 0) y[(long long)row * a.channels + p.ch] = TY::store(0.0f);
+            return;
+        }
+        for (int j = 0; j < row; j += 64)  // the first row of a slot takes all
+            if (__ballot(j + lane < row && slots[min(j + lane, rows - 1)] == slot)) return;
+    }
+    float* state = states + ((long long)slot * a.channels + p.ch) * a.state;
+    float a2[S], h[S];
+    load_states<S>(state, n0, a.state, 0.0f, h);
+    load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
+    const float skip = d ? d[p.ch] : 0.0f, bias = dt_bias ? dt_bias[p.ch] : 0.0f;
+    b += p.group * a.bg;
+    c += p.group * a.cg;
+    while (row < rows) {
+        const float xv = TY::load(x[row * a.xt + p.ch]), pre = TY::load(dt[row * a.dtt + p.ch]) + bias;
+        const float step = a.softplus ? softplus_of(pre) : pre, u = step * xv;
+        float v = 0.0f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const bool in = n0 + s < a.state;
+            const float bv = in ? TY::load(b[row * a.bt + n0 + s]) : 0.0f, cv = in ? TY::load(c[row * a.ct + n0 + s]) : 0.0f;
+            h[s] = fmaf(exp2_of(step * a2[s] * kLog2e), h[s], u * bv);
+            v = fmaf(cv, h[s], v);
+        }
+        v += quad_perm<0xB1>(v);
+        v += quad_perm<0x4E>(v);
+        float out = fmaf(skip, xv, v);
+        if (z) {
+            const float zv = TY::load(z[row * a.zt + p.ch]);
+            out *= zv * sigmoid_of(zv);
+        }
+        if (p.in && p.j == 0) y[(long long)row * a.channels + p.ch] = TY::store(out);
+        if (!slots) break;
+        int next = rows;
+        for (int j = row + 1; j < rows; j += 64) {
+            const unsigned long long m = __ballot(j + lane < rows && slots[min(j + lane, rows - 1)] == slot);
+            if (m) {
+                next = j + __builtin_ctzll(m);
+                break;
+            }
+        }
+        row = next;
+    }
+    if (p.in) store_states<S>(state, n0, a.state, h);
+}
+
+// ---------------------------------------------------------- host helpers
+constexpr long long kMaxTokens = (1LL << 31) - (1LL << 16);
+constexpr long long kMaxBlocks = (1LL << 32) / 512 - 8;  // a grid has fewer than 2^32 work-items
+
+int check_shape(const selective_scan_shape_t* p, bool step, Scan* a) {
+    if (!p) return CFC_ERR_NULL;
+    if (p->type != CFC_TYPE_F32 && p->type != CFC_TYPE_BF16 && p->type != CFC_TYPE_F16) return CFC_ERR_UNSUPPORTED;
+    if (p->channels < 1 || p->groups < 1 || p->channels % p->groups || p->state < 1) return CFC_ERR_DIM;
+    for (const long long stride : {p->x_stride, p->dt_stride, p->z_stride, p->grad_y_stride, p->b_stride_t,
+                                   p->b_stride_g, p->c_stride_t, p->c_stride_g})
+        if (stride < 0) return CFC_ERR_DIM;
+    if (p->state > SELECTIVE_SCAN_MAX_STATE || p->n_tokens > kMaxTokens) return CFC_ERR_UNSUPPORTED;
+    if (step) {
+        if (p->n_tokens < 0) return CFC_ERR_DIM;
+        a->q = Sequences{nullptr, (int)p->n_tokens, 1, (int)p->n_tokens};
+    } else if (const int e = check_sequences(p->offsets, p->n_seq, p->seq_len, p->n_tokens, &a->q)) {
+        return e;
+    }
+    a->channels = p->channels;
+    a->groups = p->groups;
+    a->share = p->channels / p->groups;
+    a->state = p->state;
+    a->softplus = p->softplus;
+    a->clear = p->offsets ? p->clear_rest : 0;
+    a->xt = p->x_stride, a->dtt = p->dt_stride, a->zt = p->z_stride, a->gt = p->grad_y_stride;
+    a->bt = p->b_stride_t, a->bg = p->b_stride_g, a->ct = p->c_stride_t, a->cg = p->c_stride_g;
+    const long long groups = (long long)a->groups * ((a->share + kGroupCh - 1) / kGroupCh);
+    return groups * std::max(1, a->q.n_seq) > kMaxBlocks ? CFC_ERR_UNSUPPORTED : CFC_OK;
+}
+inline int channel_groups_of(const Scan& a) { return a.groups * ((a.share + kGroupCh - 1) / kGroupCh); }
+
+struct Sizes {  // bytes of the arguments
+    long long x, dt, z, gy, b, c, rows, shared, a, d, states;
+};
+bool sizes_of(const selective_scan_shape_t* p, const Scan& a, Sizes* z) {
+    const int size = size_of(p->type);
+    const long long t = p->n_tokens;
+    long long each;
+    z->a = (long long)a.channels * a.state * 4;
+    z->d = (long long)a.channels * 4;
+    return extent(t, 1, a.channels, a.xt, 0, size, &z->x) && extent(t, 1, a.channels, a.dtt, 0, size, &z->dt) &&
+           extent(t, 1, a.channels, a.zt, 0, size, &z->z) && extent(t, 1, a.channels, a.gt, 0, size, &z->gy) &&
+           extent(t, a.groups, a.state, a.bt, a.bg, size, &z->b) && extent(t, a.groups, a.state, a.ct, a.cg, size, &z->c) &&
+           mul_ok(t, (long long)a.channels * size, &z->rows) && mul_ok((long long)a.groups * a.state, size, &each) &&
+           mul_ok(t, each, &z->shared) && mul_ok(a.q.n_seq, z->a, &z->states);
+}
+
+// Calls f with the type and the states of a lane, a power of two that four lanes hold `state` in.
+template <class F>
+int with_state(int type, int state, F f) {
+    auto go = [&](auto ty) {
+        if (state <= 4) return f(ty, std::integral_constant<int, 1>{});
+        if (state <= 8) return f(ty, std::integral_constant<int, 2>{});
+        if (state <= 16) return f(ty, std::integral_constant<int, 4>{});
+        if (state <= 32) return f(ty, std::integral_constant<int, 8>{});
+        return f(ty, std::integral_constant<int, 16>{});
+    };
+    if (type == CFC_TYPE_F32) return go(F32{});
+    return type == CFC_TYPE_BF16 ? go(BF16{}) : go(F16{});
+}
+inline int lane_states(int state) { return state <= 4 ? 1 : state <= 8 ? 2 : state <= 16 ? 4 : state <= 32 ? 8 : 16; }
+
+// The sequences go to as many workgroups for each 16 channels as fill the chip, since each
+// leaves a row of partial sums.
+inline int parts_of(const Scan& a) {
+    return std::min(a.q.n_seq, std::max(1, 1024 / channel_groups_of(a)));
+}
+
+// Bytes of the backward's workspace, laid out from `base` on.
+long long lay_out(const Scan& a, void* base, Grads* g) {
+    const int s = lane_states(a.state);
+    const long long slots = a.q.n_tokens / block_of(s) + a.q.n_seq;
+    const long long in_group = channel_groups_of(a) / a.groups, parts = parts_of(a);
+    long long kept, bc, pa, all = 0;
+    g->rows = (long long)a.q.n_tokens * a.groups * a.state;
+    if (!mul_ok(slots * a.channels, 4 * s * 4, &kept) || !mul_ok(g->rows, in_group * 4, &bc) ||
+        !mul_ok(parts, (long long)a.channels * a.state * 4, &pa) ||
+        2 * g->rows + (long long)a.channels * (a.state + 2) > kMaxBlocks * 256)
+        return -1;
+    auto take = [&](long long bytes) {
+        float* at = reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(base) + all);
+        all += (bytes + 15) / 16 * 16;
+        return at;
+    };
+    g->kept = take(kept);
+    g->part_b = take(bc);
+    g->part_c = take(bc);
+    g->part_a = take(pa);
+    g->part_d = take(parts * a.channels * 4);
+    g->part_bias = take(parts * a.channels * 4);
+    return all;
+}
+
+}  // namespace
+
+// ================================================================ C ABI
+extern "C" int selective_scan_forward(const selective_scan_shape_t* shape, const void* x, const void* dt, const float* a_,
+                                      const void* b, const void* c, const float* d, const void* z, const float* dt_bias,
+                                      const float* initial_state, void* y, float* final_state, hipStream_t stream) {
+    Scan a;
+    Sizes n;
+    if (const int e = check_shape(shape, false, &a)) return e;
+    if (!sizes_of(shape, a, &n)) return CFC_ERR_DIM;
+    if (a.q.n_seq == 0) return CFC_OK;
+    if (!a_ || (a.q.n_tokens && (!x || !dt || !b || !c || !y))) return CFC_ERR_NULL;
+    if (!fits({x, dt, b, c, z, y}, size_of(shape->type)) || !fits({a_, d, dt_bias, initial_state, final_state}, 4))
+        return CFC_ERR_DIM;
+    const Range ini = bytes_of(initial_state, n.states), fin = bytes_of(final_state, n.states);
+    const Range outs[] = {bytes_of(y, n.rows), fin};
+    const Range ins[] = {bytes_of(x, n.x), bytes_of(dt, n.dt), bytes_of(a_, n.a), bytes_of(b, n.b), bytes_of(c, n.c),
+                         bytes_of(d, n.d), bytes_of(z, n.z), bytes_of(dt_bias, n.d), offsets_range(a.q),
+                         same(ini, fin) ? Range{0, 0} : ini};
+    if (!outputs_disjoint(outs, 2, ins, 10) || overlap(outs[0], ini)) return CFC_ERR_OVERLAP;
+    return with_state(shape->type, a.state, [&](auto ty, auto states) {
+        using TY = decltype(ty);
+        using E = typename TY::S;
+        constexpr int S = decltype(states)::value;
+        const int groups = channel_groups_of(a);
+        hipLaunchKernelGGL((scan_kernel<TY, S>), dim3((unsigned)(groups * (long long)a.q.n_seq)), dim3(64 * waves_of(S)),
+                           0, stream, a, groups, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d, (const E*)z,
+                           dt_bias, initial_state, (E*)y, final_state);
+        return launch_status();
+    });
+}
+
+extern "C" long long selective_scan_backward_workspace(const selective_scan_shape_t* shape) {
+    Scan a;
+    Grads g;
+    return check_shape(shape, false, &a) == CFC_OK ? lay_out(a, nullptr, &g) : -1;
+}
+
+extern "C" int selective_scan_backward(const selective_scan_shape_t* shape, const void* x, const void* dt,
+                                       const float* a_, const void* b, const void* c, const float* d, const void* z,
+                                       const float* dt_bias, const float* initial_state, const void* grad_y,
+                                       const float* grad_final_state, void* grad_x, void* grad_dt, float* grad_a,
+                                       void* grad_b, void* grad_c, float* grad_d, void* grad_z, float* grad_dt_bias,
+                                       float* grad_initial_state, void* workspace, long long workspace_bytes,
+                                       hipStream_t stream) {
+    Scan a;
+    Sizes n;
+    Grads g;
+    if (const int e = check_shape(shape, false, &a)) return e;
+    const long long need = lay_out(a, workspace, &g);
+    if (!sizes_of(shape, a, &n) || need < 0) return CFC_ERR_DIM;
+    if (!a_ || !grad_a || (need && !workspace) ||
+        (a.q.n_tokens && (!x || !dt || !b || !c || !grad_y || !grad_x || !grad_dt || !grad_b || !grad_c || (z && !grad_z))))
+        return CFC_ERR_NULL;
+    if (need && (workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16)) return CFC_ERR_DIM;
+    if (!z && grad_z) return CFC_ERR_DIM;
+    if (!fits({x, dt, b, c, z, grad_y, grad_x, grad_dt, grad_b, grad_c, grad_z}, size_of(shape->type)) ||
+        !fits({a_, d, dt_bias, initial_state, grad_final_state, grad_a, grad_d, grad_dt_bias, grad_initial_state}, 4))
+        return CFC_ERR_DIM;
+    const Range gin = bytes_of(grad_initial_state, n.states), gfin = bytes_of(grad_final_state, n.states);
+    const Range outs[] = {bytes_of(grad_x, n.rows), bytes_of(grad_dt, n.rows), bytes_of(grad_a, n.a),
+                          bytes_of(grad_b, n.shared), bytes_of(grad_c, n.shared), bytes_of(grad_d, n.d),
+                          bytes_of(grad_z, n.rows), bytes_of(grad_dt_bias, n.d), gin, bytes_of(need ? workspace : nullptr, need)};
+    const Range ins[] = {bytes_of(x, n.x), bytes_of(dt, n.dt), bytes_of(a_, n.a), bytes_of(b, n.b), bytes_of(c, n.c),
+                         bytes_of(d, n.d), bytes_of(z, n.z), bytes_of(dt_bias, n.d), bytes_of(initial_state, n.states),
+                         bytes_of(grad_y, n.gy), offsets_range(a.q), same(gin, gfin) ? Range{0, 0} : gfin};
+    if (!outputs_disjoint(outs, 10, ins, 12)) return CFC_ERR_OVERLAP;
+    for (int i = 0; same(gin, gfin) && i < 10; ++i)
+        if (i != 8 && overlap(outs[i], gfin)) return CFC_ERR_OVERLAP;
+    g.x = grad_x, g.dt = grad_dt, g.z = grad_z, g.initial = grad_initial_state;
+    return with_state(shape->type, a.state, [&](auto ty, auto states) {
+        using TY = decltype(ty);
+        using E = typename TY::S;
+        constexpr int S = decltype(states)::value;
+        const int groups = channel_groups_of(a), parts = parts_of(a);
+        if (a.q.n_seq) {
+            hipLaunchKernelGGL((scan_states_kernel<TY, S>), dim3((unsigned)(groups * (long long)a.q.n_seq)),
+                               dim3(64 * waves_of(S)), 0, stream, a, groups, (const E*)x, (const E*)dt, a_, (const E*)b,
+                               dt_bias, initial_state, g.kept);
+            hipLaunchKernelGGL((scan_backward_kernel<TY, S>), dim3((unsigned)(groups * parts)), dim3(64 * waves_of(S)), 0,
+                               stream, a, groups, parts, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
+                               (const E*)z, dt_bias, (const E*)grad_y, grad_final_state, g);
+        }
+        const long long elements = 2 * g.rows + (long long)a.channels * (a.state + 2);
+        hipLaunchKernelGGL((scan_sums_kernel<TY>), dim3((unsigned)((elements + kSumThreads - 1) / kSumThreads)),
+                           dim3(kSumThreads), 0, stream, a, g, groups / a.groups, parts, (E*)grad_b, (E*)grad_c, grad_a,
+                           grad_d, grad_dt_bias);
+        return launch_status();
+    });
+}
+
+extern "C" int selective_scan_step(const selective_scan_shape_t* shape, const void* x, const void* dt, const float* a_,
+                                   const void* b, const void* c, const float* d, const void* z, const float* dt_bias,
+                                   float* states, int pool, const int* slots, void* y, hipStream_t stream) {
+    Scan a;
+    Sizes n;
+    long long held;
+    if (const int e = check_shape(shape, true, &a)) return e;
+    if (pool < 0 || (!slots && pool < a.q.n_tokens) || !sizes_of(shape, a, &n) || !mul_ok(pool, n.a, &held))
+        return CFC_ERR_DIM;
+    if (a.q.n_tokens == 0) return CFC_OK;
+    if (!x || !dt || !a_ || !b || !c || !y || (pool && !states)) return CFC_ERR_NULL;
+    if (!fits({x, dt, b, c, z, y}, size_of(shape->type)) || !fits({a_, d, dt_bias, states, slots}, 4)) return CFC_ERR_DIM;
+    const Range outs[] = {bytes_of(y, n.rows), bytes_of(states, held)};
+    const Range ins[] = {bytes_of(x, n.x), bytes_of(dt, n.dt), bytes_of(a_, n.a), bytes_of(b, n.b), bytes_of(c, n.c),
+                         bytes_of(d, n.d), bytes_of(z, n.z), bytes_of(dt_bias, n.d),
+                         bytes_of(slots, (long long)a.q.n_tokens * 4)};
+    if (!outputs_disjoint(outs, 2, ins, 9)) return CFC_ERR_OVERLAP;
+    return with_state(shape->type, a.state, [&](auto ty, auto s) {
+        using TY = decltype(ty);
+        using E = typename TY::S;
+        constexpr int S = decltype(s)::value;
+        const int groups = channel_groups_of(a);
+        const long long waves = (long long)groups * a.q.n_tokens;
+        constexpr int per = kStepThreads / 64;
+        hipLaunchKernelGGL((scan_step_kernel<TY, S>), dim3((unsigned)((waves + per - 1) / per)), dim3(kStepThreads), 0,
+                           stream, a, waves, groups, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
+                           (const E*)z, dt_bias, states, pool, slots, (E*)y);
+        return launch_status();
+    });
+}

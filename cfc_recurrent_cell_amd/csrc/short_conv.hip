@@ -1,0 +1,576 @@
+// short_conv.hip -- gfx950 kernels and C ABI of the short causal convolution (see
+// include/short_conv.h).
+//
+// Memory is the bound: each input is read once and each output written once, so a wave
+// has a tile of tokens and 8 channels a lane (16 bytes of a 16-bit type), all of its rows'
+// loads in flight at once, and the last width - 1 inputs in registers as it goes from token
+// to token.  Rows that a tile shares with the one before are read twice, mostly from the
+// cache.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "elements.h"
+#include "functions.h"
+#include "sequences.h"
+#include "short_conv.h"
+
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kLaneCh = 8, kWaveCh = 64 * kLaneCh;
+constexpr int kTile = 16;      // tokens of a wave, forward
+constexpr int kAhead = 4;      // rows that are loaded at once, while as many are worked on
+constexpr int kGradTile = 64;  // tokens of a wave, backward: a row of partial sums each
+
+struct Conv {
+    Sequences q;
+    int channels, silu, clear;
+    long long xt, gt;
+};
+
+// The channels' weights as w[tap][channel], zero behind the last channel.
+template <class TY, int W>
+__device__ __forceinline__ void load_weights(const typename TY::S* weight, int c, int channels, float (&w)[W][8]) {
+    float f[W][8];
+#pragma unroll
+    for (int i = 0; i < W; ++i) load8<TY>(weight, c * W + 8 * i, channels * W, f[i]);
+#pragma unroll
+    for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[j][e] = f[(e * W + j) / 8][(e * W + j) % 8];
+}
+
+// The width - 1 inputs before row t of the sequence s that begins at `first`: its own rows,
+// or its initial state's.
+template <class TY, int W>
+__device__ __forceinline__ void load_window(const Conv& a, const typename TY::S* x, const typename TY::S* initial, int s,
+                                            int first, int t, int c, float (&win)[W - 1][8]) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int row = t - (W - 1) + j;
+        if (row >= first)
+            load8<TY>(x + row * a.xt, c, a.channels, win[j]);
+        else if (initial)
+            load8<TY>(initial + ((long long)s * (W - 1) + min(max(row - first + W - 1, 0), W - 2)) * a.channels, c,
+                      a.channels, win[j]);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) win[j][e] = 0.0f;
+    }
+}
+
+// p of the next token, whose input is `now`.
+template <int W>
+__device__ __forceinline__ void apply(const float (&w)[W][8], const float (&b)[8], const float (&win)[W - 1][8],
+                                      const float (&now)[8], float (&p)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        p[e] = b[e];
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) p[e] += w[j][e] * win[j][e];
+        p[e] += w[W - 1][e] * now[e];
+    }
+}
+template <int W>
+__device__ __forceinline__ void shift(float (&win)[W - 1][8], const float (&now)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+        for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
+        win[W - 2][e] = now[e];
+    }
+}
+
+// Waves `begin` ... of the tiles' waves and, behind them, of the final states', a sequence
+// and 512 channels each.
+template <class TY, int W>
+__global__ __launch_bounds__(kThreads) void conv_kernel(Conv a, long long begin, long long end_wave, long long tiles,
+                                                        const typename TY::S* __restrict__ x,
+                                                        const typename TY::S* __restrict__ weight,
+                                                        const typename TY::S* __restrict__ bias,
+                                                        const typename TY::S* initial, typename TY::S* __restrict__ y,
+                                                        typename TY::S* final) {
+    const long long wave = begin + (long long)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= end_wave) return;
+    const int parts = (a.channels + kWaveCh - 1) / kWaveCh;
+    const int c = (int)(wave % parts) * kWaveCh + (threadIdx.x & 63) * kLaneCh;
+    const long long at = wave / parts;
+    if (at >= tiles) {
+        const int s = (int)(at - tiles);
+        int first, end;
+        span_of(a.q, s, first, end);
+        float win[W - 1][8];
+        load_window<TY, W>(a, x, initial, s, first, end, c, win);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            store8<TY>(final + ((long long)s * (W - 1) + j) * a.channels, c, a.channels, win[j]);
+        return;
+    }
+    const int t0 = (int)at * kTile, n = min(kTile, a.q.n_tokens - t0);
+    int s = sequence_of(a.q, t0), first, end;
+    span_of(a.q, s, first, end);
+    Eight<TY> rows[2][kAhead];
+    auto fetch = [&](Eight<TY>(&to)[kAhead], int i0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i < n) to[i] = fetch8<TY>(x + (t0 + i0 + i) * a.xt, c, a.channels);
+    };
+    fetch(rows[0], 0);
+    fetch(rows[1], kAhead);
+    float w[W][8], b[8], win[W - 1][8];
+    load_weights<TY, W>(weight, c, a.channels, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = 0.0f;
+    if (bias) load8<TY>(bias, c, a.channels, b);
+    bool live = t0 >= first && t0 < end;  // or behind the last sequence
+    if (live) load_window<TY, W>(a, x, initial, s, first, t0, c, win);
+    auto some = [&](Eight<TY>(&from)[kAhead], int i0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int t = t0 + i0 + i;
+            if (live && t >= end) {
+                s = sequence_of(a.q, t);
+                span_of(a.q, s, first, end);
+                live = t >= first && t < end;
+                if (live) load_window<TY, W>(a, x, initial, s, first, t, c, win);
+            }
+            if (i0 + i < n && live) {
+                float now[8], p[8];
+                unpack8<TY>(from[i], now);
+                apply<W>(w, b, win, now, p);
+                shift<W>(win, now);
+                if (a.silu) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) p[e] *= sigmoid_of(p[e]);
+                }
+                store8<TY>(y + (long long)t * a.channels, c, a.channels, p);
+            } else if (i0 + i < n && a.clear) {
+                const float none[8] = {};
+                store8<TY>(y + (long long)t * a.channels, c, a.channels, none);
+            }
+        }
+    };
+    for (int i = 0; i < kTile; i += 2 * kAhead) {
+        some(rows[0], i);
+        fetch(rows[0], i + 2 * kAhead);
+        some(rows[1], i + kAhead);
+        fetch(rows[1], i + 3 * kAhead);
+    }
+}
+
+// grad_p = grad_y * y'(p)
+__device__ __forceinline__ void through(int silu, const float (&p)[8], float (&g)[8]) {
+    if (!silu) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float sig = sigmoid_of(p[e]);
+        g[e] *= sig * (1.0f + p[e] * (1.0f - sig));
+    }
+}
+
+// A wave has kGradTile tokens and 512 channels.  It computes p again for its own tokens
+// and, since grad_x_t takes grad_p of the width - 1 tokens behind t, for as many behind
+// them; `next` holds what the tokens up to now give to the gradients of the last width - 1
+// inputs.  Behind the tiles' waves the initial states', a sequence each.
+template <class TY, int W>
+__global__ __launch_bounds__(kThreads) void conv_backward_kernel(
+    Conv a, long long waves, long long tiles, const typename TY::S* __restrict__ x,
+    const typename TY::S* __restrict__ weight, const typename TY::S* __restrict__ bias,
+    const typename TY::S* __restrict__ initial, const typename TY::S* __restrict__ gy,
+    const typename TY::S* __restrict__ gfinal, typename TY::S* __restrict__ gx, typename TY::S* __restrict__ ginit,
+    float* __restrict__ part) {
+    const long long wave = (long long)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= waves) return;
+    const int parts = (a.channels + kWaveCh - 1) / kWaveCh;
+    const int c = (int)(wave % parts) * kWaveCh + (threadIdx.x & 63) * kLaneCh;
+    const long long at = wave / parts;
+    float w[W][8], b[8], win[W - 1][8];
+    load_weights<TY, W>(weight, c, a.channels, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = 0.0f;
+    if (bias) load8<TY>(bias, c, a.channels, b);
+    // next[k] of the input k + 1 tokens back, after a token's step
+    float next[W][8];
+    auto clear = [&] {
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) next[k][e] = 0.0f;
+    };
+    clear();
+    auto load_final = [&](int s, int row, float (&g)[8]) {
+        if (gfinal)
+            load8<TY>(gfinal + ((long long)s * (W - 1) + row) * a.channels, c, a.channels, g);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = 0.0f;
+    };
+    int first, end;
+    if (at >= tiles) {
+        const int s = (int)(at - tiles);
+        span_of(a.q, s, first, end);
+        load_window<TY, W>(a, x, initial, s, first, first, c, win);
+        float g0[W - 1][8];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g0[i][e] = 0.0f;
+#pragma unroll
+        for (int p = 0; p < W - 1; ++p) {
+            if (first + p >= end) break;
+            float now[8], pre[8], g[8];
+            load8<TY>(x + (first + p) * a.xt, c, a.channels, now);
+            load8<TY>(gy + (first + p) * a.gt, c, a.channels, g);
+            apply<W>(w, b, win, now, pre);
+            shift<W>(win, now);
+            through(a.silu, pre, g);
+            // kept input i is the tap i - p of place p
+#pragma unroll
+            for (int i = p; i < W - 1; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g0[i][e] += w[i - p][e] * g[e];
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            const int kept = i - (end - first);  // where it is in the final state
+            if (kept >= 0) {
+                float f[8];
+                load_final(s, kept, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g0[i][e] += f[e];
+            }
+            store8<TY>(ginit + ((long long)s * (W - 1) + i) * a.channels, c, a.channels, g0[i]);
+        }
+        return;
+    }
+    float sum[W + 1][8];
+#pragma unroll
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[j][e] = 0.0f;
+    const int t0 = (int)at * kGradTile, own = min(t0 + kGradTile, a.q.n_tokens);
+    int s = sequence_of(a.q, t0);
+    span_of(a.q, s, first, end);
+    int t = t0;
+    if (t0 >= first && t0 < end) {
+        load_window<TY, W>(a, x, initial, s, first, t0, c, win);
+        // the end of a sequence, or of the tokens whose gradients the tile's own need
+        while (true) {
+            const int until = min(end, own + W - 1);
+            for (; t < until; ++t) {
+                float now[8], p[8], g[8];
+                load8<TY>(x + t * a.xt, c, a.channels, now);
+                load8<TY>(gy + t * a.gt, c, a.channels, g);
+                apply<W>(w, b, win, now, p);
+                through(a.silu, p, g);
+                if (t < own) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) sum[j][e] += g[e] * win[j][e];
+                        sum[W - 1][e] += g[e] * now[e];
+                        sum[W][e] += g[e];
+                    }
+                }
+                shift<W>(win, now);
+                // input t - k is the tap W - 1 - k of token t
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                    for (int k = W - 1; k > 0; --k) next[k][e] = next[k - 1][e] + w[W - 1 - k][e] * g[e];
+                    next[0][e] = w[W - 1][e] * g[e];
+                }
+                const int done = t - (W - 1);
+                if (done >= t0 && done >= first) store8<TY>(gx + (long long)done * a.channels, c, a.channels, next[W - 1]);
+            }
+            if (until == end) {  // the sequence's last inputs, which its final state holds too
+#pragma unroll
+                for (int k = W - 2; k >= 0; --k) {
+                    const int done = end - 1 - k;
+                    if (done >= t0 && done >= first && done < own) {
+                        float f[8];
+                        load_final(s, W - 2 - k, f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] += next[k][e];
+                        store8<TY>(gx + (long long)done * a.channels, c, a.channels, f);
+                    }
+                }
+            }
+            if (t >= own) break;
+            s = sequence_of(a.q, t);
+            span_of(a.q, s, first, end);
+            if (t < first || t >= end) break;
+            clear();
+            load_window<TY, W>(a, x, initial, s, first, t, c, win);
+        }
+    }
+    if (a.clear) {  // behind the last sequence
+        const float none[8] = {};
+        for (; t < own; ++t) store8<TY>(gx + (long long)t * a.channels, c, a.channels, none);
+    }
+#pragma unroll
+    for (int j = 0; j <= W; ++j) store8<F32>(part + (at * (W + 1) + j) * a.channels, c, a.channels, sum[j]);
+}
+
+// Columns of part [tiles, width + 1, channels] summed in 64 bits: the last of the width + 1
+// into gb (or nowhere), the others into gw [channels, width].
+constexpr int kSumCols = 32, kSumRows = 32;
+__global__ __launch_bounds__(kSumCols* kSumRows) void conv_sums_kernel(const float* __restrict__ part, long long tiles,
+                                                                       int channels, int width, float* __restrict__ gw,
+                                                                       float* __restrict__ gb) {
+    __shared__ double red[kSumRows][kSumCols + 1];
+    const long long columns = (long long)(width + 1) * channels;
+    const int sub = threadIdx.x % kSumCols, slot = threadIdx.x / kSumCols;
+    const long long col = (long long)blockIdx.x * kSumCols + sub;
+    double x = 0.0;
+    if (col < columns)
+#pragma unroll 4
+        for (long long r = slot; r < tiles; r += kSumRows) x += part[r * columns + col];
+    red[slot][sub] = x;
+    __syncthreads();
+    if (slot != 0 || col >= columns) return;
+#pragma unroll
+    for (int i = 1; i < kSumRows; ++i) x += red[i][sub];
+    const int j = (int)(col / channels);
+    const long long ch = col % channels;
+    if (j < width)
+        gw[ch * width + j] = (float)x;
+    else if (gb)
+        gb[ch] = (float)x;
+}
+
+template <class TY, int W>
+__global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long waves, const typename TY::S* __restrict__ x,
+                                                             const typename TY::S* __restrict__ weight,
+                                                             const typename TY::S* __restrict__ bias,
+                                                             typename TY::S* states, int pool,
+                                                             const int* __restrict__ slots, typename TY::S* __restrict__ y) {
+    const long long wave = (long long)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wave >= waves) return;
+    const int parts = (a.channels + kWaveCh - 1) / kWaveCh, lane = threadIdx.x & 63;
+    const int c = (int)(wave % parts) * kWaveCh + lane * kLaneCh;
+    const int rows = a.q.n_tokens;
+    int row = (int)(wave / parts), slot = row;
+    if (slots) {
+        slot = __builtin_amdgcn_readfirstlane(slots[row]);
+        if (slot < 0 || slot >= pool) {
+            const float none[8] = {};
+            store8<TY>(y + (long long)row * a.channels, c, a.channels, none);
+            return;
+        }
+        for (int j = 0; j < row; j += 64)  // the first row of a slot takes all
+            if (__ballot(j + lane < row && slots[min(j + lane, rows - 1)] == slot)) return;
+    }
+    float w[W][8], b[8], win[W - 1][8];
+    load_weights<TY, W>(weight, c, a.channels, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b[e] = 0.0f;
+    if (bias) load8<TY>(bias, c, a.channels, b);
+    typename TY::S* state = states + (long long)slot * (W - 1) * a.channels;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) load8<TY>(state + (long long)j * a.channels, c, a.channels, win[j]);
+    while (row < rows) {
+        float now[8], p[8];
+        load8<TY>(x + row * a.xt, c, a.channels, now);
+        apply<W>(w, b, win, now, p);
+        shift<W>(win, now);
+        if (a.silu) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] *= sigmoid_of(p[e]);
+        }
+        store8<TY>(y + (long long)row * a.channels, c, a.channels, p);
+        if (!slots) break;
+        int next = rows;
+        for (int j = row + 1; j < rows; j += 64) {
+            const unsigned long long m = __ballot(j + lane < rows && slots[min(j + lane, rows - 1)] == slot);
+            if (m) {
+                next = j + __builtin_ctzll(m);
+                break;
+            }
+        }
+        row = next;
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) store8<TY>(state + (long long)j * a.channels, c, a.channels, win[j]);
+}
+
+// ---------------------------------------------------------- host helpers
+constexpr long long kMaxTokens = (1LL << 31) - (1LL << 16);
+constexpr long long kMaxGrid = (1LL << 32) / kThreads - 8;  // a grid has fewer than 2^32 work-items
+
+inline long long parts_of(const Conv& a) { return (a.channels + kWaveCh - 1) / kWaveCh; }
+inline long long blocks_of(long long waves) { return (waves + kWaves - 1) / kWaves; }
+
+int check_shape(const short_conv_shape_t* p, bool step, Conv* a) {
+    if (!p) return CFC_ERR_NULL;
+    if (p->type != CFC_TYPE_F32 && p->type != CFC_TYPE_BF16 && p->type != CFC_TYPE_F16) return CFC_ERR_UNSUPPORTED;
+    if (p->channels < 1 || p->width < 1 || p->x_stride < 0 || p->grad_y_stride < 0) return CFC_ERR_DIM;
+    if (p->width < 2 || p->width > SHORT_CONV_MAX_WIDTH) return CFC_ERR_UNSUPPORTED;
+    // a lane's first weight is at 4 times its channel
+    if (p->channels > INT_MAX / SHORT_CONV_MAX_WIDTH - kWaveCh || p->n_tokens > kMaxTokens) return CFC_ERR_UNSUPPORTED;
+    if (step) {
+        if (p->n_tokens < 0) return CFC_ERR_DIM;
+        a->q = Sequences{nullptr, (int)p->n_tokens, 1, (int)p->n_tokens};
+    } else if (const int e = check_sequences(p->offsets, p->n_seq, p->seq_len, p->n_tokens, &a->q)) {
+        return e;
+    }
+    a->channels = p->channels;
+    a->silu = p->silu;
+    a->clear = p->clear_rest && p->offsets;
+    a->xt = p->x_stride;
+    a->gt = p->grad_y_stride;
+    // (the forward's tiles are the most)
+    const long long most = ((long long)a->q.n_tokens / (step ? 1 : kTile) + 1 + a->q.n_seq) * parts_of(*a);
+    return blocks_of(most) > kMaxGrid ? CFC_ERR_UNSUPPORTED : CFC_OK;
+}
+
+struct Sizes {  // bytes of the arguments
+    long long x, gy, y, weight, bias, states;
+};
+bool sizes_of(const short_conv_shape_t* p, const Conv& a, Sizes* z) {
+    const int size = size_of(p->type);
+    long long kept;
+    z->weight = (long long)a.channels * p->width * size;
+    z->bias = (long long)a.channels * size;
+    return extent(p->n_tokens, 1, a.channels, a.xt, 0, size, &z->x) &&
+           extent(p->n_tokens, 1, a.channels, a.gt, 0, size, &z->gy) && mul_ok(p->n_tokens, (long long)a.channels * size, &z->y) &&
+           mul_ok(a.q.n_seq, p->width - 1, &kept) && mul_ok(kept, (long long)a.channels * size, &z->states);
+}
+inline long long workspace_of(const Conv& a, int width) {
+    const long long tiles = ((long long)a.q.n_tokens + kGradTile - 1) / kGradTile;
+    long long n;
+    return mul_ok(tiles * (width + 1), (long long)a.channels * 4, &n) ? (n + 15) / 16 * 16 : -1;
+}
+
+template <class F>
+int with_width(int type, int width, F f) {
+    auto go = [&](auto ty) {
+        if (width == 2) return f(ty, std::integral_constant<int, 2>{});
+        if (width == 3) return f(ty, std::integral_constant<int, 3>{});
+        return f(ty, std::integral_constant<int, 4>{});
+    };
+    if (type == CFC_TYPE_F32) return go(F32{});
+    return type == CFC_TYPE_BF16 ? go(BF16{}) : go(F16{});
+}
+
+}  // namespace
+
+// ================================================================ C ABI
+extern "C" int short_conv_forward(const short_conv_shape_t* shape, const void* x, const void* weight, const void* bias,
+                                  const void* initial_state, void* y, void* final_state, hipStream_t stream) {
+    Conv a;
+    Sizes z;
+    if (const int e = check_shape(shape, false, &a)) return e;
+    if (!sizes_of(shape, a, &z)) return CFC_ERR_DIM;
+    if (a.q.n_seq == 0) return CFC_OK;
+    if (!weight || (a.q.n_tokens && (!x || !y))) return CFC_ERR_NULL;
+    if (!fits({x, weight, bias, initial_state, y, final_state}, size_of(shape->type))) return CFC_ERR_DIM;
+    const Range ini = bytes_of(initial_state, z.states), fin = bytes_of(final_state, z.states);
+    const bool over = same(ini, fin);
+    const Range outs[] = {bytes_of(y, z.y), fin};
+    const Range ins[] = {bytes_of(x, z.x), bytes_of(weight, z.weight), bytes_of(bias, z.bias), offsets_range(a.q),
+                         over ? Range{0, 0} : ini};
+    if (!outputs_disjoint(outs, 2, ins, 5) || (over && overlap(outs[0], ini))) return CFC_ERR_OVERLAP;
+    return with_width(shape->type, shape->width, [&](auto ty, auto width) {
+        using TY = decltype(ty);
+        using S = typename TY::S;
+        constexpr int W = decltype(width)::value;
+        const long long tiles = (a.q.n_tokens + kTile - 1) / kTile, parts = parts_of(a);
+        const long long split = tiles * parts, all = (tiles + (final_state ? a.q.n_seq : 0)) * parts;
+        auto go = [&](long long from, long long to) {
+            if (from < to)
+                hipLaunchKernelGGL((conv_kernel<TY, W>), dim3((unsigned)blocks_of(to - from)), dim3(kThreads), 0, stream,
+                                   a, from, to, tiles, (const S*)x, (const S*)weight, (const S*)bias,
+                                   (const S*)initial_state, (S*)y, (S*)final_state);
+        };
+        if (over && final_state) {  // the tiles read what the final states overwrite
+            go(0, split);
+            go(split, all);
+        } else {
+            go(0, all);
+        }
+        return launch_status();
+    });
+}
+
+extern "C" long long short_conv_backward_workspace(const short_conv_shape_t* shape) {
+    Conv a;
+    return check_shape(shape, false, &a) == CFC_OK ? workspace_of(a, shape->width) : -1;
+}
+
+extern "C" int short_conv_backward(const short_conv_shape_t* shape, const void* x, const void* weight, const void* bias,
+                                   const void* initial_state, const void* grad_y, const void* grad_final_state,
+                                   void* grad_x, float* grad_weight, float* grad_bias, void* grad_initial_state,
+                                   void* workspace, long long workspace_bytes, hipStream_t stream) {
+    Conv a;
+    Sizes z;
+    if (const int e = check_shape(shape, false, &a)) return e;
+    const long long need = workspace_of(a, shape->width);
+    if (!sizes_of(shape, a, &z) || need < 0) return CFC_ERR_DIM;
+    if (!weight || !grad_weight || (a.q.n_tokens && (!x || !grad_y || !grad_x)) || (need && !workspace))
+        return CFC_ERR_NULL;
+    if (need && (workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 16)) return CFC_ERR_DIM;
+    if (!fits({x, weight, bias, initial_state, grad_y, grad_final_state, grad_x, grad_initial_state},
+              size_of(shape->type)) ||
+        !fits({grad_weight, grad_bias}, 4))
+        return CFC_ERR_DIM;
+    const Range outs[] = {bytes_of(grad_x, z.y),
+                          bytes_of(grad_weight, (long long)a.channels * shape->width * 4),
+                          bytes_of(grad_bias, (long long)a.channels * 4),
+                          bytes_of(grad_initial_state, z.states),
+                          bytes_of(need ? workspace : nullptr, need)};
+    const Range ins[] = {bytes_of(x, z.x),
+                         bytes_of(weight, z.weight),
+                         bytes_of(bias, z.bias),
+                         bytes_of(initial_state, z.states),
+                         bytes_of(grad_y, z.gy),
+                         bytes_of(grad_final_state, z.states),
+                         offsets_range(a.q)};
+    if (!outputs_disjoint(outs, 5, ins, 7)) return CFC_ERR_OVERLAP;
+    return with_width(shape->type, shape->width, [&](auto ty, auto width) {
+        using TY = decltype(ty);
+        using S = typename TY::S;
+        constexpr int W = decltype(width)::value;
+        const long long tiles = ((long long)a.q.n_tokens + kGradTile - 1) / kGradTile, parts = parts_of(a);
+        const long long waves = (tiles + (grad_initial_state ? a.q.n_seq : 0)) * parts;
+        float* part = static_cast<float*>(workspace);
+        if (waves)
+            hipLaunchKernelGGL((conv_backward_kernel<TY, W>), dim3((unsigned)blocks_of(waves)), dim3(kThreads), 0, stream,
+                               a, waves, tiles, (const S*)x, (const S*)weight, (const S*)bias, (const S*)initial_state,
+                               (const S*)grad_y, (const S*)grad_final_state, (S*)grad_x, (S*)grad_initial_state, part);
+        const long long columns = (long long)(W + 1) * a.channels;
+        hipLaunchKernelGGL(conv_sums_kernel, dim3((unsigned)((columns + kSumCols - 1) / kSumCols)),
+                           dim3(kSumCols * kSumRows), 0, stream, part, tiles, a.channels, W, grad_weight, grad_bias);
+        return launch_status();
+    });
+}
+
+extern "C" int short_conv_step(const short_conv_shape_t* shape, const void* x, const void* weight, const void* bias,
+                               void* states, int pool, const int* slots, void* y, hipStream_t stream) {
+    Conv a;
+    Sizes z;
+    long long held;
+    if (const int e = check_shape(shape, true, &a)) return e;
+    if (pool < 0 || (!slots && pool < a.q.n_tokens) || !sizes_of(shape, a, &z) ||
+        !mul_ok((long long)pool * (shape->width - 1), (long long)a.channels * size_of(shape->type), &held))
+        return CFC_ERR_DIM;
+    if (a.q.n_tokens == 0) return CFC_OK;
+    if (!x || !weight || !y || (pool && !states)) return CFC_ERR_NULL;
+    if (!fits({x, weight, bias, states, y}, size_of(shape->type)) || !fits({slots}, 4)) return CFC_ERR_DIM;
+    const Range outs[] = {bytes_of(y, z.y), bytes_of(states, held)};
+    const Range ins[] = {bytes_of(x, z.x), bytes_of(weight, z.weight), bytes_of(bias, z.bias),
+                         bytes_of(slots, (long long)a.q.n_tokens * 4)};
+    if (!outputs_disjoint(outs, 2, ins, 4)) return CFC_ERR_OVERLAP;
+    return with_width(shape->type, shape->width, [&](auto ty, auto width) {
+        using TY = decltype(ty);
+        using S = typename TY::S;
+        constexpr int W = decltype(width)::value;
+        const long long waves = (long long)a.q.n_tokens * parts_of(a);
+        hipLaunchKernelGGL((conv_step_kernel<TY, W>), dim3((unsigned)blocks_of(waves)), dim3(kThreads), 0, stream, a,
+                           waves, (const S*)x, (const S*)weight, (const S*)bias, (S*)states, pool, slots, (S*)y);
+        return launch_status();
+    });
+}
