@@ -110,15 +110,6 @@ __device__ __forceinline__ void mma(const u32x4 (&a)[NA], const u32x4 (&b)[NB], 
 // column l & 15), so a result becomes the next product's operand as it is.
 __device__ __forceinline__ int place_of(int ks, int g, int j) { return 32 * ks + (j < 4 ? 4 * g + j : 12 + 4 * g + j); }
 
-// Memory through buffer descriptors: a uniform base, a lane's 32-bit offset and a
-// uniform one cost no address arithmetic on the vector units, and what lies behind
-// the descriptor's end reads as zero and is not written, so that accesses need no
-// branches.  kNowhere is behind every end.
-constexpr uint32_t kNowhere = 0x80000000u;
-typedef __amdgpu_buffer_rsrc_t Buffer;
-__device__ __forceinline__ Buffer buffer_of(const void* p, long long bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
-}
 // The n'th operand part (64 lanes of 16 bytes) of an array of `parts`, and this lane's own of it.
 struct Parts {
     Buffer b;
@@ -248,14 +239,6 @@ __device__ __forceinline__ Chunk chunk_of(const Shape& a, long long slot) {
     k.tok0 = __builtin_amdgcn_readfirstlane(tok0 + k.c * kC);
     return k;
 }
-
-// Workgroups are dealt to the 8 dies in turn; `count` logical ones in order, so
-// that neighbours (tiles of one head, heads of one key head) share a die's L2.
-__device__ __forceinline__ long long on_die(long long block, long long count) {
-    const long long each = (count + 7) / 8;
-    return (block % 8) * each + block / 8;
-}
-inline unsigned dealt(long long count) { return (unsigned)((count + 7) / 8 * 8); }
 
 // Sums over lanes that stay on the vector units.
 template <int N>

@@ -102,6 +102,23 @@ __device__ __forceinline__ void store8(typename TY::S* row, int c, int width, co
     }
 }
 
+// Memory through buffer descriptors: a uniform base, a lane's 32-bit offset and a
+// uniform one cost no address arithmetic on the vector units, and what lies behind
+// the descriptor's end reads as zero and is not written, so that accesses need no
+// branches.  kNowhere is behind every end.
+constexpr uint32_t kNowhere = 0x80000000u;
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer_of(const void* p, long long bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+// Workgroups are dealt to the 8 dies in turn; `count` logical ones in order, so
+// that neighbours (tiles of one head, heads of one key head, channels of one row) share a die's L2.
+__device__ __forceinline__ long long on_die(long long block, long long count) {
+    const long long each = (count + 7) / 8;
+    return (block % 8) * each + block / 8;
+}
+inline unsigned dealt(long long count) { return (unsigned)((count + 7) / 8 * 8); }
+
 inline int size_of(int type) { return type == CFC_TYPE_F32 ? 4 : 2; }
 
 // An argument's bytes; none of a null pointer.

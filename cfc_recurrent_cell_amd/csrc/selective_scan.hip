@@ -40,6 +40,7 @@ struct Scan {
     int channels, groups, share, state;  // share: channels of a group
     int softplus, clear;
     long long xt, dtt, zt, gt, bt, bg, ct, cg;
+    bool single;  // sequences of one row, whose strides may be anything
 };
 
 // ------------------------------------------------------------------- lanes
@@ -97,6 +98,92 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
+// The barrier of a workgroup's exchanges through LDS; global loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// An element as it lies in memory, through a descriptor.
+template <class TY>
+__device__ __forceinline__ uint32_t load_raw(Buffer b, uint32_t at) {
+    if constexpr (sizeof(typename TY::S) == 4)
+        return __builtin_amdgcn_raw_buffer_load_b32(b, at, 0, 0);
+    else
+        return __builtin_amdgcn_raw_buffer_load_b16(b, at, 0, 0);
+}
+template <class TY>
+__device__ __forceinline__ float value_of(uint32_t raw) {
+    if constexpr (sizeof(typename TY::S) == 4)
+        return __uint_as_float(raw);
+    else
+        return TY::load(__builtin_bit_cast(typename TY::S, (uint16_t)raw));
+}
+template <class TY>
+__device__ __forceinline__ void store_to(Buffer b, uint32_t at, float x) {
+    if constexpr (sizeof(typename TY::S) == 4)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), b, at, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, TY::store(x)), b, at, 0, 0);
+}
+
+// The rows of a sequence, a block of them at a time; rows behind its end read as zeros and
+// are not written, so that nothing needs a branch.  (Where rows overlap, at a stride below
+// their width, they read as something: steps and gradients there are set to zero.)
+template <class TY>
+struct Rows {
+    const char* base;
+    long long bytes;  // from a row to the next
+    uint32_t width;   // bytes of a row
+    int len;
+    __device__ __forceinline__ Rows(const typename TY::S* p, int first, int end, long long stride, int width_)
+        : base(p ? reinterpret_cast<const char*>(p + first * stride) : nullptr), bytes(stride * (long long)sizeof(typename TY::S)),
+          width(width_ * (uint32_t)sizeof(typename TY::S)), len(end - first) {}
+    // Those from row `at` of the sequence on, of which there are none for at >= len.
+    __device__ __forceinline__ Buffer from(int at) const {
+        const long long n = at < len && base ? (len - 1 - at) * bytes + width : 0;
+        return buffer_of(base + at * bytes, n < 0x7fffffff ? n : 0x7fffffff);
+    }
+};
+// A lane's places in a block of a wave's T tokens: element (4 i + j) of the wave's rows.
+template <class TY, int Q>
+struct Places {
+    uint32_t at[Q];
+    __device__ __forceinline__ Places(bool in, long long stride, int row, int column) {
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            at[i] = in ? (uint32_t)(((row + 4 * i) * stride + column) * (long long)sizeof(typename TY::S)) : kNowhere;
+    }
+};
+// b or c of a wave's T tokens: loaded as they are, and put to LDS as 32-bit floats [T][4 S].
+template <class TY, int S, int T>
+struct Shared {
+    static constexpr int N = (T * 4 * S + 63) / 64;
+    static constexpr bool all = T * 4 * S % 64 == 0;
+    uint32_t at[N], raw[N];
+    __device__ __forceinline__ Shared(long long stride, int row, int state) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = i * 64 + (threadIdx.x & 63), n = e % (4 * S);
+            at[i] = n < state && (all || e < T * 4 * S)
+                        ? (uint32_t)(((row + e / (4 * S)) * stride + n) * (long long)sizeof(typename TY::S))
+                        : kNowhere;
+        }
+    }
+    __device__ __forceinline__ void load(Buffer b) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw[i] = load_raw<TY>(b, at[i]);
+    }
+    __device__ __forceinline__ void put(float* to) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = i * 64 + (threadIdx.x & 63);
+            if (all || e < T * 4 * S) to[e] = value_of<TY>(raw[i]);
+        }
+    }
+};
+
 // b or c of a wave's T tokens, as 32-bit floats [T][4 S], zero behind the sequence's end.
 template <class TY, int S, int T>
 __device__ __forceinline__ void stage(const typename TY::S* p, long long st, int t0, int end, int state, float* to) {
@@ -108,6 +195,43 @@ __device__ __forceinline__ void stage(const typename TY::S* p, long long st, int
     }
 }
 
+// S floats of a lane in LDS: [S / V][64 lanes][V], V of them one access.
+template <int S>
+struct Lanes {
+    static constexpr int V = S < 4 ? S : 4;
+    typedef float vec __attribute__((ext_vector_type(V)));
+    float x[S / V][64][V];
+    __device__ __forceinline__ void put(int lane, const float (&h)[S]) {
+#pragma unroll
+        for (int i = 0; i < S / V; ++i) {
+            vec v;
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = h[i * V + k];
+            *reinterpret_cast<vec*>(x[i][lane]) = v;
+        }
+    }
+    __device__ __forceinline__ void get(int lane, float (&h)[S]) const {
+#pragma unroll
+        for (int i = 0; i < S / V; ++i) {
+            const vec v = *reinterpret_cast<const vec*>(x[i][lane]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) h[i * V + k] = v[k];
+        }
+    }
+};
+// S neighbouring floats, V of them one access.
+template <int S>
+__device__ __forceinline__ void get_states(const float* p, float (&h)[S]) {
+    constexpr int V = S < 4 ? S : 4;
+    typedef float vec __attribute__((ext_vector_type(V)));
+#pragma unroll
+    for (int i = 0; i < S / V; ++i) {
+        const vec v = *reinterpret_cast<const vec*>(p + i * V);
+#pragma unroll
+        for (int k = 0; k < V; ++k) h[i * V + k] = v[k];
+    }
+}
+
 // -------------------------------------------------------------------- forward
 template <class TY, int S>
 __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
@@ -116,14 +240,16 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
     const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias,
     const float* initial, typename TY::S* __restrict__ y, float* final) {
     constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4;
-    __shared__ float sum[2][NW][2][S][64];  // P and h' of each wave
-    __shared__ float carry[2][S][64];
-    __shared__ float bc[NW][2][T * 4 * S];
-    const Place p = place_of(a, blockIdx.x % channel_groups);
-    const int seq = blockIdx.x / channel_groups, lane = threadIdx.x & 63;
+    __shared__ Lanes<S> product[2][NW], made[2][NW], carry[2];  // P and h' of each wave
+    __shared__ alignas(16) float bc[NW][2][T * 4 * S];
+    const long long count = (long long)channel_groups * a.q.n_seq, index = on_die(blockIdx.x, count);
+    if (index >= count) return;
+    const Place p = place_of(a, (int)(index % channel_groups));
+    const int seq = (int)(index / channel_groups), lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = p.j * S;
     int first, end;
     span_of(a.q, seq, first, end);
+    const int len = end - first;
     float a2[S], h[S];
     load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
 #pragma unroll
@@ -131,39 +257,59 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
     const long long kept = ((long long)seq * a.channels + p.ch) * a.state;
     if (initial) load_states<S>(initial + kept, n0, a.state, 0.0f, h);
     const float skip = d ? d[p.ch] : 0.0f, bias = dt_bias ? dt_bias[p.ch] : 0.0f;
-    b += p.group * a.bg;
-    c += p.group * a.cg;
-    int turn = 0;
-    for (int block = first; block < end; block += T * NW, turn ^= 1) {
-        const int t0 = block + w * T;
-        wave_fence();
-        stage<TY, S, T>(b, a.bt, t0, end, a.state, bc[w][0]);
-        stage<TY, S, T>(c, a.ct, t0, end, a.state, bc[w][1]);
-        wave_fence();
-        float xv[Q], step[Q], u[Q], gate[Q];
+    const Rows<TY> xs(x, first, end, a.xt, a.channels), dts(dt, first, end, a.dtt, a.channels),
+        zs(z, first, end, a.zt, a.channels), bs(b + p.group * a.bg, first, end, a.bt, a.state),
+        cs(c + p.group * a.cg, first, end, a.ct, a.state), ys(y, first, end, a.channels, a.channels);
+    const int row = w * T + p.j;
+    const Places<TY, Q> xa(true, a.single ? 0 : a.xt, row, p.ch), dta(true, a.single ? 0 : a.dtt, row, p.ch),
+        za(true, a.single ? 0 : a.zt, row, p.ch), ya(p.in, a.channels, row, p.ch);
+    Shared<TY, S, T> bl(a.single ? 0 : a.bt, w * T, a.state), cl(a.single ? 0 : a.ct, w * T, a.state);
+    uint32_t xr[Q], dtr[Q], zr[Q];
+    auto fetch = [&](int at) {
+        const Buffer xb = xs.from(at), db = dts.from(at), zb = zs.from(at);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            const int t = t0 + 4 * i + p.j;
-            const bool in = t < end;
-            xv[i] = in ? TY::load(x[t * a.xt + p.ch]) : 0.0f;
-            const float pre = (in ? TY::load(dt[t * a.dtt + p.ch]) : 0.0f) + bias;
-            const float zv = in && z ? TY::load(z[t * a.zt + p.ch]) : 0.0f;
-            step[i] = in ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
+            xr[i] = load_raw<TY>(xb, xa.at[i]);
+            dtr[i] = load_raw<TY>(db, dta.at[i]);
+            zr[i] = load_raw<TY>(zb, za.at[i]);
+        }
+        bl.load(bs.from(at));
+        cl.load(cs.from(at));
+    };
+    fetch(0);
+    int turn = 0;
+    for (int block = 0; block < len; block += T * NW, turn ^= 1) {
+        wave_fence();
+        bl.put(bc[w][0]);
+        cl.put(bc[w][1]);
+        wave_fence();
+        float xv[Q], step[Q], u[Q], gate[Q], all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            xv[i] = value_of<TY>(xr[i]);
+            const float pre = value_of<TY>(dtr[i]) + bias;
+            step[i] = block + row + 4 * i < len ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
             u[i] = step[i] * xv[i];
+            all += step[i];
+            const float zv = value_of<TY>(zr[i]);
             gate[i] = z ? zv * sigmoid_of(zv) : 1.0f;
         }
-        float at[T][S], add[T][S], hl[S], all = 0.0f;
+        fetch(block + T * NW);  // while this block is worked on
+        all += quad_perm<0xB1>(all);
+        all += quad_perm<0x4E>(all);
+        float at[T][S], add[T][S], hl[S], pw[S];
 #pragma unroll
-        for (int s = 0; s < S; ++s) hl[s] = 0.0f;
+        for (int s = 0; s < S; ++s) hl[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);
         auto one = [&](auto k, int i) {
             constexpr int J = decltype(k)::value;
             const int t = 4 * i + J;
             const float dl = from<J>(step[i]), ul = from<J>(u[i]);
-            all += dl;
+            float bv[S];
+            get_states<S>(&bc[w][0][t * 4 * S + n0], bv);
 #pragma unroll
             for (int s = 0; s < S; ++s) {
                 at[t][s] = exp2_of(dl * a2[s]);
-                add[t][s] = ul * bc[w][0][t * 4 * S + n0 + s];
+                add[t][s] = ul * bv[s];
                 hl[s] = fmaf(at[t][s], hl[s], add[t][s]);
             }
         };
@@ -174,42 +320,37 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
             one(std::integral_constant<int, 2>{}, i);
             one(std::integral_constant<int, 3>{}, i);
         }
+        product[turn][w].put(lane, pw);
+        made[turn][w].put(lane, hl);
+        lds_barrier();
+        if (block) carry[turn].get(lane, h);
+        for (int i = 0; i < w; ++i) {
+            product[turn][i].get(lane, pw);
+            made[turn][i].get(lane, hl);
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            sum[turn][w][0][s][lane] = exp2_of(all * a2[s]);
-            sum[turn][w][1][s][lane] = hl[s];
+            for (int s = 0; s < S; ++s) h[s] = fmaf(pw[s], h[s], hl[s]);
         }
-        __syncthreads();
-        if (block != first) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) h[s] = carry[turn][s][lane];
-        }
-        for (int i = 0; i < w; ++i)
-#pragma unroll
-            for (int s = 0; s < S; ++s) h[s] = fmaf(sum[turn][i][0][s][lane], h[s], sum[turn][i][1][s][lane]);
+        const Buffer yb = ys.from(block);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
             float v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int t = 4 * i + k;
+                float cv[S];
+                get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
                 v[k] = 0.0f;
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
                     h[s] = fmaf(at[t][s], h[s], add[t][s]);
-                    v[k] = fmaf(bc[w][1][t * 4 * S + n0 + s], h[s], v[k]);
+                    v[k] = fmaf(cv[s], h[s], v[k]);
                 }
             }
-            const int t = t0 + 4 * i + p.j;
-            const float out = fmaf(skip, xv[i], over_four(v)) * gate[i];
-            if (t < end && p.in) y[(long long)t * a.channels + p.ch] = TY::store(out);
+            store_to<TY>(yb, ya.at[i], fmaf(skip, xv[i], over_four(v)) * gate[i]);
         }
-        if (w == NW - 1) {
-#pragma unroll
-            for (int s = 0; s < S; ++s) carry[turn ^ 1][s][lane] = h[s];
-        }
+        if (w == NW - 1) carry[turn ^ 1].put(lane, h);
     }
-    // (the last wave has the state behind the last block, the first one the state before any)
+    // (the last wave has the state behind the last block, or the one before any)
     if (final && p.in && w == NW - 1) store_states<S>(final + kept, n0, a.state, h);
     if ((a.clear & SELECTIVE_SCAN_CLEAR_Y) && seq == a.q.n_seq - 1 && p.in)
         for (int t = end + 4 * w + p.j; t < a.q.n_tokens; t += 4 * NW)
@@ -654,6 +795,14 @@ int check_shape(const selective_scan_shape_t* p, bool step, Scan* a) {
     a->clear = p->offsets ? p->clear_rest : 0;
     a->xt = p->x_stride, a->dtt = p->dt_stride, a->zt = p->z_stride, a->gt = p->grad_y_stride;
     a->bt = p->b_stride_t, a->bg = p->b_stride_g, a->ct = p->c_stride_t, a->cg = p->c_stride_g;
+    // a block's rows are reached from its first one by 32 bits, which rows alone do not need
+    const int size = size_of(p->type);
+    a->single = (p->offsets ? p->n_tokens : step ? 1 : p->seq_len) <= 1;
+    long long far = p->channels;
+    if (!a->single)
+        for (const long long stride : {p->x_stride, p->dt_stride, p->z_stride, p->grad_y_stride, p->b_stride_t, p->c_stride_t})
+            far = std::max(far, stride);
+    if (far + p->channels + p->state > INT_MAX / (64 * size)) return CFC_ERR_UNSUPPORTED;
     const long long groups = (long long)a->groups * ((a->share + kGroupCh - 1) / kGroupCh);
     return groups * std::max(1, a->q.n_seq) > kMaxBlocks ? CFC_ERR_UNSUPPORTED : CFC_OK;
 }
@@ -746,7 +895,7 @@ extern "C" int selective_scan_forward(const selective_scan_shape_t* shape, const
         using E = typename TY::S;
         constexpr int S = decltype(states)::value;
         const int groups = channel_groups_of(a);
-        hipLaunchKernelGGL((scan_kernel<TY, S>), dim3((unsigned)(groups * (long long)a.q.n_seq)), dim3(64 * waves_of(S)),
+        hipLaunchKernelGGL((scan_kernel<TY, S>), dim3(dealt(groups * (long long)a.q.n_seq)), dim3(64 * waves_of(S)),
                            0, stream, a, groups, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d, (const E*)z,
                            dt_bias, initial_state, (E*)y, final_state);
         return launch_status();
