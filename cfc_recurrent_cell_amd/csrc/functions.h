@@ -13,20 +13,22 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 // thousandth, exp(-7), is as exact as one of one.
 __device__ __forceinline__ float exp_of(float x) {
     constexpr float low = 1.92596299e-8f;  // log2(e) - kLog2e
-    x = fmaxf(x, -1000.0f);
+    x = x < -1000.0f ? -1000.0f : x;  // (a NaN stays one)
     const float t = x * kLog2e, e = fmaf(x, low, fmaf(x, kLog2e, -t));
     const float p = exp2_of(t);
     return fmaf(p, e * kLn2, p);
 }
 __device__ __forceinline__ float reciprocal(float x) { return __builtin_amdgcn_rcpf(x); }
-__device__ __forceinline__ float sigmoid_of(float x) {
-    const float e = exp_of(-fabsf(x)), r = reciprocal(1.0f + e);
+// 1 / (1 + exp(-x)), with e = exp(-|x|)
+__device__ __forceinline__ float sigmoid_of(float x, float e) {
+    const float r = reciprocal(1.0f + e);
     return x >= 0.0f ? r : e * r;
 }
-// max(x, 0) + log(1 + exp(-|x|)); the logarithm as 2 artanh(e / (2 + e)) by its series,
-// whose argument is at most a third, so that small results lose nothing.
-__device__ __forceinline__ float softplus_of(float x) {
-    const float e = exp_of(-fabsf(x)), s = e * reciprocal(2.0f + e), z = s * s;
+__device__ __forceinline__ float sigmoid_of(float x) { return sigmoid_of(x, exp_of(-fabsf(x))); }
+// max(x, 0) + log(1 + e) with e = exp(-|x|); the logarithm as 2 artanh(e / (2 + e)) by its
+// series, whose argument is at most a third, so that small results lose nothing.
+__device__ __forceinline__ float softplus_of(float x, float e) {
+    const float s = e * reciprocal(2.0f + e), z = s * s;
     float p = 1.0f / 15;
     p = fmaf(p, z, 1.0f / 13);
     p = fmaf(p, z, 1.0f / 11);
@@ -35,7 +37,8 @@ __device__ __forceinline__ float softplus_of(float x) {
     p = fmaf(p, z, 1.0f / 5);
     p = fmaf(p, z, 1.0f / 3);
     p = fmaf(p, z, 1.0f);
-    return fmaxf(x, 0.0f) + 2.0f * s * p + (x != x ? x : 0.0f);
+    return fmaf(2.0f * s, p, fmaxf(x, 0.0f));
 }
+__device__ __forceinline__ float softplus_of(float x) { return softplus_of(x, exp_of(-fabsf(x))); }
 
 }  // namespace

@@ -184,17 +184,6 @@ struct Shared {
     }
 };
 
-// b or c of a wave's T tokens, as 32-bit floats [T][4 S], zero behind the sequence's end.
-template <class TY, int S, int T>
-__device__ __forceinline__ void stage(const typename TY::S* p, long long st, int t0, int end, int state, float* to) {
-#pragma unroll
-    for (int i = 0; i < (T * 4 * S + 63) / 64; ++i) {
-        const int e = i * 64 + (threadIdx.x & 63), t = e / (4 * S), n = e % (4 * S);
-        if (T * 4 * S % 64 == 0 || e < T * 4 * S)
-            to[e] = t0 + t < end && n < state ? TY::load(p[(t0 + t) * st + n]) : 0.0f;
-    }
-}
-
 // S floats of a lane in LDS: [S / V][64 lanes][V], V of them one access.
 template <int S>
 struct Lanes {
@@ -370,48 +359,66 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
     const float* __restrict__ decay, const typename TY::S* __restrict__ b, const float* __restrict__ dt_bias,
     const float* __restrict__ initial, float* __restrict__ kept) {
     constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4;
-    __shared__ float sum[2][NW][2][S][64];
-    __shared__ float bs[NW][T * 4 * S];
-    const Place p = place_of(a, blockIdx.x % channel_groups);
-    const int seq = blockIdx.x / channel_groups, lane = threadIdx.x & 63;
+    __shared__ Lanes<S> product[2][NW], made[2][NW];
+    __shared__ alignas(16) float bc[NW][T * 4 * S];
+    const long long count = (long long)channel_groups * a.q.n_seq, index = on_die(blockIdx.x, count);
+    if (index >= count) return;
+    const Place p = place_of(a, (int)(index % channel_groups));
+    const int seq = (int)(index / channel_groups), lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = p.j * S;
     int first, end;
     span_of(a.q, seq, first, end);
+    const int len = end - first;
     float a2[S], h[S];
     load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
 #pragma unroll
     for (int s = 0; s < S; ++s) a2[s] *= kLog2e, h[s] = 0.0f;
     if (initial) load_states<S>(initial + ((long long)seq * a.channels + p.ch) * a.state, n0, a.state, 0.0f, h);
     const float bias = dt_bias ? dt_bias[p.ch] : 0.0f;
-    b += p.group * a.bg;
-    long long slot = first / (T * NW) + seq;
-    int turn = 0;
-    for (int block = first; block < end; block += T * NW, turn ^= 1, ++slot) {
-        if (w == NW - 1 && p.in) store_states<S>(kept + (slot * a.channels + p.ch) * (4 * S), n0, 4 * S, h);
-        const int t0 = block + w * T;
-        wave_fence();
-        stage<TY, S, T>(b, a.bt, t0, end, a.state, bs[w]);
-        wave_fence();
-        float step[Q], u[Q];
+    const Rows<TY> xs(x, first, end, a.xt, a.channels), dts(dt, first, end, a.dtt, a.channels),
+        bs(b + p.group * a.bg, first, end, a.bt, a.state);
+    const int row = w * T + p.j;
+    const Places<TY, Q> xa(true, a.single ? 0 : a.xt, row, p.ch), dta(true, a.single ? 0 : a.dtt, row, p.ch);
+    Shared<TY, S, T> bl(a.single ? 0 : a.bt, w * T, a.state);
+    uint32_t xr[Q], dtr[Q];
+    auto fetch = [&](int at) {
+        const Buffer xb = xs.from(at), db = dts.from(at);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            const int t = t0 + 4 * i + p.j;
-            const bool in = t < end;
-            const float xv = in ? TY::load(x[t * a.xt + p.ch]) : 0.0f;
-            const float pre = (in ? TY::load(dt[t * a.dtt + p.ch]) : 0.0f) + bias;
-            step[i] = in ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
-            u[i] = step[i] * xv;
+            xr[i] = load_raw<TY>(xb, xa.at[i]);
+            dtr[i] = load_raw<TY>(db, dta.at[i]);
         }
-        float hl[S], all = 0.0f;
+        bl.load(bs.from(at));
+    };
+    fetch(0);
+    float* to = kept + (((long long)first / (T * NW) + seq) * a.channels + p.ch) * (4 * S);
+    int turn = 0;
+    for (int block = 0; block < len; block += T * NW, turn ^= 1, to += (long long)a.channels * (4 * S)) {
+        if (w == NW - 1 && p.in) store_states<S>(to, n0, 4 * S, h);
+        wave_fence();
+        bl.put(bc[w]);
+        wave_fence();
+        float step[Q], u[Q], all = 0.0f;
 #pragma unroll
-        for (int s = 0; s < S; ++s) hl[s] = 0.0f;
+        for (int i = 0; i < Q; ++i) {
+            const float pre = value_of<TY>(dtr[i]) + bias;
+            step[i] = block + row + 4 * i < len ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
+            u[i] = step[i] * value_of<TY>(xr[i]);
+            all += step[i];
+        }
+        fetch(block + T * NW);  // while this block is worked on
+        all += quad_perm<0xB1>(all);
+        all += quad_perm<0x4E>(all);
+        float hl[S], pw[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) hl[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);
         auto one = [&](auto k, int i) {
             constexpr int J = decltype(k)::value;
-            const int t = 4 * i + J;
             const float dl = from<J>(step[i]), ul = from<J>(u[i]);
-            all += dl;
+            float bv[S];
+            get_states<S>(&bc[w][(4 * i + J) * 4 * S + n0], bv);
 #pragma unroll
-            for (int s = 0; s < S; ++s) hl[s] = fmaf(exp2_of(dl * a2[s]), hl[s], ul * bs[w][t * 4 * S + n0 + s]);
+            for (int s = 0; s < S; ++s) hl[s] = fmaf(exp2_of(dl * a2[s]), hl[s], ul * bv[s]);
         };
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
@@ -420,16 +427,17 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
             one(std::integral_constant<int, 2>{}, i);
             one(std::integral_constant<int, 3>{}, i);
         }
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            sum[turn][w][0][s][lane] = exp2_of(all * a2[s]);
-            sum[turn][w][1][s][lane] = hl[s];
-        }
-        __syncthreads();
+        product[turn][w].put(lane, pw);
+        made[turn][w].put(lane, hl);
+        lds_barrier();
         if (w == NW - 1)
-            for (int i = 0; i < NW; ++i)
 #pragma unroll
-                for (int s = 0; s < S; ++s) h[s] = fmaf(sum[turn][i][0][s][lane], h[s], sum[turn][i][1][s][lane]);
+            for (int i = 0; i < NW; ++i) {
+                product[turn][i].get(lane, pw);
+                made[turn][i].get(lane, hl);
+#pragma unroll
+                for (int s = 0; s < S; ++s) h[s] = fmaf(pw[s], h[s], hl[s]);
+            }
     }
 }
 
@@ -439,223 +447,365 @@ struct Grads {  // the backward's outputs and workspace
     long long rows;  // of part_b and part_c: n_tokens * groups * state
 };
 
-// The sum of x over the lanes of the same j.
-__device__ __forceinline__ float over_quads(float x) {
+// Sums over the 16 lanes of the same place in their four: of 16 values, lane l gets that of
+// value sixteenth_of(l).  Two lanes' halves change places and are added, four times over.
+__device__ __forceinline__ int sixteenth_of(int lane) {
+    return (lane >> 5 & 1) + 2 * (lane >> 4 & 1) + 4 * (lane >> 3 & 1) + 8 * (lane >> 2 & 1);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float over_quads(const float (&v)[16]) {
+    float a[8], b[4], c[2];
 #pragma unroll
-    for (int off = 4; off < 64; off <<= 1) x += __shfl_xor(x, off);
-    return x;
+    for (int i = 0; i < 8; ++i) {
+        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]), false, false);
+        a[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[2 * i]), __float_as_uint(a[2 * i + 1]), false, false);
+        b[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    const bool eight = threadIdx.x & 8, four = threadIdx.x & 4;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float lo = b[2 * i] + dpp<0x128>(b[2 * i]), hi = b[2 * i + 1] + dpp<0x128>(b[2 * i + 1]);  // 8 lanes on
+        c[i] = eight ? hi : lo;
+    }
+    const float lo = c[0] + dpp<0x104>(c[0]), hi = c[1] + dpp<0x114>(c[1]);  // 4 lanes on, 4 back
+    return four ? hi : lo;
 }
 
-// A workgroup has 16 channels and every parts-th sequence.
-template <class TY, int S>
+// A workgroup has K times 16 channels of a group, one after the other for each block of
+// tokens, so that b's and c's gradients are summed over them before they leave it; and every
+// parts-th sequence.
+template <class TY, int S, int K>
 __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
-    Scan a, int channel_groups, int parts, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
+    Scan a, int wg_groups, int parts, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
     const float* __restrict__ decay, const typename TY::S* __restrict__ b, const typename TY::S* __restrict__ c,
     const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias,
     const typename TY::S* __restrict__ gy, const float* gfinal, Grads g) {
-    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4;
-    __shared__ float sum[2][NW][3][S][64];  // P, h' and e' of each wave
-    __shared__ float carry[2][S][64];
-    __shared__ float bc[NW][2][T * 4 * S];
-    const int index = blockIdx.x % channel_groups, part = blockIdx.x / channel_groups;
-    const Place p = place_of(a, index);
-    const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = p.j * S;
+    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW;
+    constexpr int N16 = (T * S + 15) / 16;
     using E = typename TY::S;
-    float a2[S];
-    double da[S], dd = 0.0, dbias = 0.0;
-    load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
+    __shared__ Lanes<S> product[2][NW], made[2][NW], given[2][NW], carry[2][K];  // P, h' and e' of each wave
+    __shared__ alignas(16) float bc[NW][2][T * 4 * S];
+    __shared__ double total[K][NW][S + 1][64];  // a's gradients, and d's and dt_bias's in lanes 0 and 1 of four
+    const long long count = (long long)wg_groups * parts, index = on_die(blockIdx.x, count);
+    if (index >= count) return;
+    const int wg = (int)(index % wg_groups), part = (int)(index / wg_groups);
+    const int per_group = wg_groups / a.groups, group = wg / per_group, in_group = wg % per_group;
+    const int sixteens = (a.share + kGroupCh - 1) / kGroupCh, k0 = in_group * K, nk = min(K, sixteens - k0);
+    const int lane = threadIdx.x & 63, j = lane & 3;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = j * S;
 #pragma unroll
-    for (int s = 0; s < S; ++s) a2[s] *= kLog2e, da[s] = 0.0;
-    const float skip = d ? d[p.ch] : 0.0f, bias = dt_bias ? dt_bias[p.ch] : 0.0f;
-    b += p.group * a.bg;
-    c += p.group * a.cg;
-    const int in_group = index % (channel_groups / a.groups);
-    float* to_b = g.part_b + in_group * g.rows + p.group * a.state;
-    float* to_c = g.part_c + in_group * g.rows + p.group * a.state;
-    const long long row = (long long)a.groups * a.state;
-    int turn = 0;
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int s = 0; s <= S; ++s) total[k][w][s][lane] = 0.0;
+    float* to_b = g.part_b + in_group * g.rows + group * a.state;
+    float* to_c = g.part_c + in_group * g.rows + group * a.state;
+    const long long row_bc = (long long)a.groups * a.state;
+    // the lane's channel of the k'th sixteen
+    auto place = [&](int k) { return place_of(a, group * sixteens + k0 + k); };
+    int turn = 0, flip = 0;
     for (int seq = part; seq < a.q.n_seq; seq += parts) {
         int first, end;
         span_of(a.q, seq, first, end);
-        const long long state_at = ((long long)seq * a.channels + p.ch) * a.state;
-        float e[S];
-#pragma unroll
-        for (int s = 0; s < S; ++s) e[s] = 0.0f;
-        if (gfinal) load_states<S>(gfinal + state_at, n0, a.state, 0.0f, e);
-        const int blocks = (end - first + T * NW - 1) / (T * NW);
-        for (int block = blocks - 1; block >= 0; --block, turn ^= 1) {
-            const int t0 = first + block * (T * NW) + w * T;
-            wave_fence();
-            stage<TY, S, T>(b, a.bt, t0, end, a.state, bc[w][0]);
-            stage<TY, S, T>(c, a.ct, t0, end, a.state, bc[w][1]);
-            wave_fence();
-            float xv[Q], pre[Q], step[Q], u[Q], gv[Q], zv[Q], gp[Q];
+        const int len = end - first, blocks = (len + BT - 1) / BT;
+        const Rows<TY> xs(x, first, end, a.xt, a.channels), dts(dt, first, end, a.dtt, a.channels),
+            zs(z, first, end, a.zt, a.channels), gs(gy, first, end, a.gt, a.channels),
+            bs(b + group * a.bg, first, end, a.bt, a.state), cs(c + group * a.cg, first, end, a.ct, a.state),
+            gxs((const E*)g.x, first, end, a.channels, a.channels), gdts((const E*)g.dt, first, end, a.channels, a.channels),
+            gzs((const E*)g.z, first, end, a.channels, a.channels);
+        const int row = w * T + j;
+        const Places<TY, Q> xa(true, a.single ? 0 : a.xt, row, 0), dta(true, a.single ? 0 : a.dtt, row, 0),
+            za(true, a.single ? 0 : a.zt, row, 0), ga(true, a.single ? 0 : a.gt, row, 0), oa(true, a.channels, row, 0);
+        Shared<TY, S, T> bl(a.single ? 0 : a.bt, w * T, a.state), cl(a.single ? 0 : a.ct, w * T, a.state);
+        uint32_t xr[Q], dtr[Q], zr[Q], gr[Q];
+        float ar[S], hr[S], skip_r, bias_r;
+        auto fetch = [&](int block, int k) {
+            const int at = block * BT;
+            const Place p = place(k);
+            const uint32_t off = p.ch * (uint32_t)sizeof(E);
+            const Buffer xb = xs.from(at), db = dts.from(at), zb = zs.from(at), gb = gs.from(at);
 #pragma unroll
             for (int i = 0; i < Q; ++i) {
-                const int t = t0 + 4 * i + p.j;
-                const bool in = t < end;
-                xv[i] = in ? TY::load(x[t * a.xt + p.ch]) : 0.0f;
-                pre[i] = (in ? TY::load(dt[t * a.dtt + p.ch]) : 0.0f) + bias;
-                zv[i] = in && z ? TY::load(z[t * a.zt + p.ch]) : 0.0f;
-                gv[i] = in && p.in ? TY::load(gy[t * a.gt + p.ch]) : 0.0f;
-                step[i] = in ? (a.softplus ? softplus_of(pre[i]) : pre[i]) : 0.0f;
-                u[i] = step[i] * xv[i];
-                gp[i] = z ? gv[i] * zv[i] * sigmoid_of(zv[i]) : gv[i];
+                xr[i] = load_raw<TY>(xb, xa.at[i] + off);
+                dtr[i] = load_raw<TY>(db, dta.at[i] + off);
+                zr[i] = load_raw<TY>(zb, za.at[i] + off);
+                gr[i] = load_raw<TY>(gb, ga.at[i] + off);
             }
-            float at[T][S], add[T][S], gl[T], hl[S], el[S], all = 0.0f;
+            if (k == 0) {
+                bl.load(bs.from(at));
+                cl.load(cs.from(at));
+            }
+            load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, ar);
+            load_states<S>(g.kept + (((long long)first / BT + seq + block) * a.channels + p.ch) * (4 * S), n0, 4 * S, 0.0f, hr);
+            skip_r = d ? d[p.ch] : 0.0f;
+            bias_r = dt_bias ? dt_bias[p.ch] : 0.0f;
+        };
+        if (blocks) fetch(blocks - 1, 0);
+        for (int block = blocks - 1; block >= 0; --block, flip ^= 1) {
+            wave_fence();
+            bl.put(bc[w][0]);
+            cl.put(bc[w][1]);
+            wave_fence();
+            // over the K times 16 channels; the lane's of T * S values are those at 16 i + mine
+            float sum_b[N16], sum_c[N16];
 #pragma unroll
-            for (int s = 0; s < S; ++s) hl[s] = el[s] = 0.0f;
-            auto one = [&](auto k, int i) {
-                constexpr int J = decltype(k)::value;
-                const int t = 4 * i + J;
-                const float dl = from<J>(step[i]), ul = from<J>(u[i]);
-                gl[t] = from<J>(gp[i]);
-                all += dl;
+            for (int i = 0; i < N16; ++i) sum_b[i] = sum_c[i] = 0.0f;
+            for (int k = 0; k < nk; ++k, turn ^= 1) {
+                const Place p = place(k);
+                float xv[Q], slope[Q], step[Q], u[Q], gv[Q], zv[Q], sig[Q], gp[Q], a2[S], h[S], e[S], all = 0.0f;
+                const float skip = skip_r, bias = bias_r;
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    at[t][s] = exp2_of(dl * a2[s]);
-                    add[t][s] = ul * bc[w][0][t * 4 * S + n0 + s];
-                    hl[s] = fmaf(at[t][s], hl[s], add[t][s]);
+                for (int s = 0; s < S; ++s) a2[s] = ar[s] * kLog2e, h[s] = hr[s];
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    const bool in = block * BT + row + 4 * i < len;
+                    xv[i] = value_of<TY>(xr[i]);
+                    const float pre = value_of<TY>(dtr[i]) + bias, ex = exp_of(-fabsf(pre));
+                    step[i] = in ? (a.softplus ? softplus_of(pre, ex) : pre) : 0.0f;
+                    slope[i] = a.softplus ? sigmoid_of(pre, ex) : 1.0f;
+                    u[i] = step[i] * xv[i];
+                    all += step[i];
+                    gv[i] = in && p.in ? value_of<TY>(gr[i]) : 0.0f;
+                    zv[i] = value_of<TY>(zr[i]);
+                    sig[i] = z ? sigmoid_of(zv[i]) : 1.0f;
+                    gp[i] = z ? gv[i] * (zv[i] * sig[i]) : gv[i];
                 }
-            };
+                if (k + 1 < nk)
+                    fetch(block, k + 1);  // while this step is worked on
+                else if (block)
+                    fetch(block - 1, 0);
+                all += quad_perm<0xB1>(all);
+                all += quad_perm<0x4E>(all);
+                float at[T][S], add[T][S], hl[S], el[S], pw[S];
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                one(std::integral_constant<int, 0>{}, i);
-                one(std::integral_constant<int, 1>{}, i);
-                one(std::integral_constant<int, 2>{}, i);
-                one(std::integral_constant<int, 3>{}, i);
-            }
+                for (int s = 0; s < S; ++s) hl[s] = el[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);
+                auto one = [&](auto kk, int i) {
+                    constexpr int J = decltype(kk)::value;
+                    const int t = 4 * i + J;
+                    const float dl = from<J>(step[i]), ul = from<J>(u[i]);
+                    float bv[S];
+                    get_states<S>(&bc[w][0][t * 4 * S + n0], bv);
 #pragma unroll
-            for (int t = T - 1; t >= 0; --t)
+                    for (int s = 0; s < S; ++s) {
+                        at[t][s] = exp2_of(dl * a2[s]);
+                        add[t][s] = ul * bv[s];
+                        hl[s] = fmaf(at[t][s], hl[s], add[t][s]);
+                    }
+                };
+                auto one_back = [&](auto kk, int i) {
+                    constexpr int J = decltype(kk)::value;
+                    const int t = 4 * i + J;
+                    const float gl = from<J>(gp[i]);
+                    float cv[S];
+                    get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
 #pragma unroll
-                for (int s = 0; s < S; ++s) el[s] = at[t][s] * fmaf(bc[w][1][t * 4 * S + n0 + s], gl[t], el[s]);
+                    for (int s = 0; s < S; ++s) el[s] = at[t][s] * fmaf(cv[s], gl, el[s]);
+                };
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                sum[turn][w][0][s][lane] = exp2_of(all * a2[s]);
-                sum[turn][w][1][s][lane] = hl[s];
-                sum[turn][w][2][s][lane] = el[s];
-            }
-            float h[S];
-            const long long slot = first / (T * NW) + seq + block;
-            load_states<S>(g.kept + (slot * a.channels + p.ch) * (4 * S), n0, 4 * S, 0.0f, h);
-            __syncthreads();
-            if (block != blocks - 1) {
+                for (int i = 0; i < Q; ++i) {
+                    one(std::integral_constant<int, 0>{}, i);
+                    one(std::integral_constant<int, 1>{}, i);
+                    one(std::integral_constant<int, 2>{}, i);
+                    one(std::integral_constant<int, 3>{}, i);
+                }
 #pragma unroll
-                for (int s = 0; s < S; ++s) e[s] = carry[turn][s][lane];
-            }
-            for (int i = 0; i < w; ++i)
+                for (int i = Q - 1; i >= 0; --i) {
+                    one_back(std::integral_constant<int, 3>{}, i);
+                    one_back(std::integral_constant<int, 2>{}, i);
+                    one_back(std::integral_constant<int, 1>{}, i);
+                    one_back(std::integral_constant<int, 0>{}, i);
+                }
+                product[turn][w].put(lane, pw);
+                made[turn][w].put(lane, hl);
+                given[turn][w].put(lane, el);
+                lds_barrier();
+                if (block != blocks - 1) {
+                    carry[flip][k].get(lane, e);
+                } else {
 #pragma unroll
-                for (int s = 0; s < S; ++s) h[s] = fmaf(sum[turn][i][0][s][lane], h[s], sum[turn][i][1][s][lane]);
-            for (int i = NW - 1; i > w; --i)
+                    for (int s = 0; s < S; ++s) e[s] = 0.0f;
+                    if (gfinal) load_states<S>(gfinal + ((long long)seq * a.channels + p.ch) * a.state, n0, a.state, 0.0f, e);
+                }
+                for (int i = 0; i < w; ++i) {
+                    product[turn][i].get(lane, pw);
+                    made[turn][i].get(lane, hl);
 #pragma unroll
-                for (int s = 0; s < S; ++s) e[s] = fmaf(sum[turn][i][0][s][lane], e[s], sum[turn][i][2][s][lane]);
-            float ypre[Q], gu[Q], ga[Q], das[S];
+                    for (int s = 0; s < S; ++s) h[s] = fmaf(pw[s], h[s], hl[s]);
+                }
+                for (int i = NW - 1; i > w; --i) {
+                    product[turn][i].get(lane, pw);
+                    given[turn][i].get(lane, el);
 #pragma unroll
-            for (int s = 0; s < S; ++s) das[s] = 0.0f;
-            // forward: `add` becomes a_t h_{t-1}
+                    for (int s = 0; s < S; ++s) e[s] = fmaf(pw[s], e[s], el[s]);
+                }
+                float ypre[Q], gu[Q], gd[Q], das[S], vb[T * S], vc[T * S];
+                auto sum16 = [&](const float* from, float& to) {
+                    float v[16];
 #pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                float v[4];
+                    for (int q = 0; q < 16; ++q) v[q] = from[q];
+                    to += over_quads(v);
+                };
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int t = 4 * i + k;
-                    v[k] = 0.0f;
+                for (int s = 0; s < S; ++s) das[s] = 0.0f;
+                // forward: `add` becomes a_t h_{t-1}
+                auto ahead = [&](auto kk, int i, float (&v)[4]) {
+                    constexpr int J = decltype(kk)::value;
+                    const int t = 4 * i + J;
+                    const float gl = from<J>(gp[i]);
+                    float cv[S];
+                    get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
+                    v[J] = 0.0f;
 #pragma unroll
                     for (int s = 0; s < S; ++s) {
                         const float ah = at[t][s] * h[s];
                         h[s] = ah + add[t][s];
                         add[t][s] = ah;
-                        v[k] = fmaf(bc[w][1][t * 4 * S + n0 + s], h[s], v[k]);
-                        const float gc = over_quads(p.in ? gl[t] * h[s] : 0.0f);
-                        if (p.quad == 0 && t0 + t < end && n0 + s < a.state) to_c[(t0 + t) * row + n0 + s] = gc;
+                        v[J] = fmaf(cv[s], h[s], v[J]);
+                        vc[t * S + s] = gl * h[s];
                     }
-                }
-                ypre[i] = over_four(v);
-            }
-            // back
-            auto back = [&](auto k, int i, float (&v)[4], float (&r)[4]) {
-                constexpr int J = decltype(k)::value;
-                const int t = 4 * i + J;
-                const float dl = from<J>(step[i]), ul = from<J>(u[i]);
-                v[J] = r[J] = 0.0f;
+                };
 #pragma unroll
-                for (int s = 0; s < S; ++s) {
-                    const float G = fmaf(bc[w][1][t * 4 * S + n0 + s], gl[t], e[s]);
-                    const float gb = over_quads(p.in ? G * ul : 0.0f);
-                    if (p.quad == 0 && t0 + t < end && n0 + s < a.state) to_b[(t0 + t) * row + n0 + s] = gb;
-                    v[J] = fmaf(G, bc[w][0][t * 4 * S + n0 + s], v[J]);
-                    const float q = G * add[t][s];
-                    r[J] = fmaf(q, a2[s], r[J]);
-                    das[s] = fmaf(q, dl, das[s]);
-                    e[s] = at[t][s] * G;
+                for (int i = 0; i < Q; ++i) {
+                    float v[4];
+                    ahead(std::integral_constant<int, 0>{}, i, v);
+                    ahead(std::integral_constant<int, 1>{}, i, v);
+                    ahead(std::integral_constant<int, 2>{}, i, v);
+                    ahead(std::integral_constant<int, 3>{}, i, v);
+                    ypre[i] = over_four(v);
+#pragma unroll
+                    for (int q = 0; q < S / 4; ++q) sum16(vc + (i * (S / 4) + q) * 16, sum_c[i * (S / 4) + q]);
                 }
+                // a lane whose channel is none adds nothing to b's and c's gradients: its gp and e are zero
+                if (!p.in)
+#pragma unroll
+                    for (int s = 0; s < S; ++s) e[s] = 0.0f;
+                auto back = [&](auto kk, int i, float (&v)[4], float (&r)[4]) {
+                    constexpr int J = decltype(kk)::value;
+                    const int t = 4 * i + J;
+                    const float dl = from<J>(step[i]), ul = from<J>(u[i]), gl = from<J>(gp[i]);
+                    float bv[S], cv[S];
+                    get_states<S>(&bc[w][0][t * 4 * S + n0], bv);
+                    get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
+                    v[J] = r[J] = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < S; ++s) {
+                        const float G = fmaf(cv[s], gl, e[s]);
+                        vb[t * S + s] = G * ul;
+                        v[J] = fmaf(G, bv[s], v[J]);
+                        const float q = G * add[t][s];
+                        r[J] = fmaf(q, a2[s], r[J]);
+                        das[s] = fmaf(q, dl, das[s]);
+                        e[s] = at[t][s] * G;
+                    }
+                };
+#pragma unroll
+                for (int i = Q - 1; i >= 0; --i) {
+                    float v[4], r[4];
+                    back(std::integral_constant<int, 3>{}, i, v, r);
+                    back(std::integral_constant<int, 2>{}, i, v, r);
+                    back(std::integral_constant<int, 1>{}, i, v, r);
+                    back(std::integral_constant<int, 0>{}, i, v, r);
+                    gu[i] = over_four(v);
+                    gd[i] = over_four(r);
+#pragma unroll
+                    for (int q = 0; q < S / 4; ++q) sum16(vb + (i * (S / 4) + q) * 16, sum_b[i * (S / 4) + q]);
+                }
+                if constexpr (S == 2) {
+                    sum16(vb, sum_b[0]);
+                    sum16(vc, sum_c[0]);
+                } else if constexpr (S == 1) {  // eight of each are sixteen
+                    float v[16];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = vb[q], v[q + 8] = vc[q];
+                    sum16(v, sum_b[0]);
+                }
+                if (w == 0) {
+                    carry[flip ^ 1][k].put(lane, e);
+                    if (block == 0 && g.initial && p.in)
+                        store_states<S>(g.initial + ((long long)seq * a.channels + p.ch) * a.state, n0, a.state, e);
+                }
+                const Buffer gxb = gxs.from(block * BT), gdb = gdts.from(block * BT), gzb = gzs.from(block * BT);
+                const uint32_t off = p.ch * (uint32_t)sizeof(E);
+                float dd = 0.0f, db = 0.0f;
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    const uint32_t to = p.in ? oa.at[i] + off : kNowhere;
+                    const float gdt = fmaf(gu[i], xv[i], gd[i] * kLn2) * slope[i];
+                    store_to<TY>(gxb, to, fmaf(gu[i], step[i], skip * gp[i]));
+                    store_to<TY>(gdb, to, gdt);
+                    if (z)
+                        store_to<TY>(gzb, to, gv[i] * fmaf(skip, xv[i], ypre[i]) * (sig[i] * (1.0f + zv[i] * (1.0f - sig[i]))));
+                    const bool in = block * BT + row + 4 * i < len;
+                    dd = fmaf(gp[i], xv[i], dd);
+                    db += in ? gdt : 0.0f;
+                }
+                dd += quad_perm<0xB1>(dd);
+                dd += quad_perm<0x4E>(dd);
+                db += quad_perm<0xB1>(db);
+                db += quad_perm<0x4E>(db);
+#pragma unroll
+                for (int s = 0; s < S; ++s) total[k][w][s][lane] += das[s];
+                total[k][w][S][lane] += j == 0 ? dd : db;
+            }
+            const int t0 = block * BT + w * T, mine = sixteenth_of(lane);
+            auto leave = [&](float v, int at, float* to) {  // of value `at` of the wave's T * S
+                const int t = at / S, n = n0 + at % S;
+                if (t0 + t < len && n < a.state) to[((long long)first + t0 + t) * row_bc + n] = v;
             };
+            if constexpr (S == 1) {
+                leave(sum_b[0], mine % 8, mine < 8 ? to_b : to_c);
+            } else {
 #pragma unroll
-            for (int i = Q - 1; i >= 0; --i) {
-                float v[4], r[4];
-                back(std::integral_constant<int, 3>{}, i, v, r);
-                back(std::integral_constant<int, 2>{}, i, v, r);
-                back(std::integral_constant<int, 1>{}, i, v, r);
-                back(std::integral_constant<int, 0>{}, i, v, r);
-                gu[i] = over_four(v);
-                ga[i] = over_four(r);
-            }
-#pragma unroll
-            for (int s = 0; s < S; ++s) da[s] += das[s];
-            if (w == 0) {
-#pragma unroll
-                for (int s = 0; s < S; ++s) carry[turn ^ 1][s][lane] = e[s];
-            }
-#pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                const int t = t0 + 4 * i + p.j;
-                if (t >= end || !p.in) continue;
-                const long long to = (long long)t * a.channels + p.ch;
-                const float gstep = fmaf(gu[i], xv[i], ga[i] * kLn2);
-                const float gdt = a.softplus ? gstep * sigmoid_of(pre[i]) : gstep;
-                static_cast<E*>(g.x)[to] = TY::store(fmaf(gu[i], step[i], skip * gp[i]));
-                static_cast<E*>(g.dt)[to] = TY::store(gdt);
-                if (z) {
-                    const float sig = sigmoid_of(zv[i]);
-                    static_cast<E*>(g.z)[to] = TY::store(gv[i] * fmaf(skip, xv[i], ypre[i]) * sig * (1.0f + zv[i] * (1.0f - sig)));
+                for (int i = 0; i < N16; ++i) {
+                    leave(sum_b[i], 16 * i + mine, to_b);
+                    leave(sum_c[i], 16 * i + mine, to_c);
                 }
-                dd += gp[i] * xv[i];
-                dbias += gdt;
             }
         }
-        if (g.initial && p.in && w == 0) store_states<S>(g.initial + state_at, n0, a.state, e);
-        if (a.clear && seq == a.q.n_seq - 1 && p.in)
-            for (int t = end + 4 * w + p.j; t < a.q.n_tokens; t += 4 * NW) {
-                const long long to = (long long)t * a.channels + p.ch;
-                if (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_X) static_cast<E*>(g.x)[to] = TY::store(0.0f);
-                if (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_DT) static_cast<E*>(g.dt)[to] = TY::store(0.0f);
-                if (z && (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_Z)) static_cast<E*>(g.z)[to] = TY::store(0.0f);
+        if (!blocks && w == 0 && g.initial)  // its final state is its initial one
+            for (int k = 0; k < nk; ++k) {
+                const Place p = place(k);
+                const long long at = ((long long)seq * a.channels + p.ch) * a.state;
+                float e[S];
+#pragma unroll
+                for (int s = 0; s < S; ++s) e[s] = 0.0f;
+                if (gfinal) load_states<S>(gfinal + at, n0, a.state, 0.0f, e);
+                if (p.in) store_states<S>(g.initial + at, n0, a.state, e);
+            }
+        if (a.clear && seq == a.q.n_seq - 1)
+            for (int k = 0; k < nk; ++k) {
+                const Place p = place(k);
+                if (!p.in) continue;
+                for (int t = end + 4 * w + j; t < a.q.n_tokens; t += 4 * NW) {
+                    const long long to = (long long)t * a.channels + p.ch;
+                    if (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_X) static_cast<E*>(g.x)[to] = TY::store(0.0f);
+                    if (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_DT) static_cast<E*>(g.dt)[to] = TY::store(0.0f);
+                    if (z && (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_Z)) static_cast<E*>(g.z)[to] = TY::store(0.0f);
+                }
             }
     }
-    // the waves' sums together
+    // the waves' sums together, a wave for each sixteen channels
     __syncthreads();
-    __shared__ double all[NW][64];
+    for (int k = w; k < nk; k += NW) {
+        const Place p = place(k);
+        if (!p.in) continue;
 #pragma unroll
-    for (int s = 0; s < S + 2; ++s) {
-        double v = s < S ? da[s < S ? s : 0] : s == S ? dd : dbias;
-        if (s >= S) {  // of the lanes' tokens
-            v += __shfl_xor(v, 1);
-            v += __shfl_xor(v, 2);
-        }
-        all[w][lane] = v;
-        __syncthreads();
-        if (w == 0 && p.in) {
-            v = all[0][lane];
+        for (int s = 0; s <= S; ++s) {
+            double v = total[k][0][s][lane];
 #pragma unroll
-            for (int i = 1; i < NW; ++i) v += all[i][lane];
+            for (int i = 1; i < NW; ++i) v += total[k][i][s][lane];
             if (s < S) {
                 if (n0 + s < a.state) g.part_a[((long long)part * a.channels + p.ch) * a.state + n0 + s] = (float)v;
-            } else if (p.j == 0) {
-                (s == S ? g.part_d : g.part_bias)[(long long)part * a.channels + p.ch] = (float)v;
+            } else if (j < 2) {
+                (j == 0 ? g.part_d : g.part_bias)[(long long)part * a.channels + p.ch] = (float)v;
             }
         }
-        __syncthreads();
     }
 }
 
@@ -839,17 +989,28 @@ int with_state(int type, int state, F f) {
 }
 inline int lane_states(int state) { return state <= 4 ? 1 : state <= 8 ? 2 : state <= 16 ? 4 : state <= 32 ? 8 : 16; }
 
-// The sequences go to as many workgroups for each 16 channels as fill the chip, since each
+// How many times 16 channels a workgroup of the backward has: more of them leave fewer partial
+// sums of b's and c's gradients and share the sums over lanes, as long as all CUs have one.
+inline int sixteens_of(const Scan& a) {
+    if (a.state > 16) return 1;
+    const long long all = (long long)channel_groups_of(a) * a.q.n_seq;
+    return all >= 4 * 256 ? 4 : all >= 2 * 256 ? 2 : 1;
+}
+inline int wg_groups_of(const Scan& a) {
+    const int k = sixteens_of(a);
+    return a.groups * ((channel_groups_of(a) / a.groups + k - 1) / k);
+}
+// The sequences go to as many workgroups of the same channels as fill the chip, since each
 // leaves a row of partial sums.
 inline int parts_of(const Scan& a) {
-    return std::min(a.q.n_seq, std::max(1, 1024 / channel_groups_of(a)));
+    return std::min(a.q.n_seq, std::max(1, 1024 / wg_groups_of(a)));
 }
 
 // Bytes of the backward's workspace, laid out from `base` on.
 long long lay_out(const Scan& a, void* base, Grads* g) {
     const int s = lane_states(a.state);
     const long long slots = a.q.n_tokens / block_of(s) + a.q.n_seq;
-    const long long in_group = channel_groups_of(a) / a.groups, parts = parts_of(a);
+    const long long in_group = wg_groups_of(a) / a.groups, parts = parts_of(a);
     long long kept, bc, pa, all = 0;
     g->rows = (long long)a.q.n_tokens * a.groups * a.state;
     if (!mul_ok(slots * a.channels, 4 * s * 4, &kept) || !mul_ok(g->rows, in_group * 4, &bc) ||
@@ -944,18 +1105,31 @@ extern "C" int selective_scan_backward(const selective_scan_shape_t* shape, cons
         using TY = decltype(ty);
         using E = typename TY::S;
         constexpr int S = decltype(states)::value;
-        const int groups = channel_groups_of(a), parts = parts_of(a);
+        const int groups = channel_groups_of(a), wg_groups = wg_groups_of(a), parts = parts_of(a);
         if (a.q.n_seq) {
-            hipLaunchKernelGGL((scan_states_kernel<TY, S>), dim3((unsigned)(groups * (long long)a.q.n_seq)),
+            hipLaunchKernelGGL((scan_states_kernel<TY, S>), dim3(dealt(groups * (long long)a.q.n_seq)),
                                dim3(64 * waves_of(S)), 0, stream, a, groups, (const E*)x, (const E*)dt, a_, (const E*)b,
                                dt_bias, initial_state, g.kept);
-            hipLaunchKernelGGL((scan_backward_kernel<TY, S>), dim3((unsigned)(groups * parts)), dim3(64 * waves_of(S)), 0,
-                               stream, a, groups, parts, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
-                               (const E*)z, dt_bias, (const E*)grad_y, grad_final_state, g);
+            auto go = [&](auto kernel) {
+                hipLaunchKernelGGL(kernel, dim3(dealt((long long)wg_groups * parts)), dim3(64 * waves_of(S)), 0, stream, a,
+                                   wg_groups, parts, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
+                                   (const E*)z, dt_bias, (const E*)grad_y, grad_final_state, g);
+            };
+            const int sixteens = sixteens_of(a);
+            if constexpr (S <= 4) {
+                if (sixteens == 4)
+                    go(scan_backward_kernel<TY, S, 4>);
+                else if (sixteens == 2)
+                    go(scan_backward_kernel<TY, S, 2>);
+                else
+                    go(scan_backward_kernel<TY, S, 1>);
+            } else {
+                go(scan_backward_kernel<TY, S, 1>);
+            }
         }
         const long long elements = 2 * g.rows + (long long)a.channels * (a.state + 2);
         hipLaunchKernelGGL((scan_sums_kernel<TY>), dim3((unsigned)((elements + kSumThreads - 1) / kSumThreads)),
-                           dim3(kSumThreads), 0, stream, a, g, groups / a.groups, parts, (E*)grad_b, (E*)grad_c, grad_a,
+                           dim3(kSumThreads), 0, stream, a, g, wg_groups / a.groups, parts, (E*)grad_b, (E*)grad_c, grad_a,
                            grad_d, grad_dt_bias);
         return launch_status();
     });
