@@ -51,7 +51,7 @@ __device__ __forceinline__ float quad_perm(float x) {
 }
 // Lane J of each four lanes' value.
 template <int J>
-__device__ __forceinline__ float from(float x) {
+__device__ __forceinline__ float from_lane(float x) {
     return quad_perm<J * 0x55>(x);
 }
 // Lane j of each four gets the sum over them of v[j].
@@ -62,20 +62,19 @@ __device__ __forceinline__ float over_four(const float (&v)[4]) {
     return (high ? b : a) + quad_perm<0x4E>(high ? a : b);
 }
 
-// A workgroup's channels: the group of b and c that they read, and the lane's own.
+// The lanes' channels of a sixteen of a group of those that share b and c.
 struct Place {
-    int group, ch, quad, j;
+    int ch, quad, j;
     bool in;
 };
-__device__ __forceinline__ Place place_of(const Scan& a, int index) {
-    const int parts = (a.share + kGroupCh - 1) / kGroupCh, lane = threadIdx.x & 63;
+__device__ __forceinline__ Place place_of(const Scan& a, int group, int sixteen) {
+    const int lane = threadIdx.x & 63;
     Place p;
-    p.group = index / parts;
     p.quad = lane >> 2;
     p.j = lane & 3;
-    const int at = index % parts * kGroupCh + p.quad;
+    const int at = sixteen * kGroupCh + p.quad;
     p.in = at < a.share;
-    p.ch = p.group * a.share + min(at, a.share - 1);
+    p.ch = group * a.share + min(at, a.share - 1);
     return p;
 }
 
@@ -97,7 +96,6 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
-
 // The barrier of a workgroup's exchanges through LDS; global loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
@@ -128,32 +126,28 @@ __device__ __forceinline__ void store_to(Buffer b, uint32_t at, float x) {
         __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, TY::store(x)), b, at, 0, 0);
 }
 
-// The rows of a sequence, a block of them at a time; rows behind its end read as zeros and
-// are not written, so that nothing needs a branch.  (Where rows overlap, at a stride below
-// their width, they read as something: steps and gradients there are set to zero.)
-template <class TY>
+// The rows of a tensor from one on, for a block of tokens at a time: those behind the
+// sequence's end read as zeros and are not written, so that nothing needs a branch.  (Where
+// rows overlap, at a stride below their width, they read as something: steps and gradients
+// there are set to zero.)
 struct Rows {
-    const char* base;
-    long long bytes;  // from a row to the next
-    uint32_t width;   // bytes of a row
-    int len;
-    __device__ __forceinline__ Rows(const typename TY::S* p, int first, int end, long long stride, int width_)
-        : base(p ? reinterpret_cast<const char*>(p + first * stride) : nullptr), bytes(stride * (long long)sizeof(typename TY::S)),
-          width(width_ * (uint32_t)sizeof(typename TY::S)), len(end - first) {}
-    // Those from row `at` of the sequence on, of which there are none for at >= len.
-    __device__ __forceinline__ Buffer from(int at) const {
-        const long long n = at < len && base ? (len - 1 - at) * bytes + width : 0;
-        return buffer_of(base + at * bytes, n < 0x7fffffff ? n : 0x7fffffff);
-    }
+    const char* at;
+    int bytes, rest;  // from a row to the next, and from there to the row's end
+    template <class E>
+    __device__ __forceinline__ Rows(const E* p, long long row, long long stride, bool single, int width)
+        : at(p ? reinterpret_cast<const char*>(p + row * stride) : nullptr),
+          bytes(p && !single ? (int)stride * (int)sizeof(E) : 0), rest(p ? width * (int)sizeof(E) - bytes : 0) {}
+    // The next n of them.
+    __device__ __forceinline__ Buffer next(int n) const { return buffer_of(at, n > 0 ? n * bytes + rest : 0); }
+    __device__ __forceinline__ void move(int n) { at += n * bytes; }
 };
-// A lane's places in a block of a wave's T tokens: element (4 i + j) of the wave's rows.
+// A lane's places in a block: its element of the rows row, row + 4, ...
 template <class TY, int Q>
 struct Places {
     uint32_t at[Q];
-    __device__ __forceinline__ Places(bool in, long long stride, int row, int column) {
+    __device__ __forceinline__ Places(const Rows& r, int row, int column) {
 #pragma unroll
-        for (int i = 0; i < Q; ++i)
-            at[i] = in ? (uint32_t)(((row + 4 * i) * stride + column) * (long long)sizeof(typename TY::S)) : kNowhere;
+        for (int i = 0; i < Q; ++i) at[i] = (row + 4 * i) * (uint32_t)r.bytes + column * (uint32_t)sizeof(typename TY::S);
     }
 };
 // b or c of a wave's T tokens: loaded as they are, and put to LDS as 32-bit floats [T][4 S].
@@ -162,12 +156,12 @@ struct Shared {
     static constexpr int N = (T * 4 * S + 63) / 64;
     static constexpr bool all = T * 4 * S % 64 == 0;
     uint32_t at[N], raw[N];
-    __device__ __forceinline__ Shared(long long stride, int row, int state) {
+    __device__ __forceinline__ Shared(const Rows& r, int row, int state) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int e = i * 64 + (threadIdx.x & 63), n = e % (4 * S);
             at[i] = n < state && (all || e < T * 4 * S)
-                        ? (uint32_t)(((row + e / (4 * S)) * stride + n) * (long long)sizeof(typename TY::S))
+                        ? (row + e / (4 * S)) * (uint32_t)r.bytes + n * (uint32_t)sizeof(typename TY::S)
                         : kNowhere;
         }
     }
@@ -184,29 +178,32 @@ struct Shared {
     }
 };
 
-// S floats of a lane in LDS: [S / V][64 lanes][V], V of them one access.
+// S floats of each lane in LDS: [S / V][64 lanes][V], V of them one access.  As a whole
+// they are 64 S floats, of channel quad_of(f) and state state_of(f).
 template <int S>
 struct Lanes {
     static constexpr int V = S < 4 ? S : 4;
     typedef float vec __attribute__((ext_vector_type(V)));
-    float x[S / V][64][V];
+    alignas(16) float x[64 * S];
     __device__ __forceinline__ void put(int lane, const float (&h)[S]) {
 #pragma unroll
         for (int i = 0; i < S / V; ++i) {
             vec v;
 #pragma unroll
             for (int k = 0; k < V; ++k) v[k] = h[i * V + k];
-            *reinterpret_cast<vec*>(x[i][lane]) = v;
+            *reinterpret_cast<vec*>(x + (i * 64 + lane) * V) = v;
         }
     }
     __device__ __forceinline__ void get(int lane, float (&h)[S]) const {
 #pragma unroll
         for (int i = 0; i < S / V; ++i) {
-            const vec v = *reinterpret_cast<const vec*>(x[i][lane]);
+            const vec v = *reinterpret_cast<const vec*>(x + (i * 64 + lane) * V);
 #pragma unroll
             for (int k = 0; k < V; ++k) h[i * V + k] = v[k];
         }
     }
+    static __device__ __forceinline__ int quad_of(int f) { return f % (64 * V) / V >> 2; }
+    static __device__ __forceinline__ int state_of(int f) { return (f % (64 * V) / V & 3) * S + f / (64 * V) * V + f % V; }
 };
 // S neighbouring floats, V of them one access.
 template <int S>
@@ -221,53 +218,83 @@ __device__ __forceinline__ void get_states(const float* p, float (&h)[S]) {
     }
 }
 
+// The waves' exchange, between two barriers: a thread has one or several of the 64 S states
+// of the workgroup's channels (of a state's gradients, with `back`), and goes along the
+// waves' stretches, leaving each the state that it begins with in the place of what it made
+// of zeros.  F states a thread, f = f0 + i * threads.
+template <int S, int NW, bool back>
+__device__ __forceinline__ float along(const Lanes<S> (&product)[NW], Lanes<S> (&made)[NW], int f, float h) {
+    float p[NW], m[NW];
+#pragma unroll
+    for (int i = 0; i < NW; ++i) p[i] = product[i].x[f], m[i] = made[i].x[f];
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+        const int i = back ? NW - 1 - k : k;
+        made[i].x[f] = h;
+        h = fmaf(p[i], h, m[i]);
+    }
+    return h;
+}
+
 // -------------------------------------------------------------------- forward
 template <class TY, int S>
-__global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
-    Scan a, int channel_groups, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
+__global__ __launch_bounds__(64 * waves_of(S), S <= 8 ? 4 : 2) void scan_kernel(
+    Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
     const float* __restrict__ decay, const typename TY::S* __restrict__ b, const typename TY::S* __restrict__ c,
     const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias,
     const float* initial, typename TY::S* __restrict__ y, float* final) {
-    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4;
-    __shared__ Lanes<S> product[2][NW], made[2][NW], carry[2];  // P and h' of each wave
+    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW, F = (S + NW - 1) / NW;
+    __shared__ Lanes<S> product[NW], made[NW];  // P and h' of each wave
     __shared__ alignas(16) float bc[NW][2][T * 4 * S];
-    const long long count = (long long)channel_groups * a.q.n_seq, index = on_die(blockIdx.x, count);
+    const long long count = (long long)a.groups * sixteens * a.q.n_seq, index = on_die(blockIdx.x, count);
     if (index >= count) return;
-    const Place p = place_of(a, (int)(index % channel_groups));
-    const int seq = (int)(index / channel_groups), lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = p.j * S;
+    const int sixteen = (int)(index % sixteens), group = (int)(index / sixteens % a.groups);
+    const int seq = (int)(index / sixteens / a.groups), lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place p = place_of(a, group, sixteen);
+    const int n0 = p.j * S, row = w * T + p.j;
     int first, end;
     span_of(a.q, seq, first, end);
     const int len = end - first;
-    float a2[S], h[S];
+    float a2[S];
     load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
 #pragma unroll
-    for (int s = 0; s < S; ++s) a2[s] *= kLog2e, h[s] = 0.0f;
-    const long long kept = ((long long)seq * a.channels + p.ch) * a.state;
-    if (initial) load_states<S>(initial + kept, n0, a.state, 0.0f, h);
+    for (int s = 0; s < S; ++s) a2[s] *= kLog2e;
     const float skip = d ? d[p.ch] : 0.0f, bias = dt_bias ? dt_bias[p.ch] : 0.0f;
-    const Rows<TY> xs(x, first, end, a.xt, a.channels), dts(dt, first, end, a.dtt, a.channels),
-        zs(z, first, end, a.zt, a.channels), bs(b + p.group * a.bg, first, end, a.bt, a.state),
-        cs(c + p.group * a.cg, first, end, a.ct, a.state), ys(y, first, end, a.channels, a.channels);
-    const int row = w * T + p.j;
-    const Places<TY, Q> xa(true, a.single ? 0 : a.xt, row, p.ch), dta(true, a.single ? 0 : a.dtt, row, p.ch),
-        za(true, a.single ? 0 : a.zt, row, p.ch), ya(p.in, a.channels, row, p.ch);
-    Shared<TY, S, T> bl(a.single ? 0 : a.bt, w * T, a.state), cl(a.single ? 0 : a.ct, w * T, a.state);
+    // the states that this thread takes along, as the exchange has them
+    const long long kept = ((long long)seq * a.channels + group * a.share) * a.state;
+    auto state_at = [&](int i, long long* at) {
+        const int f = threadIdx.x + i * 64 * NW, ch = sixteen * kGroupCh + Lanes<S>::quad_of(f), n = Lanes<S>::state_of(f);
+        *at = kept + (long long)ch * a.state + n;
+        return f < 64 * S && ch < a.share && n < a.state;
+    };
+    float h[F];
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+        long long at;
+        h[i] = state_at(i, &at) && initial ? initial[at] : 0.0f;
+    }
+    Rows xs(x, first, a.xt, a.single, a.channels), dts(dt, first, a.dtt, a.single, a.channels),
+        zs(z, first, a.zt, a.single, a.channels), bs(b + group * a.bg, first, a.bt, a.single, a.state),
+        cs(c + group * a.cg, first, a.ct, a.single, a.state), ys(y, first, a.channels, false, a.channels);
+    const Places<TY, Q> xa(xs, row, p.ch), dta(dts, row, p.ch), za(zs, row, p.ch), ya(ys, row, p.ch);
+    Shared<TY, S, T> bl(bs, w * T, a.state), cl(cs, w * T, a.state);
     uint32_t xr[Q], dtr[Q], zr[Q];
-    auto fetch = [&](int at) {
-        const Buffer xb = xs.from(at), db = dts.from(at), zb = zs.from(at);
+    auto fetch = [&](int left) {
+        const int n = min(left, BT);
+        const Buffer xb = xs.next(n), db = dts.next(n), zb = zs.next(n);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
             xr[i] = load_raw<TY>(xb, xa.at[i]);
             dtr[i] = load_raw<TY>(db, dta.at[i]);
             zr[i] = load_raw<TY>(zb, za.at[i]);
         }
-        bl.load(bs.from(at));
-        cl.load(cs.from(at));
+        bl.load(bs.next(n));
+        cl.load(cs.next(n));
+        xs.move(BT), dts.move(BT), zs.move(BT), bs.move(BT), cs.move(BT);
     };
-    fetch(0);
-    int turn = 0;
-    for (int block = 0; block < len; block += T * NW, turn ^= 1) {
+    fetch(len);
+    for (int left = len; left > 0; left -= BT) {
         wave_fence();
         bl.put(bc[w][0]);
         cl.put(bc[w][1]);
@@ -277,13 +304,13 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
         for (int i = 0; i < Q; ++i) {
             xv[i] = value_of<TY>(xr[i]);
             const float pre = value_of<TY>(dtr[i]) + bias;
-            step[i] = block + row + 4 * i < len ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
+            step[i] = row + 4 * i < left ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
             u[i] = step[i] * xv[i];
             all += step[i];
             const float zv = value_of<TY>(zr[i]);
             gate[i] = z ? zv * sigmoid_of(zv) : 1.0f;
         }
-        fetch(block + T * NW);  // while this block is worked on
+        fetch(left - BT);  // while this block is worked on
         all += quad_perm<0xB1>(all);
         all += quad_perm<0x4E>(all);
         float at[T][S], add[T][S], hl[S], pw[S];
@@ -292,7 +319,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
         auto one = [&](auto k, int i) {
             constexpr int J = decltype(k)::value;
             const int t = 4 * i + J;
-            const float dl = from<J>(step[i]), ul = from<J>(u[i]);
+            const float dl = from_lane<J>(step[i]), ul = from_lane<J>(u[i]);
             float bv[S];
             get_states<S>(&bc[w][0][t * 4 * S + n0], bv);
 #pragma unroll
@@ -309,17 +336,16 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
             one(std::integral_constant<int, 2>{}, i);
             one(std::integral_constant<int, 3>{}, i);
         }
-        product[turn][w].put(lane, pw);
-        made[turn][w].put(lane, hl);
+        product[w].put(lane, pw);
+        made[w].put(lane, hl);
         lds_barrier();
-        if (block) carry[turn].get(lane, h);
-        for (int i = 0; i < w; ++i) {
-            product[turn][i].get(lane, pw);
-            made[turn][i].get(lane, hl);
 #pragma unroll
-            for (int s = 0; s < S; ++s) h[s] = fmaf(pw[s], h[s], hl[s]);
-        }
-        const Buffer yb = ys.from(block);
+        for (int i = 0; i < F; ++i)
+            if (w * 64 + i * 64 * NW < 64 * S) h[i] = along<S, NW, false>(product, made, threadIdx.x + i * 64 * NW, h[i]);
+        lds_barrier();
+        made[w].get(lane, hl);
+        const Buffer yb = ys.next(min(left, BT));
+        ys.move(BT);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
             float v[4];
@@ -331,16 +357,19 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
                 v[k] = 0.0f;
 #pragma unroll
                 for (int s = 0; s < S; ++s) {
-                    h[s] = fmaf(at[t][s], h[s], add[t][s]);
-                    v[k] = fmaf(cv[s], h[s], v[k]);
+                    hl[s] = fmaf(at[t][s], hl[s], add[t][s]);
+                    v[k] = fmaf(cv[s], hl[s], v[k]);
                 }
             }
-            store_to<TY>(yb, ya.at[i], fmaf(skip, xv[i], over_four(v)) * gate[i]);
+            store_to<TY>(yb, p.in ? ya.at[i] : kNowhere, fmaf(skip, xv[i], over_four(v)) * gate[i]);
         }
-        if (w == NW - 1) carry[turn ^ 1].put(lane, h);
     }
-    // (the last wave has the state behind the last block, or the one before any)
-    if (final && p.in && w == NW - 1) store_states<S>(final + kept, n0, a.state, h);
+    if (final)
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            long long at;
+            if (state_at(i, &at)) final[at] = h[i];
+        }
     if ((a.clear & SELECTIVE_SCAN_CLEAR_Y) && seq == a.q.n_seq - 1 && p.in)
         for (int t = end + 4 * w + p.j; t < a.q.n_tokens; t += 4 * NW)
             y[(long long)t * a.channels + p.ch] = TY::store(0.0f);
@@ -351,50 +380,60 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_kernel(
 //   G_t = c_t gy_t + e,  e' = a_t G_t,
 // which is linear in e as the forward is in h, and is cut into the same stretches.
 
-// The states before each block of block_of(S) tokens, to kept[slot][channel][4 S].  The last
-// wave goes along the blocks; the others' part is their stretches.
+// The states before each block of block_of(S) tokens, to kept[slot][group][sixteen][64 S] as
+// the exchange has them.
 template <class TY, int S>
 __global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
-    Scan a, int channel_groups, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
+    Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
     const float* __restrict__ decay, const typename TY::S* __restrict__ b, const float* __restrict__ dt_bias,
     const float* __restrict__ initial, float* __restrict__ kept) {
-    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4;
+    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW, F = (S + NW - 1) / NW;
     __shared__ Lanes<S> product[2][NW], made[2][NW];
     __shared__ alignas(16) float bc[NW][T * 4 * S];
-    const long long count = (long long)channel_groups * a.q.n_seq, index = on_die(blockIdx.x, count);
+    const long long count = (long long)a.groups * sixteens * a.q.n_seq, index = on_die(blockIdx.x, count);
     if (index >= count) return;
-    const Place p = place_of(a, (int)(index % channel_groups));
-    const int seq = (int)(index / channel_groups), lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = p.j * S;
+    const int sixteen = (int)(index % sixteens), group = (int)(index / sixteens % a.groups);
+    const int seq = (int)(index / sixteens / a.groups), lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Place p = place_of(a, group, sixteen);
+    const int n0 = p.j * S, row = w * T + p.j;
     int first, end;
     span_of(a.q, seq, first, end);
     const int len = end - first;
-    float a2[S], h[S];
+    float a2[S];
     load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
 #pragma unroll
-    for (int s = 0; s < S; ++s) a2[s] *= kLog2e, h[s] = 0.0f;
-    if (initial) load_states<S>(initial + ((long long)seq * a.channels + p.ch) * a.state, n0, a.state, 0.0f, h);
+    for (int s = 0; s < S; ++s) a2[s] *= kLog2e;
     const float bias = dt_bias ? dt_bias[p.ch] : 0.0f;
-    const Rows<TY> xs(x, first, end, a.xt, a.channels), dts(dt, first, end, a.dtt, a.channels),
-        bs(b + p.group * a.bg, first, end, a.bt, a.state);
-    const int row = w * T + p.j;
-    const Places<TY, Q> xa(true, a.single ? 0 : a.xt, row, p.ch), dta(true, a.single ? 0 : a.dtt, row, p.ch);
-    Shared<TY, S, T> bl(a.single ? 0 : a.bt, w * T, a.state);
+    float h[F];
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+        const int f = threadIdx.x + i * 64 * NW, ch = sixteen * kGroupCh + Lanes<S>::quad_of(f), n = Lanes<S>::state_of(f);
+        h[i] = initial && f < 64 * S && ch < a.share && n < a.state
+                   ? initial[((long long)seq * a.channels + group * a.share + ch) * a.state + n]
+                   : 0.0f;
+    }
+    Rows xs(x, first, a.xt, a.single, a.channels), dts(dt, first, a.dtt, a.single, a.channels),
+        bs(b + group * a.bg, first, a.bt, a.single, a.state);
+    const Places<TY, Q> xa(xs, row, p.ch), dta(dts, row, p.ch);
+    Shared<TY, S, T> bl(bs, w * T, a.state);
     uint32_t xr[Q], dtr[Q];
-    auto fetch = [&](int at) {
-        const Buffer xb = xs.from(at), db = dts.from(at);
+    auto fetch = [&](int left) {
+        const int n = min(left, BT);
+        const Buffer xb = xs.next(n), db = dts.next(n);
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
             xr[i] = load_raw<TY>(xb, xa.at[i]);
             dtr[i] = load_raw<TY>(db, dta.at[i]);
         }
-        bl.load(bs.from(at));
+        bl.load(bs.next(n));
+        xs.move(BT), dts.move(BT), bs.move(BT);
     };
-    fetch(0);
-    float* to = kept + (((long long)first / (T * NW) + seq) * a.channels + p.ch) * (4 * S);
-    int turn = 0;
-    for (int block = 0; block < len; block += T * NW, turn ^= 1, to += (long long)a.channels * (4 * S)) {
-        if (w == NW - 1 && p.in) store_states<S>(to, n0, 4 * S, h);
+    fetch(len);
+    const long long pitch = (long long)a.groups * sixteens * (64 * S);
+    float* to = kept + ((long long)first / BT + seq) * pitch + ((long long)group * sixteens + sixteen) * (64 * S);
+    int turn = 0;  // one barrier a block: the exchange is done with one while the next is made
+    for (int left = len; left > 0; left -= BT, to += pitch, turn ^= 1) {
         wave_fence();
         bl.put(bc[w]);
         wave_fence();
@@ -402,11 +441,11 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
             const float pre = value_of<TY>(dtr[i]) + bias;
-            step[i] = block + row + 4 * i < len ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
+            step[i] = row + 4 * i < left ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
             u[i] = step[i] * value_of<TY>(xr[i]);
             all += step[i];
         }
-        fetch(block + T * NW);  // while this block is worked on
+        fetch(left - BT);  // while this block is worked on
         all += quad_perm<0xB1>(all);
         all += quad_perm<0x4E>(all);
         float hl[S], pw[S];
@@ -414,7 +453,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
         for (int s = 0; s < S; ++s) hl[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);
         auto one = [&](auto k, int i) {
             constexpr int J = decltype(k)::value;
-            const float dl = from<J>(step[i]), ul = from<J>(u[i]);
+            const float dl = from_lane<J>(step[i]), ul = from_lane<J>(u[i]);
             float bv[S];
             get_states<S>(&bc[w][(4 * i + J) * 4 * S + n0], bv);
 #pragma unroll
@@ -430,13 +469,13 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
         product[turn][w].put(lane, pw);
         made[turn][w].put(lane, hl);
         lds_barrier();
-        if (w == NW - 1)
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                product[turn][i].get(lane, pw);
-                made[turn][i].get(lane, hl);
+        for (int i = 0; i < F; ++i)
+            if (w * 64 + i * 64 * NW < 64 * S) {
+                const int f = threadIdx.x + i * 64 * NW;
+                to[f] = h[i];
 #pragma unroll
-                for (int s = 0; s < S; ++s) h[s] = fmaf(pw[s], h[s], hl[s]);
+                for (int k = 0; k < NW; ++k) h[i] = fmaf(product[turn][k].x[f], h[i], made[turn][k].x[f]);
             }
     }
 }
@@ -451,10 +490,6 @@ struct Grads {  // the backward's outputs and workspace
 // value sixteenth_of(l).  Two lanes' halves change places and are added, four times over.
 __device__ __forceinline__ int sixteenth_of(int lane) {
     return (lane >> 5 & 1) + 2 * (lane >> 4 & 1) + 4 * (lane >> 3 & 1) + 8 * (lane >> 2 & 1);
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp(float x) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), CTRL, 0xf, 0xf, true));
 }
 __device__ __forceinline__ float over_quads(const float (&v)[16]) {
     float a[8], b[4], c[2];
@@ -471,10 +506,11 @@ __device__ __forceinline__ float over_quads(const float (&v)[16]) {
     const bool eight = threadIdx.x & 8, four = threadIdx.x & 4;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float lo = b[2 * i] + dpp<0x128>(b[2 * i]), hi = b[2 * i + 1] + dpp<0x128>(b[2 * i + 1]);  // 8 lanes on
+        // 8 lanes on
+        const float lo = b[2 * i] + quad_perm<0x128>(b[2 * i]), hi = b[2 * i + 1] + quad_perm<0x128>(b[2 * i + 1]);
         c[i] = eight ? hi : lo;
     }
-    const float lo = c[0] + dpp<0x104>(c[0]), hi = c[1] + dpp<0x114>(c[1]);  // 4 lanes on, 4 back
+    const float lo = c[0] + quad_perm<0x104>(c[0]), hi = c[1] + quad_perm<0x114>(c[1]);  // 4 lanes on, 4 back
     return four ? hi : lo;
 }
 
@@ -483,304 +519,323 @@ __device__ __forceinline__ float over_quads(const float (&v)[16]) {
 // parts-th sequence.
 template <class TY, int S, int K>
 __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
-    Scan a, int wg_groups, int parts, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
-    const float* __restrict__ decay, const typename TY::S* __restrict__ b, const typename TY::S* __restrict__ c,
-    const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias,
-    const typename TY::S* __restrict__ gy, const float* gfinal, Grads g) {
-    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW;
+    Scan a, int sixteens, int wg_groups, int parts, const typename TY::S* __restrict__ x,
+    const typename TY::S* __restrict__ dt, const float* __restrict__ decay, const typename TY::S* __restrict__ b,
+    const typename TY::S* __restrict__ c, const float* __restrict__ d, const typename TY::S* __restrict__ z,
+    const float* __restrict__ dt_bias, const typename TY::S* __restrict__ gy, const float* gfinal, Grads g) {
+    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW, F = (2 * S + NW - 1) / NW;
     constexpr int N16 = (T * S + 15) / 16;
     using E = typename TY::S;
-    __shared__ Lanes<S> product[2][NW], made[2][NW], given[2][NW], carry[2][K];  // P, h' and e' of each wave
+    __shared__ Lanes<S> product[NW], made[NW], given[NW];  // P, h' and e' of each wave
+    __shared__ Lanes<S> carry[K], rate[K];                 // e before a block, and log2(e) a
+    __shared__ float2 skip_bias[K][kGroupCh];
     __shared__ alignas(16) float bc[NW][2][T * 4 * S];
     __shared__ double total[K][NW][S + 1][64];  // a's gradients, and d's and dt_bias's in lanes 0 and 1 of four
     const long long count = (long long)wg_groups * parts, index = on_die(blockIdx.x, count);
     if (index >= count) return;
     const int wg = (int)(index % wg_groups), part = (int)(index / wg_groups);
     const int per_group = wg_groups / a.groups, group = wg / per_group, in_group = wg % per_group;
-    const int sixteens = (a.share + kGroupCh - 1) / kGroupCh, k0 = in_group * K, nk = min(K, sixteens - k0);
-    const int lane = threadIdx.x & 63, j = lane & 3;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = j * S;
+    const int k0 = in_group * K, nk = min(K, sixteens - k0);
+    const int lane = threadIdx.x & 63, quad = lane >> 2, j = lane & 3;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = j * S, row = w * T + j;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
 #pragma unroll
         for (int s = 0; s <= S; ++s) total[k][w][s][lane] = 0.0;
+        if (w == k % NW && k < nk) {
+            const Place p = place_of(a, group, k0 + k);
+            float r[S];
+            load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, r);
+#pragma unroll
+            for (int s = 0; s < S; ++s) r[s] *= kLog2e;
+            rate[k].put(lane, r);
+            if (j == 0) skip_bias[k][quad] = float2{d ? d[p.ch] : 0.0f, dt_bias ? dt_bias[p.ch] : 0.0f};
+        }
+    }
     float* to_b = g.part_b + in_group * g.rows + group * a.state;
     float* to_c = g.part_c + in_group * g.rows + group * a.state;
-    const long long row_bc = (long long)a.groups * a.state;
-    // the lane's channel of the k'th sixteen
-    auto place = [&](int k) { return place_of(a, group * sixteens + k0 + k); };
-    int turn = 0, flip = 0;
+    const long long row_bc = (long long)a.groups * a.state, pitch = (long long)a.groups * sixteens * (64 * S);
+    const int last_ch = a.share - 1;
+    __syncthreads();
     for (int seq = part; seq < a.q.n_seq; seq += parts) {
         int first, end;
         span_of(a.q, seq, first, end);
         const int len = end - first, blocks = (len + BT - 1) / BT;
-        const Rows<TY> xs(x, first, end, a.xt, a.channels), dts(dt, first, end, a.dtt, a.channels),
-            zs(z, first, end, a.zt, a.channels), gs(gy, first, end, a.gt, a.channels),
-            bs(b + group * a.bg, first, end, a.bt, a.state), cs(c + group * a.cg, first, end, a.ct, a.state),
-            gxs((const E*)g.x, first, end, a.channels, a.channels), gdts((const E*)g.dt, first, end, a.channels, a.channels),
-            gzs((const E*)g.z, first, end, a.channels, a.channels);
-        const int row = w * T + j;
-        const Places<TY, Q> xa(true, a.single ? 0 : a.xt, row, 0), dta(true, a.single ? 0 : a.dtt, row, 0),
-            za(true, a.single ? 0 : a.zt, row, 0), ga(true, a.single ? 0 : a.gt, row, 0), oa(true, a.channels, row, 0);
-        Shared<TY, S, T> bl(a.single ? 0 : a.bt, w * T, a.state), cl(a.single ? 0 : a.ct, w * T, a.state);
-        uint32_t xr[Q], dtr[Q], zr[Q], gr[Q];
-        float ar[S], hr[S], skip_r, bias_r;
-        auto fetch = [&](int block, int k) {
-            const int at = block * BT;
-            const Place p = place(k);
-            const uint32_t off = p.ch * (uint32_t)sizeof(E);
-            const Buffer xb = xs.from(at), db = dts.from(at), zb = zs.from(at), gb = gs.from(at);
-#pragma unroll
-            for (int i = 0; i < Q; ++i) {
-                xr[i] = load_raw<TY>(xb, xa.at[i] + off);
-                dtr[i] = load_raw<TY>(db, dta.at[i] + off);
-                zr[i] = load_raw<TY>(zb, za.at[i] + off);
-                gr[i] = load_raw<TY>(gb, ga.at[i] + off);
-            }
-            if (k == 0) {
-                bl.load(bs.from(at));
-                cl.load(cs.from(at));
-            }
-            load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, ar);
-            load_states<S>(g.kept + (((long long)first / BT + seq + block) * a.channels + p.ch) * (4 * S), n0, 4 * S, 0.0f, hr);
-            skip_r = d ? d[p.ch] : 0.0f;
-            bias_r = dt_bias ? dt_bias[p.ch] : 0.0f;
+        // states in the exchange's order: where they lie in a state array
+        const long long state0 = ((long long)seq * a.channels + group * a.share) * a.state;
+        auto state_at = [&](int f, int k, long long* at) {
+            const int ch = (k0 + k) * kGroupCh + Lanes<S>::quad_of(f), n = Lanes<S>::state_of(f);
+            *at = state0 + (long long)ch * a.state + n;
+            return ch < a.share && n < a.state;
         };
-        if (blocks) fetch(blocks - 1, 0);
-        for (int block = blocks - 1; block >= 0; --block, flip ^= 1) {
-            wave_fence();
-            bl.put(bc[w][0]);
-            cl.put(bc[w][1]);
-            wave_fence();
-            // over the K times 16 channels; the lane's of T * S values are those at 16 i + mine
-            float sum_b[N16], sum_c[N16];
+        // (a thread reads and writes its own of `carry` alone)
+        for (int k = 0; k < nk; ++k)
 #pragma unroll
-            for (int i = 0; i < N16; ++i) sum_b[i] = sum_c[i] = 0.0f;
-            for (int k = 0; k < nk; ++k, turn ^= 1) {
-                const Place p = place(k);
-                float xv[Q], slope[Q], step[Q], u[Q], gv[Q], zv[Q], sig[Q], gp[Q], a2[S], h[S], e[S], all = 0.0f;
-                const float skip = skip_r, bias = bias_r;
-#pragma unroll
-                for (int s = 0; s < S; ++s) a2[s] = ar[s] * kLog2e, h[s] = hr[s];
+            for (int i = 0; i < F; ++i) {
+                const int f = threadIdx.x + i * 64 * NW - 64 * S;
+                long long at;
+                if (f >= 0 && f < 64 * S) carry[k].x[f] = state_at(f, k, &at) && gfinal ? gfinal[at] : 0.0f;
+            }
+        if (blocks) {
+            const long long from = first + (blocks - 1) * (long long)BT;
+            Rows xs(x, from, a.xt, a.single, a.channels), dts(dt, from, a.dtt, a.single, a.channels),
+                zs(z, from, a.zt, a.single, a.channels), gs(gy, from, a.gt, a.single, a.channels),
+                bs(b + group * a.bg, from, a.bt, a.single, a.state), cs(c + group * a.cg, from, a.ct, a.single, a.state),
+                gxs((const E*)g.x, from, a.channels, false, a.channels), gdts((const E*)g.dt, from, a.channels, false, a.channels),
+                gzs((const E*)g.z, from, a.channels, false, a.channels);
+            const Places<TY, Q> xa(xs, row, group * a.share), dta(dts, row, group * a.share), za(zs, row, group * a.share),
+                ga(gs, row, group * a.share), oa(gxs, row, group * a.share);
+            Shared<TY, S, T> bl(bs, w * T, a.state), cl(cs, w * T, a.state);
+            const float* kept = g.kept + ((long long)first / BT + seq + blocks - 1) * pitch +
+                                ((long long)group * sixteens + k0) * (64 * S);
+            uint32_t xr[Q], dtr[Q], zr[Q], gr[Q];
+            float hr[F];
+            auto fetch = [&](int n, int k) {
+                const uint32_t off = min((k0 + k) * kGroupCh + quad, last_ch) * (uint32_t)sizeof(E);
+                const Buffer xb = xs.next(n), db = dts.next(n), zb = zs.next(n), gb = gs.next(n);
 #pragma unroll
                 for (int i = 0; i < Q; ++i) {
-                    const bool in = block * BT + row + 4 * i < len;
-                    xv[i] = value_of<TY>(xr[i]);
-                    const float pre = value_of<TY>(dtr[i]) + bias, ex = exp_of(-fabsf(pre));
-                    step[i] = in ? (a.softplus ? softplus_of(pre, ex) : pre) : 0.0f;
-                    slope[i] = a.softplus ? sigmoid_of(pre, ex) : 1.0f;
-                    u[i] = step[i] * xv[i];
-                    all += step[i];
-                    gv[i] = in && p.in ? value_of<TY>(gr[i]) : 0.0f;
-                    zv[i] = value_of<TY>(zr[i]);
-                    sig[i] = z ? sigmoid_of(zv[i]) : 1.0f;
-                    gp[i] = z ? gv[i] * (zv[i] * sig[i]) : gv[i];
+                    xr[i] = load_raw<TY>(xb, xa.at[i] + off);
+                    dtr[i] = load_raw<TY>(db, dta.at[i] + off);
+                    zr[i] = load_raw<TY>(zb, za.at[i] + off);
+                    gr[i] = load_raw<TY>(gb, ga.at[i] + off);
                 }
-                if (k + 1 < nk)
-                    fetch(block, k + 1);  // while this step is worked on
-                else if (block)
-                    fetch(block - 1, 0);
-                all += quad_perm<0xB1>(all);
-                all += quad_perm<0x4E>(all);
-                float at[T][S], add[T][S], hl[S], el[S], pw[S];
+                if (k == 0) {
+                    bl.load(bs.next(n));
+                    cl.load(cs.next(n));
+                }
 #pragma unroll
-                for (int s = 0; s < S; ++s) hl[s] = el[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);
-                auto one = [&](auto kk, int i) {
-                    constexpr int J = decltype(kk)::value;
-                    const int t = 4 * i + J;
-                    const float dl = from<J>(step[i]), ul = from<J>(u[i]);
-                    float bv[S];
-                    get_states<S>(&bc[w][0][t * 4 * S + n0], bv);
+                for (int i = 0; i < F; ++i)
+                    if (w * 64 + i * 64 * NW < 64 * S) hr[i] = kept[k * (64 * S) + threadIdx.x + i * 64 * NW];
+            };
+            int n = len - (blocks - 1) * BT;  // tokens of the block
+            fetch(n, 0);
+            for (int block = blocks - 1; block >= 0; --block, n = BT) {
+                wave_fence();
+                bl.put(bc[w][0]);
+                cl.put(bc[w][1]);
+                wave_fence();
+                // over the K times 16 channels; the lane's of T * S values are those at 16 i + mine
+                float sum_b[N16], sum_c[N16];
 #pragma unroll
-                    for (int s = 0; s < S; ++s) {
-                        at[t][s] = exp2_of(dl * a2[s]);
-                        add[t][s] = ul * bv[s];
-                        hl[s] = fmaf(at[t][s], hl[s], add[t][s]);
+                for (int i = 0; i < N16; ++i) sum_b[i] = sum_c[i] = 0.0f;
+                for (int k = 0; k < nk; ++k) {
+                    const int ch = (k0 + k) * kGroupCh + quad;
+                    const bool here = ch < a.share;
+                    const float2 sb = skip_bias[k][quad];
+                    float xv[Q], slope[Q], step[Q], u[Q], gv[Q], zv[Q], sig[Q], gp[Q], a2[S], all = 0.0f;
+                    rate[k].get(lane, a2);
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        const bool in = row + 4 * i < n;
+                        xv[i] = value_of<TY>(xr[i]);
+                        const float pre = value_of<TY>(dtr[i]) + sb.y, ex = exp_of(-fabsf(pre));
+                        step[i] = in ? (a.softplus ? softplus_of(pre, ex) : pre) : 0.0f;
+                        slope[i] = a.softplus ? sigmoid_of(pre, ex) : 1.0f;
+                        u[i] = step[i] * xv[i];
+                        all += step[i];
+                        gv[i] = in && here ? value_of<TY>(gr[i]) : 0.0f;
+                        zv[i] = value_of<TY>(zr[i]);
+                        sig[i] = z ? sigmoid_of(zv[i]) : 1.0f;
+                        gp[i] = z ? gv[i] * (zv[i] * sig[i]) : gv[i];
                     }
-                };
-                auto one_back = [&](auto kk, int i) {
-                    constexpr int J = decltype(kk)::value;
-                    const int t = 4 * i + J;
-                    const float gl = from<J>(gp[i]);
-                    float cv[S];
-                    get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
+                    float h0[F];
 #pragma unroll
-                    for (int s = 0; s < S; ++s) el[s] = at[t][s] * fmaf(cv[s], gl, el[s]);
-                };
+                    for (int i = 0; i < F; ++i) h0[i] = hr[i];
+                    if (k + 1 < nk) {  // while this step is worked on
+                        fetch(n, k + 1);
+                    } else if (block) {
+                        xs.move(-BT), dts.move(-BT), zs.move(-BT), gs.move(-BT), bs.move(-BT), cs.move(-BT);
+                        kept -= pitch;
+                        fetch(BT, 0);
+                    }
+                    all += quad_perm<0xB1>(all);
+                    all += quad_perm<0x4E>(all);
+                    float at[T][S], add[T][S], h[S], e[S], pw[S];
 #pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    one(std::integral_constant<int, 0>{}, i);
-                    one(std::integral_constant<int, 1>{}, i);
-                    one(std::integral_constant<int, 2>{}, i);
-                    one(std::integral_constant<int, 3>{}, i);
+                    for (int s = 0; s < S; ++s) h[s] = e[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);
+                    auto one = [&](auto kk, int i) {
+                        constexpr int J = decltype(kk)::value;
+                        const int t = 4 * i + J;
+                        const float dl = from_lane<J>(step[i]), ul = from_lane<J>(u[i]);
+                        float bv[S];
+                        get_states<S>(&bc[w][0][t * 4 * S + n0], bv);
+#pragma unroll
+                        for (int s = 0; s < S; ++s) {
+                            at[t][s] = exp2_of(dl * a2[s]);
+                            add[t][s] = ul * bv[s];
+                            h[s] = fmaf(at[t][s], h[s], add[t][s]);
+                        }
+                    };
+                    auto one_back = [&](auto kk, int i) {
+                        constexpr int J = decltype(kk)::value;
+                        const int t = 4 * i + J;
+                        const float gl = from_lane<J>(gp[i]);
+                        float cv[S];
+                        get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
+#pragma unroll
+                        for (int s = 0; s < S; ++s) e[s] = at[t][s] * fmaf(cv[s], gl, e[s]);
+                    };
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        one(std::integral_constant<int, 0>{}, i);
+                        one(std::integral_constant<int, 1>{}, i);
+                        one(std::integral_constant<int, 2>{}, i);
+                        one(std::integral_constant<int, 3>{}, i);
+                    }
+#pragma unroll
+                    for (int i = Q - 1; i >= 0; --i) {
+                        one_back(std::integral_constant<int, 3>{}, i);
+                        one_back(std::integral_constant<int, 2>{}, i);
+                        one_back(std::integral_constant<int, 1>{}, i);
+                        one_back(std::integral_constant<int, 0>{}, i);
+                    }
+                    product[w].put(lane, pw);
+                    made[w].put(lane, h);
+                    given[w].put(lane, e);
+                    lds_barrier();
+#pragma unroll
+                    for (int i = 0; i < F; ++i) {
+                        const int f = threadIdx.x + i * 64 * NW, wave0 = w * 64 + i * 64 * NW;
+                        if (wave0 < 64 * S) {
+                            along<S, NW, false>(product, made, f, h0[i]);
+                        } else if (wave0 < 2 * 64 * S) {
+                            const int r = f - 64 * S;
+                            const float before = along<S, NW, true>(product, given, r, carry[k].x[r]);
+                            carry[k].x[r] = before;
+                            long long to;
+                            if (block == 0 && g.initial && state_at(r, k, &to)) g.initial[to] = before;
+                        }
+                    }
+                    lds_barrier();
+                    made[w].get(lane, h);
+                    given[w].get(lane, e);
+                    float ypre[Q], gu[Q], gd[Q], das[S], vb[T * S], vc[T * S];
+                    auto sum16 = [&](const float* from, float& to) {
+                        float v[16];
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) v[q] = from[q];
+                        to += over_quads(v);
+                    };
+#pragma unroll
+                    for (int s = 0; s < S; ++s) das[s] = 0.0f;
+                    // forward: `add` becomes a_t h_{t-1}
+                    auto ahead = [&](auto kk, int i, float (&v)[4]) {
+                        constexpr int J = decltype(kk)::value;
+                        const int t = 4 * i + J;
+                        const float gl = from_lane<J>(gp[i]);
+                        float cv[S];
+                        get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
+                        v[J] = 0.0f;
+#pragma unroll
+                        for (int s = 0; s < S; ++s) {
+                            const float ah = at[t][s] * h[s];
+                            h[s] = ah + add[t][s];
+                            add[t][s] = ah;
+                            v[J] = fmaf(cv[s], h[s], v[J]);
+                            vc[t * S + s] = gl * h[s];
+                        }
+                    };
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        float v[4];
+                        ahead(std::integral_constant<int, 0>{}, i, v);
+                        ahead(std::integral_constant<int, 1>{}, i, v);
+                        ahead(std::integral_constant<int, 2>{}, i, v);
+                        ahead(std::integral_constant<int, 3>{}, i, v);
+                        ypre[i] = over_four(v);
+#pragma unroll
+                        for (int q = 0; q < S / 4; ++q) sum16(vc + (i * (S / 4) + q) * 16, sum_c[i * (S / 4) + q]);
+                    }
+                    auto back = [&](auto kk, int i, float (&v)[4], float (&r)[4]) {
+                        constexpr int J = decltype(kk)::value;
+                        const int t = 4 * i + J;
+                        const float dl = from_lane<J>(step[i]), ul = from_lane<J>(u[i]), gl = from_lane<J>(gp[i]);
+                        float bv[S], cv[S];
+                        get_states<S>(&bc[w][0][t * 4 * S + n0], bv);
+                        get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
+                        v[J] = r[J] = 0.0f;
+#pragma unroll
+                        for (int s = 0; s < S; ++s) {
+                            const float G = fmaf(cv[s], gl, e[s]);
+                            vb[t * S + s] = G * ul;
+                            v[J] = fmaf(G, bv[s], v[J]);
+                            const float q = G * add[t][s];
+                            r[J] = fmaf(q, a2[s], r[J]);
+                            das[s] = fmaf(q, dl, das[s]);
+                            e[s] = at[t][s] * G;
+                        }
+                    };
+#pragma unroll
+                    for (int i = Q - 1; i >= 0; --i) {
+                        float v[4], r[4];
+                        back(std::integral_constant<int, 3>{}, i, v, r);
+                        back(std::integral_constant<int, 2>{}, i, v, r);
+                        back(std::integral_constant<int, 1>{}, i, v, r);
+                        back(std::integral_constant<int, 0>{}, i, v, r);
+                        gu[i] = over_four(v);
+                        gd[i] = over_four(r);
+#pragma unroll
+                        for (int q = 0; q < S / 4; ++q) sum16(vb + (i * (S / 4) + q) * 16, sum_b[i * (S / 4) + q]);
+                    }
+                    if constexpr (S == 2) {
+                        sum16(vb, sum_b[0]);
+                        sum16(vc, sum_c[0]);
+                    } else if constexpr (S == 1) {  // eight of each are sixteen
+                        float v[16];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[q] = vb[q], v[q + 8] = vc[q];
+                        sum16(v, sum_b[0]);
+                    }
+                    const Buffer gxb = gxs.next(n), gdb = gdts.next(n), gzb = gzs.next(n);
+                    float dd = 0.0f, db = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < Q; ++i) {
+                        const uint32_t to = here ? oa.at[i] + ch * (uint32_t)sizeof(E) : kNowhere;
+                        const float gdt = fmaf(gu[i], xv[i], gd[i] * kLn2) * slope[i];
+                        store_to<TY>(gxb, to, fmaf(gu[i], step[i], sb.x * gp[i]));
+                        store_to<TY>(gdb, to, gdt);
+                        if (z)
+                            store_to<TY>(gzb, to, gv[i] * fmaf(sb.x, xv[i], ypre[i]) * (sig[i] * (1.0f + zv[i] * (1.0f - sig[i]))));
+                        dd = fmaf(gp[i], xv[i], dd);
+                        db += row + 4 * i < n ? gdt : 0.0f;
+                    }
+                    dd += quad_perm<0xB1>(dd);
+                    dd += quad_perm<0x4E>(dd);
+                    db += quad_perm<0xB1>(db);
+                    db += quad_perm<0x4E>(db);
+#pragma unroll
+                    for (int s = 0; s < S; ++s) total[k][w][s][lane] += das[s];
+                    total[k][w][S][lane] += j == 0 ? dd : db;
                 }
-#pragma unroll
-                for (int i = Q - 1; i >= 0; --i) {
-                    one_back(std::integral_constant<int, 3>{}, i);
-                    one_back(std::integral_constant<int, 2>{}, i);
-                    one_back(std::integral_constant<int, 1>{}, i);
-                    one_back(std::integral_constant<int, 0>{}, i);
-                }
-                product[turn][w].put(lane, pw);
-                made[turn][w].put(lane, hl);
-                given[turn][w].put(lane, el);
-                lds_barrier();
-                if (block != blocks - 1) {
-                    carry[flip][k].get(lane, e);
+                gxs.move(-BT), gdts.move(-BT), gzs.move(-BT);
+                const int mine = sixteenth_of(lane);
+                auto leave = [&](float v, int at, float* to) {  // of value `at` of the wave's T * S
+                    const int t = w * T + at / S, state = n0 + at % S;
+                    if (t < n && state < a.state) to[((long long)first + block * BT + t) * row_bc + state] = v;
+                };
+                if constexpr (S == 1) {
+                    leave(sum_b[0], mine % 8, mine < 8 ? to_b : to_c);
                 } else {
 #pragma unroll
-                    for (int s = 0; s < S; ++s) e[s] = 0.0f;
-                    if (gfinal) load_states<S>(gfinal + ((long long)seq * a.channels + p.ch) * a.state, n0, a.state, 0.0f, e);
-                }
-                for (int i = 0; i < w; ++i) {
-                    product[turn][i].get(lane, pw);
-                    made[turn][i].get(lane, hl);
-#pragma unroll
-                    for (int s = 0; s < S; ++s) h[s] = fmaf(pw[s], h[s], hl[s]);
-                }
-                for (int i = NW - 1; i > w; --i) {
-                    product[turn][i].get(lane, pw);
-                    given[turn][i].get(lane, el);
-#pragma unroll
-                    for (int s = 0; s < S; ++s) e[s] = fmaf(pw[s], e[s], el[s]);
-                }
-                float ypre[Q], gu[Q], gd[Q], das[S], vb[T * S], vc[T * S];
-                auto sum16 = [&](const float* from, float& to) {
-                    float v[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) v[q] = from[q];
-                    to += over_quads(v);
-                };
-#pragma unroll
-                for (int s = 0; s < S; ++s) das[s] = 0.0f;
-                // forward: `add` becomes a_t h_{t-1}
-                auto ahead = [&](auto kk, int i, float (&v)[4]) {
-                    constexpr int J = decltype(kk)::value;
-                    const int t = 4 * i + J;
-                    const float gl = from<J>(gp[i]);
-                    float cv[S];
-                    get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
-                    v[J] = 0.0f;
-#pragma unroll
-                    for (int s = 0; s < S; ++s) {
-                        const float ah = at[t][s] * h[s];
-                        h[s] = ah + add[t][s];
-                        add[t][s] = ah;
-                        v[J] = fmaf(cv[s], h[s], v[J]);
-                        vc[t * S + s] = gl * h[s];
+                    for (int i = 0; i < N16; ++i) {
+                        leave(sum_b[i], 16 * i + mine, to_b);
+                        leave(sum_c[i], 16 * i + mine, to_c);
                     }
-                };
-#pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    float v[4];
-                    ahead(std::integral_constant<int, 0>{}, i, v);
-                    ahead(std::integral_constant<int, 1>{}, i, v);
-                    ahead(std::integral_constant<int, 2>{}, i, v);
-                    ahead(std::integral_constant<int, 3>{}, i, v);
-                    ypre[i] = over_four(v);
-#pragma unroll
-                    for (int q = 0; q < S / 4; ++q) sum16(vc + (i * (S / 4) + q) * 16, sum_c[i * (S / 4) + q]);
-                }
-                // a lane whose channel is none adds nothing to b's and c's gradients: its gp and e are zero
-                if (!p.in)
-#pragma unroll
-                    for (int s = 0; s < S; ++s) e[s] = 0.0f;
-                auto back = [&](auto kk, int i, float (&v)[4], float (&r)[4]) {
-                    constexpr int J = decltype(kk)::value;
-                    const int t = 4 * i + J;
-                    const float dl = from<J>(step[i]), ul = from<J>(u[i]), gl = from<J>(gp[i]);
-                    float bv[S], cv[S];
-                    get_states<S>(&bc[w][0][t * 4 * S + n0], bv);
-                    get_states<S>(&bc[w][1][t * 4 * S + n0], cv);
-                    v[J] = r[J] = 0.0f;
-#pragma unroll
-                    for (int s = 0; s < S; ++s) {
-                        const float G = fmaf(cv[s], gl, e[s]);
-                        vb[t * S + s] = G * ul;
-                        v[J] = fmaf(G, bv[s], v[J]);
-                        const float q = G * add[t][s];
-                        r[J] = fmaf(q, a2[s], r[J]);
-                        das[s] = fmaf(q, dl, das[s]);
-                        e[s] = at[t][s] * G;
-                    }
-                };
-#pragma unroll
-                for (int i = Q - 1; i >= 0; --i) {
-                    float v[4], r[4];
-                    back(std::integral_constant<int, 3>{}, i, v, r);
-                    back(std::integral_constant<int, 2>{}, i, v, r);
-                    back(std::integral_constant<int, 1>{}, i, v, r);
-                    back(std::integral_constant<int, 0>{}, i, v, r);
-                    gu[i] = over_four(v);
-                    gd[i] = over_four(r);
-#pragma unroll
-                    for (int q = 0; q < S / 4; ++q) sum16(vb + (i * (S / 4) + q) * 16, sum_b[i * (S / 4) + q]);
-                }
-                if constexpr (S == 2) {
-                    sum16(vb, sum_b[0]);
-                    sum16(vc, sum_c[0]);
-                } else if constexpr (S == 1) {  // eight of each are sixteen
-                    float v[16];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = vb[q], v[q + 8] = vc[q];
-                    sum16(v, sum_b[0]);
-                }
-                if (w == 0) {
-                    carry[flip ^ 1][k].put(lane, e);
-                    if (block == 0 && g.initial && p.in)
-                        store_states<S>(g.initial + ((long long)seq * a.channels + p.ch) * a.state, n0, a.state, e);
-                }
-                const Buffer gxb = gxs.from(block * BT), gdb = gdts.from(block * BT), gzb = gzs.from(block * BT);
-                const uint32_t off = p.ch * (uint32_t)sizeof(E);
-                float dd = 0.0f, db = 0.0f;
-#pragma unroll
-                for (int i = 0; i < Q; ++i) {
-                    const uint32_t to = p.in ? oa.at[i] + off : kNowhere;
-                    const float gdt = fmaf(gu[i], xv[i], gd[i] * kLn2) * slope[i];
-                    store_to<TY>(gxb, to, fmaf(gu[i], step[i], skip * gp[i]));
-                    store_to<TY>(gdb, to, gdt);
-                    if (z)
-                        store_to<TY>(gzb, to, gv[i] * fmaf(skip, xv[i], ypre[i]) * (sig[i] * (1.0f + zv[i] * (1.0f - sig[i]))));
-                    const bool in = block * BT + row + 4 * i < len;
-                    dd = fmaf(gp[i], xv[i], dd);
-                    db += in ? gdt : 0.0f;
-                }
-                dd += quad_perm<0xB1>(dd);
-                dd += quad_perm<0x4E>(dd);
-                db += quad_perm<0xB1>(db);
-                db += quad_perm<0x4E>(db);
-#pragma unroll
-                for (int s = 0; s < S; ++s) total[k][w][s][lane] += das[s];
-                total[k][w][S][lane] += j == 0 ? dd : db;
-            }
-            const int t0 = block * BT + w * T, mine = sixteenth_of(lane);
-            auto leave = [&](float v, int at, float* to) {  // of value `at` of the wave's T * S
-                const int t = at / S, n = n0 + at % S;
-                if (t0 + t < len && n < a.state) to[((long long)first + t0 + t) * row_bc + n] = v;
-            };
-            if constexpr (S == 1) {
-                leave(sum_b[0], mine % 8, mine < 8 ? to_b : to_c);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N16; ++i) {
-                    leave(sum_b[i], 16 * i + mine, to_b);
-                    leave(sum_c[i], 16 * i + mine, to_c);
                 }
             }
+        } else if (g.initial) {  // its final state is its initial one
+            for (int k = 0; k < nk; ++k)
+#pragma unroll
+                for (int i = 0; i < F; ++i) {
+                    const int f = threadIdx.x + i * 64 * NW - 64 * S;
+                    long long at;
+                    if (f >= 0 && f < 64 * S && state_at(f, k, &at)) g.initial[at] = carry[k].x[f];
+                }
         }
-        if (!blocks && w == 0 && g.initial)  // its final state is its initial one
-            for (int k = 0; k < nk; ++k) {
-                const Place p = place(k);
-                const long long at = ((long long)seq * a.channels + p.ch) * a.state;
-                float e[S];
-#pragma unroll
-                for (int s = 0; s < S; ++s) e[s] = 0.0f;
-                if (gfinal) load_states<S>(gfinal + at, n0, a.state, 0.0f, e);
-                if (p.in) store_states<S>(g.initial + at, n0, a.state, e);
-            }
         if (a.clear && seq == a.q.n_seq - 1)
             for (int k = 0; k < nk; ++k) {
-                const Place p = place(k);
+                const Place p = place_of(a, group, k0 + k);
                 if (!p.in) continue;
                 for (int t = end + 4 * w + j; t < a.q.n_tokens; t += 4 * NW) {
                     const long long to = (long long)t * a.channels + p.ch;
@@ -793,7 +848,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
     // the waves' sums together, a wave for each sixteen channels
     __syncthreads();
     for (int k = w; k < nk; k += NW) {
-        const Place p = place(k);
+        const Place p = place_of(a, group, k0 + k);
         if (!p.in) continue;
 #pragma unroll
         for (int s = 0; s <= S; ++s) {
@@ -859,7 +914,7 @@ __global__ __launch_bounds__(kSumThreads) void scan_sums_kernel(Scan a, Grads g,
 constexpr int kStepThreads = 256;
 template <class TY, int S>
 __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
-    Scan a, long long waves, int channel_groups, const typename TY::S* __restrict__ x,
+    Scan a, long long waves, int sixteens, const typename TY::S* __restrict__ x,
     const typename TY::S* __restrict__ dt, const float* __restrict__ decay, const typename TY::S* __restrict__ b,
     const typename TY::S* __restrict__ c, const float* __restrict__ d, const typename TY::S* __restrict__ z,
     const float* __restrict__ dt_bias, float* states, int pool, const int* __restrict__ slots,
@@ -867,9 +922,10 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
     const long long wave =
         (long long)blockIdx.x * (kStepThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= waves) return;
-    const Place p = place_of(a, (int)(wave % channel_groups));
+    const int sixteen = (int)(wave % sixteens), group = (int)(wave / sixteens % a.groups);
+    const Place p = place_of(a, group, sixteen);
     const int lane = threadIdx.x & 63, n0 = p.j * S, rows = a.q.n_tokens;
-    int row = (int)(wave / channel_groups), slot = row;
+    int row = (int)(wave / sixteens / a.groups), slot = row;
     if (slots) {
         slot = __builtin_amdgcn_readfirstlane(slots[row]);
         if (slot < 0 || slot >= pool) {
@@ -884,8 +940,8 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
     load_states<S>(state, n0, a.state, 0.0f, h);
     load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
     const float skip = d ? d[p.ch] : 0.0f, bias = dt_bias ? dt_bias[p.ch] : 0.0f;
-    b += p.group * a.bg;
-    c += p.group * a.cg;
+    b += group * a.bg;
+    c += group * a.cg;
     while (row < rows) {
         const float xv = TY::load(x[row * a.xt + p.ch]), pre = TY::load(dt[row * a.dtt + p.ch]) + bias;
         const float step = a.softplus ? softplus_of(pre) : pre, u = step * xv;
@@ -956,7 +1012,7 @@ int check_shape(const selective_scan_shape_t* p, bool step, Scan* a) {
     const long long groups = (long long)a->groups * ((a->share + kGroupCh - 1) / kGroupCh);
     return groups * std::max(1, a->q.n_seq) > kMaxBlocks ? CFC_ERR_UNSUPPORTED : CFC_OK;
 }
-inline int channel_groups_of(const Scan& a) { return a.groups * ((a.share + kGroupCh - 1) / kGroupCh); }
+inline int sixteens_of(const Scan& a) { return (a.share + kGroupCh - 1) / kGroupCh; }
 
 struct Sizes {  // bytes of the arguments
     long long x, dt, z, gy, b, c, rows, shared, a, d, states;
@@ -991,14 +1047,14 @@ inline int lane_states(int state) { return state <= 4 ? 1 : state <= 8 ? 2 : sta
 
 // How many times 16 channels a workgroup of the backward has: more of them leave fewer partial
 // sums of b's and c's gradients and share the sums over lanes, as long as all CUs have one.
-inline int sixteens_of(const Scan& a) {
+inline int sixteens_at_once(const Scan& a) {
     if (a.state > 16) return 1;
-    const long long all = (long long)channel_groups_of(a) * a.q.n_seq;
+    const long long all = (long long)a.groups * sixteens_of(a) * a.q.n_seq;
     return all >= 4 * 256 ? 4 : all >= 2 * 256 ? 2 : 1;
 }
 inline int wg_groups_of(const Scan& a) {
-    const int k = sixteens_of(a);
-    return a.groups * ((channel_groups_of(a) / a.groups + k - 1) / k);
+    const int k = sixteens_at_once(a);
+    return a.groups * ((sixteens_of(a) + k - 1) / k);
 }
 // The sequences go to as many workgroups of the same channels as fill the chip, since each
 // leaves a row of partial sums.
@@ -1013,7 +1069,7 @@ long long lay_out(const Scan& a, void* base, Grads* g) {
     const long long in_group = wg_groups_of(a) / a.groups, parts = parts_of(a);
     long long kept, bc, pa, all = 0;
     g->rows = (long long)a.q.n_tokens * a.groups * a.state;
-    if (!mul_ok(slots * a.channels, 4 * s * 4, &kept) || !mul_ok(g->rows, in_group * 4, &bc) ||
+    if (!mul_ok(slots * a.groups, (long long)sixteens_of(a) * (64 * s * 4), &kept) || !mul_ok(g->rows, in_group * 4, &bc) ||
         !mul_ok(parts, (long long)a.channels * a.state * 4, &pa) ||
         2 * g->rows + (long long)a.channels * (a.state + 2) > kMaxBlocks * 256)
         return -1;
@@ -1055,9 +1111,9 @@ extern "C" int selective_scan_forward(const selective_scan_shape_t* shape, const
         using TY = decltype(ty);
         using E = typename TY::S;
         constexpr int S = decltype(states)::value;
-        const int groups = channel_groups_of(a);
-        hipLaunchKernelGGL((scan_kernel<TY, S>), dim3(dealt(groups * (long long)a.q.n_seq)), dim3(64 * waves_of(S)),
-                           0, stream, a, groups, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d, (const E*)z,
+        const int sixteens = sixteens_of(a);
+        const long long count = (long long)a.groups * sixteens * a.q.n_seq;
+        hipLaunchKernelGGL((scan_kernel<TY, S>), dim3(dealt(count)), dim3(64 * waves_of(S)), 0, stream, a, sixteens, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d, (const E*)z,
                            dt_bias, initial_state, (E*)y, final_state);
         return launch_status();
     });
@@ -1105,21 +1161,21 @@ extern "C" int selective_scan_backward(const selective_scan_shape_t* shape, cons
         using TY = decltype(ty);
         using E = typename TY::S;
         constexpr int S = decltype(states)::value;
-        const int groups = channel_groups_of(a), wg_groups = wg_groups_of(a), parts = parts_of(a);
+        const int sixteens = sixteens_of(a), wg_groups = wg_groups_of(a), parts = parts_of(a);
         if (a.q.n_seq) {
-            hipLaunchKernelGGL((scan_states_kernel<TY, S>), dim3(dealt(groups * (long long)a.q.n_seq)),
-                               dim3(64 * waves_of(S)), 0, stream, a, groups, (const E*)x, (const E*)dt, a_, (const E*)b,
+            hipLaunchKernelGGL((scan_states_kernel<TY, S>), dim3(dealt((long long)a.groups * sixteens * a.q.n_seq)),
+                               dim3(64 * waves_of(S)), 0, stream, a, sixteens, (const E*)x, (const E*)dt, a_, (const E*)b,
                                dt_bias, initial_state, g.kept);
             auto go = [&](auto kernel) {
                 hipLaunchKernelGGL(kernel, dim3(dealt((long long)wg_groups * parts)), dim3(64 * waves_of(S)), 0, stream, a,
-                                   wg_groups, parts, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
+                                   sixteens, wg_groups, parts, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
                                    (const E*)z, dt_bias, (const E*)grad_y, grad_final_state, g);
             };
-            const int sixteens = sixteens_of(a);
+            const int at_once = sixteens_at_once(a);
             if constexpr (S <= 4) {
-                if (sixteens == 4)
+                if (at_once == 4)
                     go(scan_backward_kernel<TY, S, 4>);
-                else if (sixteens == 2)
+                else if (at_once == 2)
                     go(scan_backward_kernel<TY, S, 2>);
                 else
                     go(scan_backward_kernel<TY, S, 1>);
@@ -1156,11 +1212,10 @@ extern "C" int selective_scan_step(const selective_scan_shape_t* shape, const vo
         using TY = decltype(ty);
         using E = typename TY::S;
         constexpr int S = decltype(s)::value;
-        const int groups = channel_groups_of(a);
-        const long long waves = (long long)groups * a.q.n_tokens;
+        const long long waves = (long long)a.groups * sixteens_of(a) * a.q.n_tokens;
         constexpr int per = kStepThreads / 64;
         hipLaunchKernelGGL((scan_step_kernel<TY, S>), dim3((unsigned)((waves + per - 1) / per)), dim3(kStepThreads), 0,
-                           stream, a, waves, groups, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
+                           stream, a, waves, sixteens_of(a), (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
                            (const E*)z, dt_bias, states, pool, slots, (E*)y);
         return launch_status();
     });

@@ -53,7 +53,8 @@ extern "C" {
  * arrays' bounds.
  *   x, dt, z, grad_y [n_tokens, channels]: row r at r * stride elements (>= 0), the last
  * axis dense.  b, c [n_tokens, groups, state]: row r, group g at r * stride_t + g *
- * stride_g, the last axis dense.  a [channels, state], d, dt_bias [channels] float32,
+ * stride_g, the last axis dense; 64 rows of each are less than 2^31 bytes from the first to
+ * the last, except for sequences of one row and for a step.  a [channels, state], d, dt_bias [channels] float32,
  * dense, a finite.  States [n_seq, channels, state] float32, dense. */
 typedef struct selective_scan_shape {
     int type;           /* CFC_TYPE_* of x, dt, z, b, c, y and their gradients */

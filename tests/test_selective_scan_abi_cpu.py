@@ -61,8 +61,7 @@ def test_exports_every_declared_symbol(lib):
 SHAPES = [(dict(type=3), C.CFC_ERR_UNSUPPORTED), (dict(channels=0), C.CFC_ERR_DIM), (dict(groups=0), C.CFC_ERR_DIM),
           (dict(groups=3), C.CFC_ERR_DIM), (dict(state=0), C.CFC_ERR_DIM), (dict(state=65), C.CFC_ERR_UNSUPPORTED),
           (dict(x_stride=-1), C.CFC_ERR_DIM), (dict(c_stride_g=-1), C.CFC_ERR_DIM), (dict(n_tokens=-1), C.CFC_ERR_DIM),
-          (dict(n_tokens=1 << 31), C.CFC_ERR_UNSUPPORTED), (dict(x_stride=1 << 62), C.CFC_ERR_DIM),
-          (dict(b_stride_t=1 << 62), C.CFC_ERR_DIM)]
+          (dict(n_tokens=1 << 31), C.CFC_ERR_UNSUPPORTED)]
 SEQUENCES = [(dict(n_seq=-1), C.CFC_ERR_DIM), (dict(seq_len=49), C.CFC_ERR_DIM), (dict(seq_len=-1), C.CFC_ERR_DIM),
              (dict(n_seq=(1 << 31) - 1, offsets=AT["offsets"]), C.CFC_ERR_UNSUPPORTED),
              (dict(n_seq=1 << 30, offsets=AT["offsets"]), C.CFC_ERR_UNSUPPORTED)]
@@ -71,6 +70,18 @@ SEQUENCES = [(dict(n_seq=-1), C.CFC_ERR_DIM), (dict(seq_len=49), C.CFC_ERR_DIM),
 @pytest.mark.parametrize("bad,code", SHAPES)
 def test_shapes_that_are_refused(lib, bad, code):
     assert forward(lib, **bad) == backward(lib, **bad) == step(lib, **bad) == code
+
+
+def test_strides_that_are_refused(lib):
+    """Of sequences, 64 rows are less than 2^31 bytes, and rows alone anything that has an address."""
+    for n in ("x_stride", "dt_stride", "z_stride", "b_stride_t", "c_stride_t"):
+        assert step(lib, **{n: 1 << 62}) == C.CFC_ERR_DIM, n
+        for stride in (1 << 62, 1 << 24):
+            assert forward(lib, **{n: stride}) == backward(lib, **{n: stride}) == C.CFC_ERR_UNSUPPORTED, n
+        alone = dict(n_seq=100, seq_len=1)
+        assert forward(lib, **alone, **{n: 1 << 62}) == backward(lib, **alone, **{n: 1 << 62}) == C.CFC_ERR_DIM, n
+    assert backward(lib, grad_y_stride=1 << 24) == C.CFC_ERR_UNSUPPORTED
+    assert forward(lib, channels=1 << 24, groups=1) == step(lib, channels=1 << 24, groups=1) == C.CFC_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("bad,code", SEQUENCES)
