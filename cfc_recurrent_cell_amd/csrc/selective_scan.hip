@@ -33,6 +33,8 @@ constexpr int kGroupCh = 16;  // channels of a workgroup
 // token are 2 S registers.
 constexpr int tokens_of(int s) { return s <= 4 ? 8 : 4; }
 constexpr int waves_of(int s) { return s <= 8 ? 8 : 4; }
+constexpr int forward_tokens(int s) { return s <= 2 ? 8 : 4; }
+constexpr long long kFewWorkgroups = 256;
 constexpr int block_of(int s) { return tokens_of(s) * waves_of(s); }
 
 struct Scan {
@@ -67,14 +69,14 @@ struct Place {
     int ch, quad, j;
     bool in;
 };
-__device__ __forceinline__ Place place_of(const Scan& a, int group, int sixteen) {
+__device__ __forceinline__ Place place_of(int share, int group, int sixteen) {
     const int lane = threadIdx.x & 63;
     Place p;
     p.quad = lane >> 2;
     p.j = lane & 3;
     const int at = sixteen * kGroupCh + p.quad;
-    p.in = at < a.share;
-    p.ch = group * a.share + min(at, a.share - 1);
+    p.in = at < share;
+    p.ch = group * share + min(at, share - 1);
     return p;
 }
 
@@ -137,7 +139,8 @@ struct Rows {
     __device__ __forceinline__ Rows(const E* p, long long row, long long stride, bool single, int width)
         : at(p ? reinterpret_cast<const char*>(p + row * stride) : nullptr),
           bytes(p && !single ? (int)stride * (int)sizeof(E) : 0), rest(p ? width * (int)sizeof(E) - bytes : 0) {}
-    // The next n of them.
+    // The next n of them, of which there are some (or there may be none).
+    __device__ __forceinline__ Buffer some(int n) const { return buffer_of(at, n * bytes + rest); }
     __device__ __forceinline__ Buffer next(int n) const { return buffer_of(at, n > 0 ? n * bytes + rest : 0); }
     __device__ __forceinline__ void move(int n) { at += n * bytes; }
 };
@@ -237,13 +240,13 @@ __device__ __forceinline__ float along(const Lanes<S> (&product)[NW], Lanes<S> (
 }
 
 // -------------------------------------------------------------------- forward
-template <class TY, int S>
-__global__ __launch_bounds__(64 * waves_of(S), S <= 8 ? 4 : 2) void scan_kernel(
+template <class TY, int S, int NW>
+__global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16 ? 4 : 6) void scan_kernel(
     Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
     const float* __restrict__ decay, const typename TY::S* __restrict__ b, const typename TY::S* __restrict__ c,
     const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias,
     const float* initial, typename TY::S* __restrict__ y, float* final) {
-    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW, F = (S + NW - 1) / NW;
+    constexpr int T = forward_tokens(S), Q = T / 4, BT = T * NW, F = (S + NW - 1) / NW;
     __shared__ Lanes<S> product[NW], made[NW];  // P and h' of each wave
     __shared__ alignas(16) float bc[NW][2][T * 4 * S];
     const long long count = (long long)a.groups * sixteens * a.q.n_seq, index = on_die(blockIdx.x, count);
@@ -251,7 +254,7 @@ __global__ __launch_bounds__(64 * waves_of(S), S <= 8 ? 4 : 2) void scan_kernel(
     const int sixteen = (int)(index % sixteens), group = (int)(index / sixteens % a.groups);
     const int seq = (int)(index / sixteens / a.groups), lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Place p = place_of(a, group, sixteen);
+    const Place p = place_of(a.share, group, sixteen);
     const int n0 = p.j * S, row = w * T + p.j;
     int first, end;
     span_of(a.q, seq, first, end);
@@ -395,7 +398,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
     const int sixteen = (int)(index % sixteens), group = (int)(index / sixteens % a.groups);
     const int seq = (int)(index / sixteens / a.groups), lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Place p = place_of(a, group, sixteen);
+    const Place p = place_of(a.share, group, sixteen);
     const int n0 = p.j * S, row = w * T + p.j;
     int first, end;
     span_of(a.q, seq, first, end);
@@ -517,12 +520,26 @@ __device__ __forceinline__ float over_quads(const float (&v)[16]) {
 // A workgroup has K times 16 channels of a group, one after the other for each block of
 // tokens, so that b's and c's gradients are summed over them before they leave it; and every
 // parts-th sequence.
+//
+// What only a sequence's or the kernel's beginning and end need of the arguments is read from
+// their segment again there (`fresh`): kept in scalar registers all along, it had those of the
+// inner loop spilled to vector lanes, 150 of its 1400 instructions.
+struct BackwardArgs {
+    Scan a;
+    int sixteens, wg_groups, parts;
+    const void *x, *dt, *b, *c, *z, *gy;
+    const float *decay, *d, *dt_bias, *gfinal;
+    Grads g;
+};
+template <class A>
+__device__ __forceinline__ const __attribute__((address_space(4))) A* fresh() {
+    auto p = (const __attribute__((address_space(4))) A*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
+
 template <class TY, int S, int K>
-__global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
-    Scan a, int sixteens, int wg_groups, int parts, const typename TY::S* __restrict__ x,
-    const typename TY::S* __restrict__ dt, const float* __restrict__ decay, const typename TY::S* __restrict__ b,
-    const typename TY::S* __restrict__ c, const float* __restrict__ d, const typename TY::S* __restrict__ z,
-    const float* __restrict__ dt_bias, const typename TY::S* __restrict__ gy, const float* gfinal, Grads g) {
+__global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(BackwardArgs) {
     constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW, F = (2 * S + NW - 1) / NW;
     constexpr int N16 = (T * S + 15) / 16;
     using E = typename TY::S;
@@ -531,10 +548,14 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
     __shared__ float2 skip_bias[K][kGroupCh];
     __shared__ alignas(16) float bc[NW][2][T * 4 * S];
     __shared__ double total[K][NW][S + 1][64];  // a's gradients, and d's and dt_bias's in lanes 0 and 1 of four
+    const auto* const args = fresh<BackwardArgs>();
+    const int wg_groups = args->wg_groups, parts = args->parts, sixteens = args->sixteens, groups = args->a.groups;
+    const int share = args->a.share, state_size = args->a.state, channels = args->a.channels, n_seq = args->a.q.n_seq;
+    const bool softplus = args->a.softplus, gated = args->z != nullptr;
     const long long count = (long long)wg_groups * parts, index = on_die(blockIdx.x, count);
     if (index >= count) return;
     const int wg = (int)(index % wg_groups), part = (int)(index / wg_groups);
-    const int per_group = wg_groups / a.groups, group = wg / per_group, in_group = wg % per_group;
+    const int per_group = wg_groups / groups, group = wg / per_group, in_group = wg % per_group;
     const int k0 = in_group * K, nk = min(K, sixteens - k0);
     const int lane = threadIdx.x & 63, quad = lane >> 2, j = lane & 3;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n0 = j * S, row = w * T + j;
@@ -543,31 +564,31 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
 #pragma unroll
         for (int s = 0; s <= S; ++s) total[k][w][s][lane] = 0.0;
         if (w == k % NW && k < nk) {
-            const Place p = place_of(a, group, k0 + k);
+            const Place p = place_of(share, group, k0 + k);
             float r[S];
-            load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, r);
+            load_states<S>(args->decay + (long long)p.ch * state_size, n0, state_size, 0.0f, r);
 #pragma unroll
             for (int s = 0; s < S; ++s) r[s] *= kLog2e;
             rate[k].put(lane, r);
-            if (j == 0) skip_bias[k][quad] = float2{d ? d[p.ch] : 0.0f, dt_bias ? dt_bias[p.ch] : 0.0f};
+            if (j == 0) skip_bias[k][quad] = float2{args->d ? args->d[p.ch] : 0.0f, args->dt_bias ? args->dt_bias[p.ch] : 0.0f};
         }
     }
-    float* to_b = g.part_b + in_group * g.rows + group * a.state;
-    float* to_c = g.part_c + in_group * g.rows + group * a.state;
-    const long long row_bc = (long long)a.groups * a.state, pitch = (long long)a.groups * sixteens * (64 * S);
-    const int last_ch = a.share - 1;
+    const long long pitch = (long long)groups * sixteens * (64 * S);
     __syncthreads();
-    for (int seq = part; seq < a.q.n_seq; seq += parts) {
+    for (int seq = part; seq < n_seq; seq += parts) {
+        const auto* const in = fresh<BackwardArgs>();
         int first, end;
-        span_of(a.q, seq, first, end);
+        span_of(Sequences{in->a.q.offsets, n_seq, in->a.q.seq_len, in->a.q.n_tokens}, seq, first, end);
         const int len = end - first, blocks = (len + BT - 1) / BT;
         // states in the exchange's order: where they lie in a state array
-        const long long state0 = ((long long)seq * a.channels + group * a.share) * a.state;
+        const long long state0 = ((long long)seq * channels + group * share) * state_size;
         auto state_at = [&](int f, int k, long long* at) {
             const int ch = (k0 + k) * kGroupCh + Lanes<S>::quad_of(f), n = Lanes<S>::state_of(f);
-            *at = state0 + (long long)ch * a.state + n;
-            return ch < a.share && n < a.state;
+            *at = state0 + (long long)ch * state_size + n;
+            return ch < share && n < state_size;
         };
+        const float* const gfinal = in->gfinal;
+        float* const initial = in->g.initial;
         // (a thread reads and writes its own of `carry` alone)
         for (int k = 0; k < nk; ++k)
 #pragma unroll
@@ -578,21 +599,25 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
             }
         if (blocks) {
             const long long from = first + (blocks - 1) * (long long)BT;
-            Rows xs(x, from, a.xt, a.single, a.channels), dts(dt, from, a.dtt, a.single, a.channels),
-                zs(z, from, a.zt, a.single, a.channels), gs(gy, from, a.gt, a.single, a.channels),
-                bs(b + group * a.bg, from, a.bt, a.single, a.state), cs(c + group * a.cg, from, a.ct, a.single, a.state),
-                gxs((const E*)g.x, from, a.channels, false, a.channels), gdts((const E*)g.dt, from, a.channels, false, a.channels),
-                gzs((const E*)g.z, from, a.channels, false, a.channels);
-            const Places<TY, Q> xa(xs, row, group * a.share), dta(dts, row, group * a.share), za(zs, row, group * a.share),
-                ga(gs, row, group * a.share), oa(gxs, row, group * a.share);
-            Shared<TY, S, T> bl(bs, w * T, a.state), cl(cs, w * T, a.state);
-            const float* kept = g.kept + ((long long)first / BT + seq + blocks - 1) * pitch +
+            const bool single = in->a.single;
+            Rows xs((const E*)in->x, from, in->a.xt, single, channels), dts((const E*)in->dt, from, in->a.dtt, single, channels),
+                zs((const E*)in->z, from, in->a.zt, single, channels), gs((const E*)in->gy, from, in->a.gt, single, channels),
+                bs((const E*)in->b + group * in->a.bg, from, in->a.bt, single, state_size),
+                cs((const E*)in->c + group * in->a.cg, from, in->a.ct, single, state_size),
+                gxs((const E*)in->g.x, from, channels, false, channels), gdts((const E*)in->g.dt, from, channels, false, channels),
+                gzs((const E*)in->g.z, from, channels, false, channels);
+            const Places<TY, Q> xa(xs, row, group * share), dta(dts, row, group * share), za(zs, row, group * share),
+                ga(gs, row, group * share), oa(gxs, row, group * share);
+            Shared<TY, S, T> bl(bs, w * T, state_size), cl(cs, w * T, state_size);
+            const float* kept = in->g.kept + ((long long)first / BT + seq + blocks - 1) * pitch +
                                 ((long long)group * sixteens + k0) * (64 * S);
+            // where b's and c's gradients of the block go
+            const long long row_bc = (long long)groups * state_size, leave0 = in_group * in->g.rows + group * state_size;
             uint32_t xr[Q], dtr[Q], zr[Q], gr[Q];
             float hr[F];
             auto fetch = [&](int n, int k) {
-                const uint32_t off = min((k0 + k) * kGroupCh + quad, last_ch) * (uint32_t)sizeof(E);
-                const Buffer xb = xs.next(n), db = dts.next(n), zb = zs.next(n), gb = gs.next(n);
+                const uint32_t off = min((k0 + k) * kGroupCh + quad, share - 1) * (uint32_t)sizeof(E);
+                const Buffer xb = xs.some(n), db = dts.some(n), zb = zs.some(n), gb = gs.some(n);
 #pragma unroll
                 for (int i = 0; i < Q; ++i) {
                     xr[i] = load_raw<TY>(xb, xa.at[i] + off);
@@ -601,8 +626,8 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                     gr[i] = load_raw<TY>(gb, ga.at[i] + off);
                 }
                 if (k == 0) {
-                    bl.load(bs.next(n));
-                    cl.load(cs.next(n));
+                    bl.load(bs.some(n));
+                    cl.load(cs.some(n));
                 }
 #pragma unroll
                 for (int i = 0; i < F; ++i)
@@ -621,7 +646,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                 for (int i = 0; i < N16; ++i) sum_b[i] = sum_c[i] = 0.0f;
                 for (int k = 0; k < nk; ++k) {
                     const int ch = (k0 + k) * kGroupCh + quad;
-                    const bool here = ch < a.share;
+                    const bool here = ch < share;
                     const float2 sb = skip_bias[k][quad];
                     float xv[Q], slope[Q], step[Q], u[Q], gv[Q], zv[Q], sig[Q], gp[Q], a2[S], all = 0.0f;
                     rate[k].get(lane, a2);
@@ -630,14 +655,14 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                         const bool in = row + 4 * i < n;
                         xv[i] = value_of<TY>(xr[i]);
                         const float pre = value_of<TY>(dtr[i]) + sb.y, ex = exp_of(-fabsf(pre));
-                        step[i] = in ? (a.softplus ? softplus_of(pre, ex) : pre) : 0.0f;
-                        slope[i] = a.softplus ? sigmoid_of(pre, ex) : 1.0f;
+                        step[i] = in ? (softplus ? softplus_of(pre, ex) : pre) : 0.0f;
+                        slope[i] = softplus ? sigmoid_of(pre, ex) : 1.0f;
                         u[i] = step[i] * xv[i];
                         all += step[i];
                         gv[i] = in && here ? value_of<TY>(gr[i]) : 0.0f;
                         zv[i] = value_of<TY>(zr[i]);
-                        sig[i] = z ? sigmoid_of(zv[i]) : 1.0f;
-                        gp[i] = z ? gv[i] * (zv[i] * sig[i]) : gv[i];
+                        sig[i] = gated ? sigmoid_of(zv[i]) : 1.0f;
+                        gp[i] = gated ? gv[i] * (zv[i] * sig[i]) : gv[i];
                     }
                     float h0[F];
 #pragma unroll
@@ -704,7 +729,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                             const float before = along<S, NW, true>(product, given, r, carry[k].x[r]);
                             carry[k].x[r] = before;
                             long long to;
-                            if (block == 0 && g.initial && state_at(r, k, &to)) g.initial[to] = before;
+                            if (block == 0 && initial && state_at(r, k, &to)) initial[to] = before;
                         }
                     }
                     lds_barrier();
@@ -719,7 +744,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                     };
 #pragma unroll
                     for (int s = 0; s < S; ++s) das[s] = 0.0f;
-                    // forward: `add` becomes a_t h_{t-1}
+                    // forward: `add` becomes h_{t-1}
                     auto ahead = [&](auto kk, int i, float (&v)[4]) {
                         constexpr int J = decltype(kk)::value;
                         const int t = 4 * i + J;
@@ -729,9 +754,9 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                         v[J] = 0.0f;
 #pragma unroll
                         for (int s = 0; s < S; ++s) {
-                            const float ah = at[t][s] * h[s];
-                            h[s] = ah + add[t][s];
-                            add[t][s] = ah;
+                            const float before = h[s];
+                            h[s] = fmaf(at[t][s], before, add[t][s]);
+                            add[t][s] = before;
                             v[J] = fmaf(cv[s], h[s], v[J]);
                             vc[t * S + s] = gl * h[s];
                         }
@@ -760,10 +785,10 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                             const float G = fmaf(cv[s], gl, e[s]);
                             vb[t * S + s] = G * ul;
                             v[J] = fmaf(G, bv[s], v[J]);
-                            const float q = G * add[t][s];
+                            e[s] = at[t][s] * G;
+                            const float q = e[s] * add[t][s];
                             r[J] = fmaf(q, a2[s], r[J]);
                             das[s] = fmaf(q, dl, das[s]);
-                            e[s] = at[t][s] * G;
                         }
                     };
 #pragma unroll
@@ -787,7 +812,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                         for (int q = 0; q < 8; ++q) v[q] = vb[q], v[q + 8] = vc[q];
                         sum16(v, sum_b[0]);
                     }
-                    const Buffer gxb = gxs.next(n), gdb = gdts.next(n), gzb = gzs.next(n);
+                    const Buffer gxb = gxs.some(n), gdb = gdts.some(n), gzb = gzs.some(n);
                     float dd = 0.0f, db = 0.0f;
 #pragma unroll
                     for (int i = 0; i < Q; ++i) {
@@ -795,7 +820,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                         const float gdt = fmaf(gu[i], xv[i], gd[i] * kLn2) * slope[i];
                         store_to<TY>(gxb, to, fmaf(gu[i], step[i], sb.x * gp[i]));
                         store_to<TY>(gdb, to, gdt);
-                        if (z)
+                        if (gated)
                             store_to<TY>(gzb, to, gv[i] * fmaf(sb.x, xv[i], ypre[i]) * (sig[i] * (1.0f + zv[i] * (1.0f - sig[i]))));
                         dd = fmaf(gp[i], xv[i], dd);
                         db += row + 4 * i < n ? gdt : 0.0f;
@@ -812,8 +837,10 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                 const int mine = sixteenth_of(lane);
                 auto leave = [&](float v, int at, float* to) {  // of value `at` of the wave's T * S
                     const int t = w * T + at / S, state = n0 + at % S;
-                    if (t < n && state < a.state) to[((long long)first + block * BT + t) * row_bc + state] = v;
+                    if (t < n && state < state_size) to[(first + block * (long long)BT + t) * row_bc + leave0 + state] = v;
                 };
+                const auto* const out = fresh<BackwardArgs>();
+                float *const to_b = out->g.part_b, *const to_c = out->g.part_c;
                 if constexpr (S == 1) {
                     leave(sum_b[0], mine % 8, mine < 8 ? to_b : to_c);
                 } else {
@@ -824,31 +851,34 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
                     }
                 }
             }
-        } else if (g.initial) {  // its final state is its initial one
+        } else if (initial) {  // its final state is its initial one
             for (int k = 0; k < nk; ++k)
 #pragma unroll
                 for (int i = 0; i < F; ++i) {
                     const int f = threadIdx.x + i * 64 * NW - 64 * S;
                     long long at;
-                    if (f >= 0 && f < 64 * S && state_at(f, k, &at)) g.initial[at] = carry[k].x[f];
+                    if (f >= 0 && f < 64 * S && state_at(f, k, &at)) initial[at] = carry[k].x[f];
                 }
         }
-        if (a.clear && seq == a.q.n_seq - 1)
+        const auto* const out = fresh<BackwardArgs>();
+        const int clear = out->a.clear;
+        if (clear && seq == n_seq - 1)
             for (int k = 0; k < nk; ++k) {
-                const Place p = place_of(a, group, k0 + k);
+                const Place p = place_of(share, group, k0 + k);
                 if (!p.in) continue;
-                for (int t = end + 4 * w + j; t < a.q.n_tokens; t += 4 * NW) {
-                    const long long to = (long long)t * a.channels + p.ch;
-                    if (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_X) static_cast<E*>(g.x)[to] = TY::store(0.0f);
-                    if (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_DT) static_cast<E*>(g.dt)[to] = TY::store(0.0f);
-                    if (z && (a.clear & SELECTIVE_SCAN_CLEAR_GRAD_Z)) static_cast<E*>(g.z)[to] = TY::store(0.0f);
+                for (int t = end + 4 * w + j; t < out->a.q.n_tokens; t += 4 * NW) {
+                    const long long to = (long long)t * channels + p.ch;
+                    if (clear & SELECTIVE_SCAN_CLEAR_GRAD_X) ((E*)out->g.x)[to] = TY::store(0.0f);
+                    if (clear & SELECTIVE_SCAN_CLEAR_GRAD_DT) ((E*)out->g.dt)[to] = TY::store(0.0f);
+                    if (gated && (clear & SELECTIVE_SCAN_CLEAR_GRAD_Z)) ((E*)out->g.z)[to] = TY::store(0.0f);
                 }
             }
     }
     // the waves' sums together, a wave for each sixteen channels
     __syncthreads();
+    const auto* const out = fresh<BackwardArgs>();
     for (int k = w; k < nk; k += NW) {
-        const Place p = place_of(a, group, k0 + k);
+        const Place p = place_of(share, group, k0 + k);
         if (!p.in) continue;
 #pragma unroll
         for (int s = 0; s <= S; ++s) {
@@ -856,9 +886,9 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(
 #pragma unroll
             for (int i = 1; i < NW; ++i) v += total[k][i][s][lane];
             if (s < S) {
-                if (n0 + s < a.state) g.part_a[((long long)part * a.channels + p.ch) * a.state + n0 + s] = (float)v;
+                if (n0 + s < state_size) out->g.part_a[((long long)part * channels + p.ch) * state_size + n0 + s] = (float)v;
             } else if (j < 2) {
-                (j == 0 ? g.part_d : g.part_bias)[(long long)part * a.channels + p.ch] = (float)v;
+                (j == 0 ? out->g.part_d : out->g.part_bias)[(long long)part * channels + p.ch] = (float)v;
             }
         }
     }
@@ -923,7 +953,7 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
         (long long)blockIdx.x * (kStepThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= waves) return;
     const int sixteen = (int)(wave % sixteens), group = (int)(wave / sixteens % a.groups);
-    const Place p = place_of(a, group, sixteen);
+    const Place p = place_of(a.share, group, sixteen);
     const int lane = threadIdx.x & 63, n0 = p.j * S, rows = a.q.n_tokens;
     int row = (int)(wave / sixteens / a.groups), slot = row;
     if (slots) {
@@ -1113,8 +1143,18 @@ extern "C" int selective_scan_forward(const selective_scan_shape_t* shape, const
         constexpr int S = decltype(states)::value;
         const int sixteens = sixteens_of(a);
         const long long count = (long long)a.groups * sixteens * a.q.n_seq;
-        hipLaunchKernelGGL((scan_kernel<TY, S>), dim3(dealt(count)), dim3(64 * waves_of(S)), 0, stream, a, sixteens, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d, (const E*)z,
-                           dt_bias, initial_state, (E*)y, final_state);
+        auto go = [&](auto kernel, int waves) {
+            hipLaunchKernelGGL(kernel, dim3(dealt(count)), dim3(64 * waves), 0, stream, a, sixteens, (const E*)x,
+                               (const E*)dt, a_, (const E*)b, (const E*)c, d, (const E*)z, dt_bias, initial_state, (E*)y,
+                               final_state);
+        };
+        if constexpr (S <= 8) {
+            if (count <= kFewWorkgroups) {
+                go(scan_kernel<TY, S, 16>, 16);
+                return launch_status();
+            }
+        }
+        go(scan_kernel<TY, S, 8>, 8);
         return launch_status();
     });
 }
@@ -1166,10 +1206,9 @@ extern "C" int selective_scan_backward(const selective_scan_shape_t* shape, cons
             hipLaunchKernelGGL((scan_states_kernel<TY, S>), dim3(dealt((long long)a.groups * sixteens * a.q.n_seq)),
                                dim3(64 * waves_of(S)), 0, stream, a, sixteens, (const E*)x, (const E*)dt, a_, (const E*)b,
                                dt_bias, initial_state, g.kept);
+            const BackwardArgs args{a, sixteens, wg_groups, parts, x, dt, b, c, z, grad_y, a_, d, dt_bias, grad_final_state, g};
             auto go = [&](auto kernel) {
-                hipLaunchKernelGGL(kernel, dim3(dealt((long long)wg_groups * parts)), dim3(64 * waves_of(S)), 0, stream, a,
-                                   sixteens, wg_groups, parts, (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
-                                   (const E*)z, dt_bias, (const E*)grad_y, grad_final_state, g);
+                hipLaunchKernelGGL(kernel, dim3(dealt((long long)wg_groups * parts)), dim3(64 * waves_of(S)), 0, stream, args);
             };
             const int at_once = sixteens_at_once(a);
             if constexpr (S <= 4) {
