@@ -134,14 +134,14 @@ __device__ __forceinline__ void store_to(Buffer b, uint32_t at, float x) {
 // there are set to zero.)
 struct Rows {
     const char* at;
-    int bytes, rest;  // from a row to the next, and from there to the row's end
+    int bytes, width;  // from a row to the next, and of a row
     template <class E>
-    __device__ __forceinline__ Rows(const E* p, long long row, long long stride, bool single, int width)
+    __device__ __forceinline__ Rows(const E* p, long long row, long long stride, bool single, int elements)
         : at(p ? reinterpret_cast<const char*>(p + row * stride) : nullptr),
-          bytes(p && !single ? (int)stride * (int)sizeof(E) : 0), rest(p ? width * (int)sizeof(E) - bytes : 0) {}
+          bytes(p && !single ? (int)stride * (int)sizeof(E) : 0), width(p ? elements * (int)sizeof(E) : 0) {}
     // The next n of them, of which there are some (or there may be none).
-    __device__ __forceinline__ Buffer some(int n) const { return buffer_of(at, n * bytes + rest); }
-    __device__ __forceinline__ Buffer next(int n) const { return buffer_of(at, n > 0 ? n * bytes + rest : 0); }
+    __device__ __forceinline__ Buffer some(int n) const { return buffer_of(at, (n - 1) * bytes + width); }
+    __device__ __forceinline__ Buffer next(int n) const { return buffer_of(at, n > 0 ? (n - 1) * bytes + width : 0); }
     __device__ __forceinline__ void move(int n) { at += n * bytes; }
 };
 // A lane's places in a block: its element of the rows row, row + 4, ...
@@ -603,11 +603,11 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
             Rows xs((const E*)in->x, from, in->a.xt, single, channels), dts((const E*)in->dt, from, in->a.dtt, single, channels),
                 zs((const E*)in->z, from, in->a.zt, single, channels), gs((const E*)in->gy, from, in->a.gt, single, channels),
                 bs((const E*)in->b + group * in->a.bg, from, in->a.bt, single, state_size),
-                cs((const E*)in->c + group * in->a.cg, from, in->a.ct, single, state_size),
-                gxs((const E*)in->g.x, from, channels, false, channels), gdts((const E*)in->g.dt, from, channels, false, channels),
-                gzs((const E*)in->g.z, from, channels, false, channels);
+                cs((const E*)in->c + group * in->a.cg, from, in->a.ct, single, state_size);
+            const int pitch_out = channels * (int)sizeof(E);  // bytes of an output's row
+            long long out_at = from * pitch_out;              // of the block's first
             const Places<TY, Q> xa(xs, row, group * share), dta(dts, row, group * share), za(zs, row, group * share),
-                ga(gs, row, group * share), oa(gxs, row, group * share);
+                ga(gs, row, group * share);
             Shared<TY, S, T> bl(bs, w * T, state_size), cl(cs, w * T, state_size);
             const float* kept = in->g.kept + ((long long)first / BT + seq + blocks - 1) * pitch +
                                 ((long long)group * sixteens + k0) * (64 * S);
@@ -812,11 +812,15 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
                         for (int q = 0; q < 8; ++q) v[q] = vb[q], v[q + 8] = vc[q];
                         sum16(v, sum_b[0]);
                     }
-                    const Buffer gxb = gxs.some(n), gdb = gdts.some(n), gzb = gzs.some(n);
+                    const auto* const out = fresh<BackwardArgs>();
+                    const Buffer gxb = buffer_of((char*)out->g.x + out_at, n * pitch_out),
+                                 gdb = buffer_of((char*)out->g.dt + out_at, n * pitch_out),
+                                 gzb = buffer_of((char*)out->g.z + out_at, n * pitch_out);
+                    const uint32_t own = row * (uint32_t)pitch_out + (group * share + ch) * (uint32_t)sizeof(E);
                     float dd = 0.0f, db = 0.0f;
 #pragma unroll
                     for (int i = 0; i < Q; ++i) {
-                        const uint32_t to = here ? oa.at[i] + ch * (uint32_t)sizeof(E) : kNowhere;
+                        const uint32_t to = here ? own + 4 * i * (uint32_t)pitch_out : kNowhere;
                         const float gdt = fmaf(gu[i], xv[i], gd[i] * kLn2) * slope[i];
                         store_to<TY>(gxb, to, fmaf(gu[i], step[i], sb.x * gp[i]));
                         store_to<TY>(gdb, to, gdt);
@@ -833,7 +837,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
                     for (int s = 0; s < S; ++s) total[k][w][s][lane] += das[s];
                     total[k][w][S][lane] += j == 0 ? dd : db;
                 }
-                gxs.move(-BT), gdts.move(-BT), gzs.move(-BT);
+                out_at -= BT * (long long)pitch_out;
                 const int mine = sixteenth_of(lane);
                 auto leave = [&](float v, int at, float* to) {  // of value `at` of the wave's T * S
                     const int t = w * T + at / S, state = n0 + at % S;
