@@ -945,56 +945,134 @@ __global__ __launch_bounds__(kSumThreads) void scan_sums_kernel(Scan a, Grads g,
 }
 
 // ----------------------------------------------------------------------- step
+// A lane's S states of a row, j of its channel's four: V neighbours at 4 V i + V j, so that
+// the four read and write whole pieces of a cache line.  At any address; zero behind `state`.
+template <class TY, int S, bool PAST>
+__device__ __forceinline__ void load_row(const typename TY::S* row, int j, int state, float (&h)[S]) {
+    using E = typename TY::S;
+    constexpr int V = S < 4 ? S : 4;
+    typedef E vec __attribute__((ext_vector_type(V), aligned(sizeof(E))));
+#pragma unroll
+    for (int i = 0; i < S / V; ++i) {
+        const int n = (4 * i + j) * V;
+        if (n + V <= state) {
+            const vec* p = reinterpret_cast<const vec*>(row + n);
+            const vec v = PAST ? __builtin_nontemporal_load(p) : *p;
+#pragma unroll
+            for (int k = 0; k < V; ++k) h[i * V + k] = TY::load(v[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) h[i * V + k] = n + k < state ? TY::load(row[n + k]) : 0.0f;
+        }
+    }
+}
+template <int S, bool PAST>
+__device__ __forceinline__ void store_row(float* row, int j, int state, const float (&h)[S]) {
+    constexpr int V = S < 4 ? S : 4;
+    typedef float vec __attribute__((ext_vector_type(V), aligned(4)));
+#pragma unroll
+    for (int i = 0; i < S / V; ++i) {
+        const int n = (4 * i + j) * V;
+        if (n + V <= state) {
+            vec v;
+#pragma unroll
+            for (int k = 0; k < V; ++k) v[k] = h[i * V + k];
+            vec* p = reinterpret_cast<vec*>(row + n);
+            if constexpr (PAST)
+                __builtin_nontemporal_store(v, p);
+            else
+                *p = v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (n + k < state) row[n + k] = h[i * V + k];
+        }
+    }
+}
+
+// A wave has C times 16 channels of a row, their states in registers, all loads in flight at
+// once.  The steps and the gates are computed by a lane for each channel and taken from there
+// by the channel's four.  Bound by reading and writing the states.
 constexpr int kStepThreads = 256;
-template <class TY, int S>
+constexpr long long kPastCache = 32LL << 20, kStepFew = 8192;
+template <class TY, int S, int C, bool PAST>
 __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
-    Scan a, long long waves, int sixteens, const typename TY::S* __restrict__ x,
-    const typename TY::S* __restrict__ dt, const float* __restrict__ decay, const typename TY::S* __restrict__ b,
-    const typename TY::S* __restrict__ c, const float* __restrict__ d, const typename TY::S* __restrict__ z,
-    const float* __restrict__ dt_bias, float* states, int pool, const int* __restrict__ slots,
-    typename TY::S* __restrict__ y) {
-    const long long wave =
-        (long long)blockIdx.x * (kStepThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Scan a, long long waves, int parts, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
+    const float* __restrict__ decay, const typename TY::S* __restrict__ b, const typename TY::S* __restrict__ c,
+    const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias, float* states,
+    int pool, const int* __restrict__ slots, typename TY::S* __restrict__ y) {
+    const long long index = on_die(blockIdx.x, (waves + kStepThreads / 64 - 1) / (kStepThreads / 64));
+    const long long wave = index * (kStepThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= waves) return;
-    const int sixteen = (int)(wave % sixteens), group = (int)(wave / sixteens % a.groups);
-    const Place p = place_of(a.share, group, sixteen);
-    const int lane = threadIdx.x & 63, n0 = p.j * S, rows = a.q.n_tokens;
-    int row = (int)(wave / sixteens / a.groups), slot = row;
+    const int part = (int)(wave % parts), group = (int)(wave / parts % a.groups), rows = a.q.n_tokens;
+    const int lane = threadIdx.x & 63, quad = lane >> 2, four = lane & 3;
+    int row = (int)(wave / parts / a.groups), slot = row;
+    // the lane's channel, of those of the group
+    const int ch = part * (C * kGroupCh) + lane;
+    const bool own = lane < C * kGroupCh && ch < a.share;
+    const int at = group * a.share + min(ch, a.share - 1);
     if (slots) {
         slot = __builtin_amdgcn_readfirstlane(slots[row]);
         if (slot < 0 || slot >= pool) {
-            if (p.in && p.j == 0) y[(long long)row * a.channels + p.ch] = TY::store(0.0f);
+            if (own) y[(long long)row * a.channels + at] = TY::store(0.0f);
             return;
         }
-        for (int j = 0; j < row; j += 64)  // the first row of a slot takes all
-            if (__ballot(j + lane < row && slots[min(j + lane, rows - 1)] == slot)) return;
     }
-    float* state = states + ((long long)slot * a.channels + p.ch) * a.state;
-    float a2[S], h[S];
-    load_states<S>(state, n0, a.state, 0.0f, h);
-    load_states<S>(decay + (long long)p.ch * a.state, n0, a.state, 0.0f, a2);
-    const float skip = d ? d[p.ch] : 0.0f, bias = dt_bias ? dt_bias[p.ch] : 0.0f;
+    float h[C][S], a2[C][S];
+    auto state_of = [&](int i, bool* in) {
+        const int k = part * (C * kGroupCh) + i * kGroupCh + quad;
+        *in = k < a.share;
+        return group * a.share + min(k, a.share - 1);
+    };
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        bool in;
+        const int k = state_of(i, &in);
+        load_row<F32, S, PAST>(states + ((long long)slot * a.channels + k) * a.state, four, a.state, h[i]);
+        load_row<F32, S, false>(decay + (long long)k * a.state, four, a.state, a2[i]);
+    }
+    const float skip = d ? d[at] : 0.0f, bias = dt_bias ? dt_bias[at] : 0.0f;
     b += group * a.bg;
     c += group * a.cg;
-    while (row < rows) {
-        const float xv = TY::load(x[row * a.xt + p.ch]), pre = TY::load(dt[row * a.dtt + p.ch]) + bias;
-        const float step = a.softplus ? softplus_of(pre) : pre, u = step * xv;
-        float v = 0.0f;
+    struct Row {
+        float x, dt, z, b[S], c[S];
+    };
+    auto fetch = [&](Row& r) {
+        r.x = TY::load(x[row * a.xt + at]);
+        r.dt = TY::load(dt[row * a.dtt + at]);
+        r.z = z ? TY::load(z[row * a.zt + at]) : 0.0f;
+        load_row<TY, S, false>(b + row * a.bt, four, a.state, r.b);
+        load_row<TY, S, false>(c + row * a.ct, four, a.state, r.c);
+    };
+    Row r;
+    fetch(r);
+    if (slots)  // the first row of a slot takes all
+        for (int j = 0; j < row; j += 64)
+            if (__ballot(j + lane < row && slots[min(j + lane, rows - 1)] == slot)) return;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const bool in = n0 + s < a.state;
-            const float bv = in ? TY::load(b[row * a.bt + n0 + s]) : 0.0f, cv = in ? TY::load(c[row * a.ct + n0 + s]) : 0.0f;
-            h[s] = fmaf(exp2_of(step * a2[s] * kLog2e), h[s], u * bv);
-            v = fmaf(cv, h[s], v);
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int s = 0; s < S; ++s) a2[i][s] *= kLog2e;
+    while (true) {
+        const float pre = r.dt + bias, step = a.softplus ? softplus_of(pre) : pre, u = step * r.x;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const float dl = __shfl(step, i * kGroupCh + quad), ul = __shfl(u, i * kGroupCh + quad);
+            float v = 0.0f;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                h[i][s] = fmaf(exp2_of(dl * a2[i][s]), h[i][s], ul * r.b[s]);
+                v = fmaf(r.c[s], h[i][s], v);
+            }
+            v += quad_perm<0xB1>(v);
+            v += quad_perm<0x4E>(v);
+            const float mine = __shfl(v, 4 * (lane & 15));
+            if (lane >> 4 == i) sum = mine;
         }
-        v += quad_perm<0xB1>(v);
-        v += quad_perm<0x4E>(v);
-        float out = fmaf(skip, xv, v);
-        if (z) {
-            const float zv = TY::load(z[row * a.zt + p.ch]);
-            out *= zv * sigmoid_of(zv);
-        }
-        if (p.in && p.j == 0) y[(long long)row * a.channels + p.ch] = TY::store(out);
+        float out = fmaf(skip, r.x, sum);
+        if (z) out *= r.z * sigmoid_of(r.z);
+        if (own) y[(long long)row * a.channels + at] = TY::store(out);
         if (!slots) break;
         int next = rows;
         for (int j = row + 1; j < rows; j += 64) {
@@ -1004,9 +1082,16 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
                 break;
             }
         }
+        if (next >= rows) break;
         row = next;
+        fetch(r);
     }
-    if (p.in) store_states<S>(state, n0, a.state, h);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        bool in;
+        const int k = state_of(i, &in);
+        if (in) store_row<S, PAST>(states + ((long long)slot * a.channels + k) * a.state, four, a.state, h[i]);
+    }
 }
 
 // ---------------------------------------------------------- host helpers
@@ -1255,11 +1340,21 @@ extern "C" int selective_scan_step(const selective_scan_shape_t* shape, const vo
         using TY = decltype(ty);
         using E = typename TY::S;
         constexpr int S = decltype(s)::value;
-        const long long waves = (long long)a.groups * sixteens_of(a) * a.q.n_tokens;
-        constexpr int per = kStepThreads / 64;
-        hipLaunchKernelGGL((scan_step_kernel<TY, S>), dim3((unsigned)((waves + per - 1) / per)), dim3(kStepThreads), 0,
-                           stream, a, waves, sixteens_of(a), (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d,
-                           (const E*)z, dt_bias, states, pool, slots, (E*)y);
+        constexpr int per = kStepThreads / 64, C = S <= 4 ? 4 : S == 8 ? 2 : 1;
+        auto go = [&](auto kernel, int at_once) {
+            const int parts = (sixteens_of(a) + at_once - 1) / at_once;
+            const long long waves = (long long)a.groups * parts * a.q.n_tokens;
+            hipLaunchKernelGGL(kernel, dim3(dealt((waves + per - 1) / per)), dim3(kStepThreads), 0, stream, a, waves, parts,
+                               (const E*)x, (const E*)dt, a_, (const E*)b, (const E*)c, d, (const E*)z, dt_bias, states,
+                               pool, slots, (E*)y);
+        };
+        const bool past = (long long)a.q.n_tokens * n.a >= kPastCache;
+        if ((long long)a.groups * sixteens_of(a) * a.q.n_tokens < kStepFew)
+            go(scan_step_kernel<TY, S, 1, false>, 1);
+        else if (past)
+            go(scan_step_kernel<TY, S, C, true>, C);
+        else
+            go(scan_step_kernel<TY, S, C, false>, C);
         return launch_status();
     });
 }
