@@ -31,32 +31,37 @@ struct F16 {
     static __device__ __forceinline__ S store(float x) { return (_Float16)x; }
 };
 
-// 16 bytes at an address that the element's size divides; the memory takes them at any.
+// 16 and 8 bytes at an address that the element's size divides; the memory takes them at any.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 
-// Eight consecutive elements as they lie in memory.
-template <class TY>
-struct Eight {
-    uint32_t w[2 * sizeof(typename TY::S)];
+// V consecutive elements as they lie in memory, 8 bytes of them or a multiple of 16.
+template <class TY, int V>
+struct Packed {
+    uint32_t w[V * sizeof(typename TY::S) / 4];
 };
 
-// Columns c ... c + 7 of a row; zero from `width` on.
-template <class TY>
-__device__ __forceinline__ Eight<TY> fetch8(const typename TY::S* row, int c, int width) {
-    Eight<TY> e;
-    if (c + 8 <= width) {
+// Columns c ... c + V - 1 of a row; zero from `width` on.
+template <class TY, int V>
+__device__ __forceinline__ Packed<TY, V> fetch(const typename TY::S* row, int c, int width) {
+    Packed<TY, V> e;
+    if (c + V <= width) {
+        if constexpr (sizeof(e) == 8) {
+            const u32x2_any a = *reinterpret_cast<const u32x2_any*>(row + c);
+            e.w[0] = a[0], e.w[1] = a[1];
+        } else {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(e) / 16; ++i) {
-            const u32x4_any a = *reinterpret_cast<const u32x4_any*>(row + c + 4 * i);
+            for (int i = 0; i < (int)sizeof(e) / 16; ++i) {
+                const u32x4_any a = *reinterpret_cast<const u32x4_any*>(reinterpret_cast<const char*>(row + c) + 16 * i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) e.w[4 * i + j] = a[j];
+                for (int j = 0; j < 4; ++j) e.w[4 * i + j] = a[j];
+            }
         }
     } else {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(e) / 4; ++i) e.w[i] = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < V; ++j)
             if (c + j < width) {
                 if constexpr (sizeof(typename TY::S) == 4)
                     e.w[j] = __builtin_bit_cast(uint32_t, row[c + j]);
@@ -66,10 +71,10 @@ __device__ __forceinline__ Eight<TY> fetch8(const typename TY::S* row, int c, in
     }
     return e;
 }
-template <class TY>
-__device__ __forceinline__ void unpack8(const Eight<TY>& e, float (&x)[8]) {
+template <class TY, int V>
+__device__ __forceinline__ void unpack(const Packed<TY, V>& e, float (&x)[V]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < V; ++j) {
         if constexpr (sizeof(typename TY::S) == 4)
             x[j] = __builtin_bit_cast(float, e.w[j]);
         else
@@ -77,27 +82,34 @@ __device__ __forceinline__ void unpack8(const Eight<TY>& e, float (&x)[8]) {
                                                (uint16_t)(j & 1 ? e.w[j >> 1] >> 16 : e.w[j >> 1] & 0xffff)));
     }
 }
-template <class TY>
-__device__ __forceinline__ void load8(const typename TY::S* row, int c, int width, float (&x)[8]) {
-    unpack8<TY>(fetch8<TY>(row, c, width), x);
+template <class TY, int V>
+__device__ __forceinline__ void load(const typename TY::S* row, int c, int width, float (&x)[V]) {
+    unpack<TY, V>(fetch<TY, V>(row, c, width), x);
 }
-template <class TY>
-__device__ __forceinline__ void store8(typename TY::S* row, int c, int width, const float (&x)[8]) {
-    if (c + 8 <= width) {
+template <class TY, int V>
+__device__ __forceinline__ void store(typename TY::S* row, int c, int width, const float (&x)[V]) {
+    if (c + V <= width) {
+        Packed<TY, V> e;
         if constexpr (sizeof(typename TY::S) == 4) {
-            *reinterpret_cast<f32x4_any*>(row + c) = f32x4_any{x[0], x[1], x[2], x[3]};
-            *reinterpret_cast<f32x4_any*>(row + c + 4) = f32x4_any{x[4], x[5], x[6], x[7]};
-        } else {
-            u32x4_any a;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                a[j] = (uint32_t)__builtin_bit_cast(uint16_t, TY::store(x[2 * j])) |
-                       (uint32_t)__builtin_bit_cast(uint16_t, TY::store(x[2 * j + 1])) << 16;
-            *reinterpret_cast<u32x4_any*>(row + c) = a;
+            for (int j = 0; j < V; ++j) e.w[j] = __builtin_bit_cast(uint32_t, x[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j)
+                e.w[j] = (uint32_t)__builtin_bit_cast(uint16_t, TY::store(x[2 * j])) |
+                         (uint32_t)__builtin_bit_cast(uint16_t, TY::store(x[2 * j + 1])) << 16;
+        }
+        if constexpr (sizeof(e) == 8) {
+            *reinterpret_cast<u32x2_any*>(row + c) = u32x2_any{e.w[0], e.w[1]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(e) / 16; ++i)
+                *reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(row + c) + 16 * i) =
+                    u32x4_any{e.w[4 * i], e.w[4 * i + 1], e.w[4 * i + 2], e.w[4 * i + 3]};
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < V; ++j)
             if (c + j < width) row[c + j] = TY::store(x[j]);
     }
 }

@@ -25,6 +25,15 @@ __device__ __forceinline__ float sigmoid_of(float x, float e) {
     return x >= 0.0f ? r : e * r;
 }
 __device__ __forceinline__ float sigmoid_of(float x) { return sigmoid_of(x, exp_of(-fabsf(x))); }
+// The same for what is rounded to a type of 16 bits: off by |x| 2^-24, where exp_of's and the
+// choice of sides cost as much again.
+template <class TY>
+__device__ __forceinline__ float gate_of(float x) {
+    if constexpr (sizeof(typename TY::S) == 4)
+        return sigmoid_of(x);
+    else
+        return reciprocal(1.0f + exp2_of(-kLog2e * x));
+}
 // max(x, 0) + log(1 + e) with e = exp(-|x|); the logarithm as 2 artanh(e / (2 + e)) by its
 // series, whose argument is at most a third, so that small results lose nothing.
 __device__ __forceinline__ float softplus_of(float x, float e) {

@@ -53,19 +53,37 @@ __device__ __forceinline__ int tensor_of(const Batch& b, unsigned chunk) {
     return lo;
 }
 
+// Calls f(first element, elements as they lie in memory, how many of the eight there are) for
+// a thread's eights of [at, end); kUnroll of them are loaded at once.
+constexpr int kUnroll = 4;
+template <class TY, class F>
+__device__ __forceinline__ void each_eight(const void* grad, long long at, long long end, F f) {
+    const auto* p = static_cast<const typename TY::S*>(grad);
+    long long i = at + 8 * threadIdx.x;
+    for (; i + (kUnroll - 1) * kStep + 8 <= end; i += kUnroll * kStep) {
+        Packed<TY, 8> e[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) e[k] = fetch<TY, 8>(p + i + k * kStep, 0, 8);
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) f(i + k * kStep, e[k], 8);
+    }
+    for (; i < end; i += kStep) {
+        const int n = (int)min(end - i, 8LL);
+        f(i, fetch<TY, 8>(p + i, 0, n), n);
+    }
+}
 template <class TY>
 __device__ __forceinline__ void squares(const void* grad, long long at, long long end, double& s0, double& s1) {
-    const auto* p = static_cast<const typename TY::S*>(grad);
-    for (long long i = at + 8 * threadIdx.x; i < end; i += kStep) {
+    each_eight<TY>(grad, at, end, [&](long long, const Packed<TY, 8>& e, int) {
         float x[8];
-        load8<TY>(p + i, 0, (int)min(end - i, 8LL), x);
+        unpack<TY, 8>(e, x);
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             const double a = x[j], b = x[j + 1];
             s0 += a * a;
             s1 += b * b;
         }
-    }
+    });
 }
 
 __device__ __forceinline__ double over_block(double x, double* red) {
@@ -117,16 +135,14 @@ __global__ __launch_bounds__(kThreads) void total_kernel(const double* __restric
 
 template <class TY>
 __device__ __forceinline__ void scale(const void* grad, void* out, long long at, long long end, float factor) {
-    const auto* p = static_cast<const typename TY::S*>(grad);
     auto* o = static_cast<typename TY::S*>(out);
-    for (long long i = at + 8 * threadIdx.x; i < end; i += kStep) {
+    each_eight<TY>(grad, at, end, [&](long long i, const Packed<TY, 8>& e, int n) {
         float x[8];
-        const int n = (int)min(end - i, 8LL);
-        load8<TY>(p + i, 0, n, x);
+        unpack<TY, 8>(e, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= factor;
-        store8<TY>(o + i, 0, n, x);
-    }
+        store<TY, 8>(o + i, 0, n, x);
+    });
 }
 
 __global__ __launch_bounds__(kThreads) void clip_kernel(Batch b, const double* __restrict__ part, int parts,
@@ -138,7 +154,9 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Batch b, const double* _
     if (ratio > 1.0) ratio = 1.0;  // not where it is NaN
     if (isinf(max_norm) && whole != whole) ratio = whole;
     const float factor = (float)ratio;
-    for (unsigned chunk = blockIdx.x; chunk < b.chunks; chunk += gridDim.x) {
+    // from the last chunk on, which the norm has read last and the last-level cache still holds
+    for (unsigned k = blockIdx.x; k < b.chunks; k += gridDim.x) {
+        const unsigned chunk = b.chunks - 1 - k;
         const int t = tensor_of(b, chunk);
         const long long at = (long long)(chunk - b.chunk0[t]) * b.steps * kStep;
         const long long end = min(at + (long long)b.steps * kStep, b.numel[t]);
@@ -238,7 +256,7 @@ int run(const grad_tensor_t* tensors, int count, bool clip, float max_norm, floa
     if (joined)
         hipLaunchKernelGGL(total_kernel, dim3(1), dim3(kThreads), 0, stream, part, parts, norm, clip ? total : nullptr);
     if (clip && parts) {
-        for (int i = 0; i < batches; ++i) {
+        for (int i = batches - 1; i >= 0; --i) {
             const Batch b = batch_of(tensors, count, i * kBatch);
             if (b.chunks == 0) continue;
             hipLaunchKernelGGL(clip_kernel, dim3(blocks_of(b)), dim3(kThreads), 0, stream, b, joined ? total : part,

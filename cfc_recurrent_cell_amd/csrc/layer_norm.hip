@@ -21,6 +21,21 @@ namespace {
 
 __device__ __forceinline__ float plus(float p, float q) { return p + q; }
 
+// over_row of two sums at once, with one barrier.
+template <int TPR>
+__device__ __forceinline__ void over_row_two(float2& s, float (*red)[2][16], int turn) {
+#pragma unroll
+    for (int off = 1; off < (TPR < 64 ? TPR : 64); off <<= 1) s.x += __shfl_xor(s.x, off), s.y += __shfl_xor(s.y, off);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) red[turn][0][threadIdx.x >> 6] = s.x, red[turn][1][threadIdx.x >> 6] = s.y;
+        __syncthreads();
+        const int first = threadIdx.x / TPR * (TPR / 64);
+        s = {red[turn][0][first], red[turn][1][first]};
+#pragma unroll
+        for (int i = 1; i < TPR / 64; ++i) s.x += red[turn][0][first + i], s.y += red[turn][1][first + i];
+    }
+}
+
 template <class TX, class TH, int TPR, int NV>
 __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
     long long rows, int width, const typename TX::S* x, const typename TH::S* residual,
@@ -32,10 +47,10 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
     float w[NV][8], b[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        load8<TX>(weight, 8 * (v * TPR + sub), width, w[v]);
+        load<TX, 8>(weight, 8 * (v * TPR + sub), width, w[v]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
-        if (bias) load8<TX>(bias, 8 * (v * TPR + sub), width, b[v]);
+        if (bias) load<TX, 8>(bias, 8 * (v * TPR + sub), width, b[v]);
     }
     for (long long r0 = (long long)blockIdx.x * RPW; r0 < rows; r0 += (long long)gridDim.x * RPW) {
         const long long row = r0 + threadIdx.x / TPR;
@@ -43,16 +58,16 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
         const long long at = (in ? row : rows - 1) * width;
         float a[NV][8];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) load8<TX>(x + at, 8 * (v * TPR + sub), width, a[v]);
+        for (int v = 0; v < NV; ++v) load<TX, 8>(x + at, 8 * (v * TPR + sub), width, a[v]);
         if (residual) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 float e[8];
                 const int c = 8 * (v * TPR + sub);
-                load8<TH>(residual + at, c, width, e);
+                load<TH, 8>(residual + at, c, width, e);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) a[v][j] = TH::load(TH::store(a[v][j] + e[j]));
-                if (h && in) store8<TH>(h + at, c, width, a[v]);
+                if (h && in) store<TH, 8>(h + at, c, width, a[v]);
             }
         }
         float s = 0.0f;
@@ -79,12 +94,13 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
             for (int v = 0; v < NV; ++v) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) a[v][j] = a[v][j] * rs * w[v][j] + b[v][j];
-                store8<TX>(y + at, 8 * (v * TPR + sub), width, a[v]);
+                store<TX, 8>(y + at, 8 * (v * TPR + sub), width, a[v]);
             }
         }
     }
 }
 
+// A row's loads are in flight while the row before is worked on.
 // The weight's and the bias's terms are summed over the workgroup's rows in registers,
 // in 64 bits, then over its row slots through LDS, into part[2 * blockIdx.x] and the
 // row behind it; column_sums_kernel sums those.
@@ -94,57 +110,71 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
     const typename TX::S* __restrict__ weight, const float* __restrict__ mean, const float* __restrict__ rstd,
     const typename TH::S* gh, typename TH::S* gx, float* __restrict__ part) {
     constexpr int RPW = threads_of(TPR) / TPR;
-    __shared__ float red[2][16];
+    __shared__ float red[2][2][16];
     const int sub = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     float w[NV][8];
-    double gw[NV][8], gb[NV][8];
+    // (two vectors a lane would not fit the registers in 64 bits: few rows a workgroup instead)
+    using Sum = std::conditional_t<NV == 1, double, float>;
+    Sum gw[NV][8], gb[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        load8<TX>(weight, 8 * (v * TPR + sub), width, w[v]);
+        load<TX, 8>(weight, 8 * (v * TPR + sub), width, w[v]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) gw[v][j] = gb[v][j] = 0.0;
     }
-    for (long long r0 = (long long)blockIdx.x * RPW; r0 < rows; r0 += (long long)gridDim.x * RPW) {
-        const long long row = r0 + slot;
-        const bool in = row < rows;
-        const long long at = (in ? row : rows - 1) * width;
-        const float rs = in ? rstd[row] : 0.0f, m = in ? mean[row] : 0.0f;
-        float n[NV][8], d[NV][8];
+    Packed<TH, 8> hr[NV], gr[NV];
+    Packed<TX, 8> yr[NV];
+    float rs = 0.0f, m = 0.0f;
+    auto fetch_row = [&](long long r0) {
+        const long long row = min(r0 + slot, rows - 1);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            load8<TH>(h + at, 8 * (v * TPR + sub), width, n[v]);
-            load8<TX>(gy + at, 8 * (v * TPR + sub), width, d[v]);
+            const int c = 8 * (v * TPR + sub);
+            hr[v] = fetch<TH, 8>(h + row * width, c, width);
+            yr[v] = fetch<TX, 8>(gy + row * width, c, width);
+            if (gh) gr[v] = fetch<TH, 8>(gh + row * width, c, width);
         }
-        float s = 0.0f, sn = 0.0f;
+        rs = rstd[row], m = mean[row];
+    };
+    int turn = 0;
+    const long long stride = (long long)gridDim.x * RPW;
+    if constexpr (NV == 1) fetch_row((long long)blockIdx.x * RPW);
+    for (long long r0 = (long long)blockIdx.x * RPW; r0 < rows; r0 += stride) {
+        const long long row = r0 + slot;
+        const bool in = row < rows;  // lanes of a row behind the last compute and write nothing
+        float n[NV][8], d[NV][8], o[NV][8];
+        if constexpr (NV > 1) fetch_row(r0);
+        const float rsn = rs;
+        float2 s = {0.0f, 0.0f};
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v) {
+            unpack<TH, 8>(hr[v], n[v]);
+            unpack<TX, 8>(yr[v], d[v]);
+            if (gh) unpack<TH, 8>(gr[v], o[v]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                n[v][j] = (n[v][j] - m) * rs;  // columns behind the last have d = 0
+                n[v][j] = (n[v][j] - m) * rsn;  // columns behind the last have d = 0
                 if (in) {
                     gw[v][j] += d[v][j] * n[v][j];
                     gb[v][j] += d[v][j];
                 }
                 d[v][j] *= w[v][j];
-                s += d[v][j];
-                sn += d[v][j] * n[v][j];
+                s.x += d[v][j];
+                s.y += d[v][j] * n[v][j];
+                if (!gh) o[v][j] = 0.0f;
             }
-        s = over_row<TPR>(s, plus, red, 0) / (float)width;
-        sn = over_row<TPR>(sn, plus, red, 1) / (float)width;
+        }
+        if constexpr (NV == 1)  // while the sums are exchanged
+            if (r0 + stride < rows) fetch_row(r0 + stride);
+        over_row_two<TPR>(s, red, turn);
+        const float s1 = s.x / (float)width, sn = s.y / (float)width;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int c = 8 * (v * TPR + sub);
-            float o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = rs * (d[v][j] - s - n[v][j] * sn);
-            if (gh) {
-                float e[8];
-                load8<TH>(gh + at, c, width, e);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] += e[j];
-            }
-            if (in) store8<TH>(gx + at, c, width, o);
+            for (int j = 0; j < 8; ++j) o[v][j] += rsn * (d[v][j] - s1 - n[v][j] * sn);
+            if (in) store<TH, 8>(gx + row * width, 8 * (v * TPR + sub), width, o[v]);
         }
+        turn ^= 1;
     }
     float* to = part + 2LL * blockIdx.x * width;
     if constexpr (RPW > 1) {
@@ -170,10 +200,10 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = (float)gw[v][j];
-            store8<F32>(to, 8 * (v * TPR + sub), width, x);
+            store<F32, 8>(to, 8 * (v * TPR + sub), width, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = (float)gb[v][j];
-            store8<F32>(to + width, 8 * (v * TPR + sub), width, x);
+            store<F32, 8>(to + width, 8 * (v * TPR + sub), width, x);
         }
     }
 }
@@ -205,7 +235,8 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sums_kernel(const f
 // Workgroups of the backward, each with two rows of partial sums.
 inline long long parts_of(long long rows, long long width) {
     const long long need = (rows + rows_at_once(width) - 1) / rows_at_once(width);
-    return std::min(need, width <= 2048 ? 1024LL : 512LL);
+    // 32-bit sums, beyond 8192 columns, are over 16 rows at most
+    return std::max(std::min(need, width <= 2048 ? 1024LL : 512LL), width <= 8192 ? 0 : (rows + 15) / 16);
 }
 
 }  // namespace

@@ -311,7 +311,7 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
             u[i] = step[i] * xv[i];
             all += step[i];
             const float zv = value_of<TY>(zr[i]);
-            gate[i] = z ? zv * sigmoid_of(zv) : 1.0f;
+            gate[i] = z ? zv * gate_of<TY>(zv) : 1.0f;
         }
         fetch(left - BT);  // while this block is worked on
         all += quad_perm<0xB1>(all);
@@ -661,7 +661,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
                         all += step[i];
                         gv[i] = in && here ? value_of<TY>(gr[i]) : 0.0f;
                         zv[i] = value_of<TY>(zr[i]);
-                        sig[i] = gated ? sigmoid_of(zv[i]) : 1.0f;
+                        sig[i] = gated ? gate_of<TY>(zv[i]) : 1.0f;
                         gp[i] = gated ? gv[i] * (zv[i] * sig[i]) : gv[i];
                     }
                     float h0[F];
@@ -1071,7 +1071,7 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
             if (lane >> 4 == i) sum = mine;
         }
         float out = fmaf(skip, r.x, sum);
-        if (z) out *= r.z * sigmoid_of(r.z);
+        if (z) out *= r.z * gate_of<TY>(r.z);
         if (own) y[(long long)row * a.channels + at] = TY::store(out);
         if (!slots) break;
         int next = rows;

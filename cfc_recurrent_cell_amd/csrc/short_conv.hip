@@ -20,64 +20,71 @@
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kLaneCh = 8, kWaveCh = 64 * kLaneCh;
 constexpr int kTile = 16;      // tokens of a wave, forward
-constexpr int kAhead = 4;      // rows that are loaded at once, while as many are worked on
 constexpr int kGradTile = 64;  // tokens of a wave, backward: a row of partial sums each
+constexpr int kAhead = 4;      // rows that are loaded at once, while as many are worked on
+// Channels of a lane: 16 bytes of a 16-bit type forward; half of them backward, where a
+// channel takes twice the registers.
+constexpr int kForward = 8, kBackward = 4;
 
 struct Conv {
     Sequences q;
     int channels, silu, clear;
     long long xt, gt;
 };
+inline __host__ __device__ int parts_of(int channels, int v) { return (channels + 64 * v - 1) / (64 * v); }
 
 // The channels' weights as w[tap][channel], zero behind the last channel.
-template <class TY, int W>
-__device__ __forceinline__ void load_weights(const typename TY::S* weight, int c, int channels, float (&w)[W][8]) {
-    float f[W][8];
+template <class TY, int W, int V>
+__device__ __forceinline__ void load_weights(const typename TY::S* weight, int c, int channels, float (&w)[W][V]) {
+    float f[W][V];
 #pragma unroll
-    for (int i = 0; i < W; ++i) load8<TY>(weight, c * W + 8 * i, channels * W, f[i]);
+    for (int i = 0; i < W; ++i) load<TY, V>(weight, c * W + V * i, channels * W, f[i]);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[j][e] = f[(e * W + j) / 8][(e * W + j) % 8];
+        for (int e = 0; e < V; ++e) w[j][e] = f[(e * W + j) / V][(e * W + j) % V];
+}
+template <class TY, int V>
+__device__ __forceinline__ void load_or_zero(const typename TY::S* row, int c, int channels, float (&x)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) x[e] = 0.0f;
+    if (row) load<TY, V>(row, c, channels, x);
 }
 
 // The width - 1 inputs before row t of the sequence s that begins at `first`: its own rows,
 // or its initial state's.
-template <class TY, int W>
+template <class TY, int W, int V>
 __device__ __forceinline__ void load_window(const Conv& a, const typename TY::S* x, const typename TY::S* initial, int s,
-                                            int first, int t, int c, float (&win)[W - 1][8]) {
+                                            int first, int t, int c, float (&win)[W - 1][V]) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
         const int row = t - (W - 1) + j;
+        const typename TY::S* from = nullptr;
         if (row >= first)
-            load8<TY>(x + row * a.xt, c, a.channels, win[j]);
+            from = x + row * a.xt;
         else if (initial)
-            load8<TY>(initial + ((long long)s * (W - 1) + min(max(row - first + W - 1, 0), W - 2)) * a.channels, c,
-                      a.channels, win[j]);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) win[j][e] = 0.0f;
+            from = initial + ((long long)s * (W - 1) + min(max(row - first + W - 1, 0), W - 2)) * a.channels;
+        load_or_zero<TY, V>(from, c, a.channels, win[j]);
     }
 }
 
 // p of the next token, whose input is `now`.
-template <int W>
-__device__ __forceinline__ void apply(const float (&w)[W][8], const float (&b)[8], const float (&win)[W - 1][8],
-                                      const float (&now)[8], float (&p)[8]) {
+template <int W, int V>
+__device__ __forceinline__ void apply(const float (&w)[W][V], const float (&b)[V], const float (&win)[W - 1][V],
+                                      const float (&now)[V], float (&p)[V]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < V; ++e) {
         p[e] = b[e];
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) p[e] += w[j][e] * win[j][e];
         p[e] += w[W - 1][e] * now[e];
     }
 }
-template <int W>
-__device__ __forceinline__ void shift(float (&win)[W - 1][8], const float (&now)[8]) {
+template <int W, int V>
+__device__ __forceinline__ void shift(float (&win)[W - 1][V], const float (&now)[V]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < V; ++e) {
 #pragma unroll
         for (int j = 0; j + 1 < W - 1; ++j) win[j][e] = win[j + 1][e];
         win[W - 2][e] = now[e];
@@ -93,41 +100,41 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(Conv a, long long begin,
                                                         const typename TY::S* __restrict__ bias,
                                                         const typename TY::S* initial, typename TY::S* __restrict__ y,
                                                         typename TY::S* final) {
-    const long long wave = begin + (long long)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int V = kForward;
+    const long long block = on_die(blockIdx.x, (end_wave - begin + kWaves - 1) / kWaves);
+    const long long wave = begin + block * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= end_wave) return;
-    const int parts = (a.channels + kWaveCh - 1) / kWaveCh;
-    const int c = (int)(wave % parts) * kWaveCh + (threadIdx.x & 63) * kLaneCh;
+    const int parts = parts_of(a.channels, V);
+    const int c = (int)(wave % parts) * 64 * V + (threadIdx.x & 63) * V;
     const long long at = wave / parts;
+    int first, end;
     if (at >= tiles) {
         const int s = (int)(at - tiles);
-        int first, end;
         span_of(a.q, s, first, end);
-        float win[W - 1][8];
-        load_window<TY, W>(a, x, initial, s, first, end, c, win);
+        float win[W - 1][V];
+        load_window<TY, W, V>(a, x, initial, s, first, end, c, win);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            store8<TY>(final + ((long long)s * (W - 1) + j) * a.channels, c, a.channels, win[j]);
+            store<TY, V>(final + ((long long)s * (W - 1) + j) * a.channels, c, a.channels, win[j]);
         return;
     }
     const int t0 = (int)at * kTile, n = min(kTile, a.q.n_tokens - t0);
-    int s = sequence_of(a.q, t0), first, end;
+    int s = sequence_of(a.q, t0);
     span_of(a.q, s, first, end);
-    Eight<TY> rows[2][kAhead];
-    auto fetch = [&](Eight<TY>(&to)[kAhead], int i0) {
+    Packed<TY, V> rows[2][kAhead];
+    auto ahead = [&](Packed<TY, V>(&to)[kAhead], int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (i0 + i < n) to[i] = fetch8<TY>(x + (t0 + i0 + i) * a.xt, c, a.channels);
+            if (i0 + i < n) to[i] = fetch<TY, V>(x + (t0 + i0 + i) * a.xt, c, a.channels);
     };
-    fetch(rows[0], 0);
-    fetch(rows[1], kAhead);
-    float w[W][8], b[8], win[W - 1][8];
-    load_weights<TY, W>(weight, c, a.channels, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = 0.0f;
-    if (bias) load8<TY>(bias, c, a.channels, b);
+    ahead(rows[0], 0);
+    ahead(rows[1], kAhead);
+    float w[W][V], b[V], win[W - 1][V];
+    load_weights<TY, W, V>(weight, c, a.channels, w);
+    load_or_zero<TY, V>(bias, c, a.channels, b);
     bool live = t0 >= first && t0 < end;  // or behind the last sequence
-    if (live) load_window<TY, W>(a, x, initial, s, first, t0, c, win);
-    auto some = [&](Eight<TY>(&from)[kAhead], int i0) {
+    if (live) load_window<TY, W, V>(a, x, initial, s, first, t0, c, win);
+    auto some = [&](Packed<TY, V>(&from)[kAhead], int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int t = t0 + i0 + i;
@@ -135,43 +142,44 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(Conv a, long long begin,
                 s = sequence_of(a.q, t);
                 span_of(a.q, s, first, end);
                 live = t >= first && t < end;
-                if (live) load_window<TY, W>(a, x, initial, s, first, t, c, win);
+                if (live) load_window<TY, W, V>(a, x, initial, s, first, t, c, win);
             }
             if (i0 + i < n && live) {
-                float now[8], p[8];
-                unpack8<TY>(from[i], now);
-                apply<W>(w, b, win, now, p);
-                shift<W>(win, now);
+                float now[V], p[V];
+                unpack<TY, V>(from[i], now);
+                apply<W, V>(w, b, win, now, p);
+                shift<W, V>(win, now);
                 if (a.silu) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] *= sigmoid_of(p[e]);
+                    for (int e = 0; e < V; ++e) p[e] *= gate_of<TY>(p[e]);
                 }
-                store8<TY>(y + (long long)t * a.channels, c, a.channels, p);
+                store<TY, V>(y + (long long)t * a.channels, c, a.channels, p);
             } else if (i0 + i < n && a.clear) {
-                const float none[8] = {};
-                store8<TY>(y + (long long)t * a.channels, c, a.channels, none);
+                const float none[V] = {};
+                store<TY, V>(y + (long long)t * a.channels, c, a.channels, none);
             }
         }
     };
     for (int i = 0; i < kTile; i += 2 * kAhead) {
         some(rows[0], i);
-        fetch(rows[0], i + 2 * kAhead);
+        ahead(rows[0], i + 2 * kAhead);
         some(rows[1], i + kAhead);
-        fetch(rows[1], i + 3 * kAhead);
+        ahead(rows[1], i + 3 * kAhead);
     }
 }
 
 // grad_p = grad_y * y'(p)
-__device__ __forceinline__ void through(int silu, const float (&p)[8], float (&g)[8]) {
+template <class TY, int V>
+__device__ __forceinline__ void through(int silu, const float (&p)[V], float (&g)[V]) {
     if (!silu) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float sig = sigmoid_of(p[e]);
+    for (int e = 0; e < V; ++e) {
+        const float sig = gate_of<TY>(p[e]);
         g[e] *= sig * (1.0f + p[e] * (1.0f - sig));
     }
 }
 
-// A wave has kGradTile tokens and 512 channels.  It computes p again for its own tokens
+// A wave has kGradTile tokens and 256 channels.  It computes p again for its own tokens
 // and, since grad_x_t takes grad_p of the width - 1 tokens behind t, for as many behind
 // them; `next` holds what the tokens up to now give to the gradients of the last width - 1
 // inputs.  Behind the tiles' waves the initial states', a sequence each.
@@ -182,137 +190,150 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
     const typename TY::S* __restrict__ initial, const typename TY::S* __restrict__ gy,
     const typename TY::S* __restrict__ gfinal, typename TY::S* __restrict__ gx, typename TY::S* __restrict__ ginit,
     float* __restrict__ part) {
-    const long long wave = (long long)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int V = kBackward;
+    const long long block = on_die(blockIdx.x, (waves + kWaves - 1) / kWaves);
+    const long long wave = block * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= waves) return;
-    const int parts = (a.channels + kWaveCh - 1) / kWaveCh;
-    const int c = (int)(wave % parts) * kWaveCh + (threadIdx.x & 63) * kLaneCh;
+    const int parts = parts_of(a.channels, V);
+    const int c = (int)(wave % parts) * 64 * V + (threadIdx.x & 63) * V;
     const long long at = wave / parts;
-    float w[W][8], b[8], win[W - 1][8];
-    load_weights<TY, W>(weight, c, a.channels, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = 0.0f;
-    if (bias) load8<TY>(bias, c, a.channels, b);
-    // next[k] of the input k + 1 tokens back, after a token's step
-    float next[W][8];
-    auto clear = [&] {
-#pragma unroll
-        for (int k = 0; k < W; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) next[k][e] = 0.0f;
-    };
-    clear();
-    auto load_final = [&](int s, int row, float (&g)[8]) {
-        if (gfinal)
-            load8<TY>(gfinal + ((long long)s * (W - 1) + row) * a.channels, c, a.channels, g);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = 0.0f;
+    float w[W][V], b[V], win[W - 1][V];
+    auto final_row = [&](int s, int row) {
+        return gfinal ? gfinal + ((long long)s * (W - 1) + row) * a.channels : nullptr;
     };
     int first, end;
     if (at >= tiles) {
+        load_weights<TY, W, V>(weight, c, a.channels, w);
+        load_or_zero<TY, V>(bias, c, a.channels, b);
         const int s = (int)(at - tiles);
         span_of(a.q, s, first, end);
-        load_window<TY, W>(a, x, initial, s, first, first, c, win);
-        float g0[W - 1][8];
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g0[i][e] = 0.0f;
+        load_window<TY, W, V>(a, x, initial, s, first, first, c, win);
+        float g0[W - 1][V] = {};
 #pragma unroll
         for (int p = 0; p < W - 1; ++p) {
             if (first + p >= end) break;
-            float now[8], pre[8], g[8];
-            load8<TY>(x + (first + p) * a.xt, c, a.channels, now);
-            load8<TY>(gy + (first + p) * a.gt, c, a.channels, g);
-            apply<W>(w, b, win, now, pre);
-            shift<W>(win, now);
-            through(a.silu, pre, g);
+            float now[V], pre[V], g[V];
+            load<TY, V>(x + (first + p) * a.xt, c, a.channels, now);
+            load<TY, V>(gy + (first + p) * a.gt, c, a.channels, g);
+            apply<W, V>(w, b, win, now, pre);
+            shift<W, V>(win, now);
+            through<TY, V>(a.silu, pre, g);
             // kept input i is the tap i - p of place p
 #pragma unroll
             for (int i = p; i < W - 1; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g0[i][e] += w[i - p][e] * g[e];
+                for (int e = 0; e < V; ++e) g0[i][e] += w[i - p][e] * g[e];
         }
 #pragma unroll
         for (int i = 0; i < W - 1; ++i) {
             const int kept = i - (end - first);  // where it is in the final state
             if (kept >= 0) {
-                float f[8];
-                load_final(s, kept, f);
+                float f[V];
+                load_or_zero<TY, V>(final_row(s, kept), c, a.channels, f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) g0[i][e] += f[e];
+                for (int e = 0; e < V; ++e) g0[i][e] += f[e];
             }
-            store8<TY>(ginit + ((long long)s * (W - 1) + i) * a.channels, c, a.channels, g0[i]);
+            store<TY, V>(ginit + ((long long)s * (W - 1) + i) * a.channels, c, a.channels, g0[i]);
         }
         return;
     }
-    float sum[W + 1][8];
-#pragma unroll
-    for (int j = 0; j <= W; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[j][e] = 0.0f;
     const int t0 = (int)at * kGradTile, own = min(t0 + kGradTile, a.q.n_tokens);
+    const int all = min(own + W - 1, a.q.n_tokens) - t0;  // rows that it reads
     int s = sequence_of(a.q, t0);
     span_of(a.q, s, first, end);
-    int t = t0;
-    if (t0 >= first && t0 < end) {
-        load_window<TY, W>(a, x, initial, s, first, t0, c, win);
-        // the end of a sequence, or of the tokens whose gradients the tile's own need
-        while (true) {
-            const int until = min(end, own + W - 1);
-            for (; t < until; ++t) {
-                float now[8], p[8], g[8];
-                load8<TY>(x + t * a.xt, c, a.channels, now);
-                load8<TY>(gy + t * a.gt, c, a.channels, g);
-                apply<W>(w, b, win, now, p);
-                through(a.silu, p, g);
+    Packed<TY, V> xr[2][kAhead], gr[2][kAhead];
+    auto ahead = [&](int k, int i0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i0 + i < all) {
+                xr[k][i] = fetch<TY, V>(x + (t0 + i0 + i) * a.xt, c, a.channels);
+                gr[k][i] = fetch<TY, V>(gy + (t0 + i0 + i) * a.gt, c, a.channels);
+            }
+    };
+    ahead(0, 0);
+    ahead(1, kAhead);
+    load_weights<TY, W, V>(weight, c, a.channels, w);
+    load_or_zero<TY, V>(bias, c, a.channels, b);
+    bool live = t0 >= first && t0 < end;  // or behind the last sequence, or done
+    if (live) load_window<TY, W, V>(a, x, initial, s, first, t0, c, win);
+    float next[W - 1][V] = {};  // next[k] of the input k tokens back
+    float sum[W + 1][V] = {};
+    // the gradients of a sequence's last inputs, which its final state holds too
+    auto finish = [&] {
+#pragma unroll
+        for (int k = W - 2; k >= 0; --k) {
+            const int done = end - 1 - k;
+            if (done >= t0 && done >= first && done < own) {
+                float f[V];
+                load_or_zero<TY, V>(final_row(s, W - 2 - k), c, a.channels, f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) f[e] += next[k][e];
+                store<TY, V>(gx + (long long)done * a.channels, c, a.channels, f);
+            }
+        }
+    };
+    auto some = [&](int k, int i0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int t = t0 + i0 + i;
+            if (live && t >= end) {
+                finish();
+                live = t < own;
+                if (live) {
+                    s = sequence_of(a.q, t);
+                    span_of(a.q, s, first, end);
+                    live = t >= first && t < end;
+                }
+                if (live) {
+                    load_window<TY, W, V>(a, x, initial, s, first, t, c, win);
+#pragma unroll
+                    for (int q = 0; q < W - 1; ++q)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) next[q][e] = 0.0f;
+                }
+            }
+            if (live && i0 + i < all) {
+                float now[V], p[V], g[V];
+                unpack<TY, V>(xr[k][i], now);
+                unpack<TY, V>(gr[k][i], g);
+                apply<W, V>(w, b, win, now, p);
+                through<TY, V>(a.silu, p, g);
                 if (t < own) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                    for (int e = 0; e < V; ++e) {
 #pragma unroll
                         for (int j = 0; j < W - 1; ++j) sum[j][e] += g[e] * win[j][e];
                         sum[W - 1][e] += g[e] * now[e];
                         sum[W][e] += g[e];
                     }
                 }
-                shift<W>(win, now);
+                shift<W, V>(win, now);
                 // input t - k is the tap W - 1 - k of token t
+                float done[V];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < V; ++e) {
+                    done[e] = next[W - 2][e] + w[0][e] * g[e];
 #pragma unroll
-                    for (int k = W - 1; k > 0; --k) next[k][e] = next[k - 1][e] + w[W - 1 - k][e] * g[e];
+                    for (int q = W - 2; q > 0; --q) next[q][e] = next[q - 1][e] + w[W - 1 - q][e] * g[e];
                     next[0][e] = w[W - 1][e] * g[e];
                 }
-                const int done = t - (W - 1);
-                if (done >= t0 && done >= first) store8<TY>(gx + (long long)done * a.channels, c, a.channels, next[W - 1]);
+                const int which = t - (W - 1);
+                if (which >= t0 && which >= first) store<TY, V>(gx + (long long)which * a.channels, c, a.channels, done);
+            } else if (a.clear && t < own && !live) {
+                const float none[V] = {};
+                store<TY, V>(gx + (long long)t * a.channels, c, a.channels, none);
             }
-            if (until == end) {  // the sequence's last inputs, which its final state holds too
-#pragma unroll
-                for (int k = W - 2; k >= 0; --k) {
-                    const int done = end - 1 - k;
-                    if (done >= t0 && done >= first && done < own) {
-                        float f[8];
-                        load_final(s, W - 2 - k, f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] += next[k][e];
-                        store8<TY>(gx + (long long)done * a.channels, c, a.channels, f);
-                    }
-                }
-            }
-            if (t >= own) break;
-            s = sequence_of(a.q, t);
-            span_of(a.q, s, first, end);
-            if (t < first || t >= end) break;
-            clear();
-            load_window<TY, W>(a, x, initial, s, first, t, c, win);
         }
+    };
+    for (int i = 0; i < kGradTile + W - 1; i += 2 * kAhead) {
+        some(0, i);
+        ahead(0, i + 2 * kAhead);
+        some(1, i + kAhead);
+        ahead(1, i + 3 * kAhead);
     }
-    if (a.clear) {  // behind the last sequence
-        const float none[8] = {};
-        for (; t < own; ++t) store8<TY>(gx + (long long)t * a.channels, c, a.channels, none);
-    }
+    if (live && end <= t0 + all) finish();
 #pragma unroll
-    for (int j = 0; j <= W; ++j) store8<F32>(part + (at * (W + 1) + j) * a.channels, c, a.channels, sum[j]);
+    for (int j = 0; j <= W; ++j) store<F32, V>(part + (at * (W + 1) + j) * a.channels, c, a.channels, sum[j]);
 }
 
 // Columns of part [tiles, width + 1, channels] summed in 64 bits: the last of the width + 1
@@ -350,38 +371,37 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long w
                                                              const int* __restrict__ slots, typename TY::S* __restrict__ y) {
     const long long wave = (long long)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= waves) return;
-    const int parts = (a.channels + kWaveCh - 1) / kWaveCh, lane = threadIdx.x & 63;
-    const int c = (int)(wave % parts) * kWaveCh + lane * kLaneCh;
+    constexpr int V = kForward;
+    const int parts = parts_of(a.channels, V), lane = threadIdx.x & 63;
+    const int c = (int)(wave % parts) * 64 * V + lane * V;
     const int rows = a.q.n_tokens;
     int row = (int)(wave / parts), slot = row;
     if (slots) {
         slot = __builtin_amdgcn_readfirstlane(slots[row]);
         if (slot < 0 || slot >= pool) {
-            const float none[8] = {};
-            store8<TY>(y + (long long)row * a.channels, c, a.channels, none);
+            const float none[V] = {};
+            store<TY, V>(y + (long long)row * a.channels, c, a.channels, none);
             return;
         }
         for (int j = 0; j < row; j += 64)  // the first row of a slot takes all
             if (__ballot(j + lane < row && slots[min(j + lane, rows - 1)] == slot)) return;
     }
-    float w[W][8], b[8], win[W - 1][8];
-    load_weights<TY, W>(weight, c, a.channels, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = 0.0f;
-    if (bias) load8<TY>(bias, c, a.channels, b);
+    float w[W][V], b[V], win[W - 1][V];
+    load_weights<TY, W, V>(weight, c, a.channels, w);
+    load_or_zero<TY, V>(bias, c, a.channels, b);
     typename TY::S* state = states + (long long)slot * (W - 1) * a.channels;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load8<TY>(state + (long long)j * a.channels, c, a.channels, win[j]);
+    for (int j = 0; j < W - 1; ++j) load<TY, V>(state + (long long)j * a.channels, c, a.channels, win[j]);
     while (row < rows) {
-        float now[8], p[8];
-        load8<TY>(x + row * a.xt, c, a.channels, now);
-        apply<W>(w, b, win, now, p);
-        shift<W>(win, now);
+        float now[V], p[V];
+        load<TY, V>(x + row * a.xt, c, a.channels, now);
+        apply<W, V>(w, b, win, now, p);
+        shift<W, V>(win, now);
         if (a.silu) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] *= sigmoid_of(p[e]);
+            for (int e = 0; e < V; ++e) p[e] *= gate_of<TY>(p[e]);
         }
-        store8<TY>(y + (long long)row * a.channels, c, a.channels, p);
+        store<TY, V>(y + (long long)row * a.channels, c, a.channels, p);
         if (!slots) break;
         int next = rows;
         for (int j = row + 1; j < rows; j += 64) {
@@ -394,14 +414,13 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long w
         row = next;
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) store8<TY>(state + (long long)j * a.channels, c, a.channels, win[j]);
+    for (int j = 0; j < W - 1; ++j) store<TY, V>(state + (long long)j * a.channels, c, a.channels, win[j]);
 }
 
 // ---------------------------------------------------------- host helpers
 constexpr long long kMaxTokens = (1LL << 31) - (1LL << 16);
 constexpr long long kMaxGrid = (1LL << 32) / kThreads - 8;  // a grid has fewer than 2^32 work-items
 
-inline long long parts_of(const Conv& a) { return (a.channels + kWaveCh - 1) / kWaveCh; }
 inline long long blocks_of(long long waves) { return (waves + kWaves - 1) / kWaves; }
 
 int check_shape(const short_conv_shape_t* p, bool step, Conv* a) {
@@ -410,7 +429,7 @@ int check_shape(const short_conv_shape_t* p, bool step, Conv* a) {
     if (p->channels < 1 || p->width < 1 || p->x_stride < 0 || p->grad_y_stride < 0) return CFC_ERR_DIM;
     if (p->width < 2 || p->width > SHORT_CONV_MAX_WIDTH) return CFC_ERR_UNSUPPORTED;
     // a lane's first weight is at 4 times its channel
-    if (p->channels > INT_MAX / SHORT_CONV_MAX_WIDTH - kWaveCh || p->n_tokens > kMaxTokens) return CFC_ERR_UNSUPPORTED;
+    if (p->channels > INT_MAX / SHORT_CONV_MAX_WIDTH - 64 * kForward || p->n_tokens > kMaxTokens) return CFC_ERR_UNSUPPORTED;
     if (step) {
         if (p->n_tokens < 0) return CFC_ERR_DIM;
         a->q = Sequences{nullptr, (int)p->n_tokens, 1, (int)p->n_tokens};
@@ -422,8 +441,8 @@ int check_shape(const short_conv_shape_t* p, bool step, Conv* a) {
     a->clear = p->clear_rest && p->offsets;
     a->xt = p->x_stride;
     a->gt = p->grad_y_stride;
-    // (the forward's tiles are the most)
-    const long long most = ((long long)a->q.n_tokens / (step ? 1 : kTile) + 1 + a->q.n_seq) * parts_of(*a);
+    // (the forward's tiles and the backward's parts are the most)
+    const long long most = ((long long)a->q.n_tokens / (step ? 1 : kTile) + 1 + a->q.n_seq) * parts_of(a->channels, kBackward);
     return blocks_of(most) > kMaxGrid ? CFC_ERR_UNSUPPORTED : CFC_OK;
 }
 
@@ -478,11 +497,11 @@ extern "C" int short_conv_forward(const short_conv_shape_t* shape, const void* x
         using TY = decltype(ty);
         using S = typename TY::S;
         constexpr int W = decltype(width)::value;
-        const long long tiles = (a.q.n_tokens + kTile - 1) / kTile, parts = parts_of(a);
+        const long long tiles = (a.q.n_tokens + kTile - 1) / kTile, parts = parts_of(a.channels, kForward);
         const long long split = tiles * parts, all = (tiles + (final_state ? a.q.n_seq : 0)) * parts;
         auto go = [&](long long from, long long to) {
             if (from < to)
-                hipLaunchKernelGGL((conv_kernel<TY, W>), dim3((unsigned)blocks_of(to - from)), dim3(kThreads), 0, stream,
+                hipLaunchKernelGGL((conv_kernel<TY, W>), dim3(dealt(blocks_of(to - from))), dim3(kThreads), 0, stream,
                                    a, from, to, tiles, (const S*)x, (const S*)weight, (const S*)bias,
                                    (const S*)initial_state, (S*)y, (S*)final_state);
         };
@@ -534,11 +553,11 @@ extern "C" int short_conv_backward(const short_conv_shape_t* shape, const void* 
         using TY = decltype(ty);
         using S = typename TY::S;
         constexpr int W = decltype(width)::value;
-        const long long tiles = ((long long)a.q.n_tokens + kGradTile - 1) / kGradTile, parts = parts_of(a);
+        const long long tiles = ((long long)a.q.n_tokens + kGradTile - 1) / kGradTile, parts = parts_of(a.channels, kBackward);
         const long long waves = (tiles + (grad_initial_state ? a.q.n_seq : 0)) * parts;
         float* part = static_cast<float*>(workspace);
         if (waves)
-            hipLaunchKernelGGL((conv_backward_kernel<TY, W>), dim3((unsigned)blocks_of(waves)), dim3(kThreads), 0, stream,
+            hipLaunchKernelGGL((conv_backward_kernel<TY, W>), dim3(dealt(blocks_of(waves))), dim3(kThreads), 0, stream,
                                a, waves, tiles, (const S*)x, (const S*)weight, (const S*)bias, (const S*)initial_state,
                                (const S*)grad_y, (const S*)grad_final_state, (S*)grad_x, (S*)grad_initial_state, part);
         const long long columns = (long long)(W + 1) * a.channels;
@@ -568,7 +587,7 @@ extern "C" int short_conv_step(const short_conv_shape_t* shape, const void* x, c
         using TY = decltype(ty);
         using S = typename TY::S;
         constexpr int W = decltype(width)::value;
-        const long long waves = (long long)a.q.n_tokens * parts_of(a);
+        const long long waves = (long long)a.q.n_tokens * parts_of(a.channels, kForward);
         hipLaunchKernelGGL((conv_step_kernel<TY, W>), dim3((unsigned)blocks_of(waves)), dim3(kThreads), 0, stream, a,
                            waves, (const S*)x, (const S*)weight, (const S*)bias, (S*)states, pool, slots, (S*)y);
         return launch_status();
