@@ -41,25 +41,30 @@ struct Packed {
     uint32_t w[V * sizeof(typename TY::S) / 4];
 };
 
-// Columns c ... c + V - 1 of a row; zero from `width` on.
-template <class TY, int V>
+// Columns c ... c + V - 1 of a row, zero from `width` on, in two steps: `fetch` loads them,
+// `unpack` turns them to 32-bit floats.  TAIL: the width need be no multiple of V; where a row
+// ends among the columns its last V are loaded, so that no lane's load waits for another's,
+// and moved to where they belong when they are unpacked.
+template <class TY, int V, bool TAIL>
 __device__ __forceinline__ Packed<TY, V> fetch(const typename TY::S* row, int c, int width) {
+    constexpr int N = V * sizeof(typename TY::S) / 4;
     Packed<TY, V> e;
-    if (c + V <= width) {
-        if constexpr (sizeof(e) == 8) {
-            const u32x2_any a = *reinterpret_cast<const u32x2_any*>(row + c);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e.w[i] = 0;
+    if (TAIL ? width >= V : c < width) {
+        const char* from = reinterpret_cast<const char*>(row + (TAIL ? min(c, width - V) : c));
+        if constexpr (N == 2) {
+            const u32x2_any a = *reinterpret_cast<const u32x2_any*>(from);
             e.w[0] = a[0], e.w[1] = a[1];
         } else {
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(e) / 16; ++i) {
-                const u32x4_any a = *reinterpret_cast<const u32x4_any*>(reinterpret_cast<const char*>(row + c) + 16 * i);
+            for (int i = 0; i < N / 4; ++i) {
+                const u32x4_any a = *reinterpret_cast<const u32x4_any*>(from + 16 * i);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) e.w[4 * i + j] = a[j];
             }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(e) / 4; ++i) e.w[i] = 0;
+    } else if constexpr (TAIL) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (c + j < width) {
@@ -71,8 +76,8 @@ __device__ __forceinline__ Packed<TY, V> fetch(const typename TY::S* row, int c,
     }
     return e;
 }
-template <class TY, int V>
-__device__ __forceinline__ void unpack(const Packed<TY, V>& e, float (&x)[V]) {
+template <class TY, int V, bool TAIL>
+__device__ __forceinline__ void unpack(const Packed<TY, V>& e, int c, int width, float (&x)[V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if constexpr (sizeof(typename TY::S) == 4)
@@ -81,14 +86,25 @@ __device__ __forceinline__ void unpack(const Packed<TY, V>& e, float (&x)[V]) {
             x[j] = TY::load(__builtin_bit_cast(typename TY::S,
                                                (uint16_t)(j & 1 ? e.w[j >> 1] >> 16 : e.w[j >> 1] & 0xffff)));
     }
+    const int over = TAIL && width >= V ? c + V - width : 0;  // columns that the row has not
+    if (over > 0) {
+#pragma unroll
+        for (int by = V / 2; by > 0; by >>= 1)
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = over & by ? (j + by < V ? x[j + by] : 0.0f) : x[j];
+        if (over >= V) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = 0.0f;
+        }
+    }
 }
-template <class TY, int V>
+template <class TY, int V, bool TAIL>
 __device__ __forceinline__ void load(const typename TY::S* row, int c, int width, float (&x)[V]) {
-    unpack<TY, V>(fetch<TY, V>(row, c, width), x);
+    unpack<TY, V, TAIL>(fetch<TY, V, TAIL>(row, c, width), c, width, x);
 }
-template <class TY, int V>
+template <class TY, int V, bool TAIL>
 __device__ __forceinline__ void store(typename TY::S* row, int c, int width, const float (&x)[V]) {
-    if (c + V <= width) {
+    if (TAIL ? c + V <= width : c < width) {
         Packed<TY, V> e;
         if constexpr (sizeof(typename TY::S) == 4) {
 #pragma unroll
@@ -107,7 +123,7 @@ __device__ __forceinline__ void store(typename TY::S* row, int c, int width, con
                 *reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(row + c) + 16 * i) =
                     u32x4_any{e.w[4 * i], e.w[4 * i + 1], e.w[4 * i + 2], e.w[4 * i + 3]};
         }
-    } else {
+    } else if constexpr (TAIL) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
             if (c + j < width) row[c + j] = TY::store(x[j]);

@@ -53,7 +53,7 @@ __device__ __forceinline__ int tensor_of(const Batch& b, unsigned chunk) {
     return lo;
 }
 
-// Calls f(first element, elements as they lie in memory, how many of the eight there are) for
+// Calls f(first element, eight as they lie in memory, whether some are missing, how many there are) for
 // a thread's eights of [at, end); kUnroll of them are loaded at once.
 constexpr int kUnroll = 4;
 template <class TY, class F>
@@ -63,20 +63,20 @@ __device__ __forceinline__ void each_eight(const void* grad, long long at, long 
     for (; i + (kUnroll - 1) * kStep + 8 <= end; i += kUnroll * kStep) {
         Packed<TY, 8> e[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) e[k] = fetch<TY, 8>(p + i + k * kStep, 0, 8);
+        for (int k = 0; k < kUnroll; ++k) e[k] = fetch<TY, 8, false>(p + i + k * kStep, 0, 8);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) f(i + k * kStep, e[k], 8);
+        for (int k = 0; k < kUnroll; ++k) f(i + k * kStep, e[k], std::false_type{}, 8);
     }
     for (; i < end; i += kStep) {
         const int n = (int)min(end - i, 8LL);
-        f(i, fetch<TY, 8>(p + i, 0, n), n);
+        f(i, fetch<TY, 8, true>(p + i, 0, n), std::true_type{}, n);
     }
 }
 template <class TY>
 __device__ __forceinline__ void squares(const void* grad, long long at, long long end, double& s0, double& s1) {
-    each_eight<TY>(grad, at, end, [&](long long, const Packed<TY, 8>& e, int) {
+    each_eight<TY>(grad, at, end, [&](long long, const Packed<TY, 8>& e, auto tail, int n) {
         float x[8];
-        unpack<TY, 8>(e, x);
+        unpack<TY, 8, decltype(tail)::value>(e, 0, n, x);
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             const double a = x[j], b = x[j + 1];
@@ -136,12 +136,12 @@ __global__ __launch_bounds__(kThreads) void total_kernel(const double* __restric
 template <class TY>
 __device__ __forceinline__ void scale(const void* grad, void* out, long long at, long long end, float factor) {
     auto* o = static_cast<typename TY::S*>(out);
-    each_eight<TY>(grad, at, end, [&](long long i, const Packed<TY, 8>& e, int n) {
+    each_eight<TY>(grad, at, end, [&](long long i, const Packed<TY, 8>& e, auto tail, int n) {
         float x[8];
-        unpack<TY, 8>(e, x);
+        unpack<TY, 8, decltype(tail)::value>(e, 0, n, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] *= factor;
-        store<TY, 8>(o + i, 0, n, x);
+        store<TY, 8, decltype(tail)::value>(o + i, 0, n, x);
     });
 }
 

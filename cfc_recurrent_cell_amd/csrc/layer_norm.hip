@@ -36,7 +36,7 @@ __device__ __forceinline__ void over_row_two(float2& s, float (*red)[2][16], int
     }
 }
 
-template <class TX, class TH, int TPR, int NV>
+template <class TX, class TH, int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
     long long rows, int width, const typename TX::S* x, const typename TH::S* residual,
     const typename TX::S* __restrict__ weight, const typename TX::S* __restrict__ bias, float eps,
@@ -47,27 +47,34 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
     float w[NV][8], b[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        load<TX, 8>(weight, 8 * (v * TPR + sub), width, w[v]);
+        load<TX, 8, TAIL>(weight, 8 * (v * TPR + sub), width, w[v]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
-        if (bias) load<TX, 8>(bias, 8 * (v * TPR + sub), width, b[v]);
+        if (bias) load<TX, 8, TAIL>(bias, 8 * (v * TPR + sub), width, b[v]);
     }
     for (long long r0 = (long long)blockIdx.x * RPW; r0 < rows; r0 += (long long)gridDim.x * RPW) {
         const long long row = r0 + threadIdx.x / TPR;
         const bool in = row < rows;  // lanes of a row behind the last compute and write nothing
         const long long at = (in ? row : rows - 1) * width;
         float a[NV][8];
+        Packed<TX, 8> xr[NV];
+        Packed<TH, 8> rr[NV];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) load<TX, 8>(x + at, 8 * (v * TPR + sub), width, a[v]);
+        for (int v = 0; v < NV; ++v) {
+            xr[v] = fetch<TX, 8, TAIL>(x + at, 8 * (v * TPR + sub), width);
+            if (residual) rr[v] = fetch<TH, 8, TAIL>(residual + at, 8 * (v * TPR + sub), width);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) unpack<TX, 8, TAIL>(xr[v], 8 * (v * TPR + sub), width, a[v]);
         if (residual) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 float e[8];
                 const int c = 8 * (v * TPR + sub);
-                load<TH, 8>(residual + at, c, width, e);
+                unpack<TH, 8, TAIL>(rr[v], c, width, e);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) a[v][j] = TH::load(TH::store(a[v][j] + e[j]));
-                if (h && in) store<TH, 8>(h + at, c, width, a[v]);
+                if (h && in) store<TH, 8, TAIL>(h + at, c, width, a[v]);
             }
         }
         float s = 0.0f;
@@ -94,7 +101,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
             for (int v = 0; v < NV; ++v) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) a[v][j] = a[v][j] * rs * w[v][j] + b[v][j];
-                store<TX, 8>(y + at, 8 * (v * TPR + sub), width, a[v]);
+                store<TX, 8, TAIL>(y + at, 8 * (v * TPR + sub), width, a[v]);
             }
         }
     }
@@ -104,7 +111,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
 // The weight's and the bias's terms are summed over the workgroup's rows in registers,
 // in 64 bits, then over its row slots through LDS, into part[2 * blockIdx.x] and the
 // row behind it; column_sums_kernel sums those.
-template <class TX, class TH, int TPR, int NV>
+template <class TX, class TH, int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
     long long rows, int width, const typename TX::S* __restrict__ gy, const typename TH::S* __restrict__ h,
     const typename TX::S* __restrict__ weight, const float* __restrict__ mean, const float* __restrict__ rstd,
@@ -118,7 +125,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
     Sum gw[NV][8], gb[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        load<TX, 8>(weight, 8 * (v * TPR + sub), width, w[v]);
+        load<TX, 8, TAIL>(weight, 8 * (v * TPR + sub), width, w[v]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) gw[v][j] = gb[v][j] = 0.0;
     }
@@ -130,9 +137,9 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = 8 * (v * TPR + sub);
-            hr[v] = fetch<TH, 8>(h + row * width, c, width);
-            yr[v] = fetch<TX, 8>(gy + row * width, c, width);
-            if (gh) gr[v] = fetch<TH, 8>(gh + row * width, c, width);
+            hr[v] = fetch<TH, 8, TAIL>(h + row * width, c, width);
+            yr[v] = fetch<TX, 8, TAIL>(gy + row * width, c, width);
+            if (gh) gr[v] = fetch<TH, 8, TAIL>(gh + row * width, c, width);
         }
         rs = rstd[row], m = mean[row];
     };
@@ -148,9 +155,10 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
         float2 s = {0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            unpack<TH, 8>(hr[v], n[v]);
-            unpack<TX, 8>(yr[v], d[v]);
-            if (gh) unpack<TH, 8>(gr[v], o[v]);
+            const int c = 8 * (v * TPR + sub);
+            unpack<TH, 8, TAIL>(hr[v], c, width, n[v]);
+            unpack<TX, 8, TAIL>(yr[v], c, width, d[v]);
+            if (gh) unpack<TH, 8, TAIL>(gr[v], c, width, o[v]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 n[v][j] = (n[v][j] - m) * rsn;  // columns behind the last have d = 0
@@ -172,7 +180,7 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
         for (int v = 0; v < NV; ++v) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[v][j] += rsn * (d[v][j] - s1 - n[v][j] * sn);
-            if (in) store<TH, 8>(gx + row * width, 8 * (v * TPR + sub), width, o[v]);
+            if (in) store<TH, 8, TAIL>(gx + row * width, 8 * (v * TPR + sub), width, o[v]);
         }
         turn ^= 1;
     }
@@ -200,10 +208,10 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
             float x[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = (float)gw[v][j];
-            store<F32, 8>(to, 8 * (v * TPR + sub), width, x);
+            store<F32, 8, TAIL>(to, 8 * (v * TPR + sub), width, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[j] = (float)gb[v][j];
-            store<F32, 8>(to + width, 8 * (v * TPR + sub), width, x);
+            store<F32, 8, TAIL>(to + width, 8 * (v * TPR + sub), width, x);
         }
     }
 }
@@ -239,6 +247,13 @@ inline long long parts_of(long long rows, long long width) {
     return std::max(std::min(need, width <= 2048 ? 1024LL : 512LL), width <= 8192 ? 0 : (rows + 15) / 16);
 }
 
+template <class F>
+int with_rows(long long width, F f) {
+    return with_tiling(width, [&](auto tpr, auto nv) {
+        return width % 8 ? f(tpr, nv, std::true_type{}) : f(tpr, nv, std::false_type{});
+    });
+}
+
 }  // namespace
 
 // ================================================================ C ABI
@@ -262,13 +277,14 @@ extern "C" int layer_norm_forward(int type, int stream_type, long long rows, lon
                          over_x ? Range{0, 0} : rx, over_r ? Range{0, 0} : rr};
     if (!outputs_disjoint(outs, 4, ins, 4)) return CFC_ERR_OVERLAP;
     return with_types(type, stream_type, [&](auto tx, auto th) {
-        return with_tiling(width, [&](auto tpr, auto nv) {
+        return with_rows(width, [&](auto tpr, auto nv, auto tail) {
             using TX = decltype(tx);
             using TH = decltype(th);
             constexpr int T = decltype(tpr)::value, V = decltype(nv)::value;
+            constexpr bool TAIL = decltype(tail)::value;
             const long long need = (rows + rows_at_once(width) - 1) / rows_at_once(width);
             const unsigned grid = (unsigned)std::min(need, (long long)256 * 8 * 256 / threads_of(T));
-            hipLaunchKernelGGL((layer_norm_kernel<TX, TH, T, V>), dim3(grid), dim3(threads_of(T)), 0, stream, rows,
+            hipLaunchKernelGGL((layer_norm_kernel<TX, TH, T, V, TAIL>), dim3(grid), dim3(threads_of(T)), 0, stream, rows,
                                (int)width, (const typename TX::S*)x, (const typename TH::S*)residual,
                                (const typename TX::S*)weight, (const typename TX::S*)bias, eps, (typename TX::S*)y,
                                (typename TH::S*)h, mean, rstd);
@@ -310,11 +326,12 @@ extern "C" int layer_norm_backward(int type, int stream_type, long long rows, lo
     float* part = static_cast<float*>(workspace);
     if (rows) {
         const int e = with_types(type, stream_type, [&](auto tx, auto th) {
-            return with_tiling(width, [&](auto tpr, auto nv) {
+            return with_rows(width, [&](auto tpr, auto nv, auto tail) {
                 using TX = decltype(tx);
                 using TH = decltype(th);
                 constexpr int T = decltype(tpr)::value, V = decltype(nv)::value;
-                hipLaunchKernelGGL((layer_norm_backward_kernel<TX, TH, T, V>), dim3((unsigned)parts),
+            constexpr bool TAIL = decltype(tail)::value;
+                hipLaunchKernelGGL((layer_norm_backward_kernel<TX, TH, T, V, TAIL>), dim3((unsigned)parts),
                                    dim3(threads_of(T)), 0, stream, rows, (int)width, (const typename TX::S*)grad_y,
                                    (const typename TH::S*)h, (const typename TX::S*)weight, mean, rstd,
                                    (const typename TH::S*)grad_h, (typename TH::S*)grad_x, part);

@@ -2,8 +2,8 @@
 // include/short_conv.h).
 //
 // Memory is the bound: each input is read once and each output written once, so a wave
-// has a tile of tokens and 8 channels a lane (16 bytes of a 16-bit type), all of its rows'
-// loads in flight at once, and the last width - 1 inputs in registers as it goes from token
+// has a tile of tokens and 4 channels a lane, four to eight rows' loads in flight at once,
+// and the last width - 1 inputs in registers as it goes from token
 // to token.  Rows that a tile shares with the one before are read twice, mostly from the
 // cache.
 #include <hip/hip_runtime.h>
@@ -20,41 +20,42 @@
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kTile = 16;      // tokens of a wave, forward
-constexpr int kGradTile = 64;  // tokens of a wave, backward: a row of partial sums each
-constexpr int kAhead = 4;      // rows that are loaded at once, while as many are worked on
-// Channels of a lane: 16 bytes of a 16-bit type forward; half of them backward, where a
-// channel takes twice the registers.
-constexpr int kForward = 8, kBackward = 4;
+constexpr int kTile = 16;  // tokens of a wave, forward
+constexpr int kAhead = 4;  // rows that are loaded at once, while as many are worked on
+// Channels of a lane, 8 bytes of a 16-bit type.  Eight of them take twice the registers, so
+// half the waves: the forward of 16 packed prompts of 8192 channels 55 us instead of 45, the
+// gradients of 4 x 2048 x 4096 75 instead of 70.
+constexpr int kLane = 4;
 
 struct Conv {
     Sequences q;
     int channels, silu, clear;
+    int grad_tile;  // tokens of a wave, backward: a row of partial sums each
     long long xt, gt;
 };
-inline __host__ __device__ int parts_of(int channels, int v) { return (channels + 64 * v - 1) / (64 * v); }
+inline __host__ __device__ int parts_of(const Conv& a) { return (a.channels + 64 * kLane - 1) / (64 * kLane); }
 
 // The channels' weights as w[tap][channel], zero behind the last channel.
-template <class TY, int W, int V>
+template <class TY, int W, int V, bool TAIL>
 __device__ __forceinline__ void load_weights(const typename TY::S* weight, int c, int channels, float (&w)[W][V]) {
     float f[W][V];
 #pragma unroll
-    for (int i = 0; i < W; ++i) load<TY, V>(weight, c * W + V * i, channels * W, f[i]);
+    for (int i = 0; i < W; ++i) load<TY, V, TAIL>(weight, c * W + V * i, channels * W, f[i]);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
         for (int e = 0; e < V; ++e) w[j][e] = f[(e * W + j) / V][(e * W + j) % V];
 }
-template <class TY, int V>
+template <class TY, int V, bool TAIL>
 __device__ __forceinline__ void load_or_zero(const typename TY::S* row, int c, int channels, float (&x)[V]) {
 #pragma unroll
     for (int e = 0; e < V; ++e) x[e] = 0.0f;
-    if (row) load<TY, V>(row, c, channels, x);
+    if (row) load<TY, V, TAIL>(row, c, channels, x);
 }
 
 // The width - 1 inputs before row t of the sequence s that begins at `first`: its own rows,
 // or its initial state's.
-template <class TY, int W, int V>
+template <class TY, int W, int V, bool TAIL>
 __device__ __forceinline__ void load_window(const Conv& a, const typename TY::S* x, const typename TY::S* initial, int s,
                                             int first, int t, int c, float (&win)[W - 1][V]) {
 #pragma unroll
@@ -65,7 +66,7 @@ __device__ __forceinline__ void load_window(const Conv& a, const typename TY::S*
             from = x + row * a.xt;
         else if (initial)
             from = initial + ((long long)s * (W - 1) + min(max(row - first + W - 1, 0), W - 2)) * a.channels;
-        load_or_zero<TY, V>(from, c, a.channels, win[j]);
+        load_or_zero<TY, V, TAIL>(from, c, a.channels, win[j]);
     }
 }
 
@@ -92,19 +93,19 @@ __device__ __forceinline__ void shift(float (&win)[W - 1][V], const float (&now)
 }
 
 // Waves `begin` ... of the tiles' waves and, behind them, of the final states', a sequence
-// and 512 channels each.
-template <class TY, int W>
+// and 256 channels each.
+template <class TY, int W, bool TAIL>
 __global__ __launch_bounds__(kThreads) void conv_kernel(Conv a, long long begin, long long end_wave, long long tiles,
                                                         const typename TY::S* __restrict__ x,
                                                         const typename TY::S* __restrict__ weight,
                                                         const typename TY::S* __restrict__ bias,
                                                         const typename TY::S* initial, typename TY::S* __restrict__ y,
                                                         typename TY::S* final) {
-    constexpr int V = kForward;
+    constexpr int V = kLane;
     const long long block = on_die(blockIdx.x, (end_wave - begin + kWaves - 1) / kWaves);
     const long long wave = begin + block * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= end_wave) return;
-    const int parts = parts_of(a.channels, V);
+    const int parts = parts_of(a);
     const int c = (int)(wave % parts) * 64 * V + (threadIdx.x & 63) * V;
     const long long at = wave / parts;
     int first, end;
@@ -112,10 +113,10 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(Conv a, long long begin,
         const int s = (int)(at - tiles);
         span_of(a.q, s, first, end);
         float win[W - 1][V];
-        load_window<TY, W, V>(a, x, initial, s, first, end, c, win);
+        load_window<TY, W, V, TAIL>(a, x, initial, s, first, end, c, win);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j)
-            store<TY, V>(final + ((long long)s * (W - 1) + j) * a.channels, c, a.channels, win[j]);
+            store<TY, V, TAIL>(final + ((long long)s * (W - 1) + j) * a.channels, c, a.channels, win[j]);
         return;
     }
     const int t0 = (int)at * kTile, n = min(kTile, a.q.n_tokens - t0);
@@ -125,15 +126,15 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(Conv a, long long begin,
     auto ahead = [&](Packed<TY, V>(&to)[kAhead], int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (i0 + i < n) to[i] = fetch<TY, V>(x + (t0 + i0 + i) * a.xt, c, a.channels);
+            if (i0 + i < n) to[i] = fetch<TY, V, TAIL>(x + (t0 + i0 + i) * a.xt, c, a.channels);
     };
     ahead(rows[0], 0);
     ahead(rows[1], kAhead);
     float w[W][V], b[V], win[W - 1][V];
-    load_weights<TY, W, V>(weight, c, a.channels, w);
-    load_or_zero<TY, V>(bias, c, a.channels, b);
+    load_weights<TY, W, V, TAIL>(weight, c, a.channels, w);
+    load_or_zero<TY, V, TAIL>(bias, c, a.channels, b);
     bool live = t0 >= first && t0 < end;  // or behind the last sequence
-    if (live) load_window<TY, W, V>(a, x, initial, s, first, t0, c, win);
+    if (live) load_window<TY, W, V, TAIL>(a, x, initial, s, first, t0, c, win);
     auto some = [&](Packed<TY, V>(&from)[kAhead], int i0) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -142,21 +143,21 @@ __global__ __launch_bounds__(kThreads) void conv_kernel(Conv a, long long begin,
                 s = sequence_of(a.q, t);
                 span_of(a.q, s, first, end);
                 live = t >= first && t < end;
-                if (live) load_window<TY, W, V>(a, x, initial, s, first, t, c, win);
+                if (live) load_window<TY, W, V, TAIL>(a, x, initial, s, first, t, c, win);
             }
             if (i0 + i < n && live) {
                 float now[V], p[V];
-                unpack<TY, V>(from[i], now);
+                unpack<TY, V, TAIL>(from[i], c, a.channels, now);
                 apply<W, V>(w, b, win, now, p);
                 shift<W, V>(win, now);
                 if (a.silu) {
 #pragma unroll
                     for (int e = 0; e < V; ++e) p[e] *= gate_of<TY>(p[e]);
                 }
-                store<TY, V>(y + (long long)t * a.channels, c, a.channels, p);
+                store<TY, V, TAIL>(y + (long long)t * a.channels, c, a.channels, p);
             } else if (i0 + i < n && a.clear) {
                 const float none[V] = {};
-                store<TY, V>(y + (long long)t * a.channels, c, a.channels, none);
+                store<TY, V, TAIL>(y + (long long)t * a.channels, c, a.channels, none);
             }
         }
     };
@@ -179,22 +180,22 @@ __device__ __forceinline__ void through(int silu, const float (&p)[V], float (&g
     }
 }
 
-// A wave has kGradTile tokens and 256 channels.  It computes p again for its own tokens
+// A wave has a.grad_tile tokens and 256 channels.  It computes p again for its own tokens
 // and, since grad_x_t takes grad_p of the width - 1 tokens behind t, for as many behind
 // them; `next` holds what the tokens up to now give to the gradients of the last width - 1
 // inputs.  Behind the tiles' waves the initial states', a sequence each.
-template <class TY, int W>
+template <class TY, int W, bool TAIL>
 __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
     Conv a, long long waves, long long tiles, const typename TY::S* __restrict__ x,
     const typename TY::S* __restrict__ weight, const typename TY::S* __restrict__ bias,
     const typename TY::S* __restrict__ initial, const typename TY::S* __restrict__ gy,
     const typename TY::S* __restrict__ gfinal, typename TY::S* __restrict__ gx, typename TY::S* __restrict__ ginit,
     float* __restrict__ part) {
-    constexpr int V = kBackward;
+    constexpr int V = kLane;
     const long long block = on_die(blockIdx.x, (waves + kWaves - 1) / kWaves);
     const long long wave = block * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= waves) return;
-    const int parts = parts_of(a.channels, V);
+    const int parts = parts_of(a);
     const int c = (int)(wave % parts) * 64 * V + (threadIdx.x & 63) * V;
     const long long at = wave / parts;
     float w[W][V], b[V], win[W - 1][V];
@@ -203,18 +204,18 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
     };
     int first, end;
     if (at >= tiles) {
-        load_weights<TY, W, V>(weight, c, a.channels, w);
-        load_or_zero<TY, V>(bias, c, a.channels, b);
+        load_weights<TY, W, V, TAIL>(weight, c, a.channels, w);
+        load_or_zero<TY, V, TAIL>(bias, c, a.channels, b);
         const int s = (int)(at - tiles);
         span_of(a.q, s, first, end);
-        load_window<TY, W, V>(a, x, initial, s, first, first, c, win);
+        load_window<TY, W, V, TAIL>(a, x, initial, s, first, first, c, win);
         float g0[W - 1][V] = {};
 #pragma unroll
         for (int p = 0; p < W - 1; ++p) {
             if (first + p >= end) break;
             float now[V], pre[V], g[V];
-            load<TY, V>(x + (first + p) * a.xt, c, a.channels, now);
-            load<TY, V>(gy + (first + p) * a.gt, c, a.channels, g);
+            load<TY, V, TAIL>(x + (first + p) * a.xt, c, a.channels, now);
+            load<TY, V, TAIL>(gy + (first + p) * a.gt, c, a.channels, g);
             apply<W, V>(w, b, win, now, pre);
             shift<W, V>(win, now);
             through<TY, V>(a.silu, pre, g);
@@ -229,15 +230,15 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
             const int kept = i - (end - first);  // where it is in the final state
             if (kept >= 0) {
                 float f[V];
-                load_or_zero<TY, V>(final_row(s, kept), c, a.channels, f);
+                load_or_zero<TY, V, TAIL>(final_row(s, kept), c, a.channels, f);
 #pragma unroll
                 for (int e = 0; e < V; ++e) g0[i][e] += f[e];
             }
-            store<TY, V>(ginit + ((long long)s * (W - 1) + i) * a.channels, c, a.channels, g0[i]);
+            store<TY, V, TAIL>(ginit + ((long long)s * (W - 1) + i) * a.channels, c, a.channels, g0[i]);
         }
         return;
     }
-    const int t0 = (int)at * kGradTile, own = min(t0 + kGradTile, a.q.n_tokens);
+    const int t0 = (int)at * a.grad_tile, own = min(t0 + a.grad_tile, a.q.n_tokens);
     const int all = min(own + W - 1, a.q.n_tokens) - t0;  // rows that it reads
     int s = sequence_of(a.q, t0);
     span_of(a.q, s, first, end);
@@ -246,16 +247,16 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (i0 + i < all) {
-                xr[k][i] = fetch<TY, V>(x + (t0 + i0 + i) * a.xt, c, a.channels);
-                gr[k][i] = fetch<TY, V>(gy + (t0 + i0 + i) * a.gt, c, a.channels);
+                xr[k][i] = fetch<TY, V, TAIL>(x + (t0 + i0 + i) * a.xt, c, a.channels);
+                gr[k][i] = fetch<TY, V, TAIL>(gy + (t0 + i0 + i) * a.gt, c, a.channels);
             }
     };
     ahead(0, 0);
     ahead(1, kAhead);
-    load_weights<TY, W, V>(weight, c, a.channels, w);
-    load_or_zero<TY, V>(bias, c, a.channels, b);
+    load_weights<TY, W, V, TAIL>(weight, c, a.channels, w);
+    load_or_zero<TY, V, TAIL>(bias, c, a.channels, b);
     bool live = t0 >= first && t0 < end;  // or behind the last sequence, or done
-    if (live) load_window<TY, W, V>(a, x, initial, s, first, t0, c, win);
+    if (live) load_window<TY, W, V, TAIL>(a, x, initial, s, first, t0, c, win);
     float next[W - 1][V] = {};  // next[k] of the input k tokens back
     float sum[W + 1][V] = {};
     // the gradients of a sequence's last inputs, which its final state holds too
@@ -265,10 +266,10 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
             const int done = end - 1 - k;
             if (done >= t0 && done >= first && done < own) {
                 float f[V];
-                load_or_zero<TY, V>(final_row(s, W - 2 - k), c, a.channels, f);
+                load_or_zero<TY, V, TAIL>(final_row(s, W - 2 - k), c, a.channels, f);
 #pragma unroll
                 for (int e = 0; e < V; ++e) f[e] += next[k][e];
-                store<TY, V>(gx + (long long)done * a.channels, c, a.channels, f);
+                store<TY, V, TAIL>(gx + (long long)done * a.channels, c, a.channels, f);
             }
         }
     };
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
                     live = t >= first && t < end;
                 }
                 if (live) {
-                    load_window<TY, W, V>(a, x, initial, s, first, t, c, win);
+                    load_window<TY, W, V, TAIL>(a, x, initial, s, first, t, c, win);
 #pragma unroll
                     for (int q = 0; q < W - 1; ++q)
 #pragma unroll
@@ -294,8 +295,8 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
             }
             if (live && i0 + i < all) {
                 float now[V], p[V], g[V];
-                unpack<TY, V>(xr[k][i], now);
-                unpack<TY, V>(gr[k][i], g);
+                unpack<TY, V, TAIL>(xr[k][i], c, a.channels, now);
+                unpack<TY, V, TAIL>(gr[k][i], c, a.channels, g);
                 apply<W, V>(w, b, win, now, p);
                 through<TY, V>(a.silu, p, g);
                 if (t < own) {
@@ -318,14 +319,14 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
                     next[0][e] = w[W - 1][e] * g[e];
                 }
                 const int which = t - (W - 1);
-                if (which >= t0 && which >= first) store<TY, V>(gx + (long long)which * a.channels, c, a.channels, done);
+                if (which >= t0 && which >= first) store<TY, V, TAIL>(gx + (long long)which * a.channels, c, a.channels, done);
             } else if (a.clear && t < own && !live) {
                 const float none[V] = {};
-                store<TY, V>(gx + (long long)t * a.channels, c, a.channels, none);
+                store<TY, V, TAIL>(gx + (long long)t * a.channels, c, a.channels, none);
             }
         }
     };
-    for (int i = 0; i < kGradTile + W - 1; i += 2 * kAhead) {
+    for (int i = 0; i < a.grad_tile + W - 1; i += 2 * kAhead) {
         some(0, i);
         ahead(0, i + 2 * kAhead);
         some(1, i + kAhead);
@@ -333,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
     }
     if (live && end <= t0 + all) finish();
 #pragma unroll
-    for (int j = 0; j <= W; ++j) store<F32, V>(part + (at * (W + 1) + j) * a.channels, c, a.channels, sum[j]);
+    for (int j = 0; j <= W; ++j) store<F32, V, TAIL>(part + (at * (W + 1) + j) * a.channels, c, a.channels, sum[j]);
 }
 
 // Columns of part [tiles, width + 1, channels] summed in 64 bits: the last of the width + 1
@@ -363,7 +364,7 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void conv_sums_kernel(const flo
         gb[ch] = (float)x;
 }
 
-template <class TY, int W>
+template <class TY, int W, bool TAIL>
 __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long waves, const typename TY::S* __restrict__ x,
                                                              const typename TY::S* __restrict__ weight,
                                                              const typename TY::S* __restrict__ bias,
@@ -371,8 +372,8 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long w
                                                              const int* __restrict__ slots, typename TY::S* __restrict__ y) {
     const long long wave = (long long)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wave >= waves) return;
-    constexpr int V = kForward;
-    const int parts = parts_of(a.channels, V), lane = threadIdx.x & 63;
+    constexpr int V = kLane;
+    const int parts = parts_of(a), lane = threadIdx.x & 63;
     const int c = (int)(wave % parts) * 64 * V + lane * V;
     const int rows = a.q.n_tokens;
     int row = (int)(wave / parts), slot = row;
@@ -380,28 +381,28 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long w
         slot = __builtin_amdgcn_readfirstlane(slots[row]);
         if (slot < 0 || slot >= pool) {
             const float none[V] = {};
-            store<TY, V>(y + (long long)row * a.channels, c, a.channels, none);
+            store<TY, V, TAIL>(y + (long long)row * a.channels, c, a.channels, none);
             return;
         }
         for (int j = 0; j < row; j += 64)  // the first row of a slot takes all
             if (__ballot(j + lane < row && slots[min(j + lane, rows - 1)] == slot)) return;
     }
     float w[W][V], b[V], win[W - 1][V];
-    load_weights<TY, W, V>(weight, c, a.channels, w);
-    load_or_zero<TY, V>(bias, c, a.channels, b);
+    load_weights<TY, W, V, TAIL>(weight, c, a.channels, w);
+    load_or_zero<TY, V, TAIL>(bias, c, a.channels, b);
     typename TY::S* state = states + (long long)slot * (W - 1) * a.channels;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load<TY, V>(state + (long long)j * a.channels, c, a.channels, win[j]);
+    for (int j = 0; j < W - 1; ++j) load<TY, V, TAIL>(state + (long long)j * a.channels, c, a.channels, win[j]);
     while (row < rows) {
         float now[V], p[V];
-        load<TY, V>(x + row * a.xt, c, a.channels, now);
+        load<TY, V, TAIL>(x + row * a.xt, c, a.channels, now);
         apply<W, V>(w, b, win, now, p);
         shift<W, V>(win, now);
         if (a.silu) {
 #pragma unroll
             for (int e = 0; e < V; ++e) p[e] *= gate_of<TY>(p[e]);
         }
-        store<TY, V>(y + (long long)row * a.channels, c, a.channels, p);
+        store<TY, V, TAIL>(y + (long long)row * a.channels, c, a.channels, p);
         if (!slots) break;
         int next = rows;
         for (int j = row + 1; j < rows; j += 64) {
@@ -414,7 +415,7 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long w
         row = next;
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) store<TY, V>(state + (long long)j * a.channels, c, a.channels, win[j]);
+    for (int j = 0; j < W - 1; ++j) store<TY, V, TAIL>(state + (long long)j * a.channels, c, a.channels, win[j]);
 }
 
 // ---------------------------------------------------------- host helpers
@@ -429,7 +430,7 @@ int check_shape(const short_conv_shape_t* p, bool step, Conv* a) {
     if (p->channels < 1 || p->width < 1 || p->x_stride < 0 || p->grad_y_stride < 0) return CFC_ERR_DIM;
     if (p->width < 2 || p->width > SHORT_CONV_MAX_WIDTH) return CFC_ERR_UNSUPPORTED;
     // a lane's first weight is at 4 times its channel
-    if (p->channels > INT_MAX / SHORT_CONV_MAX_WIDTH - 64 * kForward || p->n_tokens > kMaxTokens) return CFC_ERR_UNSUPPORTED;
+    if (p->channels > INT_MAX / SHORT_CONV_MAX_WIDTH - 64 * kLane || p->n_tokens > kMaxTokens) return CFC_ERR_UNSUPPORTED;
     if (step) {
         if (p->n_tokens < 0) return CFC_ERR_DIM;
         a->q = Sequences{nullptr, (int)p->n_tokens, 1, (int)p->n_tokens};
@@ -441,8 +442,12 @@ int check_shape(const short_conv_shape_t* p, bool step, Conv* a) {
     a->clear = p->clear_rest && p->offsets;
     a->xt = p->x_stride;
     a->gt = p->grad_y_stride;
-    // (the forward's tiles and the backward's parts are the most)
-    const long long most = ((long long)a->q.n_tokens / (step ? 1 : kTile) + 1 + a->q.n_seq) * parts_of(a->channels, kBackward);
+    // 32 tokens a wave share their halo and their row of partial sums; with 16 twice as many
+    // waves hide the loads' latency where there are few: 3056 tokens of 1111 channels in 27
+    // instead of 42 us, but 8192 of 4096 in 78 instead of 70.
+    a->grad_tile = ((long long)a->q.n_tokens / 32 + 1) * parts_of(*a) < 2048 ? 16 : 32;
+    // (the forward's tiles are the most)
+    const long long most = ((long long)a->q.n_tokens / (step ? 1 : kTile) + 1 + a->q.n_seq) * parts_of(*a);
     return blocks_of(most) > kMaxGrid ? CFC_ERR_UNSUPPORTED : CFC_OK;
 }
 
@@ -459,20 +464,21 @@ bool sizes_of(const short_conv_shape_t* p, const Conv& a, Sizes* z) {
            mul_ok(a.q.n_seq, p->width - 1, &kept) && mul_ok(kept, (long long)a.channels * size, &z->states);
 }
 inline long long workspace_of(const Conv& a, int width) {
-    const long long tiles = ((long long)a.q.n_tokens + kGradTile - 1) / kGradTile;
+    const long long tiles = ((long long)a.q.n_tokens + a.grad_tile - 1) / a.grad_tile;
     long long n;
     return mul_ok(tiles * (width + 1), (long long)a.channels * 4, &n) ? (n + 15) / 16 * 16 : -1;
 }
 
 template <class F>
-int with_width(int type, int width, F f) {
-    auto go = [&](auto ty) {
-        if (width == 2) return f(ty, std::integral_constant<int, 2>{});
-        if (width == 3) return f(ty, std::integral_constant<int, 3>{});
-        return f(ty, std::integral_constant<int, 4>{});
+int with_width(const short_conv_shape_t* p, F f) {
+    auto typed = [&](auto ty, auto tail) {
+        if (p->width == 2) return f(ty, std::integral_constant<int, 2>{}, tail);
+        if (p->width == 3) return f(ty, std::integral_constant<int, 3>{}, tail);
+        return f(ty, std::integral_constant<int, 4>{}, tail);
     };
-    if (type == CFC_TYPE_F32) return go(F32{});
-    return type == CFC_TYPE_BF16 ? go(BF16{}) : go(F16{});
+    auto go = [&](auto ty) { return p->channels % kLane ? typed(ty, std::true_type{}) : typed(ty, std::false_type{}); };
+    if (p->type == CFC_TYPE_F32) return go(F32{});
+    return p->type == CFC_TYPE_BF16 ? go(BF16{}) : go(F16{});
 }
 
 }  // namespace
@@ -493,15 +499,16 @@ extern "C" int short_conv_forward(const short_conv_shape_t* shape, const void* x
     const Range ins[] = {bytes_of(x, z.x), bytes_of(weight, z.weight), bytes_of(bias, z.bias), offsets_range(a.q),
                          over ? Range{0, 0} : ini};
     if (!outputs_disjoint(outs, 2, ins, 5) || (over && overlap(outs[0], ini))) return CFC_ERR_OVERLAP;
-    return with_width(shape->type, shape->width, [&](auto ty, auto width) {
+    return with_width(shape, [&](auto ty, auto width, auto tail) {
         using TY = decltype(ty);
         using S = typename TY::S;
         constexpr int W = decltype(width)::value;
-        const long long tiles = (a.q.n_tokens + kTile - 1) / kTile, parts = parts_of(a.channels, kForward);
+        constexpr bool TAIL = decltype(tail)::value;
+        const long long tiles = (a.q.n_tokens + kTile - 1) / kTile, parts = parts_of(a);
         const long long split = tiles * parts, all = (tiles + (final_state ? a.q.n_seq : 0)) * parts;
         auto go = [&](long long from, long long to) {
             if (from < to)
-                hipLaunchKernelGGL((conv_kernel<TY, W>), dim3(dealt(blocks_of(to - from))), dim3(kThreads), 0, stream,
+                hipLaunchKernelGGL((conv_kernel<TY, W, TAIL>), dim3(dealt(blocks_of(to - from))), dim3(kThreads), 0, stream,
                                    a, from, to, tiles, (const S*)x, (const S*)weight, (const S*)bias,
                                    (const S*)initial_state, (S*)y, (S*)final_state);
         };
@@ -549,15 +556,16 @@ extern "C" int short_conv_backward(const short_conv_shape_t* shape, const void* 
                          bytes_of(grad_final_state, z.states),
                          offsets_range(a.q)};
     if (!outputs_disjoint(outs, 5, ins, 7)) return CFC_ERR_OVERLAP;
-    return with_width(shape->type, shape->width, [&](auto ty, auto width) {
+    return with_width(shape, [&](auto ty, auto width, auto tail) {
         using TY = decltype(ty);
         using S = typename TY::S;
         constexpr int W = decltype(width)::value;
-        const long long tiles = ((long long)a.q.n_tokens + kGradTile - 1) / kGradTile, parts = parts_of(a.channels, kBackward);
+        constexpr bool TAIL = decltype(tail)::value;
+        const long long tiles = ((long long)a.q.n_tokens + a.grad_tile - 1) / a.grad_tile, parts = parts_of(a);
         const long long waves = (tiles + (grad_initial_state ? a.q.n_seq : 0)) * parts;
         float* part = static_cast<float*>(workspace);
         if (waves)
-            hipLaunchKernelGGL((conv_backward_kernel<TY, W>), dim3(dealt(blocks_of(waves))), dim3(kThreads), 0, stream,
+            hipLaunchKernelGGL((conv_backward_kernel<TY, W, TAIL>), dim3(dealt(blocks_of(waves))), dim3(kThreads), 0, stream,
                                a, waves, tiles, (const S*)x, (const S*)weight, (const S*)bias, (const S*)initial_state,
                                (const S*)grad_y, (const S*)grad_final_state, (S*)grad_x, (S*)grad_initial_state, part);
         const long long columns = (long long)(W + 1) * a.channels;
@@ -583,12 +591,13 @@ extern "C" int short_conv_step(const short_conv_shape_t* shape, const void* x, c
     const Range ins[] = {bytes_of(x, z.x), bytes_of(weight, z.weight), bytes_of(bias, z.bias),
                          bytes_of(slots, (long long)a.q.n_tokens * 4)};
     if (!outputs_disjoint(outs, 2, ins, 4)) return CFC_ERR_OVERLAP;
-    return with_width(shape->type, shape->width, [&](auto ty, auto width) {
+    return with_width(shape, [&](auto ty, auto width, auto tail) {
         using TY = decltype(ty);
         using S = typename TY::S;
         constexpr int W = decltype(width)::value;
-        const long long waves = (long long)a.q.n_tokens * parts_of(a.channels, kForward);
-        hipLaunchKernelGGL((conv_step_kernel<TY, W>), dim3((unsigned)blocks_of(waves)), dim3(kThreads), 0, stream, a,
+        constexpr bool TAIL = decltype(tail)::value;
+        const long long waves = (long long)a.q.n_tokens * parts_of(a);
+        hipLaunchKernelGGL((conv_step_kernel<TY, W, TAIL>), dim3((unsigned)blocks_of(waves)), dim3(kThreads), 0, stream, a,
                            waves, (const S*)x, (const S*)weight, (const S*)bias, (S*)states, pool, slots, (S*)y);
         return launch_status();
     });

@@ -18,7 +18,7 @@
  * (capturable), argument errors (CFC_* codes of cfc.h) before anything is enqueued, no
  * atomics and fixed summation orders, so equal inputs give equal bits.  Arithmetic is
  * that of 32-bit floats; the weight's and the bias's gradients are summed in 64 bits over
- * groups of 64 tokens.
+ * groups of 16 or 32 tokens.
  */
 #ifndef SHORT_CONV_AMD_H
 #define SHORT_CONV_AMD_H

@@ -78,7 +78,7 @@ def test_null_arguments_and_workspace(lib):
     for n in ("x", "w", "gy", "gx", "gw", "ws"):
         assert backward(lib, **{n: None}) == C.CFC_ERR_NULL, n
     need = lib.short_conv_backward_workspace(byref(shape()))
-    assert need == 2 * 5 * 64 * 4  # two groups of 64 tokens
+    assert need == 7 * 5 * 64 * 4  # seven groups of 16 tokens
     assert backward(lib, size=need - 1) == C.CFC_ERR_DIM
     assert backward(lib, ws=AT["ws"] + 8) == C.CFC_ERR_DIM
 
