@@ -77,7 +77,21 @@ __device__ __forceinline__ Packed<TY, V> fetch(const typename TY::S* row, int c,
     return e;
 }
 template <class TY, int V, bool TAIL>
-__device__ __forceinline__ void unpack(const Packed<TY, V>& e, int c, int width, float (&x)[V]) {
+__device__ __forceinline__ void unpack(Packed<TY, V> e, int c, int width, float (&x)[V]) {
+    constexpr int N = V * sizeof(typename TY::S) / 4, per = V / N;  // elements of a word
+    const int over = TAIL && width >= V ? c + V - width : 0;        // columns that the row has not
+    if (over > 0) {
+#pragma unroll
+        for (int by = N / 2; by > 0; by >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) e.w[i] = over & (by * per) ? (i + by < N ? e.w[i + by] : 0) : e.w[i];
+        if constexpr (per == 2) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) e.w[i] = over & 1 ? e.w[i] >> 16 | (i + 1 < N ? e.w[i + 1] << 16 : 0) : e.w[i];
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) e.w[i] = over >= V ? 0 : e.w[i];
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if constexpr (sizeof(typename TY::S) == 4)
@@ -85,17 +99,6 @@ __device__ __forceinline__ void unpack(const Packed<TY, V>& e, int c, int width,
         else
             x[j] = TY::load(__builtin_bit_cast(typename TY::S,
                                                (uint16_t)(j & 1 ? e.w[j >> 1] >> 16 : e.w[j >> 1] & 0xffff)));
-    }
-    const int over = TAIL && width >= V ? c + V - width : 0;  // columns that the row has not
-    if (over > 0) {
-#pragma unroll
-        for (int by = V / 2; by > 0; by >>= 1)
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = over & by ? (j + by < V ? x[j + by] : 0.0f) : x[j];
-        if (over >= V) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = 0.0f;
-        }
     }
 }
 template <class TY, int V, bool TAIL>
