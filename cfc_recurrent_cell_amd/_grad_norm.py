@@ -1,6 +1,8 @@
 """Tensor checks and pointer marshalling of the gradients' norm and clipping (include/grad_norm.h)."""
 from __future__ import annotations
 
+from ctypes import c_uint64
+
 import torch
 
 from ._lib import GradTensor, _check, load_library
@@ -24,16 +26,17 @@ def _tensors(grads, out, norm):
     if not isinstance(first, torch.Tensor):
         raise TypeError("grads[0] must be a torch.Tensor" if grads else "norm must be a torch.Tensor")
     dev = first.device
-    array = (GradTensor * max(1, len(grads)))()
+    flat = []  # the descriptions' words: a tensor's are set at once, and not field by field
     for i, (g, o) in enumerate(zip(grads, outs)):
         # (the short way: what does not fit is named below)
         if not (isinstance(g, torch.Tensor) and g.is_cuda and g.device == dev and g.is_contiguous() and g.dtype in TYPES):
             element_type(g, f"grads[{i}]")
             check(g, f"grads[{i}]", g.dtype, dev if dev.type == "cuda" else None)
-        if o is not g:
+        if o is not g and not (isinstance(o, torch.Tensor) and o.dtype == g.dtype and o.shape == g.shape
+                               and o.device == dev and o.is_contiguous()):
             check(o, f"out[{i}]", g.dtype, dev, g.shape)
-        a = array[i]
-        a.grad, a.out, a.numel, a.type = g.data_ptr(), o.data_ptr(), g.numel(), TYPES[g.dtype]
+        flat += (g.data_ptr(), o.data_ptr(), g.numel(), TYPES[g.dtype])
+    array = (GradTensor * max(1, len(grads))).from_buffer((c_uint64 * max(4, len(flat)))(*flat))
     return array, len(grads), dev
 
 

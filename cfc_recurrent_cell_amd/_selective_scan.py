@@ -147,7 +147,7 @@ def selective_scan_step(x, dt, a, b, c, states, slots=None, d=None, z=None, dt_b
     dev, rows = x.device, x.shape[0]
     pool = slots_of(slots, rows, states, (s.channels, s.state), F32, dev)
     with on_device(dev, stream):
-        y = given_or_new(y, "y", x.dtype, dev, x.shape)
+        y = given_or_new(y, "y", x.dtype, dev, x.shape, x if x.is_contiguous() else None)
         _check("selective_scan_step", lib.selective_scan_step(
             byref(s), x.data_ptr(), dt.data_ptr(), a.data_ptr(), b.data_ptr(), c.data_ptr(), ptr(d), ptr(z),
             ptr(dt_bias), states.data_ptr(), pool, ptr(slots), y.data_ptr(), stream_ptr(dev, stream)))

@@ -122,7 +122,7 @@ def short_conv_step(x, weight, states, slots=None, bias=None, activation: Option
     dev, rows = x.device, x.shape[0]
     pool = slots_of(slots, rows, states, (s.width - 1, s.channels), x.dtype, dev)
     with on_device(dev, stream):
-        y = given_or_new(y, "y", x.dtype, dev, x.shape)
+        y = given_or_new(y, "y", x.dtype, dev, x.shape, x if x.is_contiguous() else None)
         _check("short_conv_step", lib.short_conv_step(
             byref(s), x.data_ptr(), weight.data_ptr(), ptr(bias), states.data_ptr(), pool, ptr(slots), y.data_ptr(),
             stream_ptr(dev, stream)))
