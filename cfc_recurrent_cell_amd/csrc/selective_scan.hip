@@ -385,12 +385,12 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
 
 // The states before each block of block_of(S) tokens, to kept[slot][group][sixteen][64 S] as
 // the exchange has them.
-template <class TY, int S>
-__global__ __launch_bounds__(64 * waves_of(S)) void scan_states_kernel(
+template <class TY, int S, int NW>
+__global__ __launch_bounds__(64 * NW) void scan_states_kernel(
     Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
     const float* __restrict__ decay, const typename TY::S* __restrict__ b, const float* __restrict__ dt_bias,
     const float* __restrict__ initial, float* __restrict__ kept) {
-    constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW, F = (S + NW - 1) / NW;
+    constexpr int BT = block_of(S), T = BT / NW, Q = T / 4, F = (S + NW - 1) / NW;
     __shared__ Lanes<S> product[2][NW], made[2][NW];
     __shared__ alignas(16) float bc[NW][T * 4 * S];
     const long long count = (long long)a.groups * sixteens * a.q.n_seq, index = on_die(blockIdx.x, count);
@@ -1292,9 +1292,19 @@ extern "C" int selective_scan_backward(const selective_scan_shape_t* shape, cons
         constexpr int S = decltype(states)::value;
         const int sixteens = sixteens_of(a), wg_groups = wg_groups_of(a), parts = parts_of(a);
         if (a.q.n_seq) {
-            hipLaunchKernelGGL((scan_states_kernel<TY, S>), dim3(dealt((long long)a.groups * sixteens * a.q.n_seq)),
-                               dim3(64 * waves_of(S)), 0, stream, a, sixteens, (const E*)x, (const E*)dt, a_, (const E*)b,
-                               dt_bias, initial_state, g.kept);
+            const long long count = (long long)a.groups * sixteens * a.q.n_seq;
+            auto states_of = [&](auto kernel, int waves) {
+                hipLaunchKernelGGL(kernel, dim3(dealt(count)), dim3(64 * waves), 0, stream, a, sixteens, (const E*)x,
+                                   (const E*)dt, a_, (const E*)b, dt_bias, initial_state, g.kept);
+            };
+            if constexpr (S <= 4) {
+                if (count <= kFewWorkgroups)
+                    states_of(scan_states_kernel<TY, S, 16>, 16);
+                else
+                    states_of(scan_states_kernel<TY, S, 8>, 8);
+            } else {
+                states_of(scan_states_kernel<TY, S, waves_of(S)>, waves_of(S));
+            }
             const BackwardArgs args{a, sixteens, wg_groups, parts, x, dt, b, c, z, grad_y, a_, d, dt_bias, grad_final_state, g};
             auto go = [&](auto kernel) {
                 hipLaunchKernelGGL(kernel, dim3(dealt((long long)wg_groups * parts)), dim3(64 * waves_of(S)), 0, stream, args);
