@@ -34,6 +34,11 @@ constexpr int kGroupCh = 16;  // channels of a workgroup
 constexpr int tokens_of(int s) { return s <= 4 ? 8 : 4; }
 constexpr int waves_of(int s) { return s <= 8 ? 8 : 4; }
 constexpr int forward_tokens(int s) { return s <= 2 ? 8 : 4; }
+// Workgroups (16 channels of a sequence each) up to which each has 16 waves instead of 8, since
+// there is at most one for a CU.  4096 channels x 16 states, bf16, in us, 16 waves | 8: one
+// sequence of 8192 tokens (256 workgroups) 200 | 250, two of 2048 (512) 106 | 99, four (1024)
+// 209 | 180.  Overlapping rows of b and c are left to 8: the branch for them (Shared::load) costs
+// the kernel of 16 waves 20 of its 200 us.
 constexpr long long kFewWorkgroups = 256;
 constexpr int block_of(int s) { return tokens_of(s) * waves_of(s); }
 
@@ -42,7 +47,8 @@ struct Scan {
     int channels, groups, share, state;  // share: channels of a group
     int softplus, clear;
     long long xt, dtt, zt, gt, bt, bg, ct, cg;
-    bool single;  // sequences of one row, whose strides may be anything
+    bool single;   // sequences of one row, whose strides may be anything
+    bool overlap;  // rows of b or c behind a sequence's end read as some of its own
 };
 
 // ------------------------------------------------------------------- lanes
@@ -130,8 +136,8 @@ __device__ __forceinline__ void store_to(Buffer b, uint32_t at, float x) {
 
 // The rows of a tensor from one on, for a block of tokens at a time: those behind the
 // sequence's end read as zeros and are not written, so that nothing needs a branch.  (Where
-// rows overlap, at a stride below their width, they read as something: steps and gradients
-// there are set to zero.)
+// rows overlap, at a stride below their width, they read as something, so what is made of
+// them is set to zero: an infinite one times a step of zero would be no number.)
 struct Rows {
     const char* at;
     int bytes, width;  // from a row to the next, and of a row
@@ -168,9 +174,19 @@ struct Shared {
                         : kNowhere;
         }
     }
-    __device__ __forceinline__ void load(Buffer b) {
+    // `left`: of the wave's tokens, those that there are.  Rows behind them read as zeros by
+    // themselves, except where rows overlap.
+    __device__ __forceinline__ void load(Buffer b, bool overlap, int left) {
+        if (overlap && left < T) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) raw[i] = load_raw<TY>(b, at[i]);
+            for (int i = 0; i < N; ++i) {
+                const int e = i * 64 + (threadIdx.x & 63);
+                raw[i] = load_raw<TY>(b, e / (4 * S) < left ? at[i] : kNowhere);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) raw[i] = load_raw<TY>(b, at[i]);
+        }
     }
     __device__ __forceinline__ void put(float* to) const {
 #pragma unroll
@@ -240,6 +256,11 @@ __device__ __forceinline__ float along(const Lanes<S> (&product)[NW], Lanes<S> (
 }
 
 // -------------------------------------------------------------------- forward
+// Bound by the vector units: an element (token, channel, state) takes an exponential (four
+// issue slots), its argument's product, D x b, the two passes' multiply-adds and c's, and a
+// token and channel's softplus and gate about 60 slots over its 16 states: 13 slots, of
+// which 8192 tokens x 4096 channels x 16 states need 177 us.  Measured 180 in four sequences,
+// 202 in one (1.33 TB/s).
 template <class TY, int S, int NW>
 __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16 ? 4 : 6) void scan_kernel(
     Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
@@ -292,8 +313,8 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
             dtr[i] = load_raw<TY>(db, dta.at[i]);
             zr[i] = load_raw<TY>(zb, za.at[i]);
         }
-        bl.load(bs.next(n));
-        cl.load(cs.next(n));
+        bl.load(bs.next(n), NW < 16 && a.overlap, n - w * T);
+        cl.load(cs.next(n), NW < 16 && a.overlap, n - w * T);
         xs.move(BT), dts.move(BT), zs.move(BT), bs.move(BT), cs.move(BT);
     };
     fetch(len);
@@ -305,9 +326,10 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
         float xv[Q], step[Q], u[Q], gate[Q], all = 0.0f;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
-            xv[i] = value_of<TY>(xr[i]);
+            const bool in = row + 4 * i < left;
+            xv[i] = in ? value_of<TY>(xr[i]) : 0.0f;
             const float pre = value_of<TY>(dtr[i]) + bias;
-            step[i] = row + 4 * i < left ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
+            step[i] = in ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
             u[i] = step[i] * xv[i];
             all += step[i];
             const float zv = value_of<TY>(zr[i]);
@@ -384,7 +406,8 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
 // which is linear in e as the forward is in h, and is cut into the same stretches.
 
 // The states before each block of block_of(S) tokens, to kept[slot][group][sixteen][64 S] as
-// the exchange has them.
+// the exchange has them: the forward without its second pass, 66 us of the 399 of the
+// gradients of 4 x 2048 tokens x 2048 channels x 16 states.
 template <class TY, int S, int NW>
 __global__ __launch_bounds__(64 * NW) void scan_states_kernel(
     Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
@@ -429,7 +452,7 @@ __global__ __launch_bounds__(64 * NW) void scan_states_kernel(
             xr[i] = load_raw<TY>(xb, xa.at[i]);
             dtr[i] = load_raw<TY>(db, dta.at[i]);
         }
-        bl.load(bs.next(n));
+        bl.load(bs.next(n), NW < 16 && a.overlap, n - w * T);
         xs.move(BT), dts.move(BT), bs.move(BT);
     };
     fetch(len);
@@ -443,9 +466,10 @@ __global__ __launch_bounds__(64 * NW) void scan_states_kernel(
         float step[Q], u[Q], all = 0.0f;
 #pragma unroll
         for (int i = 0; i < Q; ++i) {
+            const bool in = row + 4 * i < left && p.in;
             const float pre = value_of<TY>(dtr[i]) + bias;
-            step[i] = row + 4 * i < left ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
-            u[i] = step[i] * value_of<TY>(xr[i]);
+            step[i] = in ? (a.softplus ? softplus_of(pre) : pre) : 0.0f;
+            u[i] = step[i] * (in ? value_of<TY>(xr[i]) : 0.0f);
             all += step[i];
         }
         fetch(left - BT);  // while this block is worked on
@@ -519,7 +543,9 @@ __device__ __forceinline__ float over_quads(const float (&v)[16]) {
 
 // A workgroup has K times 16 channels of a group, one after the other for each block of
 // tokens, so that b's and c's gradients are summed over them before they leave it; and every
-// parts-th sequence.
+// parts-th sequence.  Bound by the vector units: 34 issue slots an element, of which the sums
+// over channels and states are 6, the passes of h and e 12, the exponential 4; 312 us of the
+// 399 above, 231 of them those slots', with two waves a SIMD between its two barriers a step.
 //
 // What only a sequence's or the kernel's beginning and end need of the arguments is read from
 // their segment again there (`fresh`): kept in scalar registers all along, it had those of the
@@ -551,7 +577,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
     const auto* const args = fresh<BackwardArgs>();
     const int wg_groups = args->wg_groups, parts = args->parts, sixteens = args->sixteens, groups = args->a.groups;
     const int share = args->a.share, state_size = args->a.state, channels = args->a.channels, n_seq = args->a.q.n_seq;
-    const bool softplus = args->a.softplus, gated = args->z != nullptr;
+    const bool softplus = args->a.softplus, gated = args->z != nullptr, overlap = args->a.overlap;
     const long long count = (long long)wg_groups * parts, index = on_die(blockIdx.x, count);
     if (index >= count) return;
     const int wg = (int)(index % wg_groups), part = (int)(index / wg_groups);
@@ -626,8 +652,8 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
                     gr[i] = load_raw<TY>(gb, ga.at[i] + off);
                 }
                 if (k == 0) {
-                    bl.load(bs.some(n));
-                    cl.load(cs.some(n));
+                    bl.load(bs.some(n), overlap, n - w * T);
+                    cl.load(cs.some(n), overlap, n - w * T);
                 }
 #pragma unroll
                 for (int i = 0; i < F; ++i)
@@ -652,15 +678,15 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
                     rate[k].get(lane, a2);
 #pragma unroll
                     for (int i = 0; i < Q; ++i) {
-                        const bool in = row + 4 * i < n;
-                        xv[i] = value_of<TY>(xr[i]);
+                        const bool in = row + 4 * i < n && here;
+                        xv[i] = in ? value_of<TY>(xr[i]) : 0.0f;
                         const float pre = value_of<TY>(dtr[i]) + sb.y, ex = exp_of(-fabsf(pre));
                         step[i] = in ? (softplus ? softplus_of(pre, ex) : pre) : 0.0f;
                         slope[i] = softplus ? sigmoid_of(pre, ex) : 1.0f;
                         u[i] = step[i] * xv[i];
                         all += step[i];
-                        gv[i] = in && here ? value_of<TY>(gr[i]) : 0.0f;
-                        zv[i] = value_of<TY>(zr[i]);
+                        gv[i] = in ? value_of<TY>(gr[i]) : 0.0f;
+                        zv[i] = in ? value_of<TY>(zr[i]) : 0.0f;
                         sig[i] = gated ? gate_of<TY>(zv[i]) : 1.0f;
                         gp[i] = gated ? gv[i] * (zv[i] * sig[i]) : gv[i];
                     }
@@ -827,7 +853,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
                         if (gated)
                             store_to<TY>(gzb, to, gv[i] * fmaf(sb.x, xv[i], ypre[i]) * (sig[i] * (1.0f + zv[i] * (1.0f - sig[i]))));
                         dd = fmaf(gp[i], xv[i], dd);
-                        db += row + 4 * i < n ? gdt : 0.0f;
+                        db += row + 4 * i < n && here ? gdt : 0.0f;
                     }
                     dd += quad_perm<0xB1>(dd);
                     dd += quad_perm<0x4E>(dd);
@@ -898,7 +924,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
     }
 }
 
-// What the workgroups left, summed: b's and c's gradients over the channels' workgroups, a's,
+// What the workgroups left, summed (21 us of the 399, 67 MB): b's and c's gradients over the channels' workgroups, a's,
 // d's and dt_bias's over the sequences' parts.  A thread has an element.
 constexpr int kSumThreads = 256;
 template <class TY>
@@ -992,9 +1018,18 @@ __device__ __forceinline__ void store_row(float* row, int j, int state, const fl
 
 // A wave has C times 16 channels of a row, their states in registers, all loads in flight at
 // once.  The steps and the gates are computed by a lane for each channel and taken from there
-// by the channel's four.  Bound by reading and writing the states.
+// by the channel's four.  Bound by reading and writing the states: 243 rows of 4096 channels x
+// 16 states (136 MB) in 33.5 us, 4.1 TB/s; one row in 4.3, latency.
 constexpr int kStepThreads = 256;
-constexpr long long kPastCache = 32LL << 20, kStepFew = 8192;
+// States of 32 MB a call and more pass the last-level cache by, since between two steps of a
+// layer all the others' states pass through it (16 states of 4096 channels in bf16, us, with |
+// without: 16 layers of 34 MB 19 | 23, 8 of 67 MB 35 | 41, 16 of 67 MB in 64 states 39 | 43; two
+// of 67 MB, which it would hold, 35 | 33).
+constexpr long long kPastCache = 32LL << 20;
+// Times 16 channels from which on a wave has C of them instead of one (4096 channels, on the
+// GPU alone, us, one | C = 4): one row 4.3 | 4.8, 16 rows 6.0 | 6.0, 32 rows 8.8 | 7.1, 64 rows
+// 13.7 | 9.4, 256 rows 44 | 33.5.
+constexpr long long kStepFew = 4096;
 template <class TY, int S, int C, bool PAST>
 __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
     Scan a, long long waves, int parts, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
@@ -1123,6 +1158,7 @@ int check_shape(const selective_scan_shape_t* p, bool step, Scan* a) {
     // a block's rows are reached from its first one by 32 bits, which rows alone do not need
     const int size = size_of(p->type);
     a->single = (p->offsets ? p->n_tokens : step ? 1 : p->seq_len) <= 1;
+    a->overlap = a->single || p->b_stride_t < p->state || p->c_stride_t < p->state;
     long long far = p->channels;
     if (!a->single)
         for (const long long stride : {p->x_stride, p->dt_stride, p->z_stride, p->grad_y_stride, p->b_stride_t, p->c_stride_t})
@@ -1165,7 +1201,8 @@ int with_state(int type, int state, F f) {
 inline int lane_states(int state) { return state <= 4 ? 1 : state <= 8 ? 2 : state <= 16 ? 4 : state <= 32 ? 8 : 16; }
 
 // How many times 16 channels a workgroup of the backward has: more of them leave fewer partial
-// sums of b's and c's gradients and share the sums over lanes, as long as all CUs have one.
+// sums of b's and c's gradients, as long as all CUs have one (4 x 2048 tokens, bf16, us, with one,
+// 2 and 4: 2048 channels 440, 399; 4096 channels 866, 788, 730).  Beyond 16 states LDS holds one.
 inline int sixteens_at_once(const Scan& a) {
     if (a.state > 16) return 1;
     const long long all = (long long)a.groups * sixteens_of(a) * a.q.n_seq;
@@ -1238,7 +1275,7 @@ extern "C" int selective_scan_forward(const selective_scan_shape_t* shape, const
                                final_state);
         };
         if constexpr (S <= 8) {
-            if (count <= kFewWorkgroups) {
+            if (count <= kFewWorkgroups && !a.overlap) {
                 go(scan_kernel<TY, S, 16>, 16);
                 return launch_status();
             }
@@ -1298,7 +1335,7 @@ extern "C" int selective_scan_backward(const selective_scan_shape_t* shape, cons
                                    (const E*)dt, a_, (const E*)b, dt_bias, initial_state, g.kept);
             };
             if constexpr (S <= 4) {
-                if (count <= kFewWorkgroups)
+                if (count <= kFewWorkgroups && !a.overlap)
                     states_of(scan_states_kernel<TY, S, 16>, 16);
                 else
                     states_of(scan_states_kernel<TY, S, 8>, 8);

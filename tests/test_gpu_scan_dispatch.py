@@ -211,3 +211,32 @@ def test_long_strides_of_single_tokens(gpu):
     for u, v in zip((*gpu.short_conv_forward(x, w), *gpu.short_conv_backward(x, w, x)),
                     (*gpu.short_conv_forward(dense, w), *gpu.short_conv_backward(dense, w, dense))):
         assert u is v is None or torch.equal(u, v)
+
+
+def test_broadcast_rows_with_infinities_are_their_copies(gpu):
+    """Rows read at a stride of nothing lie behind the sequence's end too; what is infinite in
+    them must not come back from there (0 * inf)."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    ch, state, length = 20, 16, 37
+    a, row, bc, z, gy = -torch.exp(n(ch, state)), n(1, 1, ch), n(1, 1, 1, state).abs(), n(1, 1, ch), n(1, 1, ch)
+    dt = n(1, length, ch)
+
+    def both(row, bc, z, gy):
+        wide = [t.expand(-1, length, *t.shape[2:]) for t in (row, bc, z, gy)]
+        out = []
+        for x, b, zz, g in (wide, [t.contiguous() for t in wide]):
+            out.append((*gpu.selective_scan_forward(x, dt, a, b, b, z=zz),
+                        *gpu.selective_scan_backward(x, dt, a, b, b, g, z=zz)))
+        for u, v in zip(*out):
+            assert (u is v is None) or torch.equal(torch.nan_to_num(u, 7e30), torch.nan_to_num(v, 7e30))
+        return out[0]
+
+    inf = lambda t, *at: t.clone().index_put_(tuple(torch.tensor(i, device="cuda") for i in at), torch.tensor(float("inf"), device="cuda"))  # noqa: E731
+    both(row, bc, z, gy)
+    final = both(inf(row, 0, 0, 3), bc, z, gy)[1]
+    assert (final[0, 3] == float("inf")).all() and torch.isfinite(final[0, 4:]).all()
+    final = both(row.abs(), inf(bc, 0, 0, 0, 5), z, gy)[1]
+    assert (final[0, :, 5] == float("inf")).all() and torch.isfinite(final[0, :, :5]).all()
+    both(row, bc, inf(z, 0, 0, 6), gy)
+    both(row, bc, z, inf(gy, 0, 0, 7))
