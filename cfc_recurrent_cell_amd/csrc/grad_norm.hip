@@ -6,7 +6,8 @@
 // arguments, so nothing is copied to the GPU, and its workgroups stride over the chunks of
 // all of them.  Each workgroup of the first pass leaves one partial sum of squares; those
 // of the second sum the partial ones again, each for itself, which costs less than a
-// launch.
+// launch.  62 tensors of 513 MB: 123 us for the squares and 175 for the clipping, 1540 MB at
+// 5.2 TB/s; two tensors of the smallest model 3.8 and 4.1 us, of 17 for the call on the host.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -154,7 +155,8 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Batch b, const double* _
     if (ratio > 1.0) ratio = 1.0;  // not where it is NaN
     if (isinf(max_norm) && whole != whole) ratio = whole;
     const float factor = (float)ratio;
-    // from the last chunk on, which the norm has read last and the last-level cache still holds
+    // from the last chunk on, which the norm has read last and the last-level cache still holds:
+    // 513 MB 299 us instead of 306
     for (unsigned k = blockIdx.x; k < b.chunks; k += gridDim.x) {
         const unsigned chunk = b.chunks - 1 - k;
         const int t = tensor_of(b, chunk);
@@ -215,7 +217,8 @@ int check_tensors(const grad_tensor_t* tensors, int count, const float* norm, co
 }
 
 // The batch of tensors from `at` on.  Chunks as short as one step where there is little to
-// do, so that all CUs have some of it, and longer ones where a workgroup has many.
+// do, so that all CUs have some of it, and longer ones where a workgroup has many (513 MB of
+// bf16 in chunks of 16 | 4 | 1 steps: 298 | 299 | 420 us).
 Batch batch_of(const grad_tensor_t* tensors, int count, int at) {
     Batch b;
     b.count = std::min(kBatch, count - at);
