@@ -243,9 +243,9 @@ __global__ __launch_bounds__(kSumCols* kSumRows) void column_sums_kernel(const f
 }
 
 // Workgroups of the backward, each with two rows of partial sums: enough to fill the chip, few
-// enough that the sums over them stay small.  512 | 1024 | 2048 of them, in us: 9999 x 1500 84 |
-// 59 | 66, 16384 x 768 43 | 31 | 40, 99991 x 128 21.2 | 21.5 | 26.6 (where all rows at once are
-// one vector a thread; wider ones have more).
+// enough that the sums over them stay small.  bf16, in us, 512 | 1024 | 2048 of them: 16384 x 1001
+// 49 | 36 | 44, 16384 x 768 27.5 | 26.1 | 31.9, 9999 x 1536 31.5 | 30.7 | 37.6, 99991 x 128 20.3 |
+// 21.2 | 26.6; 16384 x 4096 110 | 114 | 127.
 inline long long parts_of(long long rows, long long width) {
     const long long need = (rows + rows_at_once(width) - 1) / rows_at_once(width);
     // 32-bit sums, beyond 8192 columns, are over 16 rows at most

@@ -406,7 +406,7 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
 // which is linear in e as the forward is in h, and is cut into the same stretches.
 
 // The states before each block of block_of(S) tokens, to kept[slot][group][sixteen][64 S] as
-// the exchange has them: the forward without its second pass, 66 us of the 399 of the
+// the exchange has them: the forward without its second pass, 68 us of the 399 of the
 // gradients of 4 x 2048 tokens x 2048 channels x 16 states.
 template <class TY, int S, int NW>
 __global__ __launch_bounds__(64 * NW) void scan_states_kernel(
@@ -544,7 +544,7 @@ __device__ __forceinline__ float over_quads(const float (&v)[16]) {
 // A workgroup has K times 16 channels of a group, one after the other for each block of
 // tokens, so that b's and c's gradients are summed over them before they leave it; and every
 // parts-th sequence.  Bound by the vector units: 34 issue slots an element, of which the sums
-// over channels and states are 6, the passes of h and e 12, the exponential 4; 312 us of the
+// over channels and states are 6, the passes of h and e 12, the exponential 4; 310 us of the
 // 399 above, 231 of them those slots', with two waves a SIMD between its two barriers a step.
 //
 // What only a sequence's or the kernel's beginning and end need of the arguments is read from
@@ -924,8 +924,9 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
     }
 }
 
-// What the workgroups left, summed (21 us of the 399, 67 MB): b's and c's gradients over the channels' workgroups, a's,
-// d's and dt_bias's over the sequences' parts.  A thread has an element.
+// What the workgroups left, summed (21 us of the 399, 67 MB): b's and c's gradients over the
+// channels' workgroups, a's, d's and dt_bias's over the sequences' parts.  A thread has an
+// element.
 constexpr int kSumThreads = 256;
 template <class TY>
 __global__ __launch_bounds__(kSumThreads) void scan_sums_kernel(Scan a, Grads g, int in_group, int parts,
