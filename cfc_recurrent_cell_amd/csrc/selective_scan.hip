@@ -41,6 +41,10 @@ constexpr int forward_tokens(int s) { return s <= 2 ? 8 : 4; }
 // the kernel of 16 waves 20 of its 200 us.
 constexpr long long kFewWorkgroups = 256;
 constexpr int block_of(int s) { return tokens_of(s) * waves_of(s); }
+constexpr int forward_block(int s, int waves) { return forward_tokens(s) * waves; }
+// Rows of a block are reached from its first one by 32 bits, with kNowhere behind all of them:
+// what every call's strides leave room for.  Blocks of more rows ask for themselves (reaches).
+constexpr int kBlockRows = 64;
 
 struct Scan {
     Sequences q;
@@ -148,7 +152,7 @@ struct Rows {
     // The next n of them, of which there are some (or there may be none).
     __device__ __forceinline__ Buffer some(int n) const { return buffer_of(at, (n - 1) * bytes + width); }
     __device__ __forceinline__ Buffer next(int n) const { return buffer_of(at, n > 0 ? (n - 1) * bytes + width : 0); }
-    __device__ __forceinline__ void move(int n) { at += n * bytes; }
+    __device__ __forceinline__ void move(int n) { at += (long long)n * bytes; }
 };
 // A lane's places in a block: its element of the rows row, row + 4, ...
 template <class TY, int Q>
@@ -267,7 +271,8 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
     const float* __restrict__ decay, const typename TY::S* __restrict__ b, const typename TY::S* __restrict__ c,
     const float* __restrict__ d, const typename TY::S* __restrict__ z, const float* __restrict__ dt_bias,
     const float* initial, typename TY::S* __restrict__ y, float* final) {
-    constexpr int T = forward_tokens(S), Q = T / 4, BT = T * NW, F = (S + NW - 1) / NW;
+    constexpr int T = forward_tokens(S), Q = T / 4, BT = forward_block(S, NW), F = (S + NW - 1) / NW;
+    static_assert(NW == 16 || BT <= kBlockRows, "rows of a block");
     __shared__ Lanes<S> product[NW], made[NW];  // P and h' of each wave
     __shared__ alignas(16) float bc[NW][2][T * 4 * S];
     const long long count = (long long)a.groups * sixteens * a.q.n_seq, index = on_die(blockIdx.x, count);
@@ -414,6 +419,7 @@ __global__ __launch_bounds__(64 * NW) void scan_states_kernel(
     const float* __restrict__ decay, const typename TY::S* __restrict__ b, const float* __restrict__ dt_bias,
     const float* __restrict__ initial, float* __restrict__ kept) {
     constexpr int BT = block_of(S), T = BT / NW, Q = T / 4, F = (S + NW - 1) / NW;
+    static_assert(BT <= kBlockRows, "rows of a block");
     __shared__ Lanes<S> product[2][NW], made[2][NW];
     __shared__ alignas(16) float bc[NW][T * 4 * S];
     const long long count = (long long)a.groups * sixteens * a.q.n_seq, index = on_die(blockIdx.x, count);
@@ -568,6 +574,7 @@ template <class TY, int S, int K>
 __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(BackwardArgs) {
     constexpr int T = tokens_of(S), NW = waves_of(S), Q = T / 4, BT = T * NW, F = (2 * S + NW - 1) / NW;
     constexpr int N16 = (T * S + 15) / 16;
+    static_assert(BT <= kBlockRows, "rows of a block");
     using E = typename TY::S;
     __shared__ Lanes<S> product[NW], made[NW], given[NW];  // P, h' and e' of each wave
     __shared__ Lanes<S> carry[K], rate[K];                 // e before a block, and log2(e) a
@@ -1134,6 +1141,15 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
 constexpr long long kMaxTokens = (1LL << 31) - (1LL << 16);
 constexpr long long kMaxBlocks = (1LL << 32) / 512 - 8;  // a grid has fewer than 2^32 work-items
 
+// Whether blocks of so many rows of every argument and output are less than 2^31 bytes.
+bool reaches(const selective_scan_shape_t* p, const Scan& a, int rows) {
+    long long far = p->channels;
+    if (!a.single)
+        for (const long long stride : {p->x_stride, p->dt_stride, p->z_stride, p->grad_y_stride, p->b_stride_t, p->c_stride_t})
+            far = std::max(far, stride);
+    return far <= INT_MAX / (rows * size_of(p->type)) - (long long)p->channels - p->state;
+}
+
 int check_shape(const selective_scan_shape_t* p, bool step, Scan* a) {
     if (!p) return CFC_ERR_NULL;
     if (p->type != CFC_TYPE_F32 && p->type != CFC_TYPE_BF16 && p->type != CFC_TYPE_F16) return CFC_ERR_UNSUPPORTED;
@@ -1156,15 +1172,9 @@ int check_shape(const selective_scan_shape_t* p, bool step, Scan* a) {
     a->clear = p->offsets ? p->clear_rest : 0;
     a->xt = p->x_stride, a->dtt = p->dt_stride, a->zt = p->z_stride, a->gt = p->grad_y_stride;
     a->bt = p->b_stride_t, a->bg = p->b_stride_g, a->ct = p->c_stride_t, a->cg = p->c_stride_g;
-    // a block's rows are reached from its first one by 32 bits, which rows alone do not need
-    const int size = size_of(p->type);
     a->single = (p->offsets ? p->n_tokens : step ? 1 : p->seq_len) <= 1;
     a->overlap = a->single || p->b_stride_t < p->state || p->c_stride_t < p->state;
-    long long far = p->channels;
-    if (!a->single)
-        for (const long long stride : {p->x_stride, p->dt_stride, p->z_stride, p->grad_y_stride, p->b_stride_t, p->c_stride_t})
-            far = std::max(far, stride);
-    if (far + p->channels + p->state > INT_MAX / (64 * size)) return CFC_ERR_UNSUPPORTED;
+    if (!reaches(p, *a, kBlockRows)) return CFC_ERR_UNSUPPORTED;
     const long long groups = (long long)a->groups * ((a->share + kGroupCh - 1) / kGroupCh);
     return groups * std::max(1, a->q.n_seq) > kMaxBlocks ? CFC_ERR_UNSUPPORTED : CFC_OK;
 }
@@ -1276,7 +1286,7 @@ extern "C" int selective_scan_forward(const selective_scan_shape_t* shape, const
                                final_state);
         };
         if constexpr (S <= 8) {
-            if (count <= kFewWorkgroups && !a.overlap) {
+            if (count <= kFewWorkgroups && !a.overlap && reaches(shape, a, forward_block(S, 16))) {
                 go(scan_kernel<TY, S, 16>, 16);
                 return launch_status();
             }
