@@ -16,6 +16,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -241,6 +242,18 @@ __device__ __forceinline__ void get_states(const float* p, float (&h)[S]) {
     }
 }
 
+// The sum of a stretch's steps from four lanes' own, finite where the steps are: a rate of zero (that
+// of a lane's states behind `state` among them) keeps its state.  Only rates under 2^-120 tell the
+// largest float from what a sum beyond it should be.
+__device__ __forceinline__ float steps_of(float all) {
+    all += quad_perm<0xB1>(all);
+    all += quad_perm<0x4E>(all);
+    return __builtin_amdgcn_fmed3f(all, -FLT_MAX, FLT_MAX);
+}
+// A state behind a stretch, where going along all of them has ended in no number: P may be infinite
+// and the state zero.  (Taken at every stretch, the choice would cost 8192 tokens 242 us, not 195.)
+__device__ __forceinline__ float behind(float p, float h, float made) { return h == 0.0f ? made : fmaf(p, h, made); }
+
 // The waves' exchange, between two barriers: a thread has one or several of the 64 S states
 // of the workgroup's channels (of a state's gradients, with `back`), and goes along the
 // waves' stretches, leaving each the state that it begins with in the place of what it made
@@ -250,11 +263,21 @@ __device__ __forceinline__ float along(const Lanes<S> (&product)[NW], Lanes<S> (
     float p[NW], m[NW];
 #pragma unroll
     for (int i = 0; i < NW; ++i) p[i] = product[i].x[f], m[i] = made[i].x[f];
+    const float begin = h;
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
         const int i = back ? NW - 1 - k : k;
         made[i].x[f] = h;
         h = fmaf(p[i], h, m[i]);
+    }
+    if (__builtin_expect(__any(h != h), 0)) {
+        h = begin;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const int i = back ? NW - 1 - k : k;
+            made[i].x[f] = h;
+            h = behind(p[i], h, m[i]);
+        }
     }
     return h;
 }
@@ -263,8 +286,8 @@ __device__ __forceinline__ float along(const Lanes<S> (&product)[NW], Lanes<S> (
 // Bound by the vector units: an element (token, channel, state) takes an exponential (four
 // issue slots), its argument's product, D x b, the two passes' multiply-adds and c's, and a
 // token and channel's softplus and gate about 60 slots over its 16 states: 13 slots, of
-// which 8192 tokens x 4096 channels x 16 states need 177 us.  Measured 180 in four sequences,
-// 202 in one (1.33 TB/s).
+// which 8192 tokens x 4096 channels x 16 states need 177 us.  Measured 181 in four sequences,
+// 195 in one (1.38 TB/s).
 template <class TY, int S, int NW>
 __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16 ? 4 : 6) void scan_kernel(
     Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
@@ -341,8 +364,7 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
             gate[i] = z ? zv * gate_of<TY>(zv) : 1.0f;
         }
         fetch(left - BT);  // while this block is worked on
-        all += quad_perm<0xB1>(all);
-        all += quad_perm<0x4E>(all);
+        all = steps_of(all);
         float at[T][S], add[T][S], hl[S], pw[S];
 #pragma unroll
         for (int s = 0; s < S; ++s) hl[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);
@@ -479,8 +501,7 @@ __global__ __launch_bounds__(64 * NW) void scan_states_kernel(
             all += step[i];
         }
         fetch(left - BT);  // while this block is worked on
-        all += quad_perm<0xB1>(all);
-        all += quad_perm<0x4E>(all);
+        all = steps_of(all);
         float hl[S], pw[S];
 #pragma unroll
         for (int s = 0; s < S; ++s) hl[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);
@@ -507,8 +528,13 @@ __global__ __launch_bounds__(64 * NW) void scan_states_kernel(
             if (w * 64 + i * 64 * NW < 64 * S) {
                 const int f = threadIdx.x + i * 64 * NW;
                 to[f] = h[i];
+                const float begin = h[i];
 #pragma unroll
                 for (int k = 0; k < NW; ++k) h[i] = fmaf(product[turn][k].x[f], h[i], made[turn][k].x[f]);
+                if (__builtin_expect(__any(h[i] != h[i]), 0)) {
+                    h[i] = begin;
+                    for (int k = 0; k < NW; ++k) h[i] = behind(product[turn][k].x[f], h[i], made[turn][k].x[f]);
+                }
             }
     }
 }
@@ -707,8 +733,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
                         kept -= pitch;
                         fetch(BT, 0);
                     }
-                    all += quad_perm<0xB1>(all);
-                    all += quad_perm<0x4E>(all);
+                    all = steps_of(all);
                     float at[T][S], add[T][S], h[S], e[S], pw[S];
 #pragma unroll
                     for (int s = 0; s < S; ++s) h[s] = e[s] = 0.0f, pw[s] = exp2_of(all * a2[s]);

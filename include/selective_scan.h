@@ -20,7 +20,9 @@
  * (capturable), argument errors (CFC_* codes of cfc.h) before anything is enqueued, no
  * atomics and fixed summation orders, so equal inputs give equal bits.  Arithmetic and
  * states are those of 32-bit floats; the gradients of a, d and dt_bias are summed in 64
- * bits over groups of tokens.
+ * bits over groups of tokens.  The decays of up to 8 tokens in a row are multiplied with each
+ * other before they meet a state (or its gradient): where states grow so much that this product
+ * passes 32 bits, one that is not zero becomes infinite.
  */
 #ifndef SELECTIVE_SCAN_AMD_H
 #define SELECTIVE_SCAN_AMD_H
