@@ -69,7 +69,8 @@ def clip_grad_norm(grads, max_norm: float, out=None, norm=None, workspace=None, 
     """norm [] as grad_norm's, of the gradients as they were given; each becomes
     g * min(1, max_norm / (norm + 1e-6)), where it is or in the tensor of ``out`` (one
     for each, of its type and shape) at its place.  Nothing is read back to the host.
-    Where the norm is NaN all outputs are, where it is infinite the factor is 0."""
+    Where the norm is NaN all outputs are, where it is infinite the factor is 0 (and 1 with
+    an infinite ``max_norm``, which clips nothing)."""
     if not max_norm >= 0:
         raise ValueError(f"max_norm must be at least 0, got {max_norm}")
     return _run("clip_grad_norm", grads, out, norm, workspace, stream, float(max_norm))

@@ -150,8 +150,9 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Batch b, const double* _
                                                         float max_norm, float* __restrict__ norm) {
     __shared__ double red[kThreads / 64];
     const double whole = sqrt(total_of(part, parts, red));
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)whole;
-    double ratio = isinf(max_norm) ? 1.0 : (double)max_norm / (whole + 1e-6);
+    const float given = (float)whole;  // the norm that the caller gets: infinite where it passes 32 bits
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = given;
+    double ratio = isinf(max_norm) ? 1.0 : isinf(given) ? 0.0 : (double)max_norm / (whole + 1e-6);
     if (ratio > 1.0) ratio = 1.0;  // not where it is NaN
     if (isinf(max_norm) && whole != whole) ratio = whole;
     const float factor = (float)ratio;

@@ -45,7 +45,8 @@ int grad_norm(const grad_tensor_t *tensors, int count, float *norm, void *worksp
 /* norm [1] as above, of the gradients as they were given, and every tensor's `out`.
  *   max_norm  >= 0, or infinite: nothing is clipped
  * Outputs must not overlap each other, nor any gradient but their own.  Where the norm is
- * NaN all outputs are; where it is infinite the factor is 0. */
+ * NaN all outputs are; where it is infinite, that of finite gradients past 32 bits too, the
+ * factor is 0, and with an infinite max_norm 1. */
 int clip_grad_norm(const grad_tensor_t *tensors, int count, float max_norm, float *norm, void *workspace,
                    long long workspace_bytes, hipStream_t stream);
 
