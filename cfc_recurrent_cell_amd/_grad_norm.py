@@ -22,9 +22,11 @@ def _tensors(grads, out, norm):
             raise ValueError(f"out has {len(outs)} tensors, grads {len(grads)}")
     if not grads and norm is None:
         raise ValueError("grads must have at least one tensor, where no buffer is given for the norm")
+    if not grads:
+        check(norm, "norm", F32, None, ())
     first = grads[0] if grads else norm
     if not isinstance(first, torch.Tensor):
-        raise TypeError("grads[0] must be a torch.Tensor" if grads else "norm must be a torch.Tensor")
+        raise TypeError("grads[0] must be a torch.Tensor")
     dev = first.device
     flat = []  # the descriptions' words: a tensor's are set at once, and not field by field
     for i, (g, o) in enumerate(zip(grads, outs)):
