@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(Batch b, const double* _
 }
 
 // ---------------------------------------------------------- host helpers
-inline int batches_of(int count) { return (count + kBatch - 1) / kBatch; }
+inline int batches_of(int count) { return count / kBatch + (count % kBatch != 0); }
 
 int check_tensors(const grad_tensor_t* tensors, int count, const float* norm, const void* workspace,
                   long long workspace_bytes, bool clip) {

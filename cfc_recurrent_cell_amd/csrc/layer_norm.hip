@@ -21,6 +21,8 @@
 
 namespace {
 
+static_assert(LAYER_NORM_MAX_WIDTH == kMaxRowWidth, "the width that check_sizes holds rows to");
+
 __device__ __forceinline__ float plus(float p, float q) { return p + q; }
 
 // over_row of two sums at once, with one barrier.

@@ -23,6 +23,8 @@
 
 namespace {
 
+static_assert(RMS_NORM_MAX_WIDTH == kMaxRowWidth, "the width that check_sizes holds rows to");
+
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));

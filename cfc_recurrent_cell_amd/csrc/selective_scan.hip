@@ -97,12 +97,6 @@ __device__ __forceinline__ void load_states(const float* row, int n, int state, 
 #pragma unroll
     for (int s = 0; s < S; ++s) h[s] = n + s < state ? row[n + s] : none;
 }
-template <int S>
-__device__ __forceinline__ void store_states(float* row, int n, int state, const float (&h)[S]) {
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-        if (n + s < state) row[n + s] = h[s];
-}
 
 // What a wave's lanes write to LDS for each other: its own LDS instructions go in order.
 __device__ __forceinline__ void wave_fence() {
