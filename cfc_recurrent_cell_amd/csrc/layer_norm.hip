@@ -163,9 +163,11 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
             unpack<TH, 8, TAIL>(hr[v], c, width, n[v]);
             unpack<TX, 8, TAIL>(yr[v], c, width, d[v]);
             if (gh) unpack<TH, 8, TAIL>(gr[v], c, width, o[v]);
+            const float rsv = TAIL || c < width ? rsn : 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                n[v][j] = (n[v][j] - m) * rsn;  // columns behind the last have d = 0
+                // columns behind the last have d = 0, and n = 0: -m * rstd may be infinite
+                n[v][j] = !TAIL || c + j < width ? (n[v][j] - m) * rsv : 0.0f;
                 if (in) {
                     gw[v][j] += d[v][j] * n[v][j];
                     gb[v][j] += d[v][j];
