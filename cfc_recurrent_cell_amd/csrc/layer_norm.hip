@@ -15,6 +15,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "columns.h"
 #include "elements.h"
 #include "layer_norm.h"
 #include "rows.h"
@@ -222,29 +223,17 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
     }
 }
 
-// Columns of part [parts, 2 width] summed in 64 bits: the first half into gw, the other
-// into gb (or nowhere).  32 columns a workgroup (a cache line of each row), 32 rows at once.
-constexpr int kSumCols = 32, kSumRows = 32;
-__global__ __launch_bounds__(kSumCols* kSumRows) void column_sums_kernel(const float* __restrict__ part, int parts,
-                                                                         int width, float* __restrict__ gw,
-                                                                         float* __restrict__ gb) {
-    __shared__ double red[kSumRows][kSumCols + 1];
-    const int sub = threadIdx.x % kSumCols, slot = threadIdx.x / kSumCols;
-    const int c = blockIdx.x * kSumCols + sub;
-    double x = 0.0;
-    if (c < 2 * width)
-#pragma unroll 4
-        for (int r = slot; r < parts; r += kSumRows) x += part[2LL * r * width + c];
-    red[slot][sub] = x;
-    __syncthreads();
-    if (slot != 0 || c >= 2 * width) return;
-#pragma unroll
-    for (int i = 1; i < kSumRows; ++i) x += red[i][sub];
-    if (c < width)
-        gw[c] = (float)x;
-    else if (gb)
-        gb[c - width] = (float)x;
-}
+// Where the sums of the columns go: the first half into gw, the other into gb (or nowhere).
+struct Weights {
+    float *gw, *gb;
+    int width;
+    __device__ __forceinline__ void operator()(long long c, float x) const {
+        if (c < width)
+            gw[c] = x;
+        else if (gb)
+            gb[c - width] = x;
+    }
+};
 
 // Workgroups of the backward, each with two rows of partial sums: enough to fill the chip, few
 // enough that the sums over them stay small.  bf16, in us, 512 | 1024 | 2048 of them: 16384 x 1001
@@ -349,7 +338,6 @@ extern "C" int layer_norm_backward(int type, int stream_type, long long rows, lo
         });
         if (e != CFC_OK) return e;
     }
-    hipLaunchKernelGGL(column_sums_kernel, dim3((unsigned)((2 * width + kSumCols - 1) / kSumCols)),
-                       dim3(kSumCols * kSumRows), 0, stream, part, (int)parts, (int)width, grad_weight, grad_bias);
+    sum_columns(part, parts, 2 * width, Weights{grad_weight, grad_bias, (int)width}, stream);
     return launch_status();
 }

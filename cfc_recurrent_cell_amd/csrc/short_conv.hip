@@ -14,6 +14,7 @@
 #include <climits>
 #include <cstdint>
 
+#include "columns.h"
 #include "elements.h"
 #include "functions.h"
 #include "sequences.h"
@@ -339,32 +340,20 @@ __global__ __launch_bounds__(kThreads) void conv_backward_kernel(
     for (int j = 0; j <= W; ++j) store<F32, V, TAIL>(part + (at * (W + 1) + j) * a.channels, c, a.channels, sum[j]);
 }
 
-// Columns of part [tiles, width + 1, channels] summed in 64 bits: the last of the width + 1
-// into gb (or nowhere), the others into gw [channels, width].
-constexpr int kSumCols = 32, kSumRows = 32;
-__global__ __launch_bounds__(kSumCols* kSumRows) void conv_sums_kernel(const float* __restrict__ part, long long tiles,
-                                                                       int channels, int width, float* __restrict__ gw,
-                                                                       float* __restrict__ gb) {
-    __shared__ double red[kSumRows][kSumCols + 1];
-    const long long columns = (long long)(width + 1) * channels;
-    const int sub = threadIdx.x % kSumCols, slot = threadIdx.x / kSumCols;
-    const long long col = (long long)blockIdx.x * kSumCols + sub;
-    double x = 0.0;
-    if (col < columns)
-#pragma unroll 4
-        for (long long r = slot; r < tiles; r += kSumRows) x += part[r * columns + col];
-    red[slot][sub] = x;
-    __syncthreads();
-    if (slot != 0 || col >= columns) return;
-#pragma unroll
-    for (int i = 1; i < kSumRows; ++i) x += red[i][sub];
-    const int j = (int)(col / channels);
-    const long long ch = col % channels;
-    if (j < width)
-        gw[ch * width + j] = (float)x;
-    else if (gb)
-        gb[ch] = (float)x;
-}
+// Where the sums over the tiles of [width + 1, channels] go: the last of the width + 1 into gb (or
+// nowhere), the others into gw [channels, width].
+struct Weights {
+    float *gw, *gb;
+    int channels, width;
+    __device__ __forceinline__ void operator()(long long c, float x) const {
+        const int j = (int)(c / channels);
+        const long long ch = c % channels;
+        if (j < width)
+            gw[ch * width + j] = x;
+        else if (gb)
+            gb[ch] = x;
+    }
+};
 
 template <class TY, int W, bool TAIL>
 __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long waves, const typename TY::S* __restrict__ x,
@@ -570,9 +559,7 @@ extern "C" int short_conv_backward(const short_conv_shape_t* shape, const void* 
             hipLaunchKernelGGL((conv_backward_kernel<TY, W, TAIL>), dim3(dealt(blocks_of(waves))), dim3(kThreads), 0, stream,
                                a, waves, tiles, (const S*)x, (const S*)weight, (const S*)bias, (const S*)initial_state,
                                (const S*)grad_y, (const S*)grad_final_state, (S*)grad_x, (S*)grad_initial_state, part);
-        const long long columns = (long long)(W + 1) * a.channels;
-        hipLaunchKernelGGL(conv_sums_kernel, dim3((unsigned)((columns + kSumCols - 1) / kSumCols)),
-                           dim3(kSumCols * kSumRows), 0, stream, part, tiles, a.channels, W, grad_weight, grad_bias);
+        sum_columns(part, tiles, (long long)(W + 1) * a.channels, Weights{grad_weight, grad_bias, a.channels, W}, stream);
         return launch_status();
     });
 }
