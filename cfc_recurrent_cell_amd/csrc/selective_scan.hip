@@ -1108,9 +1108,7 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
     };
     Row r;
     fetch(r);
-    if (slots)  // the first row of a slot takes all
-        for (int j = 0; j < row; j += 64)
-            if (__ballot(j + lane < row && slots[min(j + lane, rows - 1)] == slot)) return;
+    if (slots && row_of_slot(slots, slot, 0, row) < row) return;  // the first row of a slot takes all
 #pragma unroll
     for (int i = 0; i < C; ++i)
 #pragma unroll
@@ -1136,16 +1134,8 @@ __global__ __launch_bounds__(kStepThreads) void scan_step_kernel(
         if (z) out *= r.z * gate_of<TY>(r.z);
         if (own) y[(long long)row * a.channels + at] = TY::store(out);
         if (!slots) break;
-        int next = rows;
-        for (int j = row + 1; j < rows; j += 64) {
-            const unsigned long long m = __ballot(j + lane < rows && slots[min(j + lane, rows - 1)] == slot);
-            if (m) {
-                next = j + __builtin_ctzll(m);
-                break;
-            }
-        }
-        if (next >= rows) break;
-        row = next;
+        row = row_of_slot(slots, slot, row + 1, rows);
+        if (row >= rows) break;
         fetch(r);
     }
 #pragma unroll

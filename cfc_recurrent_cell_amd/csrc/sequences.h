@@ -43,6 +43,20 @@ __device__ __forceinline__ int sequence_of(const Sequences& q, int t) {
     return lo;
 }
 
+// The first row from `from` on, of `rows` in all, that names `slot`, or `rows`; by a whole wave.  Rows
+// of a step that name one slot are taken one after the other by the waves of the first of them, so
+// each wave looks through all the slots: for 4096 channels x 16 states in bf16 256 rows of the scan
+// take 34 us with slots and 31 without, 1024 146 and 104, 4096 979 and 422; 4096 rows of the
+// convolution of 8192 channels 357 and 94.
+__device__ __forceinline__ int row_of_slot(const int* slots, int slot, int from, int rows) {
+    const int lane = threadIdx.x & 63;
+    for (int j = from; j < rows; j += 64) {
+        const unsigned long long m = __ballot(j + lane < rows && slots[min(j + lane, rows - 1)] == slot);
+        if (m) return j + __builtin_ctzll(m);
+    }
+    return rows;
+}
+
 // ---------------------------------------------------------- host helpers
 inline bool mul_ok(long long a, long long b, long long* r) {
     if (a < 0 || b < 0) return false;

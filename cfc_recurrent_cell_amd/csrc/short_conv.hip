@@ -375,8 +375,7 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long w
             store<TY, V, TAIL>(y + (long long)row * a.channels, c, a.channels, none);
             return;
         }
-        for (int j = 0; j < row; j += 64)  // the first row of a slot takes all
-            if (__ballot(j + lane < row && slots[min(j + lane, rows - 1)] == slot)) return;
+        if (row_of_slot(slots, slot, 0, row) < row) return;  // the first row of a slot takes all
     }
     float w[W][V], b[V], win[W - 1][V];
     load_weights<TY, W, V, TAIL>(weight, c, a.channels, w);
@@ -395,15 +394,7 @@ __global__ __launch_bounds__(kThreads) void conv_step_kernel(Conv a, long long w
         }
         store<TY, V, TAIL>(y + (long long)row * a.channels, c, a.channels, p);
         if (!slots) break;
-        int next = rows;
-        for (int j = row + 1; j < rows; j += 64) {
-            const unsigned long long m = __ballot(j + lane < rows && slots[min(j + lane, rows - 1)] == slot);
-            if (m) {
-                next = j + __builtin_ctzll(m);
-                break;
-            }
-        }
-        row = next;
+        row = row_of_slot(slots, slot, row + 1, rows);
     }
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) store<TY, V, TAIL>(state + (long long)j * a.channels, c, a.channels, win[j]);
