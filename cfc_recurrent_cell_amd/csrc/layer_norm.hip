@@ -114,8 +114,9 @@ __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_kernel(
 
 // A row's loads are in flight while the row before is worked on.
 // The weight's and the bias's terms are summed over the workgroup's rows in registers,
-// in 64 bits, then over its row slots through LDS, into part[2 * blockIdx.x] and the
-// row behind it; column_sums_kernel sums those.
+// in 64 bits (beyond 8192 columns in 32, over 16 rows at most), then over its row slots
+// through LDS, and rounded to 32 bits into part[2 * blockIdx.x] and the row behind it;
+// column_sums_kernel sums those in 64.
 template <class TX, class TH, int TPR, int NV, bool TAIL>
 __global__ __launch_bounds__(threads_of(TPR)) void layer_norm_backward_kernel(
     long long rows, int width, const typename TX::S* __restrict__ gy, const typename TH::S* __restrict__ h,

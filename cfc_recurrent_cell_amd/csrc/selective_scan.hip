@@ -36,10 +36,13 @@ constexpr int tokens_of(int s) { return s <= 4 ? 8 : 4; }
 constexpr int waves_of(int s) { return s <= 8 ? 8 : 4; }
 constexpr int forward_tokens(int s) { return s <= 2 ? 8 : 4; }
 // Workgroups (16 channels of a sequence each) up to which each has 16 waves instead of 8, since
-// there is at most one for a CU.  4096 channels x 16 states, bf16, in us, 16 waves | 8: one
-// sequence of 8192 tokens (256 workgroups) 200 | 250, two of 2048 (512) 106 | 99, four (1024)
-// 209 | 180.  Overlapping rows of b and c are left to 8: the branch for them (Shared::load) costs
-// the kernel of 16 waves 20 of its 200 us.
+// there is at most one for a CU.  bf16, in us, 16 waves | 8: 4096 tokens in 256 workgroups with 4
+// states 73 | 94, 8 states 79 | 100, 16 states 104 | 129, 32 states 180 | 218 (the kernel of 16
+// waves spills 11 registers there, and is faster all the same); in 16 workgroups 54 | 78, 61 | 90,
+// 96 | 128, 175 | 213; 2048 tokens in 512 workgroups 75 | 75, 82 | 83, 110 | 107, 186 | 172.  The
+// gradients' states of 4096 tokens in 256 workgroups, with all of the gradients: 4 states 273 | 282,
+// 16 states 495 | 510; 2048 in 512 the same.  Overlapping rows of b and c are left to 8: the branch
+// for them (Shared::load) costs the kernel of 16 waves 20 of its 200 us.
 constexpr long long kFewWorkgroups = 256;
 constexpr int block_of(int s) { return tokens_of(s) * waves_of(s); }
 constexpr int forward_block(int s, int waves) { return forward_tokens(s) * waves; }
@@ -277,11 +280,11 @@ __device__ __forceinline__ float along(const Lanes<S> (&product)[NW], Lanes<S> (
 }
 
 // -------------------------------------------------------------------- forward
-// Bound by the vector units: an element (token, channel, state) takes an exponential (four
-// issue slots), its argument's product, D x b, the two passes' multiply-adds and c's, and a
-// token and channel's softplus and gate about 60 slots over its 16 states: 13 slots, of
-// which 8192 tokens x 4096 channels x 16 states need 177 us.  Measured 181 in four sequences,
-// 195 in one (1.38 TB/s).
+// Bound by the vector units: an element (token, channel, state) takes an exponential, its
+// argument's product, D x b, the two passes' multiply-adds and c's, and a token and channel's
+// softplus and gate about 60 instructions over its 16 states: 10.3 instructions by the counters,
+// 11.8 issue slots, for which 8192 tokens x 4096 channels x 16 states keep the vector units
+// busy 161 us of 202.  Measured 181 in four sequences, 195 in one (1.38 TB/s).
 template <class TY, int S, int NW>
 __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16 ? 4 : 6) void scan_kernel(
     Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
@@ -427,8 +430,8 @@ __global__ __launch_bounds__(64 * NW, S == 16 ? 2 : S == 8 || S == 2 || NW == 16
 // which is linear in e as the forward is in h, and is cut into the same stretches.
 
 // The states before each block of block_of(S) tokens, to kept[slot][group][sixteen][64 S] as
-// the exchange has them: the forward without its second pass, 68 us of the 399 of the
-// gradients of 4 x 2048 tokens x 2048 channels x 16 states.
+// the exchange has them: the forward without its second pass, 69 us of the 391 of the
+// gradients of 4 x 2048 tokens x 2048 channels x 16 states, 73 % of them the vector units'.
 template <class TY, int S, int NW>
 __global__ __launch_bounds__(64 * NW) void scan_states_kernel(
     Scan a, int sixteens, const typename TY::S* __restrict__ x, const typename TY::S* __restrict__ dt,
@@ -569,9 +572,10 @@ __device__ __forceinline__ float over_quads(const float (&v)[16]) {
 
 // A workgroup has K times 16 channels of a group, one after the other for each block of
 // tokens, so that b's and c's gradients are summed over them before they leave it; and every
-// parts-th sequence.  Bound by the vector units: 34 issue slots an element, of which the sums
-// over channels and states are 6, the passes of h and e 12, the exponential 4; 310 us of the
-// 399 above, 231 of them those slots', with two waves a SIMD between its two barriers a step.
+// parts-th sequence.  Bound by the vector units: 32 instructions an element by the counters, 34.7
+// issue slots, of which the sums over channels and states are 6 and the passes of h and e 12;
+// 302 us of the 391 above, 76 % of them those slots', with two waves a SIMD between its two
+// barriers a step.
 //
 // What only a sequence's or the kernel's beginning and end need of the arguments is read from
 // their segment again there (`fresh`): kept in scalar registers all along, it had those of the
@@ -950,7 +954,7 @@ __global__ __launch_bounds__(64 * waves_of(S)) void scan_backward_kernel(Backwar
     }
 }
 
-// What the workgroups left, summed (21 us of the 399, 67 MB): b's and c's gradients over the
+// What the workgroups left, summed (21 us of the 391, 68 MB): b's and c's gradients over the
 // channels' workgroups, a's, d's and dt_bias's over the sequences' parts.  A thread has an
 // element.
 constexpr int kSumThreads = 256;
@@ -1222,7 +1226,7 @@ inline int lane_states(int state) { return state <= 4 ? 1 : state <= 8 ? 2 : sta
 
 // How many times 16 channels a workgroup of the backward has: more of them leave fewer partial
 // sums of b's and c's gradients, as long as all CUs have one (4 x 2048 tokens, bf16, us, with one,
-// 2 and 4: 2048 channels 440, 399; 4096 channels 866, 788, 730).  Beyond 16 states LDS holds one.
+// 2 and 4: 2048 channels 440, 391; 4096 channels 880, 779, 746).  Beyond 16 states LDS holds one.
 inline int sixteens_at_once(const Scan& a) {
     if (a.state > 16) return 1;
     const long long all = (long long)a.groups * sixteens_of(a) * a.q.n_seq;

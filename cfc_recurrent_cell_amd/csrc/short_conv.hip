@@ -5,9 +5,10 @@
 // has a tile of tokens and 4 channels a lane, four to eight rows' loads in flight at once,
 // and the last width - 1 inputs in registers as it goes from token to token.  Rows that a
 // tile shares with the one before are read twice, mostly from the cache.  16 packed prompts,
-// 6111 tokens of 8192 channels in bf16 (200 MB): 46 us, 4.4 TB/s; the gradients of 4 x 2048
-// tokens x 4096 channels (201 MB) 64 us and 7 for the sums of the weight's; a step of one row 2.9,
-// latency.
+// 5969 tokens of 8192 channels in bf16 (197 MB): 46 us, 4.3 TB/s (a call whose inputs all come
+// from memory 51, one whose inputs the last-level cache holds 44); the gradients of 4 x 2048
+// tokens x 4096 channels (201 MB) 64 us and 6 for the sums of the weight's (74 and 56); a step of
+// one row 2.8, latency.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

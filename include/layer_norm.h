@@ -8,8 +8,10 @@
  *   y    = (h - mean) * rstd * weight + bias
  *
  * The conventions of rms_norm.h hold.  Arithmetic and a row's sums are those of
- * 32-bit floats, the variance from differences to the mean; the weight's and the
- * bias's gradients are summed in 64 bits, in a fixed order.
+ * 32-bit floats, the variance from differences to the mean.  The weight's and the
+ * bias's gradients are summed in a fixed order, in 64 bits over a group of rows (beyond
+ * 8192 columns in 32 bits over at most 16 rows); each group's sum is rounded to 32 bits,
+ * and those are summed in 64.
  */
 #ifndef LAYER_NORM_AMD_H
 #define LAYER_NORM_AMD_H

@@ -19,8 +19,9 @@
  * allocated, synchronised or copied to the host, kernels only enqueued on `stream`
  * (capturable), argument errors (CFC_* codes of cfc.h) before anything is enqueued, no
  * atomics and fixed summation orders, so equal inputs give equal bits.  Arithmetic and
- * states are those of 32-bit floats; the gradients of a, d and dt_bias are summed in 64
- * bits over groups of tokens.  The decays of up to 8 tokens in a row are multiplied with each
+ * states are those of 32-bit floats.  The gradients of a, d and dt_bias are summed in 32 bits
+ * over the 4 or 8 tokens of a wave and in 64 over those; what a workgroup has of them is rounded
+ * to 32 bits and summed in 64 again.  The decays of up to 8 tokens in a row are multiplied with each
  * other before they meet a state (or its gradient): where states grow so much that this product
  * passes 32 bits, one that is not zero becomes infinite.
  */
@@ -68,7 +69,7 @@ typedef struct selective_scan_shape {
     int state;            /* 1 ... SELECTIVE_SCAN_MAX_STATE */
     int softplus;         /* 1, or 0: D = dt + dt_bias */
     int clear_rest;       /* SELECTIVE_SCAN_CLEAR_*: outputs whose rows behind the last packed sequence become
-                             zeros; the others' are left as they were */
+                             zeros; the others' are left as they were, and all with n_seq = 0 */
     long long x_stride, dt_stride, z_stride, grad_y_stride;
     long long b_stride_t, b_stride_g, c_stride_t, c_stride_g;
 } selective_scan_shape_t;

@@ -53,7 +53,8 @@ typedef struct short_conv_shape {
     int channels; /* >= 1 */
     int width;    /* 2, 3 or 4 */
     int silu;     /* 1: y = p sigmoid(p); 0: y = p */
-    int clear_rest; /* rows of y and grad_x behind the last packed sequence: 1 makes them zeros, 0 leaves them */
+    int clear_rest; /* rows of y and grad_x behind the last packed sequence: 1 makes them zeros, 0 leaves them
+                       (as n_seq = 0 does) */
     long long x_stride, grad_y_stride;
 } short_conv_shape_t;
 
